@@ -76,6 +76,18 @@ def _load_library():
     lib.ep_layout_dispatch.restype = I
     lib.ep_layout_dispatch.argtypes = [P, I, I, I, I, I, I, P, SZ, P, P, P, P, P, P, I, P, I, I, I,
                                        ctypes.POINTER(_DispatchOut), ctypes.POINTER(P), P]
+    lib.ep_combine_backward.restype = I
+    lib.ep_combine_backward.argtypes = [P, P, I, P, I64, P, P, P, P]
+    lib.ep_expert_ffn_workspace_bytes.restype = SZ
+    lib.ep_expert_ffn_workspace_bytes.argtypes = [I64, I, I, I]
+    lib.ep_expert_ffn.restype = I
+    lib.ep_expert_ffn.argtypes = [P, P, P, I, I, I, I64, P, P, P, P, P, P, P, SZ, P]
+    lib.ep_expert_ffn_backward.restype = I
+    lib.ep_expert_ffn_backward.argtypes = [P, P, P, P, I, I, I64, P, P, P, P, P, P, SZ, P]
+    lib.ep_adapter_workspace_bytes.restype = SZ
+    lib.ep_adapter_workspace_bytes.argtypes = [I, I, I, I]
+    lib.ep_adapter.restype = I
+    lib.ep_adapter.argtypes = [P, P, I, P, P, I, I, P, P, P, P, SZ, P]
     return lib
 
 
@@ -569,11 +581,197 @@ def ep_combine_reduce(handle: Handle, partials=None, local=None, bias=None, out=
     return out
 
 
+def _device(handle):
+    """The GPU of a handle, where every tensor of its calls must be; it must be the current one (the stream is its)."""
+    device = handle.topk_idx.device
+    if device.type == "cuda" and device.index != (_cur_device or torch.cuda.current_device)():
+        raise ValueError("the handle's device %s is not the current device" % device)
+    return device
+
+
+def _matrix(t, dtype, name, device):
+    """A 2-D tensor [rows, columns]; returns its columns."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    _need(t, dtype, name, device)
+    return t.shape[1]
+
+
+def ep_combine_backward(handle: Handle, grad_out, y=None, topk_weights=None, grad_y=None, grad_topk_weights=None,
+                        need_grad_y=True, need_grad_topk_weights=True, stream=None):
+    """Gradient of ep_combine.  grad_out: bf16 [T, H]; y: the rows given to ep_combine (needed for the weights'
+    gradient); topk_weights as given to it.  Returns (grad_y bf16 [rows, H], grad_topk_weights fp32 [T, K]), None where
+    not needed.  Rows of grad_y that no entry owns keep what the tensor held."""
+    dev, T, K = _device(handle), handle.num_tokens, handle.num_topk
+    H = _matrix(grad_out, torch.bfloat16, "grad_out", dev)
+    _need(grad_out, torch.bfloat16, "grad_out", dev, (T, H))
+    if topk_weights is not None:
+        _need(topk_weights, torch.float32, "topk_weights", dev, (T, K))
+    need_w = need_grad_topk_weights or grad_topk_weights is not None
+    rows = handle.recv_capacity
+    if y is not None:
+        if _matrix(y, torch.bfloat16, "y", dev) != H:
+            raise ValueError("y must be [rows, %d]" % H)
+        rows = y.shape[0]
+    elif need_w:
+        raise ValueError("the gradient of topk_weights needs y")
+    if grad_y is not None:
+        if y is None and isinstance(grad_y, torch.Tensor) and grad_y.dim() == 2:
+            rows = grad_y.shape[0]
+        _need(grad_y, torch.bfloat16, "grad_y", dev, (rows, H))
+    elif need_grad_y:
+        grad_y = _on_stream(stream, torch.empty, (rows, H), dtype=torch.bfloat16, device=dev)
+    if grad_topk_weights is not None:
+        _need(grad_topk_weights, torch.float32, "grad_topk_weights", dev, (T, K))
+    elif need_w:
+        grad_topk_weights = _on_stream(stream, torch.empty, (T, K), dtype=torch.float32, device=dev)
+    _check(_lib.ep_combine_backward(handle.ptr, _ptr(grad_out), H, _ptr(y), rows, _ptr(topk_weights), _ptr(grad_y),
+                                    _ptr(grad_topk_weights), _stream(stream)), "ep_combine_backward")
+    return grad_y, grad_topk_weights
+
+
+def ep_expert_ffn_workspace_bytes(handle: Handle, hidden, intermediate, backward=False) -> int:
+    """Bytes of workspace of ep_expert_ffn (or, with backward, of either pass) for the handle's rows."""
+    return int(_lib.ep_expert_ffn_workspace_bytes(handle.recv_capacity, hidden, intermediate, int(bool(backward))))
+
+
+def check_ffn_weights(w13, w2, dtype, El, H, device):
+    """w13 [El, 2 I, H] and w2 [El, H, I] of `dtype`; returns I."""
+    if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+        raise ValueError("w2 must be [num_local_experts, hidden, intermediate]")
+    I = w2.shape[2]
+    _need(w2, dtype, "w2", device, (El, H, I))
+    if w13 is not None:
+        _need(w13, dtype, "w13", device, (El, 2 * I, H))
+    return I
+
+
+def check_ffn_scales(xs, s13, s2, rows, El, H, I, device):
+    """The scales of e4m3 rows and weights: per row and 128 channels, per 128 x 128 block."""
+    for t, name, shape in ((xs, "recv_x_scales", (rows, H // 128)), (s13, "w13_scales", (El, 2 * I // 128, H // 128)),
+                           (s2, "w2_scales", (El, H // 128, I // 128))):
+        if t is None:
+            raise ValueError("e4m3 rows need %s" % name)
+        _need(t, torch.float32, name, device, shape)
+
+
+def _ffn_workspace(handle, H, I, backward, workspace, device, stream):
+    if workspace is not None:   # its length is checked by the library call itself
+        check_workspace(workspace, device)
+        return workspace
+    n = ep_expert_ffn_workspace_bytes(handle, H, I, backward)
+    if n == 0:
+        raise EPError("ep_expert_ffn_workspace_bytes rejected the sizes (hidden=%d intermediate=%d)" % (H, I))
+    return _on_stream(stream, torch.empty, n, dtype=torch.uint8, device=device)
+
+
+def ep_expert_ffn(handle: Handle, recv_x, w13, w2, recv_x_scales=None, w13_scales=None, w2_scales=None, y=None, pre=None,
+                  workspace=None, stream=None):
+    """The experts' gated feed-forward block over the rows a dispatch placed: y = (silu(x Wg^T) * (x Wu^T)) Wd^T per
+    expert.  recv_x [rows, H], w13 [El, 2 I, H] (gate rows first) and w2 [El, H, I]: all bf16, or all uint8 holding e4m3
+    with recv_x_scales [rows, H / 128], w13_scales [El, 2 I / 128, H / 128] and w2_scales [El, H / 128, I / 128].
+    pre: fp32 [rows, 2 I] to keep for ep_expert_ffn_backward (bf16 only).  Returns y bf16 [rows, H]; rows that are not
+    valid rows of an expert keep what y held."""
+    if not isinstance(recv_x, torch.Tensor) or recv_x.dtype not in (torch.bfloat16, torch.uint8):
+        raise TypeError("recv_x must be a bfloat16 or uint8 (e4m3) tensor")
+    fp8 = recv_x.dtype == torch.uint8
+    dev, El = _device(handle), handle.num_local_experts
+    H = _matrix(recv_x, recv_x.dtype, "recv_x", dev)
+    rows = recv_x.shape[0]
+    if w13 is None:
+        raise ValueError("w13 is required")
+    I = check_ffn_weights(w13, w2, recv_x.dtype, El, H, dev)
+    if fp8:
+        check_ffn_scales(recv_x_scales, w13_scales, w2_scales, rows, El, H, I, dev)
+    if y is None:
+        y = _on_stream(stream, torch.empty, (rows, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(y, torch.bfloat16, "y", dev, (rows, H))
+    if pre is not None:
+        _need(pre, torch.float32, "pre", dev, (rows, 2 * I))
+    workspace = _ffn_workspace(handle, H, I, False, workspace, dev, stream)
+    _check(_lib.ep_expert_ffn(handle.ptr, _ptr(recv_x), _ptr(recv_x_scales) if fp8 else None,
+                              EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, H, I, rows, _ptr(w13),
+                              _ptr(w13_scales) if fp8 else None, _ptr(w2), _ptr(w2_scales) if fp8 else None, _ptr(y),
+                              _ptr(pre), _ptr(workspace), workspace.numel(), _stream(stream)), "ep_expert_ffn")
+    return y
+
+
+def ep_expert_ffn_backward(handle: Handle, dy, recv_x, pre, w13, w2, dx=None, dw13=None, dw2=None, workspace=None,
+                           need_dx=True, need_dw13=True, need_dw2=True, stream=None):
+    """Gradients of ep_expert_ffn (bf16) from dy [rows, H] and the forward pass' pre.  Returns (dx [rows, H], dw13 like
+    w13, dw2 like w2), bf16, None where not needed.  Rows of dx that are not valid rows keep what it held; dw13 and dw2
+    are written whole."""
+    dev, El = _device(handle), handle.num_local_experts
+    H = _matrix(dy, torch.bfloat16, "dy", dev)
+    rows = dy.shape[0]
+    need_dx, need_dw13, need_dw2 = need_dx or dx is not None, need_dw13 or dw13 is not None, need_dw2 or dw2 is not None
+    if need_dx and w13 is None:
+        raise ValueError("dx needs w13")
+    I = check_ffn_weights(w13, w2, torch.bfloat16, El, H, dev)
+    if recv_x is not None:
+        _need(recv_x, torch.bfloat16, "recv_x", dev, (rows, H))
+    elif need_dw13:
+        raise ValueError("dw13 needs recv_x")
+    _need(pre, torch.float32, "pre", dev, (rows, 2 * I))
+
+    def grad(t, name, shape, needed):
+        if t is not None:
+            return _need(t, torch.bfloat16, name, dev, shape)
+        return _on_stream(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev) if needed else None
+
+    dx = grad(dx, "dx", (rows, H), need_dx)
+    dw13 = grad(dw13, "dw13", (El, 2 * I, H), need_dw13)
+    dw2 = grad(dw2, "dw2", (El, H, I), need_dw2)
+    workspace = _ffn_workspace(handle, H, I, True, workspace, dev, stream)
+    _check(_lib.ep_expert_ffn_backward(handle.ptr, _ptr(dy), _ptr(recv_x), _ptr(pre), H, I, rows, _ptr(w13), _ptr(w2),
+                                       _ptr(dx), _ptr(dw13), _ptr(dw2), _ptr(workspace), workspace.numel(),
+                                       _stream(stream)), "ep_expert_ffn_backward")
+    return dx, dw13, dw2
+
+
+def ep_adapter_workspace_bytes(handle: Handle, hidden, rank) -> int:
+    return int(_lib.ep_adapter_workspace_bytes(handle.num_tokens, handle.num_local_experts, hidden, rank))
+
+
+def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, workspace=None, stream=None):
+    """Low-rank adapters beside a shared projection: out[t] = base[t] + scales[i] * b[i] (a[i] x[t]), i the token's
+    adapter in the handle (a layout over the adapter ids [T, 1], -1 = none).  x bf16 [T, H], a bf16 [El, r, H], b bf16
+    [El, N, r], scales fp32 [El], base bf16 [T, N] (None: zeros).  Returns out bf16 [T, N] (may be base itself)."""
+    dev, T, El = _device(handle), handle.num_tokens, handle.num_local_experts
+    H = _matrix(x, torch.bfloat16, "x", dev)
+    _need(x, torch.bfloat16, "x", dev, (T, H))
+    if not isinstance(b, torch.Tensor) or b.dim() != 3:
+        raise ValueError("b must be [num_local_experts, out_features, rank]")
+    N, r = b.shape[1], b.shape[2]
+    _need(b, torch.bfloat16, "b", dev, (El, N, r))
+    _need(a, torch.bfloat16, "a", dev, (El, r, H))
+    if scales is not None:
+        _need(scales, torch.float32, "scales", dev, (El,))
+    if base is not None:
+        _need(base, torch.bfloat16, "base", dev, (T, N))
+    if out is None:
+        out = _on_stream(stream, torch.empty, (T, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", dev, (T, N))
+    if workspace is not None:
+        check_workspace(workspace, dev)
+    else:
+        n = ep_adapter_workspace_bytes(handle, H, r)
+        if n == 0:
+            raise EPError("ep_adapter_workspace_bytes rejected the sizes (hidden=%d rank=%d)" % (H, r))
+        workspace = _on_stream(stream, torch.empty, n, dtype=torch.uint8, device=dev)
+    _check(_lib.ep_adapter(handle.ptr, _ptr(x), H, _ptr(a), _ptr(b), r, N, _ptr(scales), _ptr(base), _ptr(out),
+                           _ptr(workspace), workspace.numel(), _stream(stream)), "ep_adapter")
+    return out
+
+
 def ep_handle_free(handle: Handle):
     handle.free()
 
 
 __all__ = ["ep_get_layout", "ep_dispatch", "ep_layout_dispatch", "ep_layout_dispatch_noalloc", "ep_combine", "ep_combine_tokens", "ep_handle_free", "ep_recv_capacity",
-           "ep_dispatch_rows", "ep_combine_reduce",
+           "ep_dispatch_rows", "ep_combine_reduce", "ep_combine_backward", "ep_expert_ffn", "ep_expert_ffn_backward",
+           "ep_expert_ffn_workspace_bytes", "ep_adapter", "ep_adapter_workspace_bytes",
            "ep_layout_workspace_bytes", "alloc_dispatch_outputs", "Handle", "EPError", "LIB_PATH",
            "hip_runtimes_loaded"]

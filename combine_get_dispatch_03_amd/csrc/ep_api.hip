@@ -308,6 +308,40 @@ ep_status_t dispatch_args(const Handle* h, const void* x, int hidden, const floa
     return EP_OK;
 }
 
+const char* ffn_shape(int hidden, int inter, bool fp8) {
+    if (hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0) return "hidden must be a multiple of 8 in [8, 32768]";
+    if (inter < 8 || inter > kMaxHidden || inter % 8 != 0) return "intermediate must be a multiple of 8 in [8, 32768]";
+    if (fp8 && (hidden % 128 != 0 || inter % 128 != 0)) return "FP8 needs hidden % 128 == 0 and intermediate % 128 == 0";
+    return nullptr;
+}
+
+const char* adapter_shape(int hidden, int rank, int n_out) {
+    if (hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0) return "hidden must be a multiple of 8 in [8, 32768]";
+    if (rank < 8 || rank > kMaxAdapterRank || rank % 8 != 0) return "rank must be a multiple of 8 in [8, 128]";
+    if (n_out < 8 || n_out > kMaxAdapterOut || n_out % 8 != 0)
+        return "out_features must be a multiple of 8 in [8, 65536]";
+    return nullptr;
+}
+
+// Scratch of the feed-forward block: h [cap, inter] bf16 first, then (backward) dp [cap, 2 * inter] bf16.
+struct FfnWorkspace {
+    size_t dp, bytes;
+};
+FfnWorkspace ffn_workspace(int64_t cap, int inter, bool backward) {
+    FfnWorkspace w;
+    w.dp = align_up((size_t)(cap > 0 ? cap : 1) * (size_t)inter * 2, 256);
+    w.bytes = backward ? 3 * w.dp : w.dp;
+    return w;
+}
+
+ep_status_t check_scratch(const void* workspace, size_t have, size_t need) {
+    if (workspace == nullptr) return fail(EP_ERR_INVALID_ARG, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(EP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (have < need) return fail(EP_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", have, need);
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -540,6 +574,167 @@ ep_status_t ep_combine_tokens(ep_handle_t handle, const void* y, int hidden, int
     a.tokens = true;
     const hipError_t err = launch_combine(*h, a, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return hip_fail(err, "combine_tokens launch");
+    return EP_OK;
+}
+
+ep_status_t ep_combine_backward(ep_handle_t handle, const void* grad_out, int hidden, const void* y, int64_t y_rows,
+                                const float* topk_weights, void* grad_y, float* grad_topk_weights, void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = check_handle(handle);
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    if (hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0)
+        return fail(EP_ERR_INVALID_ARG, "hidden must be a multiple of 8 in [8, 32768]");
+    if (h->T > 0) {
+        if (grad_y == nullptr && grad_topk_weights == nullptr)
+            return fail(EP_ERR_INVALID_ARG, "grad_y and grad_topk_weights are both NULL");
+        if (grad_out == nullptr || !aligned16(grad_out))
+            return fail(EP_ERR_INVALID_ARG, "grad_out must be non-NULL and 16-byte aligned");
+        if (grad_topk_weights != nullptr && (y == nullptr || !aligned16(y)))
+            return fail(EP_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned for grad_topk_weights");
+        if (grad_y != nullptr && !aligned16(grad_y)) return fail(EP_ERR_INVALID_ARG, "grad_y must be 16-byte aligned");
+        if (y_rows < h->cap)
+            return fail(EP_ERR_INVALID_ARG, "y_rows %lld < required %lld", (long long)y_rows, (long long)h->cap);
+    }
+    CombineBackwardArgs a;
+    a.grad_out = grad_out;
+    a.y = y;
+    a.topk_weights = topk_weights;
+    a.grad_y = grad_y;
+    a.grad_w = grad_topk_weights;
+    a.hidden = hidden;
+    const hipError_t err = launch_combine_backward(*h, a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "combine_backward launch");
+    return EP_OK;
+}
+
+size_t ep_expert_ffn_workspace_bytes(int64_t recv_capacity, int hidden, int intermediate, int backward) {
+    if (recv_capacity < 0 || recv_capacity > INT32_MAX || ffn_shape(hidden, intermediate, false) != nullptr) return 0;
+    return ffn_workspace(recv_capacity, intermediate, backward != 0).bytes;
+}
+
+ep_status_t ep_expert_ffn(ep_handle_t handle, const void* recv_x, const float* recv_x_scales, ep_dtype_t dtype, int hidden,
+                          int intermediate, int64_t rows, const void* w13, const float* w13_scales, const void* w2,
+                          const float* w2_scales, void* y, float* pre, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = check_handle(handle);
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    if (dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_FP8_E4M3)
+        return fail(EP_ERR_INVALID_ARG, "dtype must be EP_DTYPE_BF16 or EP_DTYPE_FP8_E4M3");
+    const bool fp8 = dtype == EP_DTYPE_FP8_E4M3;
+    if (const char* why = ffn_shape(hidden, intermediate, fp8)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (fp8 && pre != nullptr) return fail(EP_ERR_INVALID_ARG, "pre is written for bf16 rows only");
+    if (h->T > 0) {
+        if (rows < h->cap)
+            return fail(EP_ERR_INVALID_ARG, "rows %lld < required %lld", (long long)rows, (long long)h->cap);
+        if (recv_x == nullptr || !aligned16(recv_x))
+            return fail(EP_ERR_INVALID_ARG, "recv_x must be non-NULL and 16-byte aligned");
+        if (w13 == nullptr || !aligned16(w13) || w2 == nullptr || !aligned16(w2))
+            return fail(EP_ERR_INVALID_ARG, "w13 and w2 must be non-NULL and 16-byte aligned");
+        if (fp8 && (recv_x_scales == nullptr || w13_scales == nullptr || w2_scales == nullptr))
+            return fail(EP_ERR_INVALID_ARG, "FP8 needs recv_x_scales, w13_scales and w2_scales");
+        if (y == nullptr || !aligned16(y)) return fail(EP_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned");
+        if (pre != nullptr && !aligned16(pre)) return fail(EP_ERR_INVALID_ARG, "pre must be 16-byte aligned");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, ffn_workspace(h->cap, intermediate, false).bytes);
+        if (st != EP_OK) return st;
+    }
+    FfnArgs a;
+    a.x = recv_x;
+    a.x_scales = recv_x_scales;
+    a.w13 = w13;
+    a.w13_scales = w13_scales;
+    a.w2 = w2;
+    a.w2_scales = w2_scales;
+    a.y = y;
+    a.pre = pre;
+    a.h = static_cast<uint16_t*>(workspace);
+    a.hidden = hidden;
+    a.inter = intermediate;
+    a.fp8 = fp8;
+    const hipError_t err = launch_expert_ffn(*h, a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "expert_ffn launch");
+    return EP_OK;
+}
+
+ep_status_t ep_expert_ffn_backward(ep_handle_t handle, const void* dy, const void* recv_x, const float* pre, int hidden,
+                                   int intermediate, int64_t rows, const void* w13, const void* w2, void* dx, void* dw13,
+                                   void* dw2, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = check_handle(handle);
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    if (const char* why = ffn_shape(hidden, intermediate, false)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (h->T > 0 && dx == nullptr && dw13 == nullptr && dw2 == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "dx, dw13 and dw2 are all NULL");
+    if (!aligned16(dx) || !aligned16(dw13) || !aligned16(dw2))
+        return fail(EP_ERR_INVALID_ARG, "dx, dw13 and dw2 must be 16-byte aligned");
+    const FfnWorkspace w = ffn_workspace(h->cap, intermediate, true);
+    if (h->T > 0) {
+        if (rows < h->cap)
+            return fail(EP_ERR_INVALID_ARG, "rows %lld < required %lld", (long long)rows, (long long)h->cap);
+        if (dy == nullptr || !aligned16(dy)) return fail(EP_ERR_INVALID_ARG, "dy must be non-NULL and 16-byte aligned");
+        if (pre == nullptr || !aligned16(pre)) return fail(EP_ERR_INVALID_ARG, "pre must be non-NULL and 16-byte aligned");
+        if (w2 == nullptr || !aligned16(w2)) return fail(EP_ERR_INVALID_ARG, "w2 must be non-NULL and 16-byte aligned");
+        if (dx != nullptr && (w13 == nullptr || !aligned16(w13)))
+            return fail(EP_ERR_INVALID_ARG, "w13 must be non-NULL and 16-byte aligned for dx");
+        if (dw13 != nullptr && (recv_x == nullptr || !aligned16(recv_x)))
+            return fail(EP_ERR_INVALID_ARG, "recv_x must be non-NULL and 16-byte aligned for dw13");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, w.bytes);
+        if (st != EP_OK) return st;
+    }
+    FfnBackwardArgs a;
+    a.dy = dy;
+    a.x = recv_x;
+    a.pre = pre;
+    a.w13 = w13;
+    a.w2 = w2;
+    a.dx = dx;
+    a.dw13 = dw13;
+    a.dw2 = dw2;
+    a.h = static_cast<uint16_t*>(workspace);
+    a.dp = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w.dp);
+    a.hidden = hidden;
+    a.inter = intermediate;
+    const hipError_t err = launch_expert_ffn_backward(*h, a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "expert_ffn_backward launch");
+    return EP_OK;
+}
+
+size_t ep_adapter_workspace_bytes(int num_tokens, int num_local_experts, int hidden, int rank) {
+    if (num_tokens < 0 || num_local_experts < 1 || num_local_experts > kMaxExperts || adapter_shape(hidden, rank, 8) != nullptr)
+        return 0;
+    return adapter_workspace_bytes(num_tokens, num_local_experts, hidden, rank);
+}
+
+ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void* a, const void* b, int rank,
+                       int out_features, const float* scales, const void* base, void* out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = check_handle(handle);
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    if (h->K != 1) return fail(EP_ERR_UNSUPPORTED, "ep_adapter needs a handle with num_topk == 1, got %d", h->K);
+    if (const char* why = adapter_shape(hidden, rank, out_features)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (h->T > 0) {
+        if (x == nullptr || !aligned16(x)) return fail(EP_ERR_INVALID_ARG, "x must be non-NULL and 16-byte aligned");
+        if (a == nullptr || !aligned16(a) || b == nullptr || !aligned16(b))
+            return fail(EP_ERR_INVALID_ARG, "a and b must be non-NULL and 16-byte aligned");
+        if (base != nullptr && !aligned16(base)) return fail(EP_ERR_INVALID_ARG, "base must be 16-byte aligned");
+        if (out == nullptr || !aligned16(out)) return fail(EP_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, adapter_workspace_bytes(h->T, h->El, hidden, rank));
+        if (st != EP_OK) return st;
+    }
+    AdapterArgs p;
+    p.x = x;
+    p.a = a;
+    p.b = b;
+    p.scales = scales;
+    p.base = base;
+    p.out = out;
+    p.ws = workspace;
+    p.hidden = hidden;
+    p.rank = rank;
+    p.n_out = out_features;
+    const hipError_t err = launch_adapter(*h, p, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "adapter launch");
     return EP_OK;
 }
 

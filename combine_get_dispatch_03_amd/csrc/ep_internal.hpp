@@ -18,6 +18,8 @@ constexpr int kMaxRanks = 64;
 constexpr int kMaxAlignment = 65536;
 constexpr int kMaxHidden = 32768;
 constexpr int kMaxRowBytes = 65536;
+constexpr int kMaxAdapterRank = 128;
+constexpr int kMaxAdapterOut = 65536;
 
 // Device arrays carved out of the caller's workspace.  All int32.
 struct Workspace {
@@ -97,5 +99,58 @@ struct CombineArgs {
     bool tokens;               // true: y holds the token-major rows (one per token, unit weight)
 };
 hipError_t launch_combine(const Handle& h, const CombineArgs& a, hipStream_t stream);
+
+struct CombineBackwardArgs {
+    const void* grad_out;      // bf16 [T, hidden]
+    const void* y;             // bf16 [rows, hidden], read for the weights' gradient only
+    const float* topk_weights; // [T, K] or nullptr (weights of 1)
+    void* grad_y;              // bf16 [rows, hidden] or nullptr
+    float* grad_w;             // [T, K] or nullptr
+    int hidden;
+};
+hipError_t launch_combine_backward(const Handle& h, const CombineBackwardArgs& a, hipStream_t stream);
+
+struct FfnArgs {
+    const void* x;             // bf16 or e4m3 [rows, hidden]
+    const float* x_scales;     // e4m3: [rows, hidden / 128]
+    const void* w13;           // bf16 or e4m3 [El, 2 * inter, hidden], gate rows first
+    const float* w13_scales;   // e4m3: [El, 2 * inter / 128, hidden / 128]
+    const void* w2;            // bf16 or e4m3 [El, hidden, inter]
+    const float* w2_scales;    // e4m3: [El, hidden / 128, inter / 128]
+    void* y;                   // bf16 [rows, hidden]
+    float* pre;                // fp32 [rows, 2 * inter] or nullptr
+    uint16_t* h;               // workspace: bf16 [cap, inter]
+    int hidden, inter;
+    bool fp8;
+};
+hipError_t launch_expert_ffn(const Handle& h, const FfnArgs& a, hipStream_t stream);
+
+struct FfnBackwardArgs {
+    const void* dy;            // bf16 [rows, hidden]
+    const void* x;             // bf16 [rows, hidden]
+    const float* pre;          // fp32 [rows, 2 * inter]
+    const void* w13;
+    const void* w2;
+    void* dx;                  // bf16 [rows, hidden] or nullptr
+    void* dw13;                // bf16 like w13, or nullptr
+    void* dw2;                 // bf16 like w2, or nullptr
+    uint16_t* dp;              // workspace: bf16 [cap, 2 * inter], gradient of the pre-activations
+    uint16_t* h;               // workspace: bf16 [cap, inter]
+    int hidden, inter;
+};
+hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a, hipStream_t stream);
+
+struct AdapterArgs {
+    const void* x;             // bf16 [T, hidden]
+    const void* a;             // bf16 [El, rank, hidden]
+    const void* b;             // bf16 [El, out, rank]
+    const float* scales;       // [El] or nullptr (1)
+    const void* base;          // bf16 [T, out] or nullptr (zeros)
+    void* out;                 // bf16 [T, out]
+    void* ws;
+    int hidden, rank, n_out;
+};
+size_t adapter_workspace_bytes(int T, int El, int hidden, int rank);
+hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t stream);
 
 }  // namespace ep

@@ -13,7 +13,11 @@
  *                  (ep_combine_tokens for the token-major rows);
  *   ep_dispatch_rows / ep_combine_reduce  the receiver's placement of rows that arrived from other ranks and
  *                  the source's sum of the rows those ranks return (the two ends of the exchange);
- *   ep_layout_dispatch  ep_get_layout + ep_dispatch in one call, one kernel launch for <= 256 tokens.
+ *   ep_layout_dispatch  ep_get_layout + ep_dispatch in one call, one kernel launch for <= 256 tokens;
+ *   ep_expert_ffn / ep_expert_ffn_backward  the experts' gated feed-forward block over the rows that a dispatch
+ *                  placed, and its gradients; ep_combine_backward the gradient of ep_combine;
+ *   ep_adapter     low-rank adapters of many requests at once beside a shared projection, the requests grouped
+ *                  by a layout over their adapter ids.
  *
  * Page names used in the citations:
  *   [DeepEP->MegaMoE]  "从 DeepEP 到 Mega MoE：MoE Runtime 演进的三向验证分析" (backyes.github.io)
@@ -58,7 +62,7 @@ extern "C" {
 typedef enum ep_status {
     EP_OK = 0,
     EP_ERR_INVALID_ARG = 1,   /* an argument is out of range, misaligned, NULL where required, or a size is short */
-    EP_ERR_UNSUPPORTED = 2,   /* a mode this version does not implement (none at present; reserved)               */
+    EP_ERR_UNSUPPORTED = 2,   /* a mode this version does not implement                                            */
     EP_ERR_HIP = 3            /* a HIP launch failed; the stream state is whatever HIP reports                    */
 } ep_status_t;
 
@@ -290,6 +294,107 @@ ep_status_t ep_combine_tokens(ep_handle_t handle, const void* y, int hidden, int
  */
 ep_status_t ep_combine_reduce(ep_handle_t handle, const void* partials, int hidden, const void* local,
                               const void* bias, void* out, void* stream);
+
+/*
+ * ep_combine_backward -- gradient of ep_combine.  With out[t] = sum_k w[t,k] * y[slot(t,k)] (+ bias):
+ *   grad_y[slot(t,k)] = w[t,k] * grad_out[t]   (rounded once to bf16; w = 1 when topk_weights is NULL)
+ *   grad_topk_weights[t,k] = <grad_out[t], y[slot(t,k)]>   (products and sum in fp32; 0 where the entry has no
+ *                            local slot)
+ * The gradient of bias is grad_out itself.  Every slot has one owner, so no sum crosses tokens and the result does
+ * not depend on any order.
+ *
+ *   grad_out           device bf16 [num_tokens, hidden].
+ *   y                  device bf16 [y_rows, hidden] as given to ep_combine; read for grad_topk_weights only
+ *                      (nullable without it).
+ *   y_rows             rows of y and of grad_y, >= ep_recv_capacity(...).
+ *   topk_weights       device fp32 [num_tokens, num_topk], nullable.
+ *   grad_y             device bf16 [y_rows, hidden], nullable.  Rows no entry owns (padding rows, rows past the last
+ *                      segment) are left untouched.
+ *   grad_topk_weights  device fp32 [num_tokens, num_topk], nullable; every entry is written.
+ *   At least one of grad_y and grad_topk_weights is required.
+ */
+ep_status_t ep_combine_backward(ep_handle_t handle, const void* grad_out, int hidden, const void* y, int64_t y_rows,
+                                const float* topk_weights, void* grad_y, float* grad_topk_weights, void* stream);
+
+/* Bytes of device workspace of ep_expert_ffn (backward = 0) or ep_expert_ffn_backward (backward != 0; enough for the
+ * forward pass too) for a handle of `recv_capacity` rows.  Host only.  Returns 0 for arguments outside the limits. */
+size_t ep_expert_ffn_workspace_bytes(int64_t recv_capacity, int hidden, int intermediate, int backward);
+
+/*
+ * ep_expert_ffn -- the experts' gated feed-forward block, the computation between dispatch and combine ([MoE-comm]
+ * §一: route, dispatch, grouped GEMM, combine; [flops-record]: the grouped GEMM finds each expert's rows through the
+ * device psum).  For every valid row r of local expert e, with I = intermediate:
+ *   g = x[r] . w13[e][0..I)      u = x[r] . w13[e][I..2I)      h = silu(g) * u,  silu(g) = g / (1 + exp(-g))
+ *   y[r] = h . w2[e]
+ * Both projections, the activation and the product are one kernel, the second projection another; sums are fp32; h is
+ * rounded once to bf16 between them.
+ *
+ *   handle         the handle of the dispatch (or ep_dispatch_rows) that placed the rows.  Counts are read on the
+ *                  device; the host never learns them.
+ *   recv_x         device [rows, hidden] in the handle's row layout: bf16, or e4m3 as ep_dispatch writes it.  Only valid
+ *                  rows are read: padding rows may hold anything.
+ *   recv_x_scales  e4m3: device fp32 [rows, hidden / 128]; bf16: ignored.
+ *   dtype          type of recv_x, w13 and w2.
+ *   intermediate   I: a multiple of 8 in [8, 32768], and of 128 for e4m3.
+ *   rows           rows of recv_x, y (and pre), >= ep_recv_capacity(...).
+ *   w13            device [num_local_experts, 2 * I, hidden]: the gate projection's I rows, then the up projection's.
+ *   w2             device [num_local_experts, hidden, I].
+ *   w13_scales     e4m3: device fp32 [num_local_experts, 2 * I / 128, hidden / 128], one scale per 128 x 128 block.
+ *   w2_scales      e4m3: device fp32 [num_local_experts, hidden / 128, I / 128].
+ *   y              device bf16 [rows, hidden]: valid rows are written, all others are left untouched.  A row depends
+ *                  on its own x row and its expert's weights only.
+ *   pre            device fp32 [rows, 2 * I], nullable, bf16 only: g | u of every valid row, kept for
+ *                  ep_expert_ffn_backward (in fp32: rounding them would cost the gradients more than one bf16 step).
+ *   workspace      device scratch of ep_expert_ffn_workspace_bytes(...) bytes, 256-byte aligned; no contents
+ *                  are required and none outlive the call.  Calls that may overlap, captured graphs that may be
+ *                  replayed at the same time among them, need a workspace each.
+ *   recv_x, w13, w2, y and pre must be 16-byte aligned.  No output may overlap an input.
+ */
+ep_status_t ep_expert_ffn(ep_handle_t handle, const void* recv_x, const float* recv_x_scales, ep_dtype_t dtype, int hidden,
+                          int intermediate, int64_t rows, const void* w13, const float* w13_scales, const void* w2,
+                          const float* w2_scales, void* y, float* pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ep_expert_ffn_backward -- gradients of ep_expert_ffn with bf16 rows and weights.  With s = 1 / (1 + exp(-g)):
+ *   dh = dy . w2 ;  du = dh * g * s ;  dg = dh * u * s * (1 + g * (1 - s)) ;  dp = dg | du   (rounded once to bf16)
+ *   dx[r] = dp[r] . w13[e] ;  dw13[e] = sum over the expert's rows of dp (x) x ;  dw2[e] = sum of dy (x) h
+ *
+ *   dy, recv_x     device bf16 [rows, hidden]; only valid rows are read.
+ *   pre            device fp32 [rows, 2 * I] as the forward pass wrote it.
+ *   dx             device bf16 [rows, hidden], nullable: valid rows are written, all others are left untouched.
+ *   dw13, dw2      device bf16 like w13 and w2, nullable: written whole (zeros for an expert without rows), not added to.
+ *   w13            nullable without dx.   recv_x nullable without dw13.
+ *   At least one of dx, dw13 and dw2 is required.  workspace as in ep_expert_ffn, with backward != 0.
+ *   The sum over an expert's rows runs in a fixed order: results do not vary from run to run.
+ */
+ep_status_t ep_expert_ffn_backward(ep_handle_t handle, const void* dy, const void* recv_x, const float* pre, int hidden,
+                                   int intermediate, int64_t rows, const void* w13, const void* w2, void* dx, void* dw13,
+                                   void* dw2, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace of ep_adapter.  Host only.  Returns 0 for arguments outside the limits. */
+size_t ep_adapter_workspace_bytes(int num_tokens, int num_local_experts, int hidden, int rank);
+
+/*
+ * ep_adapter -- low-rank adapters of many requests at once beside a shared projection (e.g. of the shared expert whose
+ * output ep_combine takes as bias).  The handle is a layout over the tokens' adapter ids with num_topk = 1
+ * (num_experts = adapters, -1 = no adapter), made once per step and used for every projection:
+ *   out[t] = base[t] + scales[a] * b[a] (a[a] x[t])     a = the token's adapter
+ *   out[t] = base[t]                                    for a token without one (or with another rank's)
+ * fp32 sums; the inner vector scales[a] * a[a] x[t] is rounded once to bf16 between the two products; one rounding to
+ * bf16 at the end.
+ *
+ *   x            device bf16 [num_tokens, hidden];  hidden as everywhere (a multiple of 8 in [8, 32768]).
+ *   a            device bf16 [num_local_experts, rank, hidden];  rank: a multiple of 8 in [8, 128].
+ *   b            device bf16 [num_local_experts, out_features, rank];  out_features: a multiple of 8 in [8, 65536].
+ *   scales       device fp32 [num_local_experts], nullable (1).
+ *   base         device bf16 [num_tokens, out_features], nullable (zeros): the shared projection's output.
+ *   out          device bf16 [num_tokens, out_features]; every row is written; may be base itself.
+ *   workspace    device scratch of ep_adapter_workspace_bytes(...) bytes, 256-byte aligned, as in ep_expert_ffn.
+ *   A handle with num_topk != 1 returns EP_ERR_UNSUPPORTED.
+ */
+ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void* a, const void* b, int rank,
+                       int out_features, const float* scales, const void* base, void* out, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* End of a handle's life ([MoE-comm] §二: a handle and the buffers it refers to must outlive every operation
  * that uses them; §一: the handle carries the dispatch's grouping for the combine and backward).  Frees the host

@@ -1,0 +1,140 @@
+"""Low-rank adapters of many requests against their definition in 64 bits."""
+import pytest
+import torch
+
+import expert_reference as R
+import harness as Hn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def ep():
+    import combine_get_dispatch_03_amd as ep
+    return ep
+
+
+def make_ids(T, n, how, g):
+    ids = torch.randint(0, n, (T,), generator=g)
+    if how == "runs":
+        ids = ids.sort().values
+    elif how == "holes":
+        ids[torch.rand(T, generator=g) < 0.4] = -1
+        if T > 2:
+            ids[1], ids[2] = n + 3, -8
+    elif how == "none":
+        ids[:] = -1
+    elif how == "one":
+        ids[:] = n - 1
+    return ids.view(T, 1)
+
+
+def reference(x, a, b, scales, base, ids, lo):
+    """Values and bounds: the inner sums in fp32, their rounding to bf16, the outer sums, the output's rounding."""
+    T, N, r, H = x.shape[0], b.shape[1], a.shape[1], x.shape[1]
+    out = base.double().clone() if base is not None else torch.zeros(T, N, dtype=torch.float64, device=DEV)
+    bound = torch.zeros_like(out)
+    ids = ids.view(-1).to(DEV) - lo
+    for i in range(a.shape[0]):
+        t = (ids == i).nonzero().view(-1)
+        s = float(scales[i]) if scales is not None else 1.0
+        A, B, X = a[i].double(), b[i].double(), x[t].double()
+        v, ev = s * (X @ A.t()), abs(s) * (H + 2) * R.U32 * (X.abs() @ A.abs().t())
+        ev = ev + R.UBF * (v.abs() + ev)
+        out[t] += v @ B.t()
+        bound[t] = ev @ B.abs().t() + (r + 2) * R.U32 * ((v.abs() + ev) @ B.abs().t())
+    bound = bound + 2 * R.U32 * out.abs()
+    return out, bound + R.UBF * (out.abs() + bound) + R.TINY
+
+
+CASES = [
+    # T, H, N, adapters, ranks, rank id, r, ids
+    (1, 64, 64, 1, 1, 0, 8, "any"),
+    (1, 7168, 2112, 8, 1, 0, 64, "any"),
+    (1, 8, 8, 3, 1, 0, 16, "none"),
+    (7, 264, 136, 5, 1, 0, 24, "holes"),
+    (128, 1032, 520, 32, 1, 0, 16, "holes"),
+    (130, 512, 1000, 6, 2, 1, 40, "any"),
+    (256, 256, 264, 300, 1, 0, 128, "any"),
+    (257, 520, 264, 3, 1, 0, 72, "runs"),
+    (1000, 1040, 776, 7, 1, 0, 64, "holes"),
+    (1500, 256, 256, 2, 1, 0, 8, "one"),
+    (600, 320, 136, 4, 1, 0, 16, "none"),
+    (3000, 136, 2056, 64, 1, 0, 32, "any"),
+]
+
+
+@pytest.mark.parametrize("T,H,N,n,ranks,rank,r,how", CASES)
+@pytest.mark.parametrize("full", [True, False])
+def test_values(ep, T, H, N, n, ranks, rank, r, how, full):
+    print("[adapter] T%d H%d N%d n%d r%d %s" % (T, H, N, n, r, how), flush=True)
+    g = torch.Generator().manual_seed(T + r)
+    ids = make_ids(T, n, how, g)
+    El = n // ranks
+    gd = torch.Generator(device=DEV).manual_seed(T)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, device=DEV, generator=gd) * std).bfloat16()
+    x, a, b = rnd(T, H), rnd(El, r, H, std=H ** -0.5), rnd(El, N, r, std=r ** -0.5)
+    base = rnd(T, N) if full else None
+    scales = torch.randn(El, device=DEV, generator=gd) if full else None
+    h, _ = ep.ep_get_layout(ids.to(DEV), n, ranks, rank, 1 if T % 2 else 16)
+    out, guard = Hn.guarded_tensor((T, N), torch.bfloat16, DEV, "out")
+    ws, guard_ws = Hn.guarded_tensor((ep.ep_adapter_workspace_bytes(h, H, r),), torch.uint8, DEV, "ws")
+    ep.ep_adapter(h, x, a, b, scales=scales, base=base, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    want, bound = reference(x, a, b, scales, base, ids, rank * El)
+    R.assert_within(out, want, bound, "out")
+    bare = ((ids.view(-1) < rank * El) | (ids.view(-1) >= (rank + 1) * El)).to(DEV)
+    assert torch.equal(out[bare], base[bare] if full else torch.zeros_like(out[bare]))
+    Hn.assert_guards(guard)
+    Hn.assert_guards(guard_ws)
+    again = ep.ep_adapter(h, x, a, b, scales=scales, base=base)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+    if full:                       # in place
+        ep.ep_adapter(h, x, a, b, scales=scales, base=base, out=base)
+        assert torch.equal(base.view(torch.int16), out.view(torch.int16))
+
+
+def test_rows_do_not_touch_each_other(ep):
+    """A NaN token spoils its own output row only, also among tokens of the same adapter."""
+    T, H, N, n, r = 300, 512, 264, 3, 16
+    g = torch.Generator().manual_seed(0)
+    ids = make_ids(T, n, "any", g).to(DEV)
+    x, a, b = torch.randn(T, H, device=DEV).bfloat16(), torch.randn(n, r, H, device=DEV).bfloat16(), torch.randn(n, N, r, device=DEV).bfloat16()
+    h, _ = ep.ep_get_layout(ids, n)
+    clean = ep.ep_adapter(h, x, a, b)
+    x[7, 100] = float("nan")
+    got = ep.ep_adapter(h, x, a, b)
+    keep = torch.arange(T, device=DEV) != 7
+    assert torch.equal(got[keep], clean[keep]) and got[7].isnan().all()
+
+
+def test_no_tokens(ep):
+    h, _ = ep.ep_get_layout(torch.empty((0, 1), dtype=torch.int64, device=DEV), 2)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=DEV)
+    assert ep.ep_adapter(h, z(0, 64), z(2, 8, 64), z(2, 16, 8)).shape == (0, 16)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [40, 700])
+def test_graph_replay(ep, T):
+    H, N, n, r = 512, 264, 5, 16
+    ids = make_ids(T, n, "holes", torch.Generator().manual_seed(2)).to(DEV)
+    x, a, b = torch.randn(T, H, device=DEV).bfloat16(), torch.randn(n, r, H, device=DEV).bfloat16(), torch.randn(n, N, r, device=DEV).bfloat16()
+    base, out = torch.randn(T, N, device=DEV).bfloat16(), torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+    h, _ = ep.ep_get_layout(ids, n)
+    ws = torch.empty(ep.ep_adapter_workspace_bytes(h, H, r), dtype=torch.uint8, device=DEV)
+    ep.ep_adapter(h, x, a, b, base=base, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        ep.ep_adapter(h, x, a, b, base=base, out=out, workspace=ws, stream=side)
+    for _ in range(3):
+        x.copy_(torch.randn(T, H, device=DEV))
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = ep.ep_adapter(h, x, a, b, base=base)
+        torch.cuda.synchronize()
+        assert torch.equal(ref, out)

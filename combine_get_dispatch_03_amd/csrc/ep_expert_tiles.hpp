@@ -9,40 +9,40 @@ struct RowTile {
     int expert;   // local expert
     int m0;       // first row of the tile inside the expert's segment
     int rows;     // valid rows of the tile (1..BM)
-    int total;    // tiles of all experts
 };
 
-// The `t`-th tile of BM rows, experts in order, ceil(count / BM) tiles each.  Every wave of the workgroup works it
-// out for itself (no LDS, no barrier): lane l sums the tiles of experts [l * per, l * per + per), a wave scan finds the
-// lane, and at most `per` (16 for 1024 experts) uniform steps find the expert.  expert = -1: t is past the last tile.
+// The tiles of BM rows of all experts, in the experts' order, ceil(count / BM) each.  Every wave of a workgroup works
+// them out for itself (no LDS, no barrier): lane l sums the tiles of experts [l * per, l * per + per) and a wave scan
+// places them; find() then needs at most `per` (16 for 1024 experts) uniform steps.
 template <int BM>
-__device__ __forceinline__ RowTile find_row_tile(const int32_t* cnt, int El, int t) {
-    const int lane = lane_id();
-    const int per = (El + kWave - 1) / kWave;
-    int sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e < El) sum += (cnt[e] + BM - 1) / BM;
-    }
-    const int incl = wave_inclusive_scan(sum);
-    RowTile r;
-    r.total = readlane(incl, kWave - 1);
-    r.expert = -1;
-    r.m0 = r.rows = 0;
-    if (t >= r.total) return r;
-    const int src = __builtin_ctzll(ballot(incl > t));
-    int left = t - (readlane(incl, src) - readlane(sum, src));
-    for (int e = src * per;; ++e) {
-        const int c = __builtin_amdgcn_readfirstlane(cnt[e]);
-        const int n = (c + BM - 1) / BM;
-        if (left < n) {
-            r.expert = e;
-            r.m0 = left * BM;
-            r.rows = c - r.m0 < BM ? c - r.m0 : BM;
-            return r;
+struct RowTiles {
+    const int32_t* cnt;
+    int El, per, sum, incl, total;
+
+    __device__ __forceinline__ RowTiles(const int32_t* counts, int num_experts) : cnt(counts), El(num_experts) {
+        per = (El + kWave - 1) / kWave;
+        sum = 0;
+        for (int i = 0; i < per; ++i) {
+            const int e = lane_id() * per + i;
+            if (e < El) sum += (cnt[e] + BM - 1) / BM;
         }
-        left -= n;
+        incl = wave_inclusive_scan(sum);
+        total = readlane(incl, kWave - 1);
     }
-}
+
+    __device__ __forceinline__ RowTile find(int t) const {   // 0 <= t < total
+        const int src = __builtin_ctzll(ballot(incl > t));
+        int left = t - (readlane(incl, src) - readlane(sum, src));
+        for (int e = src * per;; ++e) {
+            const int c = __builtin_amdgcn_readfirstlane(cnt[e]);
+            const int n = (c + BM - 1) / BM;
+            if (left < n) {
+                const int m0 = left * BM;
+                return RowTile{e, m0, c - m0 < BM ? c - m0 : BM};
+            }
+            left -= n;
+        }
+    }
+};
 
 }  // namespace ep

@@ -9,7 +9,7 @@
 // the sums.
 #include "ep_device.hpp"
 #include "ep_expert_tiles.hpp"
-#include "ep_internal.hpp"
+#include "ep_ffn.hpp"
 
 namespace ep {
 namespace {
@@ -63,36 +63,6 @@ struct Down {   // S = h rows, F = W2 rows
     __device__ void put(int64_t row, int, int n, const float* v) const { y[row * H + n] = narrow(v[0]); }
 };
 
-struct DownGrad {   // S = dy rows, F = columns of W2
-    static constexpr int kSums = 1;
-    Segments seg;
-    const uint16_t* dy; const uint16_t* w; const float* pre; uint16_t* dp; uint16_t* h;
-    int H, I;
-    __device__ int N() const { return I; }
-    __device__ int K() const { return H; }
-    __device__ float s(int64_t row, int k) const { return widen(dy[row * H + k]); }
-    __device__ float f(int, int e, int n, int k) const { return widen(w[((int64_t)e * H + k) * I + n]); }
-    __device__ void put(int64_t row, int, int n, const float* v) const {
-        const float g = pre[row * 2 * I + n], u = pre[row * 2 * I + I + n];
-        const float sg = 1.0f / (1.0f + __expf(-g));
-        dp[row * 2 * I + n] = narrow(v[0] * u * sg * (1.0f + g * (1.0f - sg)));
-        dp[row * 2 * I + I + n] = narrow(v[0] * g * sg);
-        h[row * I + n] = narrow(g * sg * u);
-    }
-};
-
-struct InGrad {   // S = dp rows, F = columns of W13
-    static constexpr int kSums = 1;
-    Segments seg;
-    const uint16_t* dp; const uint16_t* w; uint16_t* dx;
-    int H, I;
-    __device__ int N() const { return H; }
-    __device__ int K() const { return 2 * I; }
-    __device__ float s(int64_t row, int k) const { return widen(dp[row * 2 * I + k]); }
-    __device__ float f(int, int e, int n, int k) const { return widen(w[((int64_t)e * 2 * I + k) * H + n]); }
-    __device__ void put(int64_t row, int, int n, const float* v) const { dx[row * H + n] = narrow(v[0]); }
-};
-
 template <class Get>
 __device__ __forceinline__ void load_tile(float (*dst)[kTile + 1], int rows, int cols_k, Get get) {
     for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
@@ -105,8 +75,9 @@ __device__ __forceinline__ void load_tile(float (*dst)[kTile + 1], int rows, int
 template <class Op>
 __global__ __launch_bounds__(kThreads) void k_rows(Op op) {
     __shared__ float S[kStep][kTile + 1], F[Op::kSums][kStep][kTile + 1];
-    const RowTile t = find_row_tile<kTile>(op.seg.cnt, op.seg.El, (int)blockIdx.y);
-    if (t.expert < 0) return;
+    const RowTiles<kTile> tiles(op.seg.cnt, op.seg.El);
+    if ((int)blockIdx.y >= tiles.total) return;
+    const RowTile t = tiles.find((int)blockIdx.y);
     const int64_t row0 = (int64_t)op.seg.psum[t.expert] + t.m0;
     const int n0 = blockIdx.x * kTile, nn = min(kTile, op.N() - n0);
     const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
@@ -134,32 +105,6 @@ __global__ __launch_bounds__(kThreads) void k_rows(Op op) {
         }
 }
 
-// out[e] [M, N] = sum over the expert's rows of s[row, m] * f[row, n].
-__global__ __launch_bounds__(kThreads) void k_weights(Segments seg, const uint16_t* s, const uint16_t* f, uint16_t* out,
-                                                      int M, int N) {
-    __shared__ float S[kStep][kTile + 1], F[kStep][kTile + 1];
-    const int e = blockIdx.z, cnt = seg.cnt[e];
-    const int64_t row0 = seg.psum[e];
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile, mm = min(kTile, M - m0), nn = min(kTile, N - n0);
-    const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < cnt; k0 += kStep) {
-        const int kk = min(kStep, cnt - k0);
-        load_tile(S, mm, kk, [&](int r, int k) { return widen(s[(row0 + k0 + k) * M + m0 + r]); });
-        load_tile(F, nn, kk, [&](int r, int k) { return widen(f[(row0 + k0 + k) * N + n0 + r]); });
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int a = 0; a < 4; ++a)
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(S[k][tm + 16 * a], F[k][tn + 16 * b], acc[a][b]);
-        __syncthreads();
-    }
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int m = tm + 16 * a, n = tn + 16 * b;
-            if (m < mm && n < nn) out[((int64_t)e * M + m0 + m) * N + n0 + n] = narrow(acc[a][b]);
-        }
-}
-
 int tiles(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 // Row tiles any routing of the handle can give: every expert may end in a short one.
@@ -175,33 +120,12 @@ hipError_t rows_launch(const Handle& h, const Op& op, int N, hipStream_t stream)
 
 hipError_t launch_expert_ffn(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     if (h.T == 0) return hipSuccess;
+    if (!a.fp8) return launch_ffn_tile(h, a, stream);
     const Segments seg{h.ws.cnt_local, h.ws.psum, h.El};
     hipError_t e = rows_launch(h, GateUp{seg, a.x, a.x_scales, a.w13, a.w13_scales, a.pre, a.h, a.hidden, a.inter, a.fp8},
                                a.inter, stream);
     if (e != hipSuccess) return e;
     return rows_launch(h, Down{seg, a.h, a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter, a.fp8}, a.hidden, stream);
-}
-
-hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a, hipStream_t stream) {
-    const Segments seg{h.ws.cnt_local, h.ws.psum, h.El};
-    hipError_t e = hipSuccess;
-    if (h.T > 0) {
-        e = rows_launch(h, DownGrad{seg, (const uint16_t*)a.dy, (const uint16_t*)a.w2, a.pre, a.dp, a.h, a.hidden, a.inter},
-                        a.inter, stream);
-        if (e == hipSuccess && a.dx)
-            e = rows_launch(h, InGrad{seg, a.dp, (const uint16_t*)a.w13, (uint16_t*)a.dx, a.hidden, a.inter}, a.hidden, stream);
-    }
-    if (e == hipSuccess && a.dw2) {
-        hipLaunchKernelGGL(k_weights, dim3((unsigned)tiles(a.inter), (unsigned)tiles(a.hidden), (unsigned)h.El), dim3(kThreads),
-                           0, stream, seg, (const uint16_t*)a.dy, a.h, (uint16_t*)a.dw2, a.hidden, a.inter);
-        e = hipGetLastError();
-    }
-    if (e == hipSuccess && a.dw13) {
-        hipLaunchKernelGGL(k_weights, dim3((unsigned)tiles(a.hidden), (unsigned)tiles(2 * a.inter), (unsigned)h.El),
-                           dim3(kThreads), 0, stream, seg, a.dp, (const uint16_t*)a.x, (uint16_t*)a.dw13, 2 * a.inter, a.hidden);
-        e = hipGetLastError();
-    }
-    return e;
 }
 
 }  // namespace ep

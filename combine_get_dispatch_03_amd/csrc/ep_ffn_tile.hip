@@ -1,0 +1,215 @@
+// ep_ffn_tile.hip -- the products of the expert block on large tiles (see ep_gemm_core.hpp).
+#include "ep_expert_tiles.hpp"
+#include "ep_gemm_core.hpp"
+#include "ep_internal.hpp"
+#include "ep_ffn.hpp"
+
+namespace ep {
+namespace {
+
+enum Product { kGateUp, kDown, kDownGrad, kInGrad };
+
+struct Params {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int El;
+    const uint16_t* s;    // rows of the segments
+    const uint16_t* f;    // the weights
+    uint16_t* out;        // kGateUp: h   kDown: y   kDownGrad: dp   kInGrad: dx
+    uint16_t* out2;       // kDownGrad: h
+    float* pre;           // kGateUp: written when given   kDownGrad: read
+    int H, I;
+};
+
+// Workgroups of one XCD (every eighth) take consecutive tiles, and a run of consecutive tiles is kGroup row tiles by
+// as many channel tiles as fit, so that what an XCD's 32 CUs read at a time is few rows and few weights, from its own L2.
+constexpr int kXcds = 8, kGroup = 4;
+
+struct TileAt {
+    int row, col;
+};
+__device__ __forceinline__ bool tile_at(int block, int rows, int cols, TileAt* t) {
+    const int total = rows * cols, share = (total + kXcds - 1) / kXcds;
+    const int at = block / kXcds, i = block % kXcds * share + at;
+    if (at >= share || i >= total) return false;
+    const int group = i / (kGroup * cols), first = group * kGroup;
+    const int height = rows - first < kGroup ? rows - first : kGroup, in = i - group * kGroup * cols;
+    t->row = first + in % height;
+    t->col = in / height;
+    return true;
+}
+
+__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
+    *reinterpret_cast<i32x2*>(p) = i32x2{(int)pack_bf16x2(a, b), (int)pack_bf16x2(c, d)};
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+
+template <Product P, int MT>
+__global__ __launch_bounds__(kGemmThreads, 2) void k_rows(Params p) {
+    constexpr bool kFks = P == kDownGrad || P == kInGrad;
+    typedef Bf16Tile<MT, false, kFks> Tile;
+    extern __shared__ __align__(1024) char smem[];
+    const RowTiles<Tile::kBM> tiles(p.cnt, p.El);
+    constexpr int kCols = P == kGateUp ? kBN / 2 : kBN;     // channels of N per tile
+    const int N = P == kGateUp || P == kDownGrad ? p.I : p.H;
+    const int K = P == kGateUp || P == kDownGrad ? p.H : P == kDown ? p.I : 2 * p.I;
+    TileAt at;
+    if (!tile_at((int)blockIdx.x, tiles.total, (N + kCols - 1) / kCols, &at)) return;
+    const RowTile t = tiles.find(at.row);
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    const int n0 = at.col * kCols;
+
+    Tile g;
+    const uint32_t lds_s = 2u * K;
+    g.s.init(p.s + row0 * K, [&](int r) { return r < t.rows ? r * lds_s : kNoElement; });
+    if constexpr (P == kGateUp) {
+        // a wave's 64 rows of F: 32 gate channels, then the same 32 up channels
+        const uint64_t up = (uint64_t)p.I * p.H * 2;
+        g.f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H, [&](int r) {
+            const int c = r / 64 * 32 + r % 32;
+            return n0 + c < N ? (uint32_t)((r % 64 >= 32 ? up : 0) + (uint64_t)c * p.H * 2) : kNoElement;
+        });
+    } else if constexpr (P == kDown) {
+        g.f.init(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) { return n0 + r < N ? (uint32_t)r * p.I * 2 : kNoElement; });
+    } else if constexpr (P == kDownGrad) {
+        g.f.init(p.f + (int64_t)t.expert * p.H * p.I + n0, (int64_t)p.I * 2, N - n0);
+    } else {
+        g.f.init(p.f + (int64_t)t.expert * 2 * p.I * p.H + n0, (int64_t)p.H * 2, N - n0);
+    }
+    g.run(smem, K);
+
+    const int wave = threadIdx.x / kWave, m_at = (wave >> 2) * MT * 16 + (lane_id() & 15), n_in = (lane_id() >> 4) * 4;
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        const int m = m_at + a * 16;
+        if (m >= t.rows) continue;
+        const int64_t row = row0 + m;
+        if constexpr (P == kGateUp) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int n = n0 + (wave & 3) * 32 + b * 16 + n_in;
+                if (n >= N) continue;
+                const f32x4 gate = g.acc[a][b], up = g.acc[a][b + 2];
+                if (p.pre) {
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + n) = gate;
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + p.I + n) = up;
+                }
+                f32x4 h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = gate[i] * sigmoid(gate[i]) * up[i];
+                store4(p.out + row * p.I + n, h[0], h[1], h[2], h[3]);
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int n = n0 + (wave & 3) * 64 + b * 16 + n_in;
+                if (n >= N) continue;
+                const f32x4 v = g.acc[a][b];
+                if constexpr (P == kDownGrad) {
+                    const f32x4 gate = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + n);
+                    const f32x4 up = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + p.I + n);
+                    f32x4 dg, du, h;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sg = sigmoid(gate[i]), act = gate[i] * sg;
+                        dg[i] = v[i] * up[i] * sg * (1.0f + gate[i] * (1.0f - sg));
+                        du[i] = v[i] * act;
+                        h[i] = act * up[i];
+                    }
+                    store4(p.out + row * 2 * p.I + n, dg[0], dg[1], dg[2], dg[3]);
+                    store4(p.out + row * 2 * p.I + p.I + n, du[0], du[1], du[2], du[3]);
+                    store4(p.out2 + row * p.I + n, h[0], h[1], h[2], h[3]);
+                } else {
+                    store4(p.out + row * N + n, v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+    }
+}
+
+// out[e] [M, N] = sum over the expert's rows of s[row, m] f[row, n]
+template <int MT>
+__global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt, const int32_t* psum, int El, const uint16_t* s,
+                                                             const uint16_t* f, uint16_t* out, int M, int N) {
+    typedef Bf16Tile<MT, true, true> Tile;
+    extern __shared__ __align__(1024) char smem[];
+    const int mt = (M + Tile::kBM - 1) / Tile::kBM, nt = (N + kBN - 1) / kBN;
+    TileAt at;
+    if (!tile_at((int)blockIdx.x, El * mt, nt, &at)) return;
+    const int e = at.row / mt, m0 = at.row % mt * Tile::kBM, n0 = at.col * kBN;
+    const int rows = __builtin_amdgcn_readfirstlane(cnt[e]);
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(psum[e]);
+    Tile g;
+    g.s.init(s + row0 * M + m0, (int64_t)M * 2, M - m0);
+    g.f.init(f + row0 * N + n0, (int64_t)N * 2, N - n0);
+    g.run(smem, rows);
+    const int wave = threadIdx.x / kWave, m_at = m0 + (wave >> 2) * MT * 16 + (lane_id() & 15);
+    const int n_at = n0 + (wave & 3) * 64 + (lane_id() >> 4) * 4;
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int m = m_at + a * 16, n = n_at + b * 16;
+            const f32x4 v = g.acc[a][b];
+            if (m < M && n < N) store4(out + ((int64_t)e * M + m) * N + n, v[0], v[1], v[2], v[3]);
+        }
+}
+
+unsigned blocks(int64_t tiles) { return (unsigned)((tiles + kXcds - 1) / kXcds * kXcds); }
+
+template <Product P, int MT>
+hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
+    typedef Bf16Tile<MT, false, P == kDownGrad || P == kInGrad> Tile;
+    const int N = P == kGateUp || P == kDownGrad ? p.I : p.H, cols = P == kGateUp ? kBN / 2 : kBN;
+    // row tiles that any routing can give: every expert may end in a short one
+    const int64_t rows = (int64_t)h.T * h.K / Tile::kBM + h.El;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows<P, MT>), Tile::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_rows<P, MT>), dim3(blocks(rows * ((N + cols - 1) / cols))), dim3(kGemmThreads), Tile::kLds, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f, uint16_t* out, int M, int N, hipStream_t stream) {
+    typedef Bf16Tile<8, true, true> Tile;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_weights<8>), Tile::kLds);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (int64_t)h.El * ((M + Tile::kBM - 1) / Tile::kBM) * ((N + kBN - 1) / kBN);
+    hipLaunchKernelGGL(k_weights<8>, dim3(blocks(tiles)), dim3(kGemmThreads), Tile::kLds, stream, h.ws.cnt_local, h.ws.psum, h.El,
+                       s, f, out, M, N);
+    return hipGetLastError();
+}
+
+template <Product P>
+hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
+    return many_rows(h) ? rows_launch<P, 8>(h, p, stream) : rows_launch<P, 4>(h, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_ffn_tile(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params up{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
+    const hipError_t e = rows_launch<kGateUp>(h, up, stream);
+    if (e != hipSuccess) return e;
+    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, (const uint16_t*)a.w2, (uint16_t*)a.y, nullptr, nullptr, a.hidden, a.inter};
+    return rows_launch<kDown>(h, down, stream);
+}
+
+hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a, hipStream_t stream) {
+    const uint16_t* dy = (const uint16_t*)a.dy;
+    hipError_t e = hipSuccess;
+    if (h.T > 0) {
+        const Params dg{h.ws.cnt_local, h.ws.psum, h.El, dy, (const uint16_t*)a.w2, a.dp, a.h, const_cast<float*>(a.pre), a.hidden, a.inter};
+        e = rows_launch<kDownGrad>(h, dg, stream);
+        if (e == hipSuccess && a.dx) {
+            const Params ig{h.ws.cnt_local, h.ws.psum, h.El, a.dp, (const uint16_t*)a.w13, (uint16_t*)a.dx, nullptr, nullptr, a.hidden, a.inter};
+            e = rows_launch<kInGrad>(h, ig, stream);
+        }
+    }
+    if (e == hipSuccess && a.dw2) e = weights_launch(h, dy, a.h, (uint16_t*)a.dw2, a.hidden, a.inter, stream);
+    if (e == hipSuccess && a.dw13)
+        e = weights_launch(h, a.dp, (const uint16_t*)a.x, (uint16_t*)a.dw13, 2 * a.inter, a.hidden, stream);
+    return e;
+}
+
+}  // namespace ep

@@ -1,0 +1,239 @@
+// ep_ffn_stream.hip -- the expert block's forward pass for few rows per expert (decode): bound by reading the weights.
+//
+// A workgroup takes up to 64 rows of an expert and 64 rows of its weights (32 gate and the same 32 up channels, or 64
+// output channels).  Its four waves split k: each streams its part of the 64 weight rows from memory straight into the
+// fragments of the matrix instruction, the next step's loads in flight while the current one is multiplied; nothing is
+// shared, so no barrier stands in the loop.  The rows' fragments come from the caches.  At the end the waves' sums meet
+// in LDS.
+#include "ep_expert_tiles.hpp"
+#include "ep_ffn.hpp"
+#include "ep_gemm_core.hpp"
+
+namespace ep {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64, kCols = 64, kNF = kCols / 16;
+constexpr int kSumPitch = kCols + 4;
+
+struct Params {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int El;
+    const void* s;
+    const float* s_scales;
+    const void* f;
+    const float* f_scales;
+    uint16_t* out;
+    float* pre;
+    int N, K;      // channels of a projection's output, of its input
+};
+
+enum Format { kBf16, kFp8 };
+
+// 128 bytes of each of a wave's weight rows: the lane's two 16-byte pieces per fragment.
+struct Weights {
+    i32x4 v[kNF][2];
+};
+template <Format F, bool UP>
+struct RowsOf;
+template <bool UP>
+struct RowsOf<kBf16, UP> { static constexpr int kPieces = 2; };     // 64 k of bf16
+template <>
+struct RowsOf<kFp8, true> { static constexpr int kPieces = 2; };    // 128 k of e4m3
+template <>
+struct RowsOf<kFp8, false> { static constexpr int kPieces = 4; };   // 128 k of bf16 beside e4m3 weights
+
+template <Format F, bool UP, int MT>
+__device__ __forceinline__ void product(const Params& p, const RowTile& t, int64_t row0, int n0, char* smem) {
+    constexpr int kPieces = RowsOf<F, UP>::kPieces;
+    constexpr int kWide = F == kFp8 ? 1 : 2;                   // bytes of a weight
+    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
+    const int f_bytes = p.K * kWide;                           // of a weight row
+    const int steps = (f_bytes + 127) / 128;
+
+    const char* f[kNF];
+    bool f_there[kNF];
+#pragma unroll
+    for (int b = 0; b < kNF; ++b) {
+        const int c = UP ? n0 + b % 2 * 16 + r : n0 + b * 16 + r;
+        f_there[b] = c < p.N;
+        const int64_t row = (int64_t)t.expert * (UP ? 2 : 1) * p.N + (UP && b >= 2 ? p.N : 0) + (f_there[b] ? c : n0);
+        f[b] = (const char*)p.f + row * f_bytes + g * 16;
+    }
+    const char* s[MT];
+    bool s_there[MT];
+    const int s_bytes = UP ? f_bytes : p.K * 2;
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        s_there[a] = a * 16 + r < t.rows;
+        s[a] = (const char*)p.s + (row0 + (s_there[a] ? a * 16 + r : 0)) * s_bytes + (F == kFp8 && !UP ? g * 32 : g * 16);
+    }
+
+    auto load_f = [&](int st) {
+        Weights w;
+        const int at = st * 128;
+#pragma unroll
+        for (int b = 0; b < kNF; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                w.v[b][j] = i32x4{0, 0, 0, 0};
+                if (at + j * 64 + g * 16 < f_bytes) w.v[b][j] = __builtin_nontemporal_load((const i32x4*)(f[b] + at + j * 64));
+            }
+        return w;
+    };
+
+    f32x4 acc[MT][kNF];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < kNF; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const f32x4 zero{0.0f, 0.0f, 0.0f, 0.0f};
+
+    Weights next = load_f(wave < steps ? wave : 0);
+    for (int st = wave; st < steps; st += kWaves) {
+        // the rows' pieces of this step, then the weights of the next: the wait for the first leaves the second in flight
+        i32x4 sv[MT][kPieces];
+        float s_scale[MT], f_scale[2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                sv[a][j] = i32x4{0, 0, 0, 0};
+                // where the pieces of 16 bytes stand: j * 64 beside weights of the rows' own format; beside e4m3 weights
+                // the lane's 16 k are 32 bytes of bf16
+                const int at = F == kFp8 && !UP ? st * 256 + (j >> 1) * 128 + (j & 1) * 16 : st * 128 + j * 64;
+                if (s_there[a] && at + (F == kFp8 && !UP ? g * 32 : g * 16) < s_bytes) sv[a][j] = *(const i32x4*)(s[a] + at);
+            }
+        if constexpr (F == kFp8) {
+            const int blocks = p.K / 128;
+            if constexpr (UP) {
+#pragma unroll
+                for (int a = 0; a < MT; ++a) s_scale[a] = s_there[a] ? p.s_scales[(row0 + a * 16 + r) * blocks + st] : 0.0f;
+                const float* fs = p.f_scales + ((int64_t)t.expert * 2 * p.N + n0) / 128 * blocks + st;
+                f_scale[0] = fs[0];
+                f_scale[1] = fs[(int64_t)p.N / 128 * blocks];
+            } else {
+                f_scale[0] = p.f_scales[((int64_t)t.expert * p.N + n0) / 128 * blocks + st];
+            }
+        }
+        const Weights cur = next;
+        next = load_f(st + kWaves < steps ? st + kWaves : st);
+        if constexpr (F == kBf16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b < kNF; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.v[b][j]),
+                                                                            __builtin_bit_cast(bf16x8, sv[a][j]), acc[a][b], 0, 0, 0);
+        } else if constexpr (UP) {
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                const i32x8 sa = __builtin_shufflevector(sv[a][0], sv[a][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int b = 0; b < kNF; ++b) {
+                    const i32x8 fb = __builtin_shufflevector(cur.v[b][0], cur.v[b][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, sa, zero, 0, 0, 0, 0, 0, 0);
+                    const float scale = s_scale[a] * f_scale[b / 2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(part[i], scale, acc[a][b][i]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < kNF; ++b) {
+                f32x4 part[MT];
+#pragma unroll
+                for (int a = 0; a < MT; ++a) part[a] = zero;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const i32x4 q = cur.v[b][j >> 1];
+                    const bf16x8 fv = widen_e4m3x8(j & 1 ? i32x2{q[2], q[3]} : i32x2{q[0], q[1]});
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+                        part[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, __builtin_bit_cast(bf16x8, sv[a][j]), part[a], 0, 0, 0);
+                }
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(part[a][i], f_scale[0], acc[a][b][i]);
+            }
+        }
+    }
+
+    // sums of the waves: [wave][16 rows][64 channels], 16 rows at a time
+    float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kNF; ++b)
+            *reinterpret_cast<f32x4*>(sums + (wave * 16 + r) * kSumPitch + b * 16 + g * 4) = acc[a][b];
+        __syncthreads();
+        const int m = threadIdx.x / 16, n4 = threadIdx.x % 16 * 4;      // 16 rows x 64 channels, 4 per thread
+        f32x4 v = zero;
+        if (!UP || n4 < 32) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kSumPitch + n4);
+        }
+        const int64_t row = row0 + a * 16 + m;
+        const bool there = a * 16 + m < t.rows && n0 + n4 < p.N;
+        if constexpr (UP) {
+            if (n4 < 32 && there) {
+                f32x4 u = zero, h;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) u += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kSumPitch + 32 + n4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = v[i] * sigmoid(v[i]) * u[i];
+                if (p.pre) {
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.N + n0 + n4) = v;
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.N + p.N + n0 + n4) = u;
+                }
+                store4(p.out + row * p.N + n0 + n4, h[0], h[1], h[2], h[3]);
+            }
+        } else if (there) {
+            store4(p.out + row * p.N + n0 + n4, v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+template <Format F, bool UP>
+__global__ __launch_bounds__(kThreads) void k_stream(Params p) {
+    __shared__ __align__(16) char smem[kWaves * 16 * kSumPitch * 4];
+    const RowTiles<kRows> tiles(p.cnt, p.El);
+    constexpr int kChannels = UP ? kCols / 2 : kCols;
+    const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
+    if (tile >= tiles.total) return;
+    const RowTile t = tiles.find(tile);
+    const int n0 = blockIdx.x % cols * kChannels;
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    switch ((t.rows + 15) / 16) {
+        case 1: product<F, UP, 1>(p, t, row0, n0, smem); break;
+        case 2: product<F, UP, 2>(p, t, row0, n0, smem); break;
+        case 3: product<F, UP, 3>(p, t, row0, n0, smem); break;
+        default: product<F, UP, 4>(p, t, row0, n0, smem); break;
+    }
+}
+
+template <Format F, bool UP>
+hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
+    constexpr int kChannels = UP ? kCols / 2 : kCols;
+    // tiles that any routing can give: no more than entries, and every expert may end in a short one
+    const int64_t entries = (int64_t)h.T * h.K, tiles = entries / kRows + h.El;
+    hipLaunchKernelGGL((k_stream<F, UP>), dim3((unsigned)((tiles < entries ? tiles : entries) * ((p.N + kChannels - 1) / kChannels))),
+                       dim3(kThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ffn_stream(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden};
+    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter};
+    const hipError_t e = a.fp8 ? stream_launch<kFp8, true>(h, up, stream) : stream_launch<kBf16, true>(h, up, stream);
+    if (e != hipSuccess) return e;
+    return a.fp8 ? stream_launch<kFp8, false>(h, down, stream) : stream_launch<kBf16, false>(h, down, stream);
+}
+
+}  // namespace ep

@@ -1,8 +1,7 @@
 // ep_ffn_tile.hip -- the products of the expert block on large tiles (see ep_gemm_core.hpp).
 #include "ep_expert_tiles.hpp"
-#include "ep_gemm_core.hpp"
-#include "ep_internal.hpp"
 #include "ep_ffn.hpp"
+#include "ep_gemm_core.hpp"
 
 namespace ep {
 namespace {
@@ -20,30 +19,6 @@ struct Params {
     float* pre;           // kGateUp: written when given   kDownGrad: read
     int H, I;
 };
-
-// Workgroups of one XCD (every eighth) take consecutive tiles, and a run of consecutive tiles is kGroup row tiles by
-// as many channel tiles as fit, so that what an XCD's 32 CUs read at a time is few rows and few weights, from its own L2.
-constexpr int kXcds = 8, kGroup = 4;
-
-struct TileAt {
-    int row, col;
-};
-__device__ __forceinline__ bool tile_at(int block, int rows, int cols, TileAt* t) {
-    const int total = rows * cols, share = (total + kXcds - 1) / kXcds;
-    const int at = block / kXcds, i = block % kXcds * share + at;
-    if (at >= share || i >= total) return false;
-    const int group = i / (kGroup * cols), first = group * kGroup;
-    const int height = rows - first < kGroup ? rows - first : kGroup, in = i - group * kGroup * cols;
-    t->row = first + in % height;
-    t->col = in / height;
-    return true;
-}
-
-__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
-    *reinterpret_cast<i32x2*>(p) = i32x2{(int)pack_bf16x2(a, b), (int)pack_bf16x2(c, d)};
-}
-
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 
 template <Product P, int MT>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_rows(Params p) {
@@ -156,8 +131,6 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt,
         }
 }
 
-unsigned blocks(int64_t tiles) { return (unsigned)((tiles + kXcds - 1) / kXcds * kXcds); }
-
 template <Product P, int MT>
 hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
     typedef Bf16Tile<MT, false, P == kDownGrad || P == kInGrad> Tile;
@@ -166,7 +139,7 @@ hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
     const int64_t rows = (int64_t)h.T * h.K / Tile::kBM + h.El;
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows<P, MT>), Tile::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_rows<P, MT>), dim3(blocks(rows * ((N + cols - 1) / cols))), dim3(kGemmThreads), Tile::kLds, stream, p);
+    hipLaunchKernelGGL((k_rows<P, MT>), dim3(tile_blocks(rows * ((N + cols - 1) / cols))), dim3(kGemmThreads), Tile::kLds, stream, p);
     return hipGetLastError();
 }
 
@@ -175,7 +148,7 @@ hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f,
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_weights<8>), Tile::kLds);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t)h.El * ((M + Tile::kBM - 1) / Tile::kBM) * ((N + kBN - 1) / kBN);
-    hipLaunchKernelGGL(k_weights<8>, dim3(blocks(tiles)), dim3(kGemmThreads), Tile::kLds, stream, h.ws.cnt_local, h.ws.psum, h.El,
+    hipLaunchKernelGGL(k_weights<8>, dim3(tile_blocks(tiles)), dim3(kGemmThreads), Tile::kLds, stream, h.ws.cnt_local, h.ws.psum, h.El,
                        s, f, out, M, N);
     return hipGetLastError();
 }

@@ -1,0 +1,116 @@
+// ep_ffn_tile_fp8.hip -- the expert block's forward pass with e4m3 rows and weights on large tiles.
+//
+// Gate and up projection: e4m3 by e4m3, twice the rate of bf16.  h stays bf16 (e4m3 would cost it 2^-4 of an element), so
+// the down projection is bf16 by e4m3 weights widened on the way to the matrix unit.
+#include "ep_expert_tiles.hpp"
+#include "ep_ffn.hpp"
+#include "ep_gemm_core.hpp"
+
+namespace ep {
+namespace {
+
+struct Params {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int El;
+    const void* s;
+    const float* s_scales;    // gate and up: [rows, H / 128]
+    const uint8_t* f;
+    const float* f_scales;
+    uint16_t* out;
+    int H, I;
+};
+
+// The scales of two rows of 128 x 128 blocks, `n` each, to LDS.
+__device__ __forceinline__ void stage_scales(char* smem, int at, const float* a, const float* b, int n) {
+    float* to = reinterpret_cast<float*>(smem + at);
+    const int i = threadIdx.x & 255;
+    if (i < n) to[threadIdx.x] = (threadIdx.x < 256 ? a : b)[i];
+}
+
+__global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
+    extern __shared__ __align__(1024) char smem[];
+    const RowTiles<Fp8Tile::kBM> tiles(p.cnt, p.El);
+    TileAt at;
+    if (!tile_at((int)blockIdx.x, tiles.total, p.I / 128, &at)) return;
+    const RowTile t = tiles.find(at.row);
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    const int n0 = at.col * 128, blocks = p.H / 128, wave = wave_id();
+
+    Fp8Tile g;
+    g.s.init((const uint8_t*)p.s + row0 * p.H, [&](int r) { return r < t.rows ? (uint32_t)(r * p.H) : kNoElement; });
+    // a wave's 64 rows of F: 32 gate channels, then the same 32 up channels
+    const uint32_t up = (uint32_t)p.I * p.H;
+    g.f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H,
+             [&](int r) { return (r % 64 >= 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + r % 32) * p.H); });
+    const int r = (wave >> 2) * 64 + lane_id();
+    g.scales = uniform64((uint64_t)(p.s_scales + row0 * blocks));
+    g.scale_offset = r < t.rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
+    const float* fs = p.f_scales + ((int64_t)t.expert * 2 * p.I + n0) / 128 * blocks;
+    stage_scales(smem, Fp8Tile::kFScales, fs, fs + (int64_t)p.I / 128 * blocks, blocks);
+    g.run(smem, blocks);
+
+    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 32 + (lane_id() >> 4) * 4;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const int m = m_at + a * 16;
+        if (m >= t.rows) continue;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const f32x4 gate = g.acc[a][b], u = g.acc[a][b + 2];
+            f32x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = gate[i] * sigmoid(gate[i]) * u[i];
+            store4(p.out + (row0 + m) * p.I + n_at + b * 16, h[0], h[1], h[2], h[3]);
+        }
+    }
+}
+
+__global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
+    extern __shared__ __align__(1024) char smem[];
+    const RowTiles<Bf16ByFp8Tile::kBM> tiles(p.cnt, p.El);
+    TileAt at;
+    if (!tile_at((int)blockIdx.x, tiles.total, (p.H + kBN - 1) / kBN, &at)) return;
+    const RowTile t = tiles.find(at.row);
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    const int n0 = at.col * kBN, blocks = p.I / 128, wave = wave_id();
+
+    Bf16ByFp8Tile g;
+    g.s.init((const uint16_t*)p.s + row0 * p.I, [&](int r) { return r < t.rows ? (uint32_t)r * p.I * 2 : kNoElement; });
+    g.init_f(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) { return n0 + r < p.H ? (uint32_t)(r * p.I) : kNoElement; });
+    const float* fs = p.f_scales + ((int64_t)t.expert * p.H + n0) / 128 * blocks;
+    const bool second = n0 + 128 < p.H;      // the tile's second 128 channels exist
+    stage_scales(smem, Bf16ByFp8Tile::kFScales, fs, second ? fs + blocks : fs, blocks);
+    g.run(smem, p.I);
+
+    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 64 + (lane_id() >> 4) * 4;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const int m = m_at + a * 16;
+        if (m >= t.rows) continue;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int n = n_at + b * 16;
+            const f32x4 v = g.acc[a][b];
+            if (n < p.H) store4(p.out + (row0 + m) * p.H + n, v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const int64_t rows = (int64_t)h.T * h.K / 128 + h.El;
+    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tile::kLds);
+    if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tile::kLds);
+    if (e != hipSuccess) return e;
+    const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
+    hipLaunchKernelGGL(k_gate_up, dim3(tile_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tile::kLds, stream, up);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};
+    hipLaunchKernelGGL(k_down, dim3(tile_blocks(rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tile::kLds, stream, down);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -68,6 +68,8 @@ SHAPES = [
     (200, 520, 328, 3, 1, 0, 1, 128, "zipf"),
     (257, 320, 200, 5, 1, 0, 2, 1, "one"),
     (40, 256, 128, 4, 1, 0, 2, 16, "none"),
+    (150, 264, 136, 32, 1, 0, 2, 16, "one"),       # few rows by the average, 300 on one expert
+    (100, 640, 384, 8, 1, 0, 2, 1, "zipf"),
     (700, 512, 264, 4, 1, 0, 3, 1, "zipf"),
     (1000, 1032, 520, 20, 4, 2, 8, 128, "holes"),
     (2100, 256, 384, 4, 1, 0, 4, 128, "zipf"),

@@ -11,7 +11,8 @@ struct RowTile {
     int rows;     // valid rows of the tile (1..BM)
 };
 
-// The tiles of BM rows of all experts, in the experts' order, ceil(count / BM) each.  Every wave of a workgroup works
+// The tiles of all experts, in the experts' order: ceil(count / BM) each, as even in height as multiples of `unit` rows
+// allow (1050 rows are five tiles of 224 and 154 rather than four of 256 and one of 26).  Every wave of a workgroup works
 // them out for itself (no LDS, no barrier): lane l sums the tiles of experts [l * per, l * per + per) and a wave scan
 // places them; find() then needs at most `per` (16 for 1024 experts) uniform steps.
 template <int BM>
@@ -30,15 +31,15 @@ struct RowTiles {
         total = readlane(incl, kWave - 1);
     }
 
-    __device__ __forceinline__ RowTile find(int t) const {   // 0 <= t < total
+    __device__ __forceinline__ RowTile find(int t, int unit = BM) const {   // 0 <= t < total
         const int src = __builtin_ctzll(ballot(incl > t));
         int left = t - (readlane(incl, src) - readlane(sum, src));
         for (int e = src * per;; ++e) {
             const int c = __builtin_amdgcn_readfirstlane(cnt[e]);
             const int n = (c + BM - 1) / BM;
             if (left < n) {
-                const int m0 = left * BM;
-                return RowTile{e, m0, c - m0 < BM ? c - m0 : BM};
+                const int height = ((c + n - 1) / n + unit - 1) / unit * unit, m0 = left * height;
+                return RowTile{e, m0, c - m0 < height ? c - m0 : height};
             }
             left -= n;
         }

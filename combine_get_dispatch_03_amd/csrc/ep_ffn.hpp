@@ -9,9 +9,6 @@ namespace ep {
 // Rows an expert gets on average.  The host knows sizes only, not the routing: of T * K entries, an expert's share.
 inline double mean_rows(const Handle& h) { return (double)h.T * h.K / h.E; }
 
-// Row tiles of 256 rather than 128.
-inline bool many_rows(const Handle& h) { return mean_rows(h) >= 192; }
-
 // Weights streamed past the rows rather than tiles of both through LDS.
 inline bool few_rows(const Handle& h) { return mean_rows(h) < 48; }
 

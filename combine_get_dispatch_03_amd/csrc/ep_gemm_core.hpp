@@ -2,22 +2,19 @@
 //
 //   acc[m][n] = sum_k S[m][k] F[n][k]        m: rows of the segment (or of a weight gradient), n: output channels
 //
-// Workgroup: 8 waves, 2 along m by 4 along n, 16x16x32 bf16 matrix instructions with fp32 sums.  The instruction's first
-// operand is F, so a lane ends up with 4 consecutive n of one m and stores them with one instruction.
+// Eight waves, 2 along m by 4 along n; 16x16x32 bf16 matrix instructions with fp32 sums.  The instruction's first operand is F, so a lane ends up with 4
+// consecutive n of one m and stores them with one instruction.
 //
-// Operands travel global -> LDS by the buffer loads that write LDS directly (no registers, no ds_write), 32 k per
-// stage, kBuffers stages deep.  An element that does not exist (a row past the segment, a channel past N, a k past
+// Operands travel global -> LDS by the buffer loads that write LDS directly (no registers, no ds_write), a few
+// stages deep.  An element that does not exist (a row past the segment, a channel past N, a k past
 // the end) is loaded from an offset past the resource's end, which the hardware answers with zero: no branch, and
 // nothing outside the tensors (or in padding rows, whose NaNs would spread) is read.
 //
 // Two LDS forms, by the operand's layout in memory:
-//   k contiguous (KC): 64 bytes a row, two rows a 128-byte line, 16-byte chunks permuted by the line number so that the
-//     16 lanes x 16 bytes of a fragment read hit every bank once.
+//   k contiguous (KC): 128 bytes a row, 16-byte chunks permuted by the row number so that a fragment read (16 rows, 16
+//     bytes at one place of each) is spread over all banks.
 //   k strided (KS): a k-row of all columns; fragments come from the transposing LDS read (four k of a column per
 //     lane), chunk pairs permuted by the k-row for the same reason.
-//
-// Schedule: the waves of the lower m half run half a step ahead of the others, so that on every SIMD one wave feeds the
-// matrix unit while the other reads its next fragments; barriers keep the two in step.
 #pragma once
 
 #include "ep_device.hpp"
@@ -81,84 +78,77 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// An operand whose k is contiguous: ROWS rows, 64 bytes of each per stage (32 bf16, or 64 e4m3).
+// An operand whose k is contiguous: ROWS rows, 128 bytes of each per stage (64 bf16, or 128 e4m3).  A row is a line of LDS,
+// its 16-byte chunks permuted by the row number.
 template <int ROWS>
 struct KcOperand {
-    static constexpr int kCopies = ROWS / 16 / kGemmWaves;   // copies of a stage per wave
-    static constexpr int kBytes = ROWS * 64;
+    static constexpr int kCopies = ROWS / 8 / kGemmWaves;     // copies of a stage per wave
+    static constexpr int kBytes = ROWS * 128;
     uint64_t base;
     uint32_t offset[kCopies];
-    int chunk;     // the lane's 16-byte chunk of its rows
+
+    static __device__ __forceinline__ int chunk() { return (lane_id() & 7) ^ (lane_id() >> 3); }   // the lane's, of 8
 
     // row_offset(r): byte offset of tile row r from `start`, or kNoElement.
     template <class RowOffset>
     __device__ __forceinline__ void init(const void* start, RowOffset row_offset) {
-        const int lane = lane_id(), wave = wave_id();
         base = uniform64((uint64_t)start);
-        const int x = (lane & 7) ^ (lane >> 3);
-        chunk = x & 3;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int line = (i * kGemmWaves + wave) * 8 + (lane >> 3);
-            const uint32_t o = row_offset(2 * line + (x >> 2));
-            offset[i] = o == kNoElement ? kNoElement : o + chunk * 16;
+            const uint32_t o = row_offset((i * kGemmWaves + wave_id()) * 8 + (lane_id() >> 3));
+            offset[i] = o == kNoElement ? kNoElement : o + chunk() * 16;
         }
     }
-    // Stage with `left` bytes of each row to go (<= 0: nothing is read, LDS is zeroed).
+    // The next stage, with `left` chunks of each row to go (none or fewer: nothing is read, LDS is zeroed).
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
         const i32x4 res = resource(base, left > 0 ? kNoElement : 0u);
-        const uint32_t to = lds + wave_id() * 1024;
+        const bool there = chunk() < left;
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const uint32_t o = left >= 64 || chunk * 16 < left ? offset[i] : kNoElement;
-            copy16_to_lds(to + i * kGemmWaves * 1024, o, res);
-        }
-        base += 64;
+        for (int i = 0; i < kCopies; ++i)
+            copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, there ? offset[i] : kNoElement, res);
+        base += 128;
     }
-    // LDS offset of the lane's 16 bytes (8 bf16) of fragment row 0; fragment j is at + j * 1024.
+    // LDS offset of the lane's 16 bytes of the rows from row0, first half of the line; the second half is at ^ 64, the
+    // next 16 rows at + 2048.
     static __device__ __forceinline__ uint32_t fragment(int row0) {
-        const int r = lane_id() & 15, g = lane_id() >> 4, line = r >> 1;
-        return row0 * 64 + line * 128 + (((((r & 1) << 2) | g) ^ line) << 4);
+        const int r = lane_id() & 15, g = lane_id() >> 4;
+        return (row0 + r) * 128 + ((g ^ (r & 7)) << 4);
     }
 };
 
-// An operand whose k is strided: 32 k-rows per stage, COLS columns of bf16.
+// An operand whose k is strided: 64 k-rows per stage, COLS columns of bf16.
 template <int COLS>
 struct KsOperand {
     static constexpr int kRowBytes = COLS * 2, kChunks = kRowBytes / 16;
-    static constexpr int kCopies = 32 * kRowBytes / 1024 / kGemmWaves;
-    static constexpr int kBytes = 32 * kRowBytes;
+    static constexpr int kCopies = 64 * kRowBytes / 1024 / kGemmWaves;
+    static constexpr int kBytes = 64 * kRowBytes;
     uint64_t base;
-    uint64_t step;     // bytes of 32 k-rows
+    uint64_t step;     // bytes of 64 k-rows
     uint32_t offset[kCopies];
-    int row[kCopies];
 
     static __device__ __forceinline__ int permute(int k) { return ((k & 3) | ((k >> 3) & 1) << 2) << 1; }
+    static __device__ __forceinline__ int row(int i) { return (i * kGemmWaves + wave_id()) * (kWave / kChunks) + lane_id() / kChunks; }
 
     // cols: columns that exist, counted from the tile's first.
     __device__ __forceinline__ void init(const void* start, int64_t stride_bytes, int cols) {
-        const int lane = lane_id(), wave = wave_id();
         base = uniform64((uint64_t)start);
-        step = uniform64((uint64_t)stride_bytes * 32);
+        step = uniform64((uint64_t)stride_bytes * 64);
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            row[i] = (i * kGemmWaves + wave) * (kWave / kChunks) + lane / kChunks;
-            const int c = (lane % kChunks) ^ permute(row[i]);
-            offset[i] = c * 8 < cols ? (uint32_t)(row[i] * stride_bytes) + c * 16 : kNoElement;
+            const int c = (lane_id() % kChunks) ^ permute(row(i));
+            offset[i] = c * 8 < cols ? (uint32_t)(row(i) * stride_bytes) + c * 16 : kNoElement;
         }
     }
-    // Stage with `left` k-rows to go.
+    // The next stage, with `left` k-rows to go.
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
         const i32x4 res = resource(base, left > 0 ? kNoElement : 0u);
-        const uint32_t to = lds + wave_id() * 1024;
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const uint32_t o = left >= 32 || row[i] < left ? offset[i] : kNoElement;
-            copy16_to_lds(to + i * kGemmWaves * 1024, o, res);
-        }
+        for (int i = 0; i < kCopies; ++i)
+            copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, row(i) < left ? offset[i] : kNoElement, res);
         base += step;
     }
-    // LDS offset of the lane's part of the 16 columns from col0: k-rows 8g .. 8g + 3, and + 4 * kRowBytes for the rest.
+    // LDS offset of the lane's part of the 16 columns from col0: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
+    // + 32 * kRowBytes for the second 32 k.
     static __device__ __forceinline__ uint32_t fragment(int col0) {
         const int lane = lane_id(), k = (lane >> 4) * 8 + ((lane & 15) >> 2), q = lane & 3;
         return k * kRowBytes + (((col0 / 8 + (q >> 1)) ^ permute(k)) << 4) + (q & 1) * 8;
@@ -188,31 +178,32 @@ struct OperandOf { typedef KcOperand<ROWS> type; };
 template <int ROWS>
 struct OperandOf<ROWS, true> { typedef KsOperand<ROWS> type; };
 
-// The tile: 2 * MT * 16 rows of S against 256 rows of F.
-template <int MT, bool SKS, bool FKS>
+// The bf16 tile: up to 256 rows of S against 256 rows of F, 64 k per stage.  A wave owns 16 * MT rows (MT of run(), up to
+// 8) by 64 channels.
+//
+// Waves 0-3 (the upper rows) run half a step ahead of waves 4-7, so that on every SIMD one wave feeds the matrix unit
+// while the other reads its next fragments; two barriers per 32 k keep them in step.  The copies of a step are issued
+// before its reads.  S is two stages deep in LDS and F three: all 160 KiB.  F's stage st + 2 and S's stage st + 1 are
+// under way while stage st is multiplied; weights come from HBM and need the longer lead, rows are read again and
+// again from L2.  Measured on 8192 x 8192 x 4096 (dense, everything in reach of L2): 1.43 PFLOP/s; 32 k per stage, four stages
+// deep, 1.39; with the copies left out 1.70, the reads too 1.86.
+template <bool SKS, bool FKS>
 struct Bf16Tile {
-    static constexpr int kBM = 2 * MT * 16, NT = 4;
+    static constexpr int kBM = 256, NT = 4;
     typedef typename OperandOf<kBM, SKS>::type SOp;
     typedef typename OperandOf<kBN, FKS>::type FOp;
-    static constexpr int kStage = SOp::kBytes + FOp::kBytes;
-    static constexpr int kBuffers = MT == 8 ? 4 : 3;     // the smaller tile: two workgroups on a CU
-    static constexpr int kLds = kStage * kBuffers;
-    static constexpr int kCopies = SOp::kCopies + FOp::kCopies;
+    static constexpr int kSBuffers = 2, kFBuffers = 3, kF = SOp::kBytes * kSBuffers;
+    static constexpr int kLds = kF + FOp::kBytes * kFBuffers;
 
     SOp s;
     FOp f;
-    f32x4 acc[MT][NT];
+    f32x4 acc[8][NT];
 
-    // `k` elements of the sum; k_unit: what the operands' copy() counts `left` in (bytes of a row, or k-rows)
-    __device__ __forceinline__ void copy_stage(uint32_t lds, int stage, int k) {
-        const int left = k - stage * 32;
-        s.copy(lds, SKS ? left : 2 * left);
-        f.copy(lds + SOp::kBytes, FKS ? left : 2 * left);
-    }
-
+    // `k` terms of the sum
+    template <int MT>
     __device__ __forceinline__ void run(char* smem, int k) {
         const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-        const int stages = (k + 31) / 32;
+        const int stages = (k + 63) / 64;
         const uint32_t lds0 = lds_address(smem);
         // the bases come out of vector registers: five wait states before a memory instruction reads them
         asm volatile("s_nop 4" : "+s"(s.base), "+s"(f.base));
@@ -222,49 +213,51 @@ struct Bf16Tile {
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
         uint32_t s_at[SKS ? MT : 1], f_at[FKS ? NT : 1];
-        if constexpr (SKS) {
 #pragma unroll
-            for (int a = 0; a < MT; ++a) s_at[a] = SOp::fragment(wm * MT * 16 + a * 16);
-        } else {
-            s_at[0] = SOp::fragment(wm * MT * 16);
-        }
-        if constexpr (FKS) {
+        for (int a = 0; a < (SKS ? MT : 1); ++a) s_at[a] = SOp::fragment((wm * MT + a) * 16);
 #pragma unroll
-            for (int b = 0; b < NT; ++b) f_at[b] = SOp::kBytes + FOp::fragment(wn * 64 + b * 16);
-        } else {
-            f_at[0] = SOp::kBytes + FOp::fragment(wn * 64);
-        }
+        for (int b = 0; b < (FKS ? NT : 1); ++b) f_at[b] = FOp::fragment(wn * 64 + b * 16);
+        auto copy_s = [&](int st) { s.copy(lds0 + (st & 1) * SOp::kBytes, SKS ? k - st * 64 : (k - st * 64) / 8); };
+        auto copy_f = [&](int st, int buf) { f.copy(lds0 + kF + buf * FOp::kBytes, FKS ? k - st * 64 : (k - st * 64) / 8); };
 
-#pragma unroll
-        for (int i = 0; i < kBuffers - 1; ++i) copy_stage(lds0 + i * kStage, i, k);
-        wait_and_meet<(kBuffers - 2) * kCopies>();
+        copy_f(0, 0);
+        copy_s(0);
+        copy_f(1, 1);
+        wait_and_meet<FOp::kCopies>();
         if (wm == 1) meet();
-        int buf = 0;
+        int fbuf = 0;
         for (int st = 0; st < stages; ++st) {
-            const char* l = smem + buf * kStage;
-            bf16x8 sv[MT], fv[NT];
+            const char* ls = smem + (st & 1) * SOp::kBytes;
+            const char* lf = smem + kF + fbuf * FOp::kBytes;
 #pragma unroll
-            for (int b = 0; b < NT; ++b) {
-                if constexpr (FKS) fv[b] = read_ks<FOp::kRowBytes>(l, f_at[b]);
-                else fv[b] = read_kc(l, f_at[0] + b * 1024);
+            for (int half = 0; half < 2; ++half) {
+                // both targets were last read in stage st - 1, which every wave had left before the last barrier
+                if (half == 0) copy_s(st + 1);
+                else copy_f(st + 2, fbuf == 0 ? 2 : fbuf - 1);
+                bf16x8 sv[MT], fv[NT];
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    if constexpr (FKS) fv[b] = read_ks<FOp::kRowBytes>(lf, f_at[b] + half * 32 * FOp::kRowBytes);
+                    else fv[b] = read_kc(lf, (f_at[0] ^ (half * 64)) + b * 2048);
+                }
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    if constexpr (SKS) sv[a] = read_ks<SOp::kRowBytes>(ls, s_at[a] + half * 32 * SOp::kRowBytes);
+                    else sv[a] = read_kc(ls, (s_at[0] ^ (half * 64)) + a * 2048);
+                }
+                // before a wave goes on to stage st + 1 all but the newest copies, F's of st + 2, have landed
+                if (half == 0) wait_and_meet<63>();
+                else wait_and_meet<FOp::kCopies>();
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv[b], sv[a], acc[a][b], 0, 0, 0);
+                __builtin_amdgcn_s_setprio(0);
+                meet();
             }
-#pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                if constexpr (SKS) sv[a] = read_ks<SOp::kRowBytes>(l, s_at[a]);
-                else sv[a] = read_kc(l, s_at[0] + a * 1024);
-            }
-            const int nbuf = buf == 0 ? kBuffers - 1 : buf - 1;      // the buffer read in the step before
-            copy_stage(lds0 + nbuf * kStage, st + kBuffers - 1, k);
-            wait_and_meet<(kBuffers - 2) * kCopies>();
-            __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv[b], sv[a], acc[a][b], 0, 0, 0);
-            __builtin_amdgcn_s_setprio(0);
-            meet();
-            buf = buf == kBuffers - 1 ? 0 : buf + 1;
+            fbuf = fbuf == 2 ? 0 : fbuf + 1;
         }
         if (wm == 0) meet();
         wait_and_meet<0>();      // no copy may land after the workgroup has left its LDS
@@ -273,50 +266,19 @@ struct Bf16Tile {
 
 // ---- e4m3 operands ----------------------------------------------------------------------------------------------
 
-// ROWS rows of e4m3, 128 k (one scale group) per stage: a row is a 128-byte line, chunks permuted by the row number.
-template <int ROWS>
-struct Kc128Operand {
-    static constexpr int kCopies = ROWS / 8 / kGemmWaves;
-    static constexpr int kBytes = ROWS * 128;
-    uint64_t base;
-    uint32_t offset[kCopies];
-
-    template <class RowOffset>
-    __device__ __forceinline__ void init(const void* start, RowOffset row_offset) {
-        const int lane = lane_id();
-        base = uniform64((uint64_t)start);
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int row = (i * kGemmWaves + wave_id()) * 8 + (lane >> 3);
-            const uint32_t o = row_offset(row);
-            offset[i] = o == kNoElement ? kNoElement : o + (((lane & 7) ^ (row & 7)) << 4);
-        }
-    }
-    __device__ __forceinline__ void copy(uint32_t lds, bool more) {
-        const i32x4 res = resource(base, more ? kNoElement : 0u);
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) copy16_to_lds(lds + wave_id() * 1024 + i * kGemmWaves * 1024, offset[i], res);
-        base += 128;
-    }
-    // LDS offset of the first 16 of the lane's 32 bytes; the other 16 are at ^ 64; fragment j is at + j * 2048.  (Which k a
-    // lane holds does not matter as long as both operands agree.)
-    static __device__ __forceinline__ uint32_t fragment(int row0) {
-        const int r = lane_id() & 15, g = lane_id() >> 4;
-        return (row0 + r) * 128 + ((g ^ (r & 7)) << 4);
-    }
-    static __device__ __forceinline__ i32x8 read(const char* lds, uint32_t at) {
-        const i32x4 a = *reinterpret_cast<const i32x4*>(lds + at), b = *reinterpret_cast<const i32x4*>(lds + (at ^ 64));
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-};
+// 32 bytes of a lane: which k they are does not matter as long as both operands agree.
+__device__ __forceinline__ i32x8 read_line(const char* lds, uint32_t at) {
+    const i32x4 a = *reinterpret_cast<const i32x4*>(lds + at), b = *reinterpret_cast<const i32x4*>(lds + (at ^ 64));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 // 128 rows of e4m3 with a scale per row and 128 k, against 256 rows of e4m3 F with a scale per half of each wave's rows
 // and 128 k: 16x16x128 matrix instructions, whose sums over one 128-block are exact products in fp32, then one FMA with the
 // product of the two scales.
 struct Fp8Tile {
     static constexpr int MT = 4, NT = 4, kBM = 128;
-    typedef Kc128Operand<kBM> SOp;
-    typedef Kc128Operand<kBN> FOp;
+    typedef KcOperand<kBM> SOp;
+    typedef KcOperand<kBN> FOp;
     static constexpr int kStage = SOp::kBytes + FOp::kBytes, kBuffers = 3;
     static constexpr int kCopies = SOp::kCopies + FOp::kCopies + 1;
     static constexpr int kRowScales = kStage * kBuffers;                          // per wave and stage 64 fp32
@@ -330,8 +292,8 @@ struct Fp8Tile {
     f32x4 acc[MT][NT];
 
     __device__ __forceinline__ void copy_stage(uint32_t lds0, int buf, bool more) {
-        s.copy(lds0 + buf * kStage, more);
-        f.copy(lds0 + buf * kStage + SOp::kBytes, more);
+        s.copy(lds0 + buf * kStage, more ? 8 : 0);
+        f.copy(lds0 + buf * kStage + SOp::kBytes, more ? 8 : 0);
         copy4_to_lds(lds0 + kRowScales + (buf * kGemmWaves + wave_id()) * 256, scale_offset, resource(scales, more ? kNoElement : 0u));
         scales += 4;
     }
@@ -358,9 +320,9 @@ struct Fp8Tile {
             i32x8 sv[MT], fv[NT];
             float row_scale[MT];
 #pragma unroll
-            for (int b = 0; b < NT; ++b) fv[b] = FOp::read(l, f_at + b * 2048);
+            for (int b = 0; b < NT; ++b) fv[b] = read_line(l, f_at + b * 2048);
 #pragma unroll
-            for (int a = 0; a < MT; ++a) sv[a] = SOp::read(l, s_at + a * 2048);
+            for (int a = 0; a < MT; ++a) sv[a] = read_line(l, s_at + a * 2048);
 #pragma unroll
             for (int a = 0; a < MT; ++a)
                 row_scale[a] = *reinterpret_cast<const float*>(smem + kRowScales + (buf * kGemmWaves + wave) * 256 + (a * 16 + (lane_id() & 15)) * 4);
@@ -391,71 +353,87 @@ struct Fp8Tile {
 };
 
 // 128 rows of bf16 against 256 rows of e4m3 F with a scale per wave and 128 k: F is widened to bf16 (exact) on its way from
-// LDS, a block's sums get the scale in fp32.
+// LDS, a block's sums get the scale in fp32.  64 k per stage: 128 bytes of a row of S, 64 of F (two rows a line of LDS).
 struct Bf16ByFp8Tile {
     static constexpr int MT = 4, NT = 4, kBM = 128;
     typedef KcOperand<kBM> SOp;
-    static constexpr int kFBytes = kBN * 32;
+    static constexpr int kFBytes = kBN * 64, kFCopies = 2;
     static constexpr int kStage = SOp::kBytes + kFBytes, kBuffers = 4;
-    static constexpr int kCopies = SOp::kCopies + 1;
+    static constexpr int kCopies = SOp::kCopies + kFCopies;
     static constexpr int kFScales = kStage * kBuffers;     // two rows of up to 256 fp32: channels 0..127, 128..255
     static constexpr int kLds = kFScales + 2048;
 
     SOp s;
     uint64_t f;
-    uint32_t f_offset;
+    uint32_t f_offset[kFCopies];
     f32x4 acc[MT][NT];
 
+    // A copy is 16 rows of 64 bytes; a row's four chunks are permuted by the pair of rows it stands in.
     template <class RowOffset>
     __device__ __forceinline__ void init_f(const void* start, RowOffset row_offset) {
         f = uniform64((uint64_t)start);
-        const uint32_t o = row_offset(wave_id() * 32 + lane_id() / 2);
-        f_offset = o == kNoElement ? kNoElement : o + (lane_id() & 1) * 16;
+        const int x = (lane_id() & 7) ^ (lane_id() >> 3);
+#pragma unroll
+        for (int i = 0; i < kFCopies; ++i) {
+            const uint32_t o = row_offset((i * kGemmWaves + wave_id()) * 16 + (lane_id() >> 3) * 2 + (x >> 2));
+            f_offset[i] = o == kNoElement ? kNoElement : o + (x & 3) * 16;
+        }
     }
-    __device__ __forceinline__ void copy_stage(uint32_t lds, int left) {
-        s.copy(lds, 2 * left);
-        copy16_to_lds(lds + SOp::kBytes + wave_id() * 1024, f_offset, resource(f, left > 0 ? kNoElement : 0u));
-        f += 32;
+    __device__ __forceinline__ void copy_stage(uint32_t lds, bool more) {
+        s.copy(lds, more ? 8 : 0);
+        const i32x4 res = resource(f, more ? kNoElement : 0u);
+#pragma unroll
+        for (int i = 0; i < kFCopies; ++i)
+            copy16_to_lds(lds + SOp::kBytes + (i * kGemmWaves + wave_id()) * 1024, f_offset[i], res);
+        f += 64;
     }
 
     __device__ __forceinline__ void run(char* smem, int k) {
-        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, stages = k / 32;
+        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, stages = k / 64;
         const uint32_t lds0 = lds_address(smem);
         asm volatile("s_nop 4" : "+s"(s.base), "+s"(f));
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint32_t s_at = SOp::fragment(wm * 64);
-        const uint32_t f_at = SOp::kBytes + (wn * 64 + (lane_id() & 15)) * 32 + (lane_id() >> 4) * 8;
+        // a lane reads 16 e4m3: k 16g .. 16g + 15 of a row; its bf16 of S are the two chunks of the same k
+        const int r = lane_id() & 15, g = lane_id() >> 4;
+        const uint32_t s_at = (wm * 64 + r) * 128 + (((2 * g) ^ (r & 7)) << 4);
+        const uint32_t f_at = SOp::kBytes + (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | g) ^ (r >> 1)) << 4);
         const float* fs = reinterpret_cast<const float*>(smem + kFScales) + (wn >> 1) * 256;
 #pragma unroll
-        for (int i = 0; i < kBuffers - 1; ++i) copy_stage(lds0 + i * kStage, k - i * 32);
+        for (int i = 0; i < kBuffers - 1; ++i) copy_stage(lds0 + i * kStage, i < stages);
         wait_and_meet<(kBuffers - 2) * kCopies>();
         if (wm == 1) meet();
-        for (int st = 0; st < stages; st += 4) {
+        int buf = 0;
+        for (int st = 0; st < stages; st += 2) {
             f32x4 part[MT][NT];
-            const float scale = fs[st / 4];
+            const float scale = fs[st / 2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {     // kBuffers = 4: the buffer is q
-                const char* l = smem + q * kStage;
-                bf16x8 sv[MT];
-                i32x2 fq[NT];
+            for (int q = 0; q < 2; ++q) {
+                const char* l = smem + buf * kStage;
+                bf16x8 sv[MT][2];
+                i32x4 fq[NT];
+                copy_stage(lds0 + (buf == 0 ? kBuffers - 1 : buf - 1) * kStage, st + q + kBuffers - 1 < stages);
 #pragma unroll
-                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x2*>(l + f_at + b * 512);
+                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x4*>(l + f_at + b * 1024);
 #pragma unroll
-                for (int a = 0; a < MT; ++a) sv[a] = read_kc(l, s_at + a * 1024);
-                copy_stage(lds0 + (q + 3) % 4 * kStage, k - (st + q + 3) * 32);
+                for (int a = 0; a < MT; ++a) {
+                    sv[a][0] = read_kc(l, s_at + a * 2048);
+                    sv[a][1] = read_kc(l, (s_at ^ 16) + a * 2048);
+                }
                 wait_and_meet<(kBuffers - 2) * kCopies>();
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    const bf16x8 fv = widen_e4m3x8(fq[b]);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int a = 0; a < MT; ++a)
-                        part[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a], q == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[a][b], 0, 0, 0);
-                }
-                if (q == 3) {
+                    for (int b = 0; b < NT; ++b) {
+                        const bf16x8 fv = widen_e4m3x8(h ? i32x2{fq[b][2], fq[b][3]} : i32x2{fq[b][0], fq[b][1]});
+#pragma unroll
+                        for (int a = 0; a < MT; ++a)
+                            part[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a][h], q + h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[a][b], 0, 0, 0);
+                    }
+                if (q == 1) {
 #pragma unroll
                     for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -465,6 +443,7 @@ struct Bf16ByFp8Tile {
                 }
                 __builtin_amdgcn_s_setprio(0);
                 meet();
+                buf = buf == kBuffers - 1 ? 0 : buf + 1;
             }
         }
         if (wm == 0) meet();

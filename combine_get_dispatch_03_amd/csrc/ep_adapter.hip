@@ -40,11 +40,11 @@ struct Params {
 };
 
 // Tokens of a tile, in the layout's order, to LDS.  Ends with a barrier.
-__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int row0, int* tok) {
+__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int* tok) {
     const int quads = p.T / 4;
     const i32x4* q = reinterpret_cast<const i32x4*>(p.slot);
     auto put = [&](int s, int token) {
-        const uint32_t m = (uint32_t)(s - row0);
+        const uint32_t m = (uint32_t)(s - t.row0);
         if (m < (uint32_t)t.rows) tok[m] = token;
     };
     for (int i = threadIdx.x; i < quads; i += kThreads) {
@@ -127,11 +127,11 @@ template <int NF>
 __global__ __launch_bounds__(kThreads) void k_shrink(Params p) {
     __shared__ __align__(16) float sums[kWaves * 16 * (NF * 16 + 4)];
     __shared__ int tok[kRows];
-    const RowTiles<kRows> tiles(p.cnt, p.El);
+    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     const int tile = blockIdx.x / p.chunks;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
-    find_tokens(p, t, __builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0, tok);
+    find_tokens(p, t, tok);
     const int chunk = blockIdx.x % p.chunks;
     if (t.rows <= 16) shrink<NF, 1>(p, t, chunk, tok, sums);
     else if (t.rows <= 32) shrink<NF, 2>(p, t, chunk, tok, sums);
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles) {
     constexpr int kPitch = NK * 32 + 8;
     __shared__ __align__(16) uint16_t v[kRows * kPitch];
     __shared__ int tok[kRows];
-    const RowTiles<kRows> tiles(p.cnt, p.El);
+    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     const int cols = (p.N + kOut - 1) / kOut, tile = blockIdx.x / cols, n0 = blockIdx.x % cols * kOut;
     if (tile >= max_tiles) {      // tokens without an adapter: base as it is
         const int t0 = (tile - max_tiles) * kRows;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles) {
                 fv[b][j] = *(const i32x4*)(p.b + ((int64_t)t.expert * p.N + n) * p.r + j * 32 + g * 8);
         }
     }
-    find_tokens(p, t, __builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0, tok);
+    find_tokens(p, t, tok);
     const float scale = p.scales ? p.scales[t.expert] : 1.0f;
     for (int i = threadIdx.x; i < kRows * NK * 8; i += kThreads) {
         const int m = i / (NK * 8), k4 = i % (NK * 8) * 4;

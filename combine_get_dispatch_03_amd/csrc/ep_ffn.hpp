@@ -16,23 +16,31 @@ hipError_t launch_ffn_tile(const Handle& h, const FfnArgs& a, hipStream_t stream
 hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream);   // e4m3
 hipError_t launch_ffn_stream(const Handle& h, const FfnArgs& a, hipStream_t stream);     // either, few rows per expert
 
-// Workgroups of one XCD (every eighth) take consecutive tiles, and a run of consecutive tiles is kGroup row tiles by
-// as many channel tiles as fit, so that what an XCD's 32 CUs read at a time is few rows and few weights, from its own L2.
-constexpr int kXcds = 8, kGroup = 4;
+// The order in which workgroups take the tiles of a rows x cols grid.  Consecutive tiles run down kGroup rows, then on to
+// the next column; 32 of them (4 x 8) are what the 32 CUs of an XCD work on at a time, few rows and few weights from its
+// own L2.  Such batches go to the XCDs (workgroup number mod 8) in turn, so that experts with many rows are spread.  With
+// fewer tiles than CUs the batches shrink, to keep every XCD at work.
+constexpr int kXcds = 8, kGroup = 4, kBatch = 32;
 
 struct TileAt {
     int row, col;
 };
-__device__ __forceinline__ bool tile_at(int block, int rows, int cols, TileAt* t) {
-    const int total = rows * cols, share = (total + kXcds - 1) / kXcds;
-    const int at = block / kXcds, i = block % kXcds * share + at;
-    if (at >= share || i >= total) return false;
+// Tile number `round` of workgroup `block` of kXcds * kBatch; false: there is none, nor in later rounds.
+__device__ __forceinline__ bool tile_at(int block, int round, int rows, int cols, TileAt* t) {
+    const int total = rows * cols, batch = total >= kXcds * kBatch ? kBatch : (total + kXcds - 1) / kXcds;
+    const int in_batch = block / kXcds;
+    const int i = (round * kXcds + block % kXcds) * batch + in_batch;
+    if (in_batch >= batch || i >= total) return false;
     const int group = i / (kGroup * cols), first = group * kGroup;
     const int height = rows - first < kGroup ? rows - first : kGroup, in = i - group * kGroup * cols;
     t->row = first + in % height;
     t->col = in / height;
     return true;
 }
+// Workgroups to launch for at most `tiles` tiles when each walks through its rounds, and when each takes one tile (round
+// block / (kXcds * kBatch)).
+inline unsigned walking_blocks(int64_t tiles) { return (unsigned)(tiles < kXcds * kBatch ? (tiles + kXcds - 1) / kXcds * kXcds : kXcds * kBatch); }
+inline unsigned single_blocks(int64_t tiles) { return (unsigned)((tiles + kXcds * kBatch - 1) / (kXcds * kBatch) * (kXcds * kBatch)); }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
@@ -40,8 +48,5 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
-
-// Workgroups for `tiles` tiles, as tile_at() deals them out.
-inline unsigned tile_blocks(int64_t tiles) { return (unsigned)((tiles + kXcds - 1) / kXcds * kXcds); }
 
 }  // namespace ep

@@ -44,7 +44,8 @@ template <>
 struct RowsOf<kFp8, false> { static constexpr int kPieces = 4; };   // 128 k of bf16 beside e4m3 weights
 
 template <Format F, bool UP, int MT>
-__device__ __forceinline__ void product(const Params& p, const RowTile& t, int64_t row0, int n0, char* smem) {
+__device__ __forceinline__ void product(const Params& p, const RowTile& t, int n0, char* smem) {
+    const int64_t row0 = t.row0;
     constexpr int kPieces = RowsOf<F, UP>::kPieces;
     constexpr int kWide = F == kFp8 ? 1 : 2;                   // bytes of a weight
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
@@ -201,18 +202,17 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int64
 template <Format F, bool UP>
 __global__ __launch_bounds__(kThreads) void k_stream(Params p) {
     __shared__ __align__(16) char smem[kWaves * 16 * kSumPitch * 4];
-    const RowTiles<kRows> tiles(p.cnt, p.El);
+    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     constexpr int kChannels = UP ? kCols / 2 : kCols;
     const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int n0 = blockIdx.x % cols * kChannels;
-    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
     switch ((t.rows + 15) / 16) {
-        case 1: product<F, UP, 1>(p, t, row0, n0, smem); break;
-        case 2: product<F, UP, 2>(p, t, row0, n0, smem); break;
-        case 3: product<F, UP, 3>(p, t, row0, n0, smem); break;
-        default: product<F, UP, 4>(p, t, row0, n0, smem); break;
+        case 1: product<F, UP, 1>(p, t, n0, smem); break;
+        case 2: product<F, UP, 2>(p, t, n0, smem); break;
+        case 3: product<F, UP, 3>(p, t, n0, smem); break;
+        default: product<F, UP, 4>(p, t, n0, smem); break;
     }
 }
 

@@ -30,11 +30,11 @@ __device__ __forceinline__ void stage_scales(char* smem, int at, const float* a,
 
 __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    const RowTiles<Fp8Tile::kBM> tiles(p.cnt, p.El);
+    const RowTiles<Fp8Tile::kBM> tiles(p.cnt, p.psum, p.El);
     TileAt at;
-    if (!tile_at((int)blockIdx.x, tiles.total, p.I / 128, &at)) return;
+    if (!tile_at((int)blockIdx.x % (kXcds * kBatch), (int)blockIdx.x / (kXcds * kBatch), tiles.total, p.I / 128, &at)) return;
     const RowTile t = tiles.find(at.row);
-    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    const int64_t row0 = t.row0;
     const int n0 = at.col * 128, blocks = p.H / 128, wave = wave_id();
 
     Fp8Tile g;
@@ -68,11 +68,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
 
 __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    const RowTiles<Bf16ByFp8Tile::kBM> tiles(p.cnt, p.El);
+    const RowTiles<Bf16ByFp8Tile::kBM> tiles(p.cnt, p.psum, p.El);
     TileAt at;
-    if (!tile_at((int)blockIdx.x, tiles.total, (p.H + kBN - 1) / kBN, &at)) return;
+    if (!tile_at((int)blockIdx.x % (kXcds * kBatch), (int)blockIdx.x / (kXcds * kBatch), tiles.total, (p.H + kBN - 1) / kBN, &at)) return;
     const RowTile t = tiles.find(at.row);
-    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(p.psum[t.expert]) + t.m0;
+    const int64_t row0 = t.row0;
     const int n0 = at.col * kBN, blocks = p.I / 128, wave = wave_id();
 
     Bf16ByFp8Tile g;
@@ -105,11 +105,11 @@ hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t st
     if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tile::kLds);
     if (e != hipSuccess) return e;
     const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_gate_up, dim3(tile_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tile::kLds, stream, up);
+    hipLaunchKernelGGL(k_gate_up, dim3(single_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tile::kLds, stream, up);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_down, dim3(tile_blocks(rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tile::kLds, stream, down);
+    hipLaunchKernelGGL(k_down, dim3(single_blocks(rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tile::kLds, stream, down);
     return hipGetLastError();
 }
 

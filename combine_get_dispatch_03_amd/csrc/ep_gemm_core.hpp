@@ -54,15 +54,13 @@ __device__ __forceinline__ i32x4 resource(uint64_t base, uint32_t bytes) {
     return r;
 }
 
-// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16.  Counted by vmcnt; the compiler does not see
+// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16 (m0 holds nothing else on this target).  Counted by vmcnt; the compiler does not see
 // it, so whoever reads the LDS waits for it (wait_stage).
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res)
-                 : "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
 }
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res)
-                 : "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
 }
 
 // All LDS reads of this wave are back, and of its copies to LDS all but the newest `LEFT`; then the workgroup meets.
@@ -86,6 +84,12 @@ struct KcOperand {
     static constexpr int kBytes = ROWS * 128;
     uint64_t base;
     uint32_t offset[kCopies];
+
+    // The base comes out of vector registers: five wait states before a memory instruction reads it.  Back into scalar registers, wherever the compiler kept it between begin() and the loop.
+    __device__ __forceinline__ void settle() {
+        base = uniform64(base);
+        asm volatile("s_nop 4" : "+s"(base));
+    }
 
     static __device__ __forceinline__ int chunk() { return (lane_id() & 7) ^ (lane_id() >> 3); }   // the lane's, of 8
 
@@ -125,6 +129,12 @@ struct KsOperand {
     uint64_t base;
     uint64_t step;     // bytes of 64 k-rows
     uint32_t offset[kCopies];
+
+    __device__ __forceinline__ void settle() {
+        base = uniform64(base);
+        step = uniform64(step);
+        asm volatile("s_nop 4" : "+s"(base), "+s"(step));
+    }
 
     static __device__ __forceinline__ int permute(int k) { return ((k & 3) | ((k >> 3) & 1) << 2) << 1; }
     static __device__ __forceinline__ int row(int i) { return (i * kGemmWaves + wave_id()) * (kWave / kChunks) + lane_id() / kChunks; }
@@ -197,16 +207,33 @@ struct Bf16Tile {
 
     SOp s;
     FOp f;
-    f32x4 acc[8][NT];
 
-    // `k` terms of the sum
+    __device__ __forceinline__ void copy_s(uint32_t lds0, int st, int k) {
+        s.copy(lds0 + (st & 1) * SOp::kBytes, SKS ? k - st * 64 : (k - st * 64) / 8);
+    }
+    __device__ __forceinline__ void copy_f(uint32_t lds0, int buf, int st, int k) {
+        f.copy(lds0 + kF + buf * FOp::kBytes, FKS ? k - st * 64 : (k - st * 64) / 8);
+    }
+
+    // The first copies of a tile whose sums have `k` terms, once s and f are set and the tile before is done with LDS.
+    __device__ __forceinline__ void begin(char* smem, int k) {
+        const uint32_t lds0 = lds_address(smem);
+        s.settle();
+        f.settle();
+        copy_f(lds0, 0, 0, k);
+        copy_s(lds0, 0, k);
+        copy_f(lds0, 1, 1, k);
+    }
+
+    // After begin(), the sums.  Global loads and stores may stand between the two (the tile before is stored there): the
+    // waits below count copies only, and copies land in order.
     template <int MT>
-    __device__ __forceinline__ void run(char* smem, int k) {
+    __device__ __forceinline__ void run(char* smem, int k, f32x4 (&acc)[MT][NT]) {
         const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
         const int stages = (k + 63) / 64;
         const uint32_t lds0 = lds_address(smem);
-        // the bases come out of vector registers: five wait states before a memory instruction reads them
-        asm volatile("s_nop 4" : "+s"(s.base), "+s"(f.base));
+        s.settle();
+        f.settle();
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -217,12 +244,6 @@ struct Bf16Tile {
         for (int a = 0; a < (SKS ? MT : 1); ++a) s_at[a] = SOp::fragment((wm * MT + a) * 16);
 #pragma unroll
         for (int b = 0; b < (FKS ? NT : 1); ++b) f_at[b] = FOp::fragment(wn * 64 + b * 16);
-        auto copy_s = [&](int st) { s.copy(lds0 + (st & 1) * SOp::kBytes, SKS ? k - st * 64 : (k - st * 64) / 8); };
-        auto copy_f = [&](int st, int buf) { f.copy(lds0 + kF + buf * FOp::kBytes, FKS ? k - st * 64 : (k - st * 64) / 8); };
-
-        copy_f(0, 0);
-        copy_s(0);
-        copy_f(1, 1);
         wait_and_meet<FOp::kCopies>();
         if (wm == 1) meet();
         int fbuf = 0;
@@ -232,8 +253,8 @@ struct Bf16Tile {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 // both targets were last read in stage st - 1, which every wave had left before the last barrier
-                if (half == 0) copy_s(st + 1);
-                else copy_f(st + 2, fbuf == 0 ? 2 : fbuf - 1);
+                if (half == 0) copy_s(lds0, st + 1, k);
+                else copy_f(lds0, fbuf == 0 ? 2 : fbuf - 1, st + 2, k);
                 bf16x8 sv[MT], fv[NT];
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {

@@ -14,14 +14,14 @@ struct RowTile {
 // The tiles of all experts, in the experts' order: ceil(count / BM) each, as even in height as multiples of `unit` rows
 // allow (1050 rows are five tiles of 224 and 154 rather than four of 256 and one of 26).  Every wave of a workgroup works
 // them out for itself (no LDS, no barrier): lane l takes experts [l * per, l * per + per), a wave scan places their tiles,
-// and up to 256 experts' counts and starts stay in registers for find().
-template <int BM>
+// and of the first KEPT experts of each lane (4: of up to 256) counts and starts stay in registers for find().
+template <int BM, int KEPT = 4>
 struct RowTiles {
-    static constexpr int kKept = 4;      // experts per lane in registers
+    static constexpr int kKept = KEPT;
     const int32_t* cnt;
     const int32_t* psum;
     int per, sum, incl, total;
-    int count[kKept], start[kKept];
+    int count[kKept > 0 ? kKept : 1], start[kKept > 0 ? kKept : 1];
 
     __device__ __forceinline__ RowTiles(const int32_t* counts, const int32_t* starts, int El) : cnt(counts), psum(starts) {
         per = (El + kWave - 1) / kWave;
@@ -60,6 +60,28 @@ struct RowTiles {
             if (left < n) return split(e, __builtin_amdgcn_readfirstlane(psum[e]), c, n, left, unit);
             left -= n;
         }
+    }
+};
+
+// Counts and starts of up to 256 experts in a wave's registers, of more in memory.
+struct ExpertRows {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int count[4], start[4];
+
+    __device__ __forceinline__ ExpertRows(const int32_t* counts, const int32_t* starts, int El) : cnt(counts), psum(starts) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = i * kWave + lane_id();
+            count[i] = e < El ? cnt[e] : 0;
+            start[i] = e < El ? psum[e] : 0;
+        }
+    }
+    __device__ __forceinline__ RowTile get(int e) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e < (i + 1) * kWave) return RowTile{e, readlane(start[i], e & 63), readlane(count[i], e & 63)};
+        return RowTile{e, __builtin_amdgcn_readfirstlane(psum[e]), __builtin_amdgcn_readfirstlane(cnt[e])};
     }
 };
 

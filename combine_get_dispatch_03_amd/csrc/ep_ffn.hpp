@@ -46,6 +46,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
     *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(a, b), pack_bf16x2(c, d)};
 }
+template <class V4>
+__device__ __forceinline__ void store8(uint16_t* p, V4 a, V4 b) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+}
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 

@@ -20,57 +20,62 @@ struct Params {
     int H, I;
 };
 
-// Where a finished tile goes.
+// Where a tile's sums go.
 struct Target {
     int64_t row0;
     int rows, n0;
 };
 
+// A lane holds 8 consecutive channels of a row in acc[a][0], acc[a][1] and, 32 channels on (kGateUp: the up projection's), 8 in
+// acc[a][2], acc[a][3].
 template <Product P, int MT>
 __device__ __forceinline__ void store_rows(const Params& p, const f32x4 (&acc)[MT][4], const Target& t, int N) {
-    const int wave = wave_id(), m_at = (wave >> 2) * MT * 16 + (lane_id() & 15), n_in = (lane_id() >> 4) * 4;
+    const int wave = wave_id(), m_at = (wave >> 2) * MT * 16 + (lane_id() & 15), n_in = (lane_id() >> 4) * 8;
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
         const int m = m_at + a * 16;
         if (m >= t.rows) continue;
         const int64_t row = t.row0 + m;
         if constexpr (P == kGateUp) {
+            const int n = t.n0 + (wave & 3) * 32 + n_in;
+            if (n >= N) continue;
+            f32x4 h[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int n = t.n0 + (wave & 3) * 32 + b * 16 + n_in;
-                if (n >= N) continue;
                 const f32x4 gate = acc[a][b], up = acc[a][b + 2];
                 if (p.pre) {
-                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + n) = gate;
-                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + p.I + n) = up;
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + n + b * 4) = gate;
+                    *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.I + p.I + n + b * 4) = up;
                 }
-                f32x4 h;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = gate[i] * sigmoid(gate[i]) * up[i];
-                store4(p.out + row * p.I + n, h[0], h[1], h[2], h[3]);
+                for (int i = 0; i < 4; ++i) h[b][i] = gate[i] * sigmoid(gate[i]) * up[i];
             }
+            store8(p.out + row * p.I + n, h[0], h[1]);
         } else {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int n = t.n0 + (wave & 3) * 64 + b * 16 + n_in;
+            for (int j = 0; j < 2; ++j) {
+                const int n = t.n0 + (wave & 3) * 64 + j * 32 + n_in;
                 if (n >= N) continue;
-                const f32x4 v = acc[a][b];
                 if constexpr (P == kDownGrad) {
-                    const f32x4 gate = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + n);
-                    const f32x4 up = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + p.I + n);
-                    f32x4 dg, du, h;
+                    f32x4 dg[2], du[2], h[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float sg = sigmoid(gate[i]), act = gate[i] * sg;
-                        dg[i] = v[i] * up[i] * sg * (1.0f + gate[i] * (1.0f - sg));
-                        du[i] = v[i] * act;
-                        h[i] = act * up[i];
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x4 v = acc[a][j * 2 + b];
+                        const f32x4 gate = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + n + b * 4);
+                        const f32x4 up = *reinterpret_cast<const f32x4*>(p.pre + row * 2 * p.I + p.I + n + b * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float sg = sigmoid(gate[i]), act = gate[i] * sg;
+                            dg[b][i] = v[i] * up[i] * sg * (1.0f + gate[i] * (1.0f - sg));
+                            du[b][i] = v[i] * act;
+                            h[b][i] = act * up[i];
+                        }
                     }
-                    store4(p.out + row * 2 * p.I + n, dg[0], dg[1], dg[2], dg[3]);
-                    store4(p.out + row * 2 * p.I + p.I + n, du[0], du[1], du[2], du[3]);
-                    store4(p.out2 + row * p.I + n, h[0], h[1], h[2], h[3]);
+                    store8(p.out + row * 2 * p.I + n, dg[0], dg[1]);
+                    store8(p.out + row * 2 * p.I + p.I + n, du[0], du[1]);
+                    store8(p.out2 + row * p.I + n, h[0], h[1]);
                 } else {
-                    store4(p.out + row * N + n, v[0], v[1], v[2], v[3]);
+                    store8(p.out + row * N + n, acc[a][j * 2], acc[a][j * 2 + 1]);
                 }
             }
         }
@@ -79,127 +84,135 @@ __device__ __forceinline__ void store_rows(const Params& p, const f32x4 (&acc)[M
 
 template <Product P>
 struct RowsKernel {
-    typedef Bf16Tile<false, P == kDownGrad || P == kInGrad> Tile;
+    typedef Bf16Tiles<false, P == kDownGrad || P == kInGrad> Tiles;
     static constexpr int kCols = P == kGateUp ? kBN / 2 : kBN;     // channels of N per tile
 
     const Params& p;
-    char* smem;
-    RowTiles<Tile::kBM> tiles;
+    RowTiles<Tiles::kBM, 0> rows;      // the registers are needed: find() reads the counts again
     int N, K;
-    Tile g;
+    Tiles g;
     int round = 0;
+    Target now, next;
 
-    __device__ __forceinline__ RowsKernel(const Params& params, char* lds)
-        : p(params), smem(lds), tiles(params.cnt, params.psum, params.El) {
+    __device__ __forceinline__ explicit RowsKernel(const Params& params)
+        : p(params), rows(params.cnt, params.psum, params.El) {
         N = P == kGateUp || P == kDownGrad ? p.I : p.H;
         K = P == kGateUp || P == kDownGrad ? p.H : P == kDown ? p.I : 2 * p.I;
     }
 
-    // The workgroup's next tile: its first copies are issued.
-    __device__ __forceinline__ bool begin(Target* next) {
+    // The workgroup's next tile: where it goes and its operands.  next.rows = 0: there is none.
+    __device__ __forceinline__ void look_ahead() {
         TileAt at;
-        if (!tile_at((int)blockIdx.x, round++, tiles.total, (N + kCols - 1) / kCols, &at)) return false;
-        const RowTile t = tiles.find(at.row, 32);
+        next.rows = g.next_k = 0;
+        if (!tile_at((int)blockIdx.x, round++, rows.total, (N + kCols - 1) / kCols, &at)) return;
+        const RowTile t = rows.find(at.row, 32);
         const int n0 = at.col * kCols;
-        *next = Target{t.row0, t.rows, n0};
-        g.s.init(p.s + (int64_t)t.row0 * K, [&](int r) { return r < t.rows ? r * (2u * K) : kNoElement; });
+        next = Target{t.row0, t.rows, n0};
+        g.next_k = K;
+        g.next_s.init(p.s + (int64_t)t.row0 * K, [&](int r) { return r < t.rows ? r * (2u * K) : kNoElement; });
         if constexpr (P == kGateUp) {
-            // a wave's 64 rows of F: 32 gate channels, then the same 32 up channels
+            // a wave's 64 rows of F: 32 gate channels (fragments 0, 1), then the same 32 up channels
             const uint64_t up = (uint64_t)p.I * p.H * 2;
-            g.f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H, [&](int r) {
-                const int c = r / 64 * 32 + r % 32;
-                return n0 + c < N ? (uint32_t)((r % 64 >= 32 ? up : 0) + (uint64_t)c * p.H * 2) : kNoElement;
+            g.next_f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H, [&](int r) {
+                const int c = r / 64 * 32 + channel_of(r / 16 & 1, r & 15);
+                return n0 + c < N ? (uint32_t)((r & 32 ? up : 0) + (uint64_t)c * p.H * 2) : kNoElement;
             });
         } else if constexpr (P == kDown) {
-            g.f.init(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) { return n0 + r < N ? (uint32_t)r * p.I * 2 : kNoElement; });
+            g.next_f.init(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) {
+                const int c = r / 64 * 64 + channel_of(r / 16 & 3, r & 15);
+                return n0 + c < N ? (uint32_t)c * p.I * 2 : kNoElement;
+            });
         } else if constexpr (P == kDownGrad) {
-            g.f.init(p.f + (int64_t)t.expert * p.H * p.I + n0, (int64_t)p.I * 2, N - n0);
+            g.next_f.init(p.f + (int64_t)t.expert * p.H * p.I + n0, (int64_t)p.I * 2, N - n0);
         } else {
-            g.f.init(p.f + (int64_t)t.expert * 2 * p.I * p.H + n0, (int64_t)p.H * 2, N - n0);
+            g.next_f.init(p.f + (int64_t)t.expert * 2 * p.I * p.H + n0, (int64_t)p.H * 2, N - n0);
         }
-        g.begin(smem, K);
-        return true;
     }
 
     template <int MT>
-    __device__ __forceinline__ bool tile(Target* t) {
+    __device__ __forceinline__ void tile() {
         f32x4 acc[MT][4];
-        g.template run<MT>(smem, K, acc);
-        const Target done = *t;
-        const bool more = begin(t);
-        store_rows<P, MT>(p, acc, done, N);
-        return more;
+        g.template run<MT>(acc);
+        store_rows<P, MT>(p, acc, now, N);
     }
 };
 
-// A workgroup stays on its CU and walks through its tiles: a tile's first copies are under way while the tile before is
-// stored.  Waves take as many 16-row steps as the tile is high.
+// A workgroup stays on its CU and walks through its tiles.  Waves take as many 16-row steps as the tile is high.
 template <Product P>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_rows(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    RowsKernel<P> k(p, smem);
-    Target t;
-    bool more = k.begin(&t);
-    while (more) {
-        switch ((t.rows + 31) / 32) {
-            case 1: more = k.template tile<1>(&t); break;
-            case 2: more = k.template tile<2>(&t); break;
-            case 3: more = k.template tile<3>(&t); break;
-            case 4: more = k.template tile<4>(&t); break;
-            case 5: more = k.template tile<5>(&t); break;
-            case 6: more = k.template tile<6>(&t); break;
-            case 7: more = k.template tile<7>(&t); break;
-            default: more = k.template tile<8>(&t); break;
+    RowsKernel<P> k(p);
+    k.look_ahead();
+    if (k.next.rows == 0) return;
+    k.g.s = k.g.next_s, k.g.f = k.g.next_f;
+    k.g.begin(smem, k.K);
+    do {
+        k.now = k.next;
+        k.look_ahead();
+        switch ((k.now.rows + 31) / 32) {
+            case 1: k.template tile<1>(); break;
+            case 2: k.template tile<2>(); break;
+            case 3: k.template tile<3>(); break;
+            case 4: k.template tile<4>(); break;
+            case 5: k.template tile<5>(); break;
+            case 6: k.template tile<6>(); break;
+            case 7: k.template tile<7>(); break;
+            default: k.template tile<8>(); break;
         }
-    }
+    } while (k.next.rows > 0);
+    k.g.end();
 }
 
 // out[e] [M, N] = sum over the expert's rows of s[row, m] f[row, n]
 __global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt, const int32_t* psum, int El, const uint16_t* s,
                                                              const uint16_t* f, uint16_t* out, int M, int N) {
-    typedef Bf16Tile<true, true> Tile;
+    typedef Bf16Tiles<true, true> Tiles;
     extern __shared__ __align__(1024) char smem[];
-    const int mt = (M + Tile::kBM - 1) / Tile::kBM, nt = (N + kBN - 1) / kBN;
-    Tile g;
-    f32x4 acc[8][4];
-    int64_t last_out = 0;
-    int last_m = 0, last_n = 0;
-    for (int round = 0;; ++round) {
+    const ExpertRows experts(cnt, psum, El);
+    const int mt = (M + Tiles::kBM - 1) / Tiles::kBM, nt = (N + kBN - 1) / kBN;
+    Tiles g;
+    struct Out {
+        int64_t at;
+        int m0, n0, k;
+    } next, now;
+    int round = 0;
+    bool more;
+    auto look_ahead = [&]() {
         TileAt at;
-        const bool more = tile_at((int)blockIdx.x, round, El * mt, nt, &at);
-        int rows = 0, m0 = 0, n0 = 0;
-        int64_t to = 0;
-        if (more) {
-            const int e = at.row / mt;
-            m0 = at.row % mt * Tile::kBM, n0 = at.col * kBN;
-            rows = __builtin_amdgcn_readfirstlane(cnt[e]);
-            const int64_t row0 = __builtin_amdgcn_readfirstlane(psum[e]);
-            to = (int64_t)e * M * N;
-            g.s.init(s + row0 * M + m0, (int64_t)M * 2, M - m0);
-            g.f.init(f + row0 * N + n0, (int64_t)N * 2, N - n0);
-            g.begin(smem, rows);
-        }
-        if (round > 0) {
-            const int wave = wave_id(), m_at = last_m + (wave >> 2) * 128 + (lane_id() & 15);
-            const int n_at = last_n + (wave & 3) * 64 + (lane_id() >> 4) * 4;
+        g.next_k = 0;
+        more = tile_at((int)blockIdx.x, round++, El * mt, nt, &at);
+        if (!more) return;
+        const RowTile e = experts.get(at.row / mt);
+        next = Out{(int64_t)e.expert * M * N, at.row % mt * Tiles::kBM, at.col * kBN, e.rows};
+        g.next_k = e.rows;
+        g.next_s.init(s + (int64_t)e.row0 * M + next.m0, (int64_t)M * 2, M - next.m0);
+        g.next_f.init(f + (int64_t)e.row0 * N + next.n0, (int64_t)N * 2, N - next.n0);
+    };
+    look_ahead();
+    if (!more) return;
+    g.s = g.next_s, g.f = g.next_f;
+    g.begin(smem, next.k);
+    do {
+        now = next;
+        look_ahead();
+        f32x4 acc[8][4];
+        g.run<8>(acc);
+        const int wave = wave_id(), m_at = now.m0 + (wave >> 2) * 128 + (lane_id() & 15);
+        const int n_at = now.n0 + (wave & 3) * 64 + (lane_id() >> 4) * 8;
 #pragma unroll
-            for (int a = 0; a < 8; ++a)
+        for (int a = 0; a < 8; ++a)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int m = m_at + a * 16, n = n_at + b * 16;
-                    const f32x4 v = acc[a][b];
-                    if (m < M && n < N) store4(out + last_out + (int64_t)m * N + n, v[0], v[1], v[2], v[3]);
-                }
-        }
-        if (!more) break;
-        g.run<8>(smem, rows, acc);
-        last_out = to, last_m = m0, last_n = n0;
-    }
+            for (int j = 0; j < 2; ++j) {
+                const int m = m_at + a * 16, n = n_at + j * 32;
+                if (m < M && n < N) store8(out + now.at + (int64_t)m * N + n, acc[a][j * 2], acc[a][j * 2 + 1]);
+            }
+    } while (more);
+    g.end();
 }
 
 template <Product P>
 hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
-    typedef Bf16Tile<false, P == kDownGrad || P == kInGrad> Tile;
+    typedef Bf16Tiles<false, P == kDownGrad || P == kInGrad> Tile;
     const int N = P == kGateUp || P == kDownGrad ? p.I : p.H, cols = P == kGateUp ? kBN / 2 : kBN;
     // row tiles that any routing can give: every expert may end in a short one
     const int64_t rows = (int64_t)h.T * h.K / Tile::kBM + h.El;
@@ -210,7 +223,7 @@ hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
 }
 
 hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f, uint16_t* out, int M, int N, hipStream_t stream) {
-    typedef Bf16Tile<true, true> Tile;
+    typedef Bf16Tiles<true, true> Tile;
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_weights), Tile::kLds);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t)h.El * ((M + Tile::kBM - 1) / Tile::kBM) * ((N + kBN - 1) / kBN);

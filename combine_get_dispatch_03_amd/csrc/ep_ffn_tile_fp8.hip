@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     // a wave's 64 rows of F: 32 gate channels, then the same 32 up channels
     const uint32_t up = (uint32_t)p.I * p.H;
     g.f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H,
-             [&](int r) { return (r % 64 >= 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + r % 32) * p.H); });
+             [&](int r) { return (r & 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + channel_of(r / 16 & 1, r & 15)) * p.H); });
     const int r = (wave >> 2) * 64 + lane_id();
     g.scales = uniform64((uint64_t)(p.s_scales + row0 * blocks));
     g.scale_offset = r < t.rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
@@ -50,19 +50,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     stage_scales(smem, Fp8Tile::kFScales, fs, fs + (int64_t)p.I / 128 * blocks, blocks);
     g.run(smem, blocks);
 
-    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 32 + (lane_id() >> 4) * 4;
+    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 32 + (lane_id() >> 4) * 8;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
         const int m = m_at + a * 16;
         if (m >= t.rows) continue;
+        f32x4 h[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const f32x4 gate = g.acc[a][b], u = g.acc[a][b + 2];
-            f32x4 h;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = gate[i] * sigmoid(gate[i]) * u[i];
-            store4(p.out + (row0 + m) * p.I + n_at + b * 16, h[0], h[1], h[2], h[3]);
-        }
+            for (int i = 0; i < 4; ++i) h[b][i] = g.acc[a][b][i] * sigmoid(g.acc[a][b][i]) * g.acc[a][b + 2][i];
+        store8(p.out + (row0 + m) * p.I + n_at, h[0], h[1]);
     }
 }
 
@@ -77,23 +75,23 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
 
     Bf16ByFp8Tile g;
     g.s.init((const uint16_t*)p.s + row0 * p.I, [&](int r) { return r < t.rows ? (uint32_t)r * p.I * 2 : kNoElement; });
-    g.init_f(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) { return n0 + r < p.H ? (uint32_t)(r * p.I) : kNoElement; });
+    g.init_f(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) {
+        const int c = r / 64 * 64 + channel_of(r / 16 & 3, r & 15);
+        return n0 + c < p.H ? (uint32_t)(c * p.I) : kNoElement;
+    });
     const float* fs = p.f_scales + ((int64_t)t.expert * p.H + n0) / 128 * blocks;
     const bool second = n0 + 128 < p.H;      // the tile's second 128 channels exist
     stage_scales(smem, Bf16ByFp8Tile::kFScales, fs, second ? fs + blocks : fs, blocks);
     g.run(smem, p.I);
 
-    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 64 + (lane_id() >> 4) * 4;
+    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 64 + (lane_id() >> 4) * 8;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
         const int m = m_at + a * 16;
         if (m >= t.rows) continue;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int n = n_at + b * 16;
-            const f32x4 v = g.acc[a][b];
-            if (n < p.H) store4(p.out + (row0 + m) * p.H + n, v[0], v[1], v[2], v[3]);
-        }
+        for (int j = 0; j < 2; ++j)
+            if (n_at + j * 32 < p.H) store8(p.out + (row0 + m) * p.H + n_at + j * 32, g.acc[a][j * 2], g.acc[a][j * 2 + 1]);
     }
 }
 

@@ -76,6 +76,11 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Which of a wave's 64 rows of F stands at row `i` (0 .. 15) of its fragment `b`.  The matrix instruction leaves lane group
+// g with its rows 4g .. 4g + 3, so fragments 2j and 2j + 1 together give it channels 32 j + 8 g .. + 7: 16 bytes of
+// bf16 to store at once, 64 bytes in a row over the four groups.
+__device__ __forceinline__ int channel_of(int b, int i) { return (b >> 1) * 32 + (i >> 2) * 8 + (b & 1) * 4 + (i & 3); }
+
 // An operand whose k is contiguous: ROWS rows, 128 bytes of each per stage (64 bf16, or 128 e4m3).  A row is a line of LDS,
 // its 16-byte chunks permuted by the row number.
 template <int ROWS>
@@ -103,10 +108,10 @@ struct KcOperand {
             offset[i] = o == kNoElement ? kNoElement : o + chunk() * 16;
         }
     }
-    // The next stage, with `left` chunks of each row to go (none or fewer: nothing is read, LDS is zeroed).
+    // The next stage, with `left` bytes of each row to go (none or fewer: nothing is read, LDS is zeroed).
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
         const i32x4 res = resource(base, left > 0 ? kNoElement : 0u);
-        const bool there = chunk() < left;
+        const bool there = chunk() * 16 < left;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
             copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, there ? offset[i] : kNoElement, res);
@@ -136,7 +141,7 @@ struct KsOperand {
         asm volatile("s_nop 4" : "+s"(base), "+s"(step));
     }
 
-    static __device__ __forceinline__ int permute(int k) { return ((k & 3) | ((k >> 3) & 1) << 2) << 1; }
+    static __device__ __forceinline__ int permute(int k) { return (k & 3) << 2; }
     static __device__ __forceinline__ int row(int i) { return (i * kGemmWaves + wave_id()) * (kWave / kChunks) + lane_id() / kChunks; }
 
     // cols: columns that exist, counted from the tile's first.
@@ -157,11 +162,16 @@ struct KsOperand {
             copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, row(i) < left ? offset[i] : kNoElement, res);
         base += step;
     }
-    // LDS offset of the lane's part of the 16 columns from col0: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
-    // + 32 * kRowBytes for the second 32 k.
+    // LDS offset of the lane's part of 16 columns: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
+    // + 32 * kRowBytes for the second 32 k.  S's fragment: the columns from col0 on.  F's fragment b of a wave's 64
+    // columns: four columns for every g, placed as channel_of() says.
     static __device__ __forceinline__ uint32_t fragment(int col0) {
         const int lane = lane_id(), k = (lane >> 4) * 8 + ((lane & 15) >> 2), q = lane & 3;
         return k * kRowBytes + (((col0 / 8 + (q >> 1)) ^ permute(k)) << 4) + (q & 1) * 8;
+    }
+    static __device__ __forceinline__ uint32_t fragment_f(int col0, int b) {
+        const int lane = lane_id(), k = (lane >> 4) * 8 + ((lane & 15) >> 2), col = col0 + channel_of(b, (lane & 3) * 4);
+        return k * kRowBytes + (((col / 8) ^ permute(k)) << 4) + (col & 4) * 2;
     }
 };
 
@@ -188,8 +198,8 @@ struct OperandOf { typedef KcOperand<ROWS> type; };
 template <int ROWS>
 struct OperandOf<ROWS, true> { typedef KsOperand<ROWS> type; };
 
-// The bf16 tile: up to 256 rows of S against 256 rows of F, 64 k per stage.  A wave owns 16 * MT rows (MT of run(), up to
-// 8) by 64 channels.
+// The bf16 tiles of a workgroup, one after the other: up to 256 rows of S against 256 rows of F, 64 k per stage.  A wave
+// owns 16 * MT rows (MT of run(), up to 8) by 64 channels.
 //
 // Waves 0-3 (the upper rows) run half a step ahead of waves 4-7, so that on every SIMD one wave feeds the matrix unit
 // while the other reads its next fragments; two barriers per 32 k keep them in step.  The copies of a step are issued
@@ -197,43 +207,62 @@ struct OperandOf<ROWS, true> { typedef KsOperand<ROWS> type; };
 // under way while stage st is multiplied; weights come from HBM and need the longer lead, rows are read again and
 // again from L2.  Measured on 8192 x 8192 x 4096 (dense, everything in reach of L2): 1.43 PFLOP/s; 32 k per stage, four stages
 // deep, 1.39; with the copies left out 1.70, the reads too 1.86.
+//
+// The stages of a workgroup's tiles form one stream: the last two stages of a tile copy the first of the next one
+// (next_s, next_f, next_k), which then starts on data that has landed, while its predecessor is being stored.
 template <bool SKS, bool FKS>
-struct Bf16Tile {
+struct Bf16Tiles {
     static constexpr int kBM = 256, NT = 4;
     typedef typename OperandOf<kBM, SKS>::type SOp;
     typedef typename OperandOf<kBN, FKS>::type FOp;
     static constexpr int kSBuffers = 2, kFBuffers = 3, kF = SOp::kBytes * kSBuffers;
     static constexpr int kLds = kF + FOp::kBytes * kFBuffers;
+    static constexpr int kSUnit = SKS ? 1 : 2, kFUnit = FKS ? 1 : 2;      // what copy() counts in: k-rows, or bytes of a row
 
-    SOp s;
-    FOp f;
+    char* smem;
+    SOp s, next_s;
+    FOp f, next_f;
+    int next_k;                // terms of the next tile's sums; 0: no next tile (next_s and next_f then only need a value)
+    int k, s_left, f_left;     // of the tile under way; k that its operands have yet to copy
+    int sbuf, fbuf;            // buffers of the stage to be multiplied next
 
-    __device__ __forceinline__ void copy_s(uint32_t lds0, int st, int k) {
-        s.copy(lds0 + (st & 1) * SOp::kBytes, SKS ? k - st * 64 : (k - st * 64) / 8);
+    __device__ __forceinline__ void copy_s(int buf) {
+        s.copy(lds_address(smem) + buf * SOp::kBytes, s_left * kSUnit);
+        s_left -= 64;
     }
-    __device__ __forceinline__ void copy_f(uint32_t lds0, int buf, int st, int k) {
-        f.copy(lds0 + kF + buf * FOp::kBytes, FKS ? k - st * 64 : (k - st * 64) / 8);
+    __device__ __forceinline__ void copy_f(int buf) {
+        f.copy(lds_address(smem) + kF + buf * FOp::kBytes, f_left * kFUnit);
+        f_left -= 64;
     }
-
-    // The first copies of a tile whose sums have `k` terms, once s and f are set and the tile before is done with LDS.
-    __device__ __forceinline__ void begin(char* smem, int k) {
-        const uint32_t lds0 = lds_address(smem);
+    // s, f and k_terms are the workgroup's first tile.
+    __device__ __forceinline__ void begin(char* lds, int k_terms) {
+        smem = lds;
+        k = s_left = f_left = k_terms;
+        sbuf = fbuf = 0;
         s.settle();
         f.settle();
-        copy_f(lds0, 0, 0, k);
-        copy_s(lds0, 0, k);
-        copy_f(lds0, 1, 1, k);
+        copy_f(0);
+        copy_s(0);
+        copy_f(1);
+        wait_and_meet<FOp::kCopies>();
     }
 
-    // After begin(), the sums.  Global loads and stores may stand between the two (the tile before is stored there): the
-    // waits below count copies only, and copies land in order.
+    // The sums of the tile under way; afterwards the next one is.  Global loads and stores may stand between two run()s: the
+    // waits below count copies, which land in order.
     template <int MT>
-    __device__ __forceinline__ void run(char* smem, int k, f32x4 (&acc)[MT][NT]) {
+    __device__ __forceinline__ void run(f32x4 (&acc)[MT][NT]) {
         const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-        const int stages = (k + 63) / 64;
-        const uint32_t lds0 = lds_address(smem);
+        // at least two, so that only one tile has to be known ahead
+        const int stages = __builtin_amdgcn_readfirstlane(k > 64 ? (k + 63) / 64 : 2);
+        s_left = __builtin_amdgcn_readfirstlane(s_left);
+        f_left = __builtin_amdgcn_readfirstlane(f_left);
+        next_k = __builtin_amdgcn_readfirstlane(next_k);
+        sbuf = __builtin_amdgcn_readfirstlane(sbuf);
+        fbuf = __builtin_amdgcn_readfirstlane(fbuf);
         s.settle();
         f.settle();
+        next_s.settle();
+        next_f.settle();
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -242,19 +271,26 @@ struct Bf16Tile {
         uint32_t s_at[SKS ? MT : 1], f_at[FKS ? NT : 1];
 #pragma unroll
         for (int a = 0; a < (SKS ? MT : 1); ++a) s_at[a] = SOp::fragment((wm * MT + a) * 16);
+        if constexpr (FKS) {
 #pragma unroll
-        for (int b = 0; b < (FKS ? NT : 1); ++b) f_at[b] = FOp::fragment(wn * 64 + b * 16);
-        wait_and_meet<FOp::kCopies>();
+            for (int b = 0; b < NT; ++b) f_at[b] = FOp::fragment_f(wn * 64, b);
+        } else {
+            f_at[0] = FOp::fragment(wn * 64);
+        }
+
+        meet();
         if (wm == 1) meet();
-        int fbuf = 0;
         for (int st = 0; st < stages; ++st) {
-            const char* ls = smem + (st & 1) * SOp::kBytes;
+            const char* ls = smem + sbuf * SOp::kBytes;
             const char* lf = smem + kF + fbuf * FOp::kBytes;
+            if (st == stages - 1) s = next_s, s_left = next_k;
+            if (st == stages - 2) f = next_f, f_left = next_k;
+            sbuf ^= 1;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // both targets were last read in stage st - 1, which every wave had left before the last barrier
-                if (half == 0) copy_s(lds0, st + 1, k);
-                else copy_f(lds0, fbuf == 0 ? 2 : fbuf - 1, st + 2, k);
+                // both targets were last read in the stage before, which every wave had left before the last barrier
+                if (half == 0) copy_s(sbuf);
+                else copy_f(fbuf == 0 ? 2 : fbuf - 1);
                 bf16x8 sv[MT], fv[NT];
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
@@ -266,7 +302,7 @@ struct Bf16Tile {
                     if constexpr (SKS) sv[a] = read_ks<SOp::kRowBytes>(ls, s_at[a] + half * 32 * SOp::kRowBytes);
                     else sv[a] = read_kc(ls, (s_at[0] ^ (half * 64)) + a * 2048);
                 }
-                // before a wave goes on to stage st + 1 all but the newest copies, F's of st + 2, have landed
+                // before a wave goes on to the next stage all but the newest copies, F's of the stage after it, have landed
                 if (half == 0) wait_and_meet<63>();
                 else wait_and_meet<FOp::kCopies>();
                 __builtin_amdgcn_s_setprio(1);
@@ -281,8 +317,11 @@ struct Bf16Tile {
             fbuf = fbuf == 2 ? 0 : fbuf + 1;
         }
         if (wm == 0) meet();
-        wait_and_meet<0>();      // no copy may land after the workgroup has left its LDS
+        k = next_k;
     }
+
+    // No copy may land after the workgroup has left its LDS.
+    static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
 };
 
 // ---- e4m3 operands ----------------------------------------------------------------------------------------------
@@ -313,8 +352,8 @@ struct Fp8Tile {
     f32x4 acc[MT][NT];
 
     __device__ __forceinline__ void copy_stage(uint32_t lds0, int buf, bool more) {
-        s.copy(lds0 + buf * kStage, more ? 8 : 0);
-        f.copy(lds0 + buf * kStage + SOp::kBytes, more ? 8 : 0);
+        s.copy(lds0 + buf * kStage, more ? 128 : 0);
+        f.copy(lds0 + buf * kStage + SOp::kBytes, more ? 128 : 0);
         copy4_to_lds(lds0 + kRowScales + (buf * kGemmWaves + wave_id()) * 256, scale_offset, resource(scales, more ? kNoElement : 0u));
         scales += 4;
     }
@@ -401,7 +440,7 @@ struct Bf16ByFp8Tile {
         }
     }
     __device__ __forceinline__ void copy_stage(uint32_t lds, bool more) {
-        s.copy(lds, more ? 8 : 0);
+        s.copy(lds, more ? 128 : 0);
         const i32x4 res = resource(f, more ? kNoElement : 0u);
 #pragma unroll
         for (int i = 0; i < kFCopies; ++i)

@@ -28,40 +28,74 @@ __device__ __forceinline__ void stage_scales(char* smem, int at, const float* a,
     if (i < n) to[threadIdx.x] = (threadIdx.x < 256 ? a : b)[i];
 }
 
+struct GateUp {
+    const Params& p;
+    RowTiles<Fp8Tiles::kBM, 0> rows;      // the registers are needed: find() reads the counts again
+    Fp8Tiles g;
+    int round = 0;
+    RowTile now, next;
+    int now_n0, next_n0;
+
+    __device__ __forceinline__ explicit GateUp(const Params& params) : p(params), rows(params.cnt, params.psum, params.El) {}
+
+    // The workgroup's next tile; next.rows = 0: there is none.
+    __device__ __forceinline__ void look_ahead() {
+        TileAt at;
+        next.rows = g.next_k = 0;
+        if (!tile_at((int)blockIdx.x, round++, rows.total, p.I / 128, &at)) return;
+        next = rows.find(at.row, 32);
+        const int n0 = next_n0 = at.col * 128, blocks = p.H / 128, mt = (next.rows + 31) / 32;
+        g.next_k = p.H;
+        g.next_s.init((const uint8_t*)p.s + (int64_t)next.row0 * p.H, [&](int r) { return r < next.rows ? (uint32_t)(r * p.H) : kNoElement; });
+        // a wave's 64 rows of F: 32 gate channels (fragments 0, 1), then the same 32 up channels
+        const uint32_t up = (uint32_t)p.I * p.H;
+        g.next_f.init(p.f + ((int64_t)next.expert * 2 * p.I + n0) * p.H,
+                      [&](int r) { return (r & 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + channel_of(r / 16 & 1, r & 15)) * p.H); });
+        g.next_row_scales(p.s_scales + (int64_t)next.row0 * blocks, blocks, next.rows, mt);
+        g.copy_next_f_scales(p.f_scales + ((int64_t)next.expert * 2 * p.I + n0) / 128 * blocks, (uint32_t)(p.I / 128 * blocks) * 4, blocks,
+                             round & 1 ? 0 : 1);
+    }
+
+    template <int MT>
+    __device__ __forceinline__ void tile() {
+        f32x4 acc[MT][4];
+        g.run<MT>(acc);
+        const int m_at = (wave_id() >> 2) * MT * 16 + (lane_id() & 15), n = now_n0 + (wave_id() & 3) * 32 + (lane_id() >> 4) * 8;
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+            const int m = m_at + a * 16;
+            if (m >= now.rows) continue;
+            f32x4 h[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[b][i] = acc[a][b][i] * sigmoid(acc[a][b][i]) * acc[a][b + 2][i];
+            store8(p.out + (int64_t)(now.row0 + m) * p.I + n, h[0], h[1]);
+        }
+    }
+};
+
+// A workgroup stays on its CU and walks through its tiles.  Waves take as many 16-row steps as the tile is high.
 __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    const RowTiles<Fp8Tile::kBM> tiles(p.cnt, p.psum, p.El);
-    TileAt at;
-    if (!tile_at((int)blockIdx.x % (kXcds * kBatch), (int)blockIdx.x / (kXcds * kBatch), tiles.total, p.I / 128, &at)) return;
-    const RowTile t = tiles.find(at.row);
-    const int64_t row0 = t.row0;
-    const int n0 = at.col * 128, blocks = p.H / 128, wave = wave_id();
-
-    Fp8Tile g;
-    g.s.init((const uint8_t*)p.s + row0 * p.H, [&](int r) { return r < t.rows ? (uint32_t)(r * p.H) : kNoElement; });
-    // a wave's 64 rows of F: 32 gate channels, then the same 32 up channels
-    const uint32_t up = (uint32_t)p.I * p.H;
-    g.f.init(p.f + ((int64_t)t.expert * 2 * p.I + n0) * p.H,
-             [&](int r) { return (r & 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + channel_of(r / 16 & 1, r & 15)) * p.H); });
-    const int r = (wave >> 2) * 64 + lane_id();
-    g.scales = uniform64((uint64_t)(p.s_scales + row0 * blocks));
-    g.scale_offset = r < t.rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
-    const float* fs = p.f_scales + ((int64_t)t.expert * 2 * p.I + n0) / 128 * blocks;
-    stage_scales(smem, Fp8Tile::kFScales, fs, fs + (int64_t)p.I / 128 * blocks, blocks);
-    g.run(smem, blocks);
-
-    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 32 + (lane_id() >> 4) * 8;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int m = m_at + a * 16;
-        if (m >= t.rows) continue;
-        f32x4 h[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[b][i] = g.acc[a][b][i] * sigmoid(g.acc[a][b][i]) * g.acc[a][b + 2][i];
-        store8(p.out + (row0 + m) * p.I + n_at, h[0], h[1]);
-    }
+    GateUp k(p);
+    k.g.smem = smem;
+    k.look_ahead();
+    if (k.next.rows == 0) return;
+    k.g.begin(p.H);
+    do {
+        k.now = k.next, k.now_n0 = k.next_n0;
+        k.look_ahead();
+        switch ((k.now.rows + 31) / 32) {
+            case 1: k.tile<1>(); break;
+            case 2: k.tile<2>(); break;
+            case 3: k.tile<3>(); break;
+            case 4: k.tile<4>(); break;
+            case 5: k.tile<5>(); break;
+            default: k.tile<6>(); break;
+        }
+    } while (k.next.rows > 0);
+    k.g.end();
 }
 
 __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
@@ -98,12 +132,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
 }  // namespace
 
 hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const int64_t rows = (int64_t)h.T * h.K / 128 + h.El;
-    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tile::kLds);
+    const int64_t entries = (int64_t)h.T * h.K, up_rows = entries / Fp8Tiles::kBM + h.El, rows = entries / Bf16ByFp8Tile::kBM + h.El;
+    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tiles::kLds);
     if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tile::kLds);
     if (e != hipSuccess) return e;
     const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_gate_up, dim3(single_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tile::kLds, stream, up);
+    hipLaunchKernelGGL(k_gate_up, dim3(walking_blocks(up_rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tiles::kLds, stream, up);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};

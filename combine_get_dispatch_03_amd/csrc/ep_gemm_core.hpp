@@ -332,84 +332,155 @@ __device__ __forceinline__ i32x8 read_line(const char* lds, uint32_t at) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 128 rows of e4m3 with a scale per row and 128 k, against 256 rows of e4m3 F with a scale per half of each wave's rows
-// and 128 k: 16x16x128 matrix instructions, whose sums over one 128-block are exact products in fp32, then one FMA with the
-// product of the two scales.
-struct Fp8Tile {
-    static constexpr int MT = 4, NT = 4, kBM = 128;
+// The e4m3 tiles of a workgroup, one after the other (as Bf16Tiles): up to 192 rows of S with a scale per row and 128 k,
+// against 256 rows of F with a scale per half of each wave's rows and 128 k.  One 16x16x128 matrix instruction gives a block's sums, which
+// take the product of the two scales on their way into acc: products and scales are exact, sums are fp32.
+//
+// 128 k per stage, in two half steps of two fragments of F each; S's fragments stay for both.
+struct Fp8Tiles {
+    static constexpr int kBM = 192, NT = 4;
     typedef KcOperand<kBM> SOp;
     typedef KcOperand<kBN> FOp;
-    static constexpr int kStage = SOp::kBytes + FOp::kBytes, kBuffers = 3;
-    static constexpr int kCopies = SOp::kCopies + FOp::kCopies + 1;
-    static constexpr int kRowScales = kStage * kBuffers;                          // per wave and stage 64 fp32
-    static constexpr int kFScales = kRowScales + kGemmWaves * kBuffers * 256;     // two rows of up to 256 fp32
-    static constexpr int kLds = kFScales + 2048;
+    static constexpr int kSBuffers = 2, kFBuffers = 3, kF = SOp::kBytes * kSBuffers;
+    static constexpr int kScaleRow = 512;                                        // a wave's row scales of a stage: up to 96 fp32
+    static constexpr int kRowScales = kF + FOp::kBytes * kFBuffers;              // [2][waves]
+    static constexpr int kFScales = kRowScales + 2 * kGemmWaves * kScaleRow;     // [2 tiles][2 rows of up to 256 fp32]
+    static constexpr int kLds = kFScales + 2 * 2048;
 
-    SOp s;
-    FOp f;
-    uint64_t scales;         // of the wave's 64 rows; 4 bytes further each stage
-    uint32_t scale_offset;
-    f32x4 acc[MT][NT];
+    char* smem;
+    SOp s, next_s;
+    FOp f, next_f;
+    uint64_t scales, next_scales;              // of the tile's rows; 4 bytes further each stage
+    uint32_t scale_offset[2], next_scale_offset[2];
+    int next_k, k, s_left, f_left, sbuf, fbuf, tile;
 
-    __device__ __forceinline__ void copy_stage(uint32_t lds0, int buf, bool more) {
-        s.copy(lds0 + buf * kStage, more ? 128 : 0);
-        f.copy(lds0 + buf * kStage + SOp::kBytes, more ? 128 : 0);
-        copy4_to_lds(lds0 + kRowScales + (buf * kGemmWaves + wave_id()) * 256, scale_offset, resource(scales, more ? kNoElement : 0u));
+    // Row scales of a tile whose waves own 16 * mt rows each.
+    __device__ __forceinline__ void next_row_scales(const float* at, int blocks, int rows, int mt) {
+        next_scales = uniform64((uint64_t)at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (wave_id() >> 2) * mt * 16 + i * 64 + lane_id();
+            next_scale_offset[i] = i * 64 + lane_id() < mt * 16 && r < rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
+        }
+    }
+    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first.
+    __device__ __forceinline__ void copy_next_f_scales(const float* at, uint32_t second, int blocks, int which) {
+        const int i = (wave_id() & 3) * 64 + lane_id();
+        uint64_t base = uniform64((uint64_t)at);
+        asm volatile("s_nop 4" : "+s"(base));
+        copy4_to_lds(lds_address(smem) + kFScales + which * 2048 + wave_id() * 256,
+                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base, kNoElement));
+    }
+    __device__ __forceinline__ void copy_s(int buf) {
+        const uint32_t lds0 = lds_address(smem);
+        s.copy(lds0 + buf * SOp::kBytes, s_left);
+        const i32x4 res = resource(scales, s_left > 0 ? kNoElement : 0u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            copy4_to_lds(lds0 + kRowScales + (buf * kGemmWaves + wave_id()) * kScaleRow + i * 256, scale_offset[i], res);
         scales += 4;
+        s_left -= 128;
+    }
+    __device__ __forceinline__ void copy_f(int buf) {
+        f.copy(lds_address(smem) + kF + buf * FOp::kBytes, f_left);
+        f_left -= 128;
+    }
+    __device__ __forceinline__ void settle() {
+        s.settle();
+        f.settle();
+        next_s.settle();
+        next_f.settle();
+        scales = uniform64(scales);
+        next_scales = uniform64(next_scales);
+        asm volatile("s_nop 4" : "+s"(scales), "+s"(next_scales));
+    }
+    __device__ __forceinline__ void take_next_s() {
+        s = next_s, scales = next_scales, s_left = next_k;
+        scale_offset[0] = next_scale_offset[0], scale_offset[1] = next_scale_offset[1];
+    }
+    // The workgroup's first tile, which next_* describe (and its F scales are on their way to buffer 0).
+    __device__ __forceinline__ void begin(int k_terms) {
+        next_k = k_terms;
+        settle();
+        f = next_f, f_left = next_k;
+        take_next_s();
+        k = next_k;
+        sbuf = fbuf = tile = 0;
+        copy_f(0);
+        copy_s(0);
+        copy_f(1);
+        wait_and_meet<FOp::kCopies>();
     }
 
-    // blocks of 128 k.  The F scales are in LDS at kFScales (written before the call): fragments 0, 1 of a wave take
-    // the first row, 2, 3 the second.
-    __device__ __forceinline__ void run(char* smem, int blocks) {
+    template <int MT>
+    __device__ __forceinline__ void run(f32x4 (&acc)[MT][NT]) {
         const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-        const uint32_t lds0 = lds_address(smem);
-        asm volatile("s_nop 4" : "+s"(s.base), "+s"(f.base), "+s"(scales));
+        const int stages = __builtin_amdgcn_readfirstlane(k > 128 ? k / 128 : 2);
+        s_left = __builtin_amdgcn_readfirstlane(s_left);
+        f_left = __builtin_amdgcn_readfirstlane(f_left);
+        next_k = __builtin_amdgcn_readfirstlane(next_k);
+        sbuf = __builtin_amdgcn_readfirstlane(sbuf);
+        fbuf = __builtin_amdgcn_readfirstlane(fbuf);
+        settle();
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint32_t s_at = SOp::fragment(wm * 64), f_at = SOp::kBytes + FOp::fragment(wn * 64);
-        const float* fs = reinterpret_cast<const float*>(smem + kFScales);
-#pragma unroll
-        for (int i = 0; i < kBuffers - 1; ++i) copy_stage(lds0, i, i < blocks);
-        wait_and_meet<(kBuffers - 2) * kCopies>();
+        const uint32_t s_at = SOp::fragment(wm * MT * 16), f_at = FOp::fragment(wn * 64);
+        const float* fs = reinterpret_cast<const float*>(smem + kFScales + tile * 2048);
+        meet();
         if (wm == 1) meet();
-        int buf = 0;
-        for (int st = 0; st < blocks; ++st) {
-            const char* l = smem + buf * kStage;
-            i32x8 sv[MT], fv[NT];
+        for (int st = 0; st < stages; ++st) {
+            const char* ls = smem + sbuf * SOp::kBytes;
+            const char* lf = smem + kF + fbuf * FOp::kBytes;
+            const float* rs = reinterpret_cast<const float*>(smem + kRowScales + (sbuf * kGemmWaves + wave) * kScaleRow) + (lane_id() & 15);
+            if (st == stages - 1) take_next_s();
+            if (st == stages - 2) f = next_f, f_left = next_k;
+            sbuf ^= 1;
+            i32x8 sv[MT];
             float row_scale[MT];
 #pragma unroll
-            for (int b = 0; b < NT; ++b) fv[b] = read_line(l, f_at + b * 2048);
+            for (int half = 0; half < 2; ++half) {
+                if (half == 0) copy_s(sbuf);
+                else copy_f(fbuf == 0 ? 2 : fbuf - 1);
+                i32x8 fv[2];
 #pragma unroll
-            for (int a = 0; a < MT; ++a) sv[a] = read_line(l, s_at + a * 2048);
+                for (int b = 0; b < 2; ++b) fv[b] = read_line(lf, f_at + (half * 2 + b) * 2048);
+                if (half == 0) {
 #pragma unroll
-            for (int a = 0; a < MT; ++a)
-                row_scale[a] = *reinterpret_cast<const float*>(smem + kRowScales + (buf * kGemmWaves + wave) * 256 + (a * 16 + (lane_id() & 15)) * 4);
-            const float f0 = fs[st], f1 = fs[256 + st];
-            const int nbuf = buf == 0 ? kBuffers - 1 : buf - 1;
-            copy_stage(lds0, nbuf, st + kBuffers - 1 < blocks);
-            wait_and_meet<(kBuffers - 2) * kCopies>();
-            __builtin_amdgcn_s_setprio(1);
+                    for (int a = 0; a < MT; ++a) sv[a] = read_line(ls, s_at + a * 2048);
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                f32x4 part[NT];
+                    for (int a = 0; a < MT; ++a) row_scale[a] = rs[a * 16];
+                }
+                const float f_scale = fs[half * 256 + (st < k / 128 ? st : 0)];
+                if (half == 0) wait_and_meet<63>();
+                else wait_and_meet<FOp::kCopies>();
+                __builtin_amdgcn_s_setprio(1);
+                f32x4 part[MT][2];
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
-                    part[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fv[b], sv[a], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-                const float g0 = row_scale[a] * f0, g1 = row_scale[a] * f1;
+                for (int a = 0; a < MT; ++a)
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
+                    for (int b = 0; b < 2; ++b)
+                        part[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fv[b], sv[a], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(part[b][i], b < 2 ? g0 : g1, acc[a][b][i]);
+                for (int a = 0; a < MT; ++a) {
+                    const float scale = row_scale[a] * f_scale;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[a][half * 2 + b][i] = fmaf(part[a][b][i], scale, acc[a][half * 2 + b][i]);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                meet();
             }
-            __builtin_amdgcn_s_setprio(0);
-            meet();
-            buf = buf == kBuffers - 1 ? 0 : buf + 1;
+            fbuf = fbuf == 2 ? 0 : fbuf + 1;
         }
         if (wm == 0) meet();
-        wait_and_meet<0>();
+        k = next_k;
+        tile ^= 1;
     }
+
+    static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
 };
 
 // 128 rows of bf16 against 256 rows of e4m3 F with a scale per wave and 128 k: F is widened to bf16 (exact) on its way from

@@ -37,10 +37,8 @@ __device__ __forceinline__ bool tile_at(int block, int round, int rows, int cols
     t->col = in / height;
     return true;
 }
-// Workgroups to launch for at most `tiles` tiles when each walks through its rounds, and when each takes one tile (round
-// block / (kXcds * kBatch)).
+// Workgroups to launch for at most `tiles` tiles: each walks through its rounds.
 inline unsigned walking_blocks(int64_t tiles) { return (unsigned)(tiles < kXcds * kBatch ? (tiles + kXcds - 1) / kXcds * kXcds : kXcds * kBatch); }
-inline unsigned single_blocks(int64_t tiles) { return (unsigned)((tiles + kXcds * kBatch - 1) / (kXcds * kBatch) * (kXcds * kBatch)); }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {

@@ -21,13 +21,6 @@ struct Params {
     int H, I;
 };
 
-// The scales of two rows of 128 x 128 blocks, `n` each, to LDS.
-__device__ __forceinline__ void stage_scales(char* smem, int at, const float* a, const float* b, int n) {
-    float* to = reinterpret_cast<float*>(smem + at);
-    const int i = threadIdx.x & 255;
-    if (i < n) to[threadIdx.x] = (threadIdx.x < 256 ? a : b)[i];
-}
-
 struct GateUp {
     const Params& p;
     RowTiles<Fp8Tiles::kBM, 0> rows;      // the registers are needed: find() reads the counts again
@@ -98,50 +91,84 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     k.g.end();
 }
 
+struct Down {
+    const Params& p;
+    RowTiles<Bf16ByFp8Tiles::kBM, 0> rows;
+    Bf16ByFp8Tiles g;
+    int round = 0;
+    RowTile now, next;
+    int now_n0, next_n0;
+
+    __device__ __forceinline__ explicit Down(const Params& params) : p(params), rows(params.cnt, params.psum, params.El) {}
+
+    // The workgroup's next tile; next.rows = 0: there is none.
+    __device__ __forceinline__ void look_ahead() {
+        TileAt at;
+        next.rows = g.next_k = 0;
+        if (!tile_at((int)blockIdx.x, round++, rows.total, (p.H + kBN - 1) / kBN, &at)) return;
+        next = rows.find(at.row, 32);
+        const int n0 = next_n0 = at.col * kBN, blocks = p.I / 128;
+        g.next_k = p.I;
+        g.next_s.init((const uint16_t*)p.s + (int64_t)next.row0 * p.I, [&](int r) { return r < next.rows ? (uint32_t)r * p.I * 2 : kNoElement; });
+        g.init_next_f(p.f + ((int64_t)next.expert * p.H + n0) * p.I, [&](int r) {
+            const int c = r / 64 * 64 + channel_of(r / 16 & 3, r & 15);
+            return n0 + c < p.H ? (uint32_t)(c * p.I) : kNoElement;
+        });
+        // (a last tile of 128 channels has no second row of scales: its first stands in for channels that do not exist)
+        g.copy_next_f_scales(p.f_scales + ((int64_t)next.expert * p.H + n0) / 128 * blocks, n0 + 128 < p.H ? blocks * 4u : 0u, blocks,
+                             round & 1 ? 0 : 1);
+    }
+
+    template <int MT>
+    __device__ __forceinline__ void tile() {
+        f32x4 acc[MT][4];
+        g.run<MT>(acc);
+        const int m_at = (wave_id() >> 2) * MT * 16 + (lane_id() & 15), n_at = now_n0 + (wave_id() & 3) * 64 + (lane_id() >> 4) * 8;
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+            const int m = m_at + a * 16;
+            if (m >= now.rows) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (n_at + j * 32 < p.H) store8(p.out + (int64_t)(now.row0 + m) * p.H + n_at + j * 32, acc[a][j * 2], acc[a][j * 2 + 1]);
+        }
+    }
+};
+
 __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    const RowTiles<Bf16ByFp8Tile::kBM> tiles(p.cnt, p.psum, p.El);
-    TileAt at;
-    if (!tile_at((int)blockIdx.x % (kXcds * kBatch), (int)blockIdx.x / (kXcds * kBatch), tiles.total, (p.H + kBN - 1) / kBN, &at)) return;
-    const RowTile t = tiles.find(at.row);
-    const int64_t row0 = t.row0;
-    const int n0 = at.col * kBN, blocks = p.I / 128, wave = wave_id();
-
-    Bf16ByFp8Tile g;
-    g.s.init((const uint16_t*)p.s + row0 * p.I, [&](int r) { return r < t.rows ? (uint32_t)r * p.I * 2 : kNoElement; });
-    g.init_f(p.f + ((int64_t)t.expert * p.H + n0) * p.I, [&](int r) {
-        const int c = r / 64 * 64 + channel_of(r / 16 & 3, r & 15);
-        return n0 + c < p.H ? (uint32_t)(c * p.I) : kNoElement;
-    });
-    const float* fs = p.f_scales + ((int64_t)t.expert * p.H + n0) / 128 * blocks;
-    const bool second = n0 + 128 < p.H;      // the tile's second 128 channels exist
-    stage_scales(smem, Bf16ByFp8Tile::kFScales, fs, second ? fs + blocks : fs, blocks);
-    g.run(smem, p.I);
-
-    const int m_at = (wave >> 2) * 64 + (lane_id() & 15), n_at = n0 + (wave & 3) * 64 + (lane_id() >> 4) * 8;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const int m = m_at + a * 16;
-        if (m >= t.rows) continue;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (n_at + j * 32 < p.H) store8(p.out + (row0 + m) * p.H + n_at + j * 32, g.acc[a][j * 2], g.acc[a][j * 2 + 1]);
-    }
+    Down k(p);
+    k.g.smem = smem;
+    k.look_ahead();
+    if (k.next.rows == 0) return;
+    k.g.begin(p.I);
+    do {
+        k.now = k.next, k.now_n0 = k.next_n0;
+        k.look_ahead();
+        switch ((k.now.rows + 31) / 32) {
+            case 1: k.tile<1>(); break;
+            case 2: k.tile<2>(); break;
+            case 3: k.tile<3>(); break;
+            case 4: k.tile<4>(); break;
+            default: k.tile<5>(); break;
+        }
+    } while (k.next.rows > 0);
+    k.g.end();
 }
 
 }  // namespace
 
 hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const int64_t entries = (int64_t)h.T * h.K, up_rows = entries / Fp8Tiles::kBM + h.El, rows = entries / Bf16ByFp8Tile::kBM + h.El;
+    const int64_t entries = (int64_t)h.T * h.K, up_rows = entries / Fp8Tiles::kBM + h.El, down_rows = entries / Bf16ByFp8Tiles::kBM + h.El;
     hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tiles::kLds);
-    if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tile::kLds);
+    if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tiles::kLds);
     if (e != hipSuccess) return e;
     const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
     hipLaunchKernelGGL(k_gate_up, dim3(walking_blocks(up_rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tiles::kLds, stream, up);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_down, dim3(single_blocks(rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tile::kLds, stream, down);
+    hipLaunchKernelGGL(k_down, dim3(walking_blocks(down_rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tiles::kLds, stream, down);
     return hipGetLastError();
 }
 

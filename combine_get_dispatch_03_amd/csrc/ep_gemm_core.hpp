@@ -483,77 +483,128 @@ struct Fp8Tiles {
     static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
 };
 
-// 128 rows of bf16 against 256 rows of e4m3 F with a scale per wave and 128 k: F is widened to bf16 (exact) on its way from
-// LDS, a block's sums get the scale in fp32.  64 k per stage: 128 bytes of a row of S, 64 of F (two rows a line of LDS).
-struct Bf16ByFp8Tile {
-    static constexpr int MT = 4, NT = 4, kBM = 128;
-    typedef KcOperand<kBM> SOp;
+// The tiles of bf16 rows by e4m3 weights, one after the other (as Bf16Tiles): up to 160 rows of S against 256 rows of F
+// with a scale per wave and 128 k.  F is widened to bf16 (exact) on its way from LDS; a block's sums are kept apart and
+// take the scale in fp32 on their way into acc.  (Those two sets of sums are what limits the rows: 5 steps of 16 per wave.)
+// 64 k per stage: 128 bytes of a row of S, 64 of F (two rows a line of LDS).  S is three stages deep and F four.
+struct Bf16ByFp8Tiles {
+    static constexpr int kBM = 160, NT = 4;
+    typedef KcOperand<192> SOp;                      // whole copies per wave; rows from 160 on do not exist
     static constexpr int kFBytes = kBN * 64, kFCopies = 2;
-    static constexpr int kStage = SOp::kBytes + kFBytes, kBuffers = 4;
-    static constexpr int kCopies = SOp::kCopies + kFCopies;
-    static constexpr int kFScales = kStage * kBuffers;     // two rows of up to 256 fp32: channels 0..127, 128..255
-    static constexpr int kLds = kFScales + 2048;
+    static constexpr int kSBuffers = 3, kFBuffers = 4, kF = SOp::kBytes * kSBuffers;
+    static constexpr int kFScales = kF + kFBytes * kFBuffers;     // [2 tiles][2 rows of up to 256 fp32]: channels 0..127, 128..255
+    static constexpr int kLds = kFScales + 2 * 2048;
+    static constexpr int kAhead = kFCopies + SOp::kCopies + kFCopies;    // copies under way past the next stage
 
-    SOp s;
-    uint64_t f;
-    uint32_t f_offset[kFCopies];
-    f32x4 acc[MT][NT];
+    char* smem;
+    SOp s, next_s;
+    uint64_t f, next_f;
+    uint32_t f_offset[kFCopies], next_f_offset[kFCopies];
+    int next_k, k, s_left, f_left, sbuf, fbuf, tile;      // sbuf, fbuf: of the stage to be multiplied next
 
-    // A copy is 16 rows of 64 bytes; a row's four chunks are permuted by the pair of rows it stands in.
+    // A copy of F is 16 rows of 64 bytes; a row's four chunks are permuted by the pair of rows it stands in.
     template <class RowOffset>
-    __device__ __forceinline__ void init_f(const void* start, RowOffset row_offset) {
-        f = uniform64((uint64_t)start);
+    __device__ __forceinline__ void init_next_f(const void* start, RowOffset row_offset) {
+        next_f = uniform64((uint64_t)start);
         const int x = (lane_id() & 7) ^ (lane_id() >> 3);
 #pragma unroll
         for (int i = 0; i < kFCopies; ++i) {
             const uint32_t o = row_offset((i * kGemmWaves + wave_id()) * 16 + (lane_id() >> 3) * 2 + (x >> 2));
-            f_offset[i] = o == kNoElement ? kNoElement : o + (x & 3) * 16;
+            next_f_offset[i] = o == kNoElement ? kNoElement : o + (x & 3) * 16;
         }
     }
-    __device__ __forceinline__ void copy_stage(uint32_t lds, bool more) {
-        s.copy(lds, more ? 128 : 0);
-        const i32x4 res = resource(f, more ? kNoElement : 0u);
+    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first.
+    __device__ __forceinline__ void copy_next_f_scales(const float* at, uint32_t second, int blocks, int which) {
+        const int i = (wave_id() & 3) * 64 + lane_id();
+        uint64_t base = uniform64((uint64_t)at);
+        asm volatile("s_nop 4" : "+s"(base));
+        copy4_to_lds(lds_address(smem) + kFScales + which * 2048 + wave_id() * 256,
+                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base, kNoElement));
+    }
+    __device__ __forceinline__ void copy_s(int buf) {
+        s.copy(lds_address(smem) + buf * SOp::kBytes, s_left * 2);
+        s_left -= 64;
+    }
+    __device__ __forceinline__ void copy_f(int buf) {
+        const i32x4 res = resource(f, f_left > 0 ? kNoElement : 0u);
 #pragma unroll
         for (int i = 0; i < kFCopies; ++i)
-            copy16_to_lds(lds + SOp::kBytes + (i * kGemmWaves + wave_id()) * 1024, f_offset[i], res);
+            copy16_to_lds(lds_address(smem) + kF + buf * kFBytes + (i * kGemmWaves + wave_id()) * 1024, f_offset[i], res);
         f += 64;
+        f_left -= 64;
+    }
+    __device__ __forceinline__ void settle() {
+        s.settle();
+        next_s.settle();
+        f = uniform64(f);
+        next_f = uniform64(next_f);
+        asm volatile("s_nop 4" : "+s"(f), "+s"(next_f));
+    }
+    __device__ __forceinline__ void take_next_s() { s = next_s, s_left = next_k; }
+    __device__ __forceinline__ void take_next_f() {
+        f = next_f, f_left = next_k;
+#pragma unroll
+        for (int i = 0; i < kFCopies; ++i) f_offset[i] = next_f_offset[i];
+    }
+    // The workgroup's first tile, which next_* describe (and its F scales are on their way to buffer 0).
+    __device__ __forceinline__ void begin(int k_terms) {
+        next_k = k_terms;
+        settle();
+        take_next_s();
+        take_next_f();
+        k = next_k;
+        sbuf = fbuf = tile = 0;
+        copy_f(0);
+        copy_s(0);
+        copy_f(1);
+        copy_s(1);
+        copy_f(2);
+        wait_and_meet<kAhead>();
     }
 
-    __device__ __forceinline__ void run(char* smem, int k) {
-        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, stages = k / 64;
-        const uint32_t lds0 = lds_address(smem);
-        asm volatile("s_nop 4" : "+s"(s.base), "+s"(f));
+    template <int MT>
+    __device__ __forceinline__ void run(f32x4 (&acc)[MT][NT]) {
+        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
+        const int stages = __builtin_amdgcn_readfirstlane(k > 256 ? k / 64 : 4);     // enough that one tile ahead will do
+        s_left = __builtin_amdgcn_readfirstlane(s_left);
+        f_left = __builtin_amdgcn_readfirstlane(f_left);
+        next_k = __builtin_amdgcn_readfirstlane(next_k);
+        sbuf = __builtin_amdgcn_readfirstlane(sbuf);
+        fbuf = __builtin_amdgcn_readfirstlane(fbuf);
+        settle();
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // a lane reads 16 e4m3: k 16g .. 16g + 15 of a row; its bf16 of S are the two chunks of the same k
         const int r = lane_id() & 15, g = lane_id() >> 4;
-        const uint32_t s_at = (wm * 64 + r) * 128 + (((2 * g) ^ (r & 7)) << 4);
-        const uint32_t f_at = SOp::kBytes + (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | g) ^ (r >> 1)) << 4);
-        const float* fs = reinterpret_cast<const float*>(smem + kFScales) + (wn >> 1) * 256;
-#pragma unroll
-        for (int i = 0; i < kBuffers - 1; ++i) copy_stage(lds0 + i * kStage, i < stages);
-        wait_and_meet<(kBuffers - 2) * kCopies>();
+        const uint32_t s_at = (wm * MT * 16 + r) * 128 + (((2 * g) ^ (r & 7)) << 4);
+        const uint32_t f_at = (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | g) ^ (r >> 1)) << 4);
+        const float* fs = reinterpret_cast<const float*>(smem + kFScales + tile * 2048) + (wn >> 1) * 256;
+        meet();
         if (wm == 1) meet();
-        int buf = 0;
         for (int st = 0; st < stages; st += 2) {
             f32x4 part[MT][NT];
-            const float scale = fs[st / 2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const char* l = smem + buf * kStage;
+                const char* ls = smem + sbuf * SOp::kBytes;
+                const char* lf = smem + kF + fbuf * kFBytes;
+                if (st + q == stages - 2) take_next_s();
+                if (st + q == stages - 3) take_next_f();
+                // the buffers of the stage before, which every wave had left before the last barrier
+                copy_s(sbuf == 0 ? kSBuffers - 1 : sbuf - 1);
+                copy_f((fbuf + kFBuffers - 1) % kFBuffers);
                 bf16x8 sv[MT][2];
                 i32x4 fq[NT];
-                copy_stage(lds0 + (buf == 0 ? kBuffers - 1 : buf - 1) * kStage, st + q + kBuffers - 1 < stages);
 #pragma unroll
-                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x4*>(l + f_at + b * 1024);
+                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x4*>(lf + f_at + b * 1024);
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
-                    sv[a][0] = read_kc(l, s_at + a * 2048);
-                    sv[a][1] = read_kc(l, (s_at ^ 16) + a * 2048);
+                    sv[a][0] = read_kc(ls, s_at + a * 2048);
+                    sv[a][1] = read_kc(ls, (s_at ^ 16) + a * 2048);
                 }
-                wait_and_meet<(kBuffers - 2) * kCopies>();
+                const float scale = q == 1 ? fs[st < k / 64 ? st / 2 : 0] : 0.0f;
+                wait_and_meet<kAhead>();
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -574,12 +625,16 @@ struct Bf16ByFp8Tile {
                 }
                 __builtin_amdgcn_s_setprio(0);
                 meet();
-                buf = buf == kBuffers - 1 ? 0 : buf + 1;
+                sbuf = sbuf == kSBuffers - 1 ? 0 : sbuf + 1;
+                fbuf = (fbuf + 1) % kFBuffers;
             }
         }
         if (wm == 0) meet();
-        wait_and_meet<0>();
+        k = next_k;
+        tile ^= 1;
     }
+
+    static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
 };
 
 }  // namespace ep

@@ -78,7 +78,7 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 w.v[b][j] = i32x4{0, 0, 0, 0};
-                if (at + j * 64 + g * 16 < f_bytes) w.v[b][j] = __builtin_nontemporal_load((const i32x4*)(f[b] + at + j * 64));
+                if (at + j * 64 + g * 16 < f_bytes) w.v[b][j] = *(const i32x4*)(f[b] + at + j * 64);
             }
         return w;
     };

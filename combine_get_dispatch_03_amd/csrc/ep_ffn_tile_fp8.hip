@@ -37,14 +37,14 @@ struct GateUp {
         next.rows = g.next_k = 0;
         if (!tile_at((int)blockIdx.x, round++, rows.total, p.I / 128, &at)) return;
         next = rows.find(at.row, 32);
-        const int n0 = next_n0 = at.col * 128, blocks = p.H / 128, mt = (next.rows + 31) / 32;
+        const int n0 = next_n0 = at.col * 128, blocks = p.H / 128;
         g.next_k = p.H;
         g.next_s.init((const uint8_t*)p.s + (int64_t)next.row0 * p.H, [&](int r) { return r < next.rows ? (uint32_t)(r * p.H) : kNoElement; });
         // a wave's 64 rows of F: 32 gate channels (fragments 0, 1), then the same 32 up channels
         const uint32_t up = (uint32_t)p.I * p.H;
         g.next_f.init(p.f + ((int64_t)next.expert * 2 * p.I + n0) * p.H,
                       [&](int r) { return (r & 32 ? up : 0u) + (uint32_t)((r / 64 * 32 + channel_of(r / 16 & 1, r & 15)) * p.H); });
-        g.next_row_scales(p.s_scales + (int64_t)next.row0 * blocks, blocks, next.rows, mt);
+        g.next_row_scales(p.s_scales + (int64_t)next.row0 * blocks, blocks, next.rows);
         g.copy_next_f_scales(p.f_scales + ((int64_t)next.expert * 2 * p.I + n0) / 128 * blocks, (uint32_t)(p.I / 128 * blocks) * 4, blocks,
                              round & 1 ? 0 : 1);
     }

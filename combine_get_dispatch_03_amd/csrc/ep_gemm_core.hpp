@@ -342,26 +342,22 @@ struct Fp8Tiles {
     typedef KcOperand<kBM> SOp;
     typedef KcOperand<kBN> FOp;
     static constexpr int kSBuffers = 2, kFBuffers = 3, kF = SOp::kBytes * kSBuffers;
-    static constexpr int kScaleRow = 512;                                        // a wave's row scales of a stage: up to 96 fp32
-    static constexpr int kRowScales = kF + FOp::kBytes * kFBuffers;              // [2][waves]
-    static constexpr int kFScales = kRowScales + 2 * kGemmWaves * kScaleRow;     // [2 tiles][2 rows of up to 256 fp32]
+    // [2][64 * waves] scales of a stage's rows.  Each is a cache line of its own in memory, so no two waves fetch the same.
+    static constexpr int kRowScales = kF + FOp::kBytes * kFBuffers, kRowScaleBytes = kGemmWaves * 256;
+    static constexpr int kFScales = kRowScales + 2 * kRowScaleBytes;             // [2 tiles][2 rows of up to 256 fp32]
     static constexpr int kLds = kFScales + 2 * 2048;
 
     char* smem;
     SOp s, next_s;
     FOp f, next_f;
     uint64_t scales, next_scales;              // of the tile's rows; 4 bytes further each stage
-    uint32_t scale_offset[2], next_scale_offset[2];
+    uint32_t scale_offset, next_scale_offset;
     int next_k, k, s_left, f_left, sbuf, fbuf, tile;
 
-    // Row scales of a tile whose waves own 16 * mt rows each.
-    __device__ __forceinline__ void next_row_scales(const float* at, int blocks, int rows, int mt) {
+    __device__ __forceinline__ void next_row_scales(const float* at, int blocks, int rows) {
         next_scales = uniform64((uint64_t)at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = (wave_id() >> 2) * mt * 16 + i * 64 + lane_id();
-            next_scale_offset[i] = i * 64 + lane_id() < mt * 16 && r < rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
-        }
+        const int r = (int)threadIdx.x;
+        next_scale_offset = r < rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
     }
     // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first.
     __device__ __forceinline__ void copy_next_f_scales(const float* at, uint32_t second, int blocks, int which) {
@@ -374,10 +370,7 @@ struct Fp8Tiles {
     __device__ __forceinline__ void copy_s(int buf) {
         const uint32_t lds0 = lds_address(smem);
         s.copy(lds0 + buf * SOp::kBytes, s_left);
-        const i32x4 res = resource(scales, s_left > 0 ? kNoElement : 0u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            copy4_to_lds(lds0 + kRowScales + (buf * kGemmWaves + wave_id()) * kScaleRow + i * 256, scale_offset[i], res);
+        copy4_to_lds(lds0 + kRowScales + buf * kRowScaleBytes + wave_id() * 256, scale_offset, resource(scales, s_left > 0 ? kNoElement : 0u));
         scales += 4;
         s_left -= 128;
     }
@@ -396,7 +389,7 @@ struct Fp8Tiles {
     }
     __device__ __forceinline__ void take_next_s() {
         s = next_s, scales = next_scales, s_left = next_k;
-        scale_offset[0] = next_scale_offset[0], scale_offset[1] = next_scale_offset[1];
+        scale_offset = next_scale_offset;
     }
     // The workgroup's first tile, which next_* describe (and its F scales are on their way to buffer 0).
     __device__ __forceinline__ void begin(int k_terms) {
@@ -433,7 +426,7 @@ struct Fp8Tiles {
         for (int st = 0; st < stages; ++st) {
             const char* ls = smem + sbuf * SOp::kBytes;
             const char* lf = smem + kF + fbuf * FOp::kBytes;
-            const float* rs = reinterpret_cast<const float*>(smem + kRowScales + (sbuf * kGemmWaves + wave) * kScaleRow) + (lane_id() & 15);
+            const float* rs = reinterpret_cast<const float*>(smem + kRowScales + sbuf * kRowScaleBytes) + wm * MT * 16 + (lane_id() & 15);
             if (st == stages - 1) take_next_s();
             if (st == stages - 2) f = next_f, f_left = next_k;
             sbuf ^= 1;
@@ -576,10 +569,10 @@ struct Bf16ByFp8Tiles {
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // a lane reads 16 e4m3: k 16g .. 16g + 15 of a row; its bf16 of S are the two chunks of the same k
+        // a lane reads the 8 e4m3 of k 8g .. 8g + 7, and 32 k on the next 8 (the chunk at ^ 32); its bf16 of S are as in Bf16Tiles
         const int r = lane_id() & 15, g = lane_id() >> 4;
-        const uint32_t s_at = (wm * MT * 16 + r) * 128 + (((2 * g) ^ (r & 7)) << 4);
-        const uint32_t f_at = (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | g) ^ (r >> 1)) << 4);
+        const uint32_t s_at = SOp::fragment(wm * MT * 16);
+        const uint32_t f_at = (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | (g >> 1)) ^ (r >> 1)) << 4) + (g & 1) * 8;
         const float* fs = reinterpret_cast<const float*>(smem + kFScales + tile * 2048) + (wn >> 1) * 256;
         meet();
         if (wm == 1) meet();
@@ -595,13 +588,16 @@ struct Bf16ByFp8Tiles {
                 copy_s(sbuf == 0 ? kSBuffers - 1 : sbuf - 1);
                 copy_f((fbuf + kFBuffers - 1) % kFBuffers);
                 bf16x8 sv[MT][2];
-                i32x4 fq[NT];
+                i32x2 fq[NT][2];
 #pragma unroll
-                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x4*>(lf + f_at + b * 1024);
+                for (int b = 0; b < NT; ++b) {
+                    fq[b][0] = *reinterpret_cast<const i32x2*>(lf + f_at + b * 1024);
+                    fq[b][1] = *reinterpret_cast<const i32x2*>(lf + (f_at ^ 32) + b * 1024);
+                }
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
                     sv[a][0] = read_kc(ls, s_at + a * 2048);
-                    sv[a][1] = read_kc(ls, (s_at ^ 16) + a * 2048);
+                    sv[a][1] = read_kc(ls, (s_at ^ 64) + a * 2048);
                 }
                 const float scale = q == 1 ? fs[st < k / 64 ? st / 2 : 0] : 0.0f;
                 wait_and_meet<kAhead>();
@@ -610,7 +606,7 @@ struct Bf16ByFp8Tiles {
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        const bf16x8 fv = widen_e4m3x8(h ? i32x2{fq[b][2], fq[b][3]} : i32x2{fq[b][0], fq[b][1]});
+                        const bf16x8 fv = widen_e4m3x8(fq[b][h]);
 #pragma unroll
                         for (int a = 0; a < MT; ++a)
                             part[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a][h], q + h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[a][b], 0, 0, 0);

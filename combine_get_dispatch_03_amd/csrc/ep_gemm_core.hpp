@@ -45,7 +45,10 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
            (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32;
 }
 
-__device__ __forceinline__ i32x4 resource(uint64_t base, uint32_t bytes) {
+// What happens once per tile stays behind a branch (the compiler would make it selects in every step of the loop).
+__device__ __forceinline__ void stay_branch() { asm volatile(""); }
+
+__device__ __forceinline__ i32x4 resource(uint64_t base, uint32_t bytes = kNoElement) {
     i32x4 r;
     r[0] = (int)(uint32_t)base;
     r[1] = (int)((uint32_t)(base >> 32) & 0xFFFFu);
@@ -108,13 +111,17 @@ struct KcOperand {
             offset[i] = o == kNoElement ? kNoElement : o + chunk() * 16;
         }
     }
-    // The next stage, with `left` bytes of each row to go (none or fewer: nothing is read, LDS is zeroed).
+    // The next stage, with `left` bytes of each row to go (none or fewer: nothing is read, LDS is zeroed).  What the last
+    // stage lacks is taken out of the offsets for good; the operand of another tile follows.
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
-        const i32x4 res = resource(base, left > 0 ? kNoElement : 0u);
-        const bool there = chunk() * 16 < left;
+        if (left < 128) {
+            stay_branch();
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i)
-            copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, there ? offset[i] : kNoElement, res);
+            for (int i = 0; i < kCopies; ++i) offset[i] = chunk() * 16 < left ? offset[i] : kNoElement;
+        }
+        const i32x4 res = resource(base);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
         base += 128;
     }
     // LDS offset of the lane's 16 bytes of the rows from row0, first half of the line; the second half is at ^ 64, the
@@ -154,12 +161,16 @@ struct KsOperand {
             offset[i] = c * 8 < cols ? (uint32_t)(row(i) * stride_bytes) + c * 16 : kNoElement;
         }
     }
-    // The next stage, with `left` k-rows to go.
+    // The next stage, with `left` k-rows to go (as KcOperand).
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
-        const i32x4 res = resource(base, left > 0 ? kNoElement : 0u);
+        if (left < 64) {
+            stay_branch();
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i)
-            copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, row(i) < left ? offset[i] : kNoElement, res);
+            for (int i = 0; i < kCopies; ++i) offset[i] = row(i) < left ? offset[i] : kNoElement;
+        }
+        const i32x4 res = resource(base);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
         base += step;
     }
     // LDS offset of the lane's part of 16 columns: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
@@ -283,8 +294,14 @@ struct Bf16Tiles {
         for (int st = 0; st < stages; ++st) {
             const char* ls = smem + sbuf * SOp::kBytes;
             const char* lf = smem + kF + fbuf * FOp::kBytes;
-            if (st == stages - 1) s = next_s, s_left = next_k;
-            if (st == stages - 2) f = next_f, f_left = next_k;
+            if (st == stages - 1) {
+                stay_branch();
+                s = next_s, s_left = next_k;
+            }
+            if (st == stages - 2) {
+                stay_branch();
+                f = next_f, f_left = next_k;
+            }
             sbuf ^= 1;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -346,6 +363,7 @@ struct Fp8Tiles {
     static constexpr int kRowScales = kF + FOp::kBytes * kFBuffers, kRowScaleBytes = kGemmWaves * 256;
     static constexpr int kFScales = kRowScales + 2 * kRowScaleBytes;             // [2 tiles][2 rows of up to 256 fp32]
     static constexpr int kLds = kFScales + 2 * 2048;
+    static constexpr int kAhead = FOp::kCopies + SOp::kCopies + 1;               // copies under way past the next stage
 
     char* smem;
     SOp s, next_s;
@@ -365,7 +383,7 @@ struct Fp8Tiles {
         uint64_t base = uniform64((uint64_t)at);
         asm volatile("s_nop 4" : "+s"(base));
         copy4_to_lds(lds_address(smem) + kFScales + which * 2048 + wave_id() * 256,
-                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base, kNoElement));
+                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base));
     }
     __device__ __forceinline__ void copy_s(int buf) {
         const uint32_t lds0 = lds_address(smem);
@@ -402,7 +420,8 @@ struct Fp8Tiles {
         copy_f(0);
         copy_s(0);
         copy_f(1);
-        wait_and_meet<FOp::kCopies>();
+        copy_s(1);
+        wait_and_meet<kAhead>();
     }
 
     template <int MT>
@@ -427,15 +446,19 @@ struct Fp8Tiles {
             const char* ls = smem + sbuf * SOp::kBytes;
             const char* lf = smem + kF + fbuf * FOp::kBytes;
             const float* rs = reinterpret_cast<const float*>(smem + kRowScales + sbuf * kRowScaleBytes) + wm * MT * 16 + (lane_id() & 15);
-            if (st == stages - 1) take_next_s();
-            if (st == stages - 2) f = next_f, f_left = next_k;
-            sbuf ^= 1;
+            if (st == stages - 2) {
+                stay_branch();
+                take_next_s();
+                f = next_f, f_left = next_k;
+            }
             i32x8 sv[MT];
             float row_scale[MT];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                if (half == 0) copy_s(sbuf);
-                else copy_f(fbuf == 0 ? 2 : fbuf - 1);
+                // stage st + 2: F where stage st - 1 was, S where stage st is, whose fragments every wave took in the
+                // first half step
+                if (half == 0) copy_f(fbuf == 0 ? 2 : fbuf - 1);
+                else copy_s(sbuf);
                 i32x8 fv[2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) fv[b] = read_line(lf, f_at + (half * 2 + b) * 2048);
@@ -447,7 +470,7 @@ struct Fp8Tiles {
                 }
                 const float f_scale = fs[half * 256 + (st < k / 128 ? st : 0)];
                 if (half == 0) wait_and_meet<63>();
-                else wait_and_meet<FOp::kCopies>();
+                else wait_and_meet<kAhead>();
                 __builtin_amdgcn_s_setprio(1);
                 f32x4 part[MT][2];
 #pragma unroll
@@ -466,6 +489,7 @@ struct Fp8Tiles {
                 __builtin_amdgcn_s_setprio(0);
                 meet();
             }
+            sbuf ^= 1;
             fbuf = fbuf == 2 ? 0 : fbuf + 1;
         }
         if (wm == 0) meet();
@@ -512,7 +536,7 @@ struct Bf16ByFp8Tiles {
         uint64_t base = uniform64((uint64_t)at);
         asm volatile("s_nop 4" : "+s"(base));
         copy4_to_lds(lds_address(smem) + kFScales + which * 2048 + wave_id() * 256,
-                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base, kNoElement));
+                     i < blocks ? (wave_id() >> 2) * second + i * 4 : kNoElement, resource(base));
     }
     __device__ __forceinline__ void copy_s(int buf) {
         s.copy(lds_address(smem) + buf * SOp::kBytes, s_left * 2);
@@ -582,8 +606,14 @@ struct Bf16ByFp8Tiles {
             for (int q = 0; q < 2; ++q) {
                 const char* ls = smem + sbuf * SOp::kBytes;
                 const char* lf = smem + kF + fbuf * kFBytes;
-                if (st + q == stages - 2) take_next_s();
-                if (st + q == stages - 3) take_next_f();
+                if (st + q == stages - 2) {
+                    stay_branch();
+                    take_next_s();
+                }
+                if (st + q == stages - 3) {
+                    stay_branch();
+                    take_next_f();
+                }
                 // the buffers of the stage before, which every wave had left before the last barrier
                 copy_s(sbuf == 0 ? kSBuffers - 1 : sbuf - 1);
                 copy_f((fbuf + kFBuffers - 1) % kFBuffers);

@@ -8,7 +8,7 @@
 //            decode batch has few tiles), and over a workgroup's four waves; each workgroup leaves its partial sums per
 //            token in the workspace.
 //   expand   the partial sums are added in order, scaled and rounded to bf16 in LDS; then B_a's rows times v, added to
-//            base and stored, 256 output channels per workgroup.  More workgroups copy base where a token has no adapter.
+//            base and stored.  More workgroups copy base where a token has no adapter.
 // Both are bound by memory (x and A; base, out and B): matrix instructions only keep the arithmetic out of the way.
 // The layout maps tokens to rows; a tile finds its tokens by going over that map once (4 bytes a token, from L2).
 #include "ep_expert_tiles.hpp"
@@ -20,8 +20,10 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64;
 constexpr int kChunkUnit = kWaves * 64;      // hidden channels of a workgroup: a multiple of this
-constexpr int kTargetBlocks = 512;           // two workgroups per CU
-constexpr int kOut = 256;                    // output channels of an expand workgroup
+constexpr int kTargetBlocks = 256;           // of shrink: more of them shorten it less than their partial sums lengthen expand
+constexpr int kExpandBlocks = 512;
+constexpr int kMaxChunks = 16;               // partial sums per token: two batches of loads in expand
+constexpr int kOut = 256;                    // output channels of an expand workgroup at a time
 
 struct Params {
     const int32_t* cnt;
@@ -39,15 +41,22 @@ struct Params {
     int chunk, chunks;    // hidden channels per chunk
 };
 
-// Tokens of a tile, in the layout's order, to LDS.  Ends with a barrier.
-__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int* tok) {
+// Tokens of a tile, in the layout's order, to LDS.  The thread's first four slots are loaded at the start of the kernel,
+// before the tile is known.  Ends with a barrier.
+__device__ __forceinline__ i32x4 first_slots(const Params& p) {
+    const int i = threadIdx.x;
+    return i < p.T / 4 ? reinterpret_cast<const i32x4*>(p.slot)[i] : i32x4{-1, -1, -1, -1};
+}
+__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, i32x4 first, int* tok) {
     const int quads = p.T / 4;
     const i32x4* q = reinterpret_cast<const i32x4*>(p.slot);
     auto put = [&](int s, int token) {
         const uint32_t m = (uint32_t)(s - t.row0);
         if (m < (uint32_t)t.rows) tok[m] = token;
     };
-    for (int i = threadIdx.x; i < quads; i += kThreads) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) put(first[j], threadIdx.x * 4 + j);
+    for (int i = threadIdx.x + kThreads; i < quads; i += kThreads) {
         const i32x4 s = q[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) put(s[j], i * 4 + j);
@@ -58,7 +67,7 @@ __device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, i
 }
 
 template <int NF, int MT>
-__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int chunk, const int* tok, float* sums) {
+__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int chunk, i32x4 slots, int* tok, float* sums) {
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
     const uint16_t* f[NF];
     bool f_there[NF];
@@ -67,6 +76,28 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ch
         f_there[b] = b * 16 + r < p.r;
         f[b] = p.a + ((int64_t)t.expert * p.r + (f_there[b] ? b * 16 + r : 0)) * p.H + g * 8;
     }
+    f32x4 acc[MT][NF];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < NF; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int end = min(p.H, (chunk + 1) * p.chunk);
+    struct Step {
+        i32x4 s[MT][2], f[NF][2];
+    };
+    const int first = chunk * p.chunk + wave * 64;
+    Step next;
+    auto load_f = [&](Step& v, int k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int b = 0; b < NF; ++b) {
+                v.f[b][j] = i32x4{0, 0, 0, 0};
+                if (k + j * 32 + g * 8 < end && f_there[b]) v.f[b][j] = *(const i32x4*)(f[b] + k + j * 32);
+            }
+    };
+    load_f(next, first);       // A's rows do not depend on the tokens
+    find_tokens(p, t, slots, tok);
     const uint16_t* s[MT];
     bool s_there[MT];
 #pragma unroll
@@ -74,36 +105,28 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ch
         s_there[a] = a * 16 + r < t.rows;
         s[a] = p.x + (int64_t)tok[s_there[a] ? a * 16 + r : 0] * p.H + g * 8;
     }
-    f32x4 acc[MT][NF];
+    auto load_s = [&](Step& v, int k) {
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int b = 0; b < NF; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int end = min(p.H, (chunk + 1) * p.chunk);
-    for (int k = chunk * p.chunk + wave * 64; k < end; k += kChunkUnit) {
-        i32x4 sv[MT][2], fv[NF][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const bool in = k + j * 32 + g * 8 < end;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
-                sv[a][j] = i32x4{0, 0, 0, 0};
-                if (in && s_there[a]) sv[a][j] = *(const i32x4*)(s[a] + k + j * 32);
+                v.s[a][j] = i32x4{0, 0, 0, 0};
+                if (k + j * 32 + g * 8 < end && s_there[a]) v.s[a][j] = *(const i32x4*)(s[a] + k + j * 32);
             }
-#pragma unroll
-            for (int b = 0; b < NF; ++b) {
-                fv[b][j] = i32x4{0, 0, 0, 0};
-                if (in && f_there[b]) fv[b][j] = *(const i32x4*)(f[b] + k + j * 32);
-            }
-        }
+    };
+    load_s(next, first);
+    for (int k = first; k < end; k += kChunkUnit) {
+        const Step cur = next;
+        load_f(next, k + kChunkUnit);     // past the end: nothing is read
+        load_s(next, k + kChunkUnit);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int b = 0; b < NF; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[b][j]),
-                                                                        __builtin_bit_cast(bf16x8, sv[a][j]), acc[a][b], 0, 0, 0);
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.f[b][j]),
+                                                                        __builtin_bit_cast(bf16x8, cur.s[a][j]), acc[a][b], 0, 0, 0);
     }
     constexpr int kPitch = NF * 16 + 4;
 #pragma unroll
@@ -127,94 +150,147 @@ template <int NF>
 __global__ __launch_bounds__(kThreads) void k_shrink(Params p) {
     __shared__ __align__(16) float sums[kWaves * 16 * (NF * 16 + 4)];
     __shared__ int tok[kRows];
+    const i32x4 slots = first_slots(p);
     const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     const int tile = blockIdx.x / p.chunks;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
-    find_tokens(p, t, tok);
     const int chunk = blockIdx.x % p.chunks;
-    if (t.rows <= 16) shrink<NF, 1>(p, t, chunk, tok, sums);
-    else if (t.rows <= 32) shrink<NF, 2>(p, t, chunk, tok, sums);
-    else shrink<NF, 4>(p, t, chunk, tok, sums);
+    if (t.rows <= 16) shrink<NF, 1>(p, t, chunk, slots, tok, sums);
+    else if (t.rows <= 32) shrink<NF, 2>(p, t, chunk, slots, tok, sums);
+    else shrink<NF, 4>(p, t, chunk, slots, tok, sums);
 }
 
-// NK: steps of 32 over the rank.
+// NK: steps of 32 over the rank.  A workgroup takes `steps` times 256 channels.
 template <int NK>
-__global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles) {
+__global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, int steps) {
     constexpr int kPitch = NK * 32 + 8;
     __shared__ __align__(16) uint16_t v[kRows * kPitch];
     __shared__ int tok[kRows];
-    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
-    const int cols = (p.N + kOut - 1) / kOut, tile = blockIdx.x / cols, n0 = blockIdx.x % cols * kOut;
+    const int cols = (p.N + kOut * steps - 1) / (kOut * steps), tile = blockIdx.x / cols, first = blockIdx.x % cols * kOut * steps;
+    const int last = min(p.N, first + kOut * steps);
     if (tile >= max_tiles) {      // tokens without an adapter: base as it is
-        const int t0 = (tile - max_tiles) * kRows;
-        for (int i = threadIdx.x; i < kRows * (kOut / 8); i += kThreads) {
-            const int t = t0 + i / (kOut / 8), n = n0 + i % (kOut / 8) * 8;
-            if (t >= p.T || n >= p.N || p.slot[t] >= 0) continue;
-            const int64_t at = (int64_t)t * p.N + n;
-            *reinterpret_cast<i32x4*>(p.out + at) = p.base ? *reinterpret_cast<const i32x4*>(p.base + at) : i32x4{0, 0, 0, 0};
+        const int t0 = (tile - max_tiles) * kRows, width = (last - first) / 8;
+        uint64_t bare = ballot(t0 + lane_id() < p.T && p.slot[min(t0 + lane_id(), p.T - 1)] < 0);
+        for (int i = 0; bare != 0; ++i, bare &= bare - 1) {
+            if (i % kWaves != wave_id()) continue;
+            const int64_t at = (int64_t)(t0 + __builtin_ctzll(bare)) * p.N + first;
+            for (int c = lane_id(); c < width; c += kWave)
+                *reinterpret_cast<i32x4*>(p.out + at + c * 8) = p.base ? *reinterpret_cast<const i32x4*>(p.base + at + c * 8) : i32x4{0, 0, 0, 0};
         }
         return;
     }
+    const i32x4 slots = first_slots(p);
+    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
-    // 64 channels per wave.  Fragment b takes channels 16 g + 4 b + i as its rows 4 g + i, so that a lane ends up with 16
+    // 64 channels per wave and step, dealt to the fragments' rows as channel_of() says: a lane ends up with twice 8
     // consecutive channels of a token.
-    const int nw = n0 + wave * 64;
-    i32x4 fv[4][NK];
+    struct Rows {
+        i32x4 v[4][NK];
+    };
+    auto load_b = [&](int nw) {
+        Rows f;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int n = nw + (r >> 2) * 16 + b * 4 + (r & 3);
+        for (int b = 0; b < 4; ++b) {
+            const int n = nw + channel_of(b, r);
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-            fv[b][j] = i32x4{0, 0, 0, 0};
-            if (n < p.N && j * 32 + g * 8 < p.r)
-                fv[b][j] = *(const i32x4*)(p.b + ((int64_t)t.expert * p.N + n) * p.r + j * 32 + g * 8);
-        }
-    }
-    find_tokens(p, t, tok);
-    const float scale = p.scales ? p.scales[t.expert] : 1.0f;
-    for (int i = threadIdx.x; i < kRows * NK * 8; i += kThreads) {
-        const int m = i / (NK * 8), k4 = i % (NK * 8) * 4;
-        f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
-        if (m < t.rows && k4 < p.r) {
-            const float* from = p.part + (int64_t)tok[m] * p.r + k4;
-            for (int c = 0; c < p.chunks; ++c) sum += *reinterpret_cast<const f32x4*>(from + (int64_t)c * p.T * p.r);
-        }
-        *reinterpret_cast<i32x2*>(v + m * kPitch + k4) =
-            i32x2{(int)pack_bf16x2(sum[0] * scale, sum[1] * scale), (int)pack_bf16x2(sum[2] * scale, sum[3] * scale)};
-    }
-    __syncthreads();
-    for (int a = 0; a * 16 < t.rows; ++a) {
-        const int m = a * 16 + r, n = nw + g * 16;
-        const bool in[2] = {m < t.rows && n < p.N, m < t.rows && n + 8 < p.N};
-        const int64_t at = in[0] ? (int64_t)tok[m] * p.N + n : 0;
-        i32x4 base[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            base[j] = i32x4{0, 0, 0, 0};
-            if (in[j] && p.base) base[j] = *reinterpret_cast<const i32x4*>(p.base + at + j * 8);
-        }
-        f32x4 acc[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-            const bf16x8 sv = *reinterpret_cast<const bf16x8*>(v + m * kPitch + j * 32 + g * 8);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[b][j]), sv, acc[b], 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            i32x4 o;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 d = acc[j * 2 + i / 2];
-                o[i] = (int)pack_bf16x2(bf16lo((uint32_t)base[j][i]) + d[i % 2 * 2], bf16hi((uint32_t)base[j][i]) + d[i % 2 * 2 + 1]);
+            for (int j = 0; j < NK; ++j) {
+                f.v[b][j] = i32x4{0, 0, 0, 0};
+                if (n < last && j * 32 + g * 8 < p.r)
+                    f.v[b][j] = *(const i32x4*)(p.b + ((int64_t)t.expert * p.N + n) * p.r + j * 32 + g * 8);
             }
-            if (in[j]) *reinterpret_cast<i32x4*>(p.out + at + j * 8) = o;
+        }
+        return f;
+    };
+    struct Base {
+        i32x4 v[kRows / 16][2];
+    };
+    auto load_base = [&](int nw) {
+        Base o;
+#pragma unroll
+        for (int a = 0; a < kRows / 16; ++a)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                o.v[a][j] = i32x4{0, 0, 0, 0};
+                const int m = a * 16 + r, n = nw + j * 32 + g * 8;
+                if (p.base && m < t.rows && n < last) o.v[a][j] = *reinterpret_cast<const i32x4*>(p.base + (int64_t)tok[m] * p.N + n);
+            }
+        return o;
+    };
+    int nw = first + wave * 64;
+    Rows next = load_b(nw);
+    find_tokens(p, t, slots, tok);
+    const float scale = p.scales ? p.scales[t.expert] : 1.0f;
+    // v of the tile's tokens, zeros past the last token and past the rank; the chunks in order, 16 loads in flight
+    constexpr int kAt = 2, kDeep = 8;
+    for (int i0 = threadIdx.x; i0 < ((t.rows + 15) & ~15) * NK * 8; i0 += kAt * kThreads) {
+        const float* from[kAt];
+        f32x4 sum[kAt];
+#pragma unroll
+        for (int q = 0; q < kAt; ++q) {
+            const int i = i0 + q * kThreads, m = i / (NK * 8), k4 = i % (NK * 8) * 4;
+            from[q] = m < t.rows && k4 < p.r ? p.part + (int64_t)tok[m] * p.r + k4 : nullptr;
+            sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        for (int c = 0; c < p.chunks; c += kDeep) {
+            f32x4 part[kDeep][kAt];
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+                for (int q = 0; q < kAt; ++q) {
+                    part[u][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (from[q] && c + u < p.chunks) part[u][q] = *reinterpret_cast<const f32x4*>(from[q] + (int64_t)(c + u) * p.T * p.r);
+                }
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+                for (int q = 0; q < kAt; ++q) sum[q] += part[u][q];
+        }
+#pragma unroll
+        for (int q = 0; q < kAt; ++q) {
+            const int i = i0 + q * kThreads, m = i / (NK * 8), k4 = i % (NK * 8) * 4;
+            if (m < kRows)
+                *reinterpret_cast<i32x2*>(v + m * kPitch + k4) = i32x2{(int)pack_bf16x2(sum[q][0] * scale, sum[q][1] * scale),
+                                                                       (int)pack_bf16x2(sum[q][2] * scale, sum[q][3] * scale)};
+        }
+    }
+    Base next_base = load_base(nw);
+    __syncthreads();
+    for (; nw < last; nw += kOut) {
+        const Rows cur = next;
+        const Base base = next_base;
+        if (nw + kOut < last) {
+            next = load_b(nw + kOut);
+            next_base = load_base(nw + kOut);
+        }
+#pragma unroll
+        for (int a = 0; a < kRows / 16; ++a) {
+            if (a * 16 >= t.rows) break;
+            const int m = a * 16 + r, n = nw + g * 8;
+            f32x4 acc[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                const bf16x8 sv = *reinterpret_cast<const bf16x8*>(v + m * kPitch + j * 32 + g * 8);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.v[b][j]), sv, acc[b], 0, 0, 0);
+            }
+            const int64_t at = m < t.rows ? (int64_t)tok[m] * p.N + n : 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                i32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 d = acc[j * 2 + i / 2];
+                    const uint32_t two = (uint32_t)base.v[a][j][i];
+                    o[i] = (int)pack_bf16x2(bf16lo(two) + d[i % 2 * 2], bf16hi(two) + d[i % 2 * 2 + 1]);
+                }
+                if (m < t.rows && n + j * 32 < last) *reinterpret_cast<i32x4*>(p.out + at + j * 32) = o;
+            }
         }
     }
 }
@@ -231,6 +307,7 @@ int chunk_of(int T, int El, int H) {
     int chunks = kTargetBlocks / tiles;
     if (chunks < 1) chunks = 1;
     if (chunks > units) chunks = units;
+    if (chunks > kMaxChunks) chunks = kMaxChunks;
     return (units + chunks - 1) / chunks * kChunkUnit;
 }
 
@@ -257,10 +334,12 @@ hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t str
     if (e != hipSuccess) return e;
     // in place, the tokens without an adapter already hold their base
     const int bare = a.out == a.base ? 0 : (h.T + kRows - 1) / kRows;
-    const dim3 expand_grid((unsigned)((int64_t)(tiles + bare) * ((a.n_out + kOut - 1) / kOut)));
-    if (a.rank <= 32) hipLaunchKernelGGL(k_expand<1>, expand_grid, block, 0, stream, p, tiles);
-    else if (a.rank <= 64) hipLaunchKernelGGL(k_expand<2>, expand_grid, block, 0, stream, p, tiles);
-    else hipLaunchKernelGGL(k_expand<4>, expand_grid, block, 0, stream, p, tiles);
+    // as many channels per workgroup as leave the chip full: a workgroup adds up v before it starts
+    const int columns = (a.n_out + kOut - 1) / kOut, want = (kExpandBlocks + tiles - 1) / tiles, steps = columns > want ? (columns + want - 1) / want : 1;
+    const dim3 expand_grid((unsigned)((int64_t)(tiles + bare) * ((columns + steps - 1) / steps)));
+    if (a.rank <= 32) hipLaunchKernelGGL(k_expand<1>, expand_grid, block, 0, stream, p, tiles, steps);
+    else if (a.rank <= 64) hipLaunchKernelGGL(k_expand<2>, expand_grid, block, 0, stream, p, tiles, steps);
+    else hipLaunchKernelGGL(k_expand<4>, expand_grid, block, 0, stream, p, tiles, steps);
     return hipGetLastError();
 }
 

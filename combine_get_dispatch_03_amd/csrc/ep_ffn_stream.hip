@@ -56,9 +56,9 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
     bool f_there[kNF];
 #pragma unroll
     for (int b = 0; b < kNF; ++b) {
-        const int c = UP ? n0 + b % 2 * 16 + r : n0 + b * 16 + r;
+        const int c = UP ? n0 + b % (kNF / 2) * 16 + r : n0 + b * 16 + r;
         f_there[b] = c < p.N;
-        const int64_t row = (int64_t)t.expert * (UP ? 2 : 1) * p.N + (UP && b >= 2 ? p.N : 0) + (f_there[b] ? c : n0);
+        const int64_t row = (int64_t)t.expert * (UP ? 2 : 1) * p.N + (UP && b >= kNF / 2 ? p.N : 0) + (f_there[b] ? c : n0);
         f[b] = (const char*)p.f + row * f_bytes + g * 16;
     }
     const char* s[MT];
@@ -136,7 +136,7 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
                 for (int b = 0; b < kNF; ++b) {
                     const i32x8 fb = __builtin_shufflevector(cur.v[b][0], cur.v[b][1], 0, 1, 2, 3, 4, 5, 6, 7);
                     const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, sa, zero, 0, 0, 0, 0, 0, 0);
-                    const float scale = s_scale[a] * f_scale[b / 2];
+                    const float scale = s_scale[a] * f_scale[b / (kNF / 2)];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(part[i], scale, acc[a][b][i]);
                 }
@@ -172,19 +172,18 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
         for (int b = 0; b < kNF; ++b)
             *reinterpret_cast<f32x4*>(sums + (wave * 16 + r) * kSumPitch + b * 16 + g * 4) = acc[a][b];
         __syncthreads();
-        const int m = threadIdx.x / 16, n4 = threadIdx.x % 16 * 4;      // 16 rows x 64 channels, 4 per thread
-        f32x4 v = zero;
-        if (!UP || n4 < 32) {
+        constexpr int kOut = UP ? kCols / 2 : kCols;      // 16 rows x kOut channels, 4 per thread
+        for (int i = threadIdx.x; i < 16 * kOut / 4; i += kThreads) {
+            const int m = i / (kOut / 4), n4 = i % (kOut / 4) * 4;
+            if (a * 16 + m >= t.rows || n0 + n4 >= p.N) continue;
+            const int64_t row = row0 + a * 16 + m;
+            f32x4 v = zero;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kSumPitch + n4);
-        }
-        const int64_t row = row0 + a * 16 + m;
-        const bool there = a * 16 + m < t.rows && n0 + n4 < p.N;
-        if constexpr (UP) {
-            if (n4 < 32 && there) {
+            if constexpr (UP) {
                 f32x4 u = zero, h;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) u += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kSumPitch + 32 + n4);
+                for (int w = 0; w < kWaves; ++w) u += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kSumPitch + kOut + n4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = v[i] * sigmoid(v[i]) * u[i];
                 if (p.pre) {
@@ -192,9 +191,9 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
                     *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.N + p.N + n0 + n4) = u;
                 }
                 store4(p.out + row * p.N + n0 + n4, h[0], h[1], h[2], h[3]);
+            } else {
+                store4(p.out + row * p.N + n0 + n4, v[0], v[1], v[2], v[3]);
             }
-        } else if (there) {
-            store4(p.out + row * p.N + n0 + n4, v[0], v[1], v[2], v[3]);
         }
     }
 }

@@ -9,12 +9,30 @@ namespace ep {
 // Rows an expert gets on average.  The host knows sizes only, not the routing: of T * K entries, an expert's share.
 inline double mean_rows(const Handle& h) { return (double)h.T * h.K / h.E; }
 
-// Weights streamed past the rows rather than tiles of both through LDS.
-inline bool few_rows(const Handle& h) { return mean_rows(h) < 48; }
+// Local experts that get a row, at most.
+inline int busy_experts(const Handle& h) { return (int64_t)h.T * h.K < h.El ? h.T * h.K : h.El; }
 
-hipError_t launch_ffn_tile(const Handle& h, const FfnArgs& a, hipStream_t stream);       // bf16
-hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream);   // e4m3
-hipError_t launch_ffn_stream(const Handle& h, const FfnArgs& a, hipStream_t stream);     // either, few rows per expert
+// Weights streamed past the rows (ep_ffn_stream.hip) rather than tiles of both through LDS: where an expert has so few rows
+// that its weights' bytes decide, or where the tiles would leave most CUs idle.  `cols`: tiles side by side in the
+// product's output.  Measured, 32 experts of 7168 x 2048, us streamed / tiled at so many rows per expert:
+//              gate, up, bf16   down, bf16    gate, up, e4m3   down, e4m3
+//    2 rows    297 / 303        171 / 209     156 / 154         88 / 104
+//    8         313 / 318        178 / 217     166 / 164         98 / 107
+//   16         327 / 320        180 / 219     185 / 167        111 / 109
+//   32         367 / 323        204 / 224     226 / 169        133 / 120
+//   64         590 / 333        305 / 233     373 / 182        234 / 140
+// (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
+inline bool few_rows(const Handle& h, double limit, int cols) {
+    const double rows = mean_rows(h);
+    return rows < limit || (rows < 64 && (int64_t)busy_experts(h) * cols < 192);
+}
+
+hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream);           // bf16
+hipError_t launch_tile_down(const Handle& h, const FfnArgs& a, hipStream_t stream);
+hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream);       // e4m3
+hipError_t launch_tile_fp8_down(const Handle& h, const FfnArgs& a, hipStream_t stream);
+hipError_t launch_stream_up(const Handle& h, const FfnArgs& a, hipStream_t stream);         // either
+hipError_t launch_stream_down(const Handle& h, const FfnArgs& a, hipStream_t stream);
 
 // The order in which workgroups take the tiles of a rows x cols grid.  Consecutive tiles run down kGroup rows, then on to
 // the next column; 32 of them (4 x 8) are what the 32 CUs of an XCD work on at a time, few rows and few weights from its

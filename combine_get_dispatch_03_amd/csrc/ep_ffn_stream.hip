@@ -1,7 +1,7 @@
 // ep_ffn_stream.hip -- the expert block's forward pass for few rows per expert (decode): bound by reading the weights.
 //
-// A workgroup takes up to 64 rows of an expert and 64 rows of its weights (32 gate and the same 32 up channels, or 64
-// output channels).  Its four waves split k: each streams its part of the 64 weight rows from memory straight into the
+// A workgroup takes up to 64 rows of an expert and 64 (or 32) rows of its weights: half gate and the same up channels, or
+// output channels.  Its four waves split k: each streams its part of the weight rows from memory straight into the
 // fragments of the matrix instruction, the next step's loads in flight while the current one is multiplied; nothing is
 // shared, so no barrier stands in the loop.  The rows' fragments come from the caches.  At the end the waves' sums meet
 // in LDS.
@@ -12,8 +12,7 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64, kCols = 64, kNF = kCols / 16;
-constexpr int kSumPitch = kCols + 4;
+constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64;
 
 struct Params {
     const int32_t* cnt;
@@ -31,8 +30,9 @@ struct Params {
 enum Format { kBf16, kFp8 };
 
 // 128 bytes of each of a wave's weight rows: the lane's two 16-byte pieces per fragment.
+template <int NF>
 struct Weights {
-    i32x4 v[kNF][2];
+    i32x4 v[NF][2];
 };
 template <Format F, bool UP>
 struct RowsOf;
@@ -43,8 +43,9 @@ struct RowsOf<kFp8, true> { static constexpr int kPieces = 2; };    // 128 k of 
 template <>
 struct RowsOf<kFp8, false> { static constexpr int kPieces = 4; };   // 128 k of bf16 beside e4m3 weights
 
-template <Format F, bool UP, int MT>
+template <Format F, bool UP, int COLS, int MT>
 __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n0, char* smem) {
+    constexpr int kCols = COLS, kNF = kCols / 16, kSumPitch = kCols + 4;
     const int64_t row0 = t.row0;
     constexpr int kPieces = RowsOf<F, UP>::kPieces;
     constexpr int kWide = F == kFp8 ? 1 : 2;                   // bytes of a weight
@@ -71,7 +72,7 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
     }
 
     auto load_f = [&](int st) {
-        Weights w;
+        Weights<kNF> w;
         const int at = st * 128;
 #pragma unroll
         for (int b = 0; b < kNF; ++b)
@@ -90,7 +91,7 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
         for (int b = 0; b < kNF; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const f32x4 zero{0.0f, 0.0f, 0.0f, 0.0f};
 
-    Weights next = load_f(wave < steps ? wave : 0);
+    Weights<kNF> next = load_f(wave < steps ? wave : 0);
     for (int st = wave; st < steps; st += kWaves) {
         // the rows' pieces of this step, then the weights of the next: the wait for the first leaves the second in flight
         i32x4 sv[MT][kPieces];
@@ -117,7 +118,7 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
                 f_scale[0] = p.f_scales[((int64_t)t.expert * p.N + n0) / 128 * blocks + st];
             }
         }
-        const Weights cur = next;
+        const Weights<kNF> cur = next;
         next = load_f(st + kWaves < steps ? st + kWaves : st);
         if constexpr (F == kBf16) {
 #pragma unroll
@@ -198,41 +199,54 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
     }
 }
 
-template <Format F, bool UP>
+template <Format F, bool UP, int COLS>
 __global__ __launch_bounds__(kThreads) void k_stream(Params p) {
-    __shared__ __align__(16) char smem[kWaves * 16 * kSumPitch * 4];
+    __shared__ __align__(16) char smem[kWaves * 16 * (COLS + 4) * 4];
     const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
-    constexpr int kChannels = UP ? kCols / 2 : kCols;
+    constexpr int kChannels = UP ? COLS / 2 : COLS;
     const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int n0 = blockIdx.x % cols * kChannels;
     switch ((t.rows + 15) / 16) {
-        case 1: product<F, UP, 1>(p, t, n0, smem); break;
-        case 2: product<F, UP, 2>(p, t, n0, smem); break;
-        case 3: product<F, UP, 3>(p, t, n0, smem); break;
-        default: product<F, UP, 4>(p, t, n0, smem); break;
+        case 1: product<F, UP, COLS, 1>(p, t, n0, smem); break;
+        case 2: product<F, UP, COLS, 2>(p, t, n0, smem); break;
+        case 3: product<F, UP, COLS, 3>(p, t, n0, smem); break;
+        default: product<F, UP, COLS, 4>(p, t, n0, smem); break;
     }
 }
 
-template <Format F, bool UP>
+template <Format F, bool UP, int COLS>
 hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
-    constexpr int kChannels = UP ? kCols / 2 : kCols;
+    constexpr int kChannels = UP ? COLS / 2 : COLS;
     // tiles that any routing can give: no more than entries, and every expert may end in a short one
     const int64_t entries = (int64_t)h.T * h.K, tiles = entries / kRows + h.El;
-    hipLaunchKernelGGL((k_stream<F, UP>), dim3((unsigned)((tiles < entries ? tiles : entries) * ((p.N + kChannels - 1) / kChannels))),
+    hipLaunchKernelGGL((k_stream<F, UP, COLS>), dim3((unsigned)((tiles < entries ? tiles : entries) * ((p.N + kChannels - 1) / kChannels))),
                        dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
+// 64 weight rows per workgroup, or 32 (bf16) where that leaves the chip short of workgroups or, in the down projection, a
+// few rows per expert make more and smaller ones the better stream.  Measured, 32 experts of 7168 x 2048: down projection
+// at 2 rows per expert 171 us with 64, 160 with 32; at 16 rows 180 and 196; gate and up 297 and 295, 327 and 388.
+// 8 experts of 256 x 512, 32 rows each: 7.0 and 6.0 us, down 7.2 and 6.4.
+bool narrow(const Handle& h, int N, bool up) {
+    const int64_t blocks = (int64_t)busy_experts(h) * ((N + (up ? 31 : 63)) / (up ? 32 : 64));
+    return blocks < 512 || (!up && mean_rows(h) <= 8);
+}
+
 }  // namespace
 
-hipError_t launch_ffn_stream(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden};
-    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter};
-    const hipError_t e = a.fp8 ? stream_launch<kFp8, true>(h, up, stream) : stream_launch<kBf16, true>(h, up, stream);
-    if (e != hipSuccess) return e;
-    return a.fp8 ? stream_launch<kFp8, false>(h, down, stream) : stream_launch<kBf16, false>(h, down, stream);
+hipError_t launch_stream_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden};
+    if (a.fp8) return stream_launch<kFp8, true, 64>(h, p, stream);
+    return narrow(h, a.inter, true) ? stream_launch<kBf16, true, 32>(h, p, stream) : stream_launch<kBf16, true, 64>(h, p, stream);
+}
+
+hipError_t launch_stream_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter};
+    if (a.fp8) return stream_launch<kFp8, false, 64>(h, p, stream);
+    return narrow(h, a.hidden, false) ? stream_launch<kBf16, false, 32>(h, p, stream) : stream_launch<kBf16, false, 64>(h, p, stream);
 }
 
 }  // namespace ep

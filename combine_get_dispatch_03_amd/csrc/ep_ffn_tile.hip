@@ -234,12 +234,14 @@ hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f,
 
 }  // namespace
 
-hipError_t launch_ffn_tile(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const Params up{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
-    const hipError_t e = rows_launch<kGateUp>(h, up, stream);
-    if (e != hipSuccess) return e;
-    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, (const uint16_t*)a.w2, (uint16_t*)a.y, nullptr, nullptr, a.hidden, a.inter};
-    return rows_launch<kDown>(h, down, stream);
+hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
+    return rows_launch<kGateUp>(h, p, stream);
+}
+
+hipError_t launch_tile_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, (const uint16_t*)a.w2, (uint16_t*)a.y, nullptr, nullptr, a.hidden, a.inter};
+    return rows_launch<kDown>(h, p, stream);
 }
 
 hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a, hipStream_t stream) {

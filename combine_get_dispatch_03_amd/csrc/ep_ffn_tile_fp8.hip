@@ -158,17 +158,22 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
 
 }  // namespace
 
-hipError_t launch_ffn_tile_fp8(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const int64_t entries = (int64_t)h.T * h.K, up_rows = entries / Fp8Tiles::kBM + h.El, down_rows = entries / Bf16ByFp8Tiles::kBM + h.El;
-    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tiles::kLds);
-    if (e == hipSuccess) e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tiles::kLds);
+hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tiles::kLds);
     if (e != hipSuccess) return e;
-    const Params up{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_gate_up, dim3(walking_blocks(up_rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tiles::kLds, stream, up);
-    e = hipGetLastError();
+    // row tiles that any routing can give: every expert may end in a short one
+    const int64_t rows = (int64_t)h.T * h.K / Fp8Tiles::kBM + h.El;
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
+    hipLaunchKernelGGL(k_gate_up, dim3(walking_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tiles::kLds, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_tile_fp8_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_down), Bf16ByFp8Tiles::kLds);
     if (e != hipSuccess) return e;
-    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_down, dim3(walking_blocks(down_rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tiles::kLds, stream, down);
+    const int64_t rows = (int64_t)h.T * h.K / Bf16ByFp8Tiles::kBM + h.El;
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, (const uint8_t*)a.w2, a.w2_scales, (uint16_t*)a.y, a.hidden, a.inter};
+    hipLaunchKernelGGL(k_down, dim3(walking_blocks(rows * ((a.hidden + kBN - 1) / kBN))), dim3(kGemmThreads), Bf16ByFp8Tiles::kLds, stream, p);
     return hipGetLastError();
 }
 

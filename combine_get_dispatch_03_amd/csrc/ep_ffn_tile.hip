@@ -82,9 +82,9 @@ __device__ __forceinline__ void store_rows(const Params& p, const f32x4 (&acc)[M
     }
 }
 
-template <Product P>
+template <Product P, bool ONCE>
 struct RowsKernel {
-    typedef Bf16Tiles<false, P == kDownGrad || P == kInGrad> Tiles;
+    typedef Bf16Tiles<false, P == kDownGrad || P == kInGrad, ONCE> Tiles;
     static constexpr int kCols = P == kGateUp ? kBN / 2 : kBN;     // channels of N per tile
 
     const Params& p;
@@ -138,10 +138,10 @@ struct RowsKernel {
 };
 
 // A workgroup stays on its CU and walks through its tiles.  Waves take as many 16-row steps as the tile is high.
-template <Product P>
+template <Product P, bool ONCE>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_rows(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    RowsKernel<P> k(p);
+    RowsKernel<P, ONCE> k(p);
     k.look_ahead();
     if (k.next.rows == 0) return;
     k.g.s = k.g.next_s, k.g.f = k.g.next_f;
@@ -210,15 +210,15 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt,
     g.end();
 }
 
-template <Product P>
+template <Product P, bool ONCE = false>
 hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
     typedef Bf16Tiles<false, P == kDownGrad || P == kInGrad> Tile;
     const int N = P == kGateUp || P == kDownGrad ? p.I : p.H, cols = P == kGateUp ? kBN / 2 : kBN;
     // row tiles that any routing can give: every expert may end in a short one
     const int64_t rows = (int64_t)h.T * h.K / Tile::kBM + h.El;
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows<P>), Tile::kLds);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_rows<P, ONCE>), Tile::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_rows<P>), dim3(walking_blocks(rows * ((N + cols - 1) / cols))), dim3(kGemmThreads), Tile::kLds, stream, p);
+    hipLaunchKernelGGL((k_rows<P, ONCE>), dim3(walking_blocks(rows * ((N + cols - 1) / cols))), dim3(kGemmThreads), Tile::kLds, stream, p);
     return hipGetLastError();
 }
 
@@ -236,7 +236,9 @@ hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f,
 
 hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
-    return rows_launch<kGateUp>(h, p, stream);
+    // Up to so many rows an expert is one row tile and its weights pass by once.  32 experts of 7168 x 2048, us with ONCE and
+    // without: 16 rows 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373; 900 rows (four row tiles) 1409 and 1262.
+    return mean_rows(h) <= 128 ? rows_launch<kGateUp, true>(h, p, stream) : rows_launch<kGateUp>(h, p, stream);
 }
 
 hipError_t launch_tile_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

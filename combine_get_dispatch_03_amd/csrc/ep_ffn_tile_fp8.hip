@@ -21,10 +21,12 @@ struct Params {
     int H, I;
 };
 
+template <bool ONCE>
 struct GateUp {
+    typedef Fp8Tiles<ONCE> Tiles;
     const Params& p;
-    RowTiles<Fp8Tiles::kBM, 0> rows;      // the registers are needed: find() reads the counts again
-    Fp8Tiles g;
+    RowTiles<Tiles::kBM, 0> rows;      // the registers are needed: find() reads the counts again
+    Tiles g;
     int round = 0;
     RowTile now, next;
     int now_n0, next_n0;
@@ -52,7 +54,7 @@ struct GateUp {
     template <int MT>
     __device__ __forceinline__ void tile() {
         f32x4 acc[MT][4];
-        g.run<MT>(acc);
+        g.template run<MT>(acc);
         const int m_at = (wave_id() >> 2) * MT * 16 + (lane_id() & 15), n = now_n0 + (wave_id() & 3) * 32 + (lane_id() >> 4) * 8;
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
@@ -69,9 +71,10 @@ struct GateUp {
 };
 
 // A workgroup stays on its CU and walks through its tiles.  Waves take as many 16-row steps as the tile is high.
+template <bool ONCE>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
     extern __shared__ __align__(1024) char smem[];
-    GateUp k(p);
+    GateUp<ONCE> k(p);
     k.g.smem = smem;
     k.look_ahead();
     if (k.next.rows == 0) return;
@@ -80,12 +83,12 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_gate_up(Params p) {
         k.now = k.next, k.now_n0 = k.next_n0;
         k.look_ahead();
         switch ((k.now.rows + 31) / 32) {
-            case 1: k.tile<1>(); break;
-            case 2: k.tile<2>(); break;
-            case 3: k.tile<3>(); break;
-            case 4: k.tile<4>(); break;
-            case 5: k.tile<5>(); break;
-            default: k.tile<6>(); break;
+            case 1: k.template tile<1>(); break;
+            case 2: k.template tile<2>(); break;
+            case 3: k.template tile<3>(); break;
+            case 4: k.template tile<4>(); break;
+            case 5: k.template tile<5>(); break;
+            default: k.template tile<6>(); break;
         }
     } while (k.next.rows > 0);
     k.g.end();
@@ -158,14 +161,22 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_down(Params p) {
 
 }  // namespace
 
-hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up), Fp8Tiles::kLds);
+template <bool ONCE>
+hipError_t up_launch(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    typedef Fp8Tiles<ONCE> Tiles;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_gate_up<ONCE>), Tiles::kLds);
     if (e != hipSuccess) return e;
     // row tiles that any routing can give: every expert may end in a short one
-    const int64_t rows = (int64_t)h.T * h.K / Fp8Tiles::kBM + h.El;
+    const int64_t rows = (int64_t)h.T * h.K / Tiles::kBM + h.El;
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, (const uint8_t*)a.w13, a.w13_scales, a.h, a.hidden, a.inter};
-    hipLaunchKernelGGL(k_gate_up, dim3(walking_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Fp8Tiles::kLds, stream, p);
+    hipLaunchKernelGGL(k_gate_up<ONCE>, dim3(walking_blocks(rows * (a.inter / 128))), dim3(kGemmThreads), Tiles::kLds, stream, p);
     return hipGetLastError();
+}
+
+// ONCE: where weights pass by once and decide the time.  256 experts of 7168 x 2048, us with it and without: 4 rows each
+// 1103 and 1209, 128 rows 1681 and 1582; 32 experts, 16 rows 158 and 167, 64 rows 183 and 184.
+hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
+    return mean_rows(h) <= 64 ? up_launch<true>(h, a, stream) : up_launch<false>(h, a, stream);
 }
 
 hipError_t launch_tile_fp8_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

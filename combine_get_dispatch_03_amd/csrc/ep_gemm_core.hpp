@@ -57,10 +57,15 @@ __device__ __forceinline__ i32x4 resource(uint64_t base, uint32_t bytes = kNoEle
     return r;
 }
 
-// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16 (m0 holds nothing else on this target).  Counted by vmcnt; the compiler does not see
-// it, so whoever reads the LDS waits for it (wait_stage).
+// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16 (m0 holds nothing else on this target).  Counted
+// by vmcnt; the compiler does not see it, so whoever reads the LDS waits for it.  ONCE: marked non-temporal, for whole
+// lines that no other workgroup reads.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(offset), "s"(res));
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
 }
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
@@ -113,6 +118,7 @@ struct KcOperand {
     }
     // The next stage, with `left` bytes of each row to go (none or fewer: nothing is read, LDS is zeroed).  What the last
     // stage lacks is taken out of the offsets for good; the operand of another tile follows.
+    template <bool ONCE = false>
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
         if (left < 128) {
             stay_branch();
@@ -121,7 +127,7 @@ struct KcOperand {
         }
         const i32x4 res = resource(base);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
         base += 128;
     }
     // LDS offset of the lane's 16 bytes of the rows from row0, first half of the line; the second half is at ^ 64, the
@@ -162,6 +168,7 @@ struct KsOperand {
         }
     }
     // The next stage, with `left` k-rows to go (as KcOperand).
+    template <bool ONCE = false>
     __device__ __forceinline__ void copy(uint32_t lds, int left) {
         if (left < 64) {
             stay_branch();
@@ -170,7 +177,7 @@ struct KsOperand {
         }
         const i32x4 res = resource(base);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) copy16_to_lds(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
         base += step;
     }
     // LDS offset of the lane's part of 16 columns: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
@@ -221,7 +228,9 @@ struct OperandOf<ROWS, true> { typedef KsOperand<ROWS> type; };
 //
 // The stages of a workgroup's tiles form one stream: the last two stages of a tile copy the first of the next one
 // (next_s, next_f, next_k), which then starts on data that has landed, while its predecessor is being stored.
-template <bool SKS, bool FKS>
+//
+// ONCE: F is read by this tile only (see copy16_to_lds).
+template <bool SKS, bool FKS, bool ONCE = false>
 struct Bf16Tiles {
     static constexpr int kBM = 256, NT = 4;
     typedef typename OperandOf<kBM, SKS>::type SOp;
@@ -242,7 +251,7 @@ struct Bf16Tiles {
         s_left -= 64;
     }
     __device__ __forceinline__ void copy_f(int buf) {
-        f.copy(lds_address(smem) + kF + buf * FOp::kBytes, f_left * kFUnit);
+        f.template copy<ONCE>(lds_address(smem) + kF + buf * FOp::kBytes, f_left * kFUnit);
         f_left -= 64;
     }
     // s, f and k_terms are the workgroup's first tile.
@@ -354,6 +363,7 @@ __device__ __forceinline__ i32x8 read_line(const char* lds, uint32_t at) {
 // take the product of the two scales on their way into acc: products and scales are exact, sums are fp32.
 //
 // 128 k per stage, in two half steps of two fragments of F each; S's fragments stay for both.
+template <bool ONCE>
 struct Fp8Tiles {
     static constexpr int kBM = 192, NT = 4;
     typedef KcOperand<kBM> SOp;
@@ -393,7 +403,7 @@ struct Fp8Tiles {
         s_left -= 128;
     }
     __device__ __forceinline__ void copy_f(int buf) {
-        f.copy(lds_address(smem) + kF + buf * FOp::kBytes, f_left);
+        f.template copy<ONCE>(lds_address(smem) + kF + buf * FOp::kBytes, f_left);
         f_left -= 128;
     }
     __device__ __forceinline__ void settle() {

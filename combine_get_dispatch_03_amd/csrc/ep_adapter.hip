@@ -22,7 +22,7 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64;
 constexpr int kChunkUnit = kWaves * 64;      // hidden channels of a workgroup: a multiple of this
 constexpr int kTargetBlocks = 256;           // of shrink: more of them shorten it less than their partial sums lengthen expand
 constexpr int kExpandBlocks = 512;
-constexpr int kMaxChunks = 16;               // partial sums per token: two batches of loads in expand
+constexpr int kMaxChunks = 32;               // partial sums per token
 constexpr int kOut = 256;                    // output channels of an expand workgroup at a time
 
 struct Params {
@@ -166,6 +166,7 @@ template <int NK>
 __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, int steps) {
     constexpr int kPitch = NK * 32 + 8;
     __shared__ __align__(16) uint16_t v[kRows * kPitch];
+    __shared__ __align__(16) f32x4 shared_sums[kThreads];
     __shared__ int tok[kRows];
     const int cols = (p.N + kOut * steps - 1) / (kOut * steps), tile = blockIdx.x / cols, first = blockIdx.x % cols * kOut * steps;
     const int last = min(p.N, first + kOut * steps);
@@ -223,37 +224,80 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
     Rows next = load_b(nw);
     find_tokens(p, t, slots, tok);
     const float scale = p.scales ? p.scales[t.expert] : 1.0f;
-    // v of the tile's tokens, zeros past the last token and past the rank; the chunks in order, 16 loads in flight
-    constexpr int kAt = 2, kDeep = 8;
-    for (int i0 = threadIdx.x; i0 < ((t.rows + 15) & ~15) * NK * 8; i0 += kAt * kThreads) {
-        const float* from[kAt];
-        f32x4 sum[kAt];
+    // v of the tile's tokens, zeros past the last token and past the rank, 4 ranks per item; the chunks are added in a fixed
+    // order.  A few tokens: the workgroup's threads share an item's chunks and meet in LDS.  Many: two items a thread,
+    // eight chunks of each in flight.
+    const int items = ((t.rows + 15) & ~15) * NK * 8;
+    auto item = [&](int i, const float** from) {
+        const int m = i / (NK * 8), k4 = i % (NK * 8) * 4;
+        *from = m < t.rows && k4 < p.r ? p.part + (int64_t)tok[m] * p.r + k4 : nullptr;
+        return m * kPitch + k4;
+    };
+    auto put = [&](int at, f32x4 sum) {
+        *reinterpret_cast<i32x2*>(v + at) = i32x2{(int)pack_bf16x2(sum[0] * scale, sum[1] * scale), (int)pack_bf16x2(sum[2] * scale, sum[3] * scale)};
+    };
+    const int64_t stride = (int64_t)p.T * p.r;
+    if (t.rows <= 16) {
+        // only rows that exist are shared out; the others' v is zero
+        constexpr int kPerRow = NK * 8;
+        int rows = 1;
+        while (rows < t.rows) rows *= 2;
+        const int live = rows * kPerRow, shares = live < kThreads ? kThreads / live : 1;
+        for (int i = threadIdx.x; i < items; i += kThreads)
+            if (i >= live) put(i / kPerRow * kPitch + i % kPerRow * 4, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int i0 = 0; i0 < live; i0 += kThreads) {
+            const int i = i0 + (int)threadIdx.x % (kThreads / shares), share = (int)threadIdx.x / (kThreads / shares);
+            const float* from;
+            const int at = item(i, &from);
+            f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c0 = share; c0 < p.chunks; c0 += 4 * shares) {
+                f32x4 part[4];
 #pragma unroll
-        for (int q = 0; q < kAt; ++q) {
-            const int i = i0 + q * kThreads, m = i / (NK * 8), k4 = i % (NK * 8) * 4;
-            from[q] = m < t.rows && k4 < p.r ? p.part + (int64_t)tok[m] * p.r + k4 : nullptr;
-            sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        for (int c = 0; c < p.chunks; c += kDeep) {
-            f32x4 part[kDeep][kAt];
-#pragma unroll
-            for (int u = 0; u < kDeep; ++u)
-#pragma unroll
-                for (int q = 0; q < kAt; ++q) {
-                    part[u][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    if (from[q] && c + u < p.chunks) part[u][q] = *reinterpret_cast<const f32x4*>(from[q] + (int64_t)(c + u) * p.T * p.r);
+                for (int u = 0; u < 4; ++u) {
+                    part[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (from && c0 + u * shares < p.chunks) part[u] = *reinterpret_cast<const f32x4*>(from + (c0 + u * shares) * stride);
                 }
 #pragma unroll
-            for (int u = 0; u < kDeep; ++u)
-#pragma unroll
-                for (int q = 0; q < kAt; ++q) sum[q] += part[u][q];
+                for (int u = 0; u < 4; ++u) sum += part[u];
+            }
+            if (shares > 1) {
+                __syncthreads();
+                shared_sums[threadIdx.x] = sum;
+                __syncthreads();
+                if (share == 0)
+                    for (int q = 1; q < shares; ++q) sum += shared_sums[threadIdx.x + q * (kThreads / shares)];
+            }
+            if (share == 0) put(at, sum);
         }
+    } else {
+        constexpr int kAt = 2, kDeep = 8;
+        for (int i0 = threadIdx.x; i0 < items; i0 += kAt * kThreads) {
+            const float* from[kAt];
+            int at[kAt];
+            f32x4 sum[kAt];
 #pragma unroll
-        for (int q = 0; q < kAt; ++q) {
-            const int i = i0 + q * kThreads, m = i / (NK * 8), k4 = i % (NK * 8) * 4;
-            if (m < kRows)
-                *reinterpret_cast<i32x2*>(v + m * kPitch + k4) = i32x2{(int)pack_bf16x2(sum[q][0] * scale, sum[q][1] * scale),
-                                                                       (int)pack_bf16x2(sum[q][2] * scale, sum[q][3] * scale)};
+            for (int q = 0; q < kAt; ++q) {
+                at[q] = i0 + q * kThreads < items ? item(i0 + q * kThreads, &from[q]) : -1;
+                if (at[q] < 0) from[q] = nullptr;
+                sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            for (int c = 0; c < p.chunks; c += kDeep) {
+                f32x4 part[kDeep][kAt];
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+                    for (int q = 0; q < kAt; ++q) {
+                        part[u][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (from[q] && c + u < p.chunks) part[u][q] = *reinterpret_cast<const f32x4*>(from[q] + (c + u) * stride);
+                    }
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+                    for (int q = 0; q < kAt; ++q) sum[q] += part[u][q];
+            }
+#pragma unroll
+            for (int q = 0; q < kAt; ++q)
+                if (at[q] >= 0) put(at[q], sum[q]);
         }
     }
     Base next_base = load_base(nw);

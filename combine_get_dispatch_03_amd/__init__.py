@@ -260,6 +260,14 @@ class Handle:
         self.num_ranks, self.rank, self.expert_alignment = num_ranks, rank, expert_alignment
         self.num_local_experts = num_experts // num_ranks
         self._cap = None
+        self._device = None
+
+    @property
+    def device(self):
+        """The device of the layout (its topk_idx)."""
+        if self._device is None:
+            self._device = self.topk_idx.device
+        return self._device
 
     @property
     def recv_capacity(self):
@@ -583,18 +591,27 @@ def ep_combine_reduce(handle: Handle, partials=None, local=None, bias=None, out=
 
 def _device(handle):
     """The GPU of a handle, where every tensor of its calls must be; it must be the current one (the stream is its)."""
-    device = handle.topk_idx.device
+    device = handle.device
     if device.type == "cuda" and device.index != (_cur_device or torch.cuda.current_device)():
         raise ValueError("the handle's device %s is not the current device" % device)
     return device
 
 
-def _matrix(t, dtype, name, device):
-    """A 2-D tensor [rows, columns]; returns its columns."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+def _columns(t, name):
+    """Columns of a 2-D tensor [rows, columns] (its type and placement are checked with its shape, by _need)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 2:
         raise ValueError("%s must be a 2-D tensor" % name)
-    _need(t, dtype, name, device)
     return t.shape[1]
+
+
+def _empty(stream, like, shape, dtype=torch.bfloat16):
+    """An output or workspace of a call, on `like`'s device, belonging to the call's stream (see _on_stream)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def ep_combine_backward(handle: Handle, grad_out, y=None, topk_weights=None, grad_y=None, grad_topk_weights=None,
@@ -603,16 +620,17 @@ def ep_combine_backward(handle: Handle, grad_out, y=None, topk_weights=None, gra
     gradient); topk_weights as given to it.  Returns (grad_y bf16 [rows, H], grad_topk_weights fp32 [T, K]), None where
     not needed.  Rows of grad_y that no entry owns keep what the tensor held."""
     dev, T, K = _device(handle), handle.num_tokens, handle.num_topk
-    H = _matrix(grad_out, torch.bfloat16, "grad_out", dev)
+    H = _columns(grad_out, "grad_out")
     _need(grad_out, torch.bfloat16, "grad_out", dev, (T, H))
     if topk_weights is not None:
         _need(topk_weights, torch.float32, "topk_weights", dev, (T, K))
     need_w = need_grad_topk_weights or grad_topk_weights is not None
     rows = handle.recv_capacity
     if y is not None:
-        if _matrix(y, torch.bfloat16, "y", dev) != H:
+        if _columns(y, "y") != H:
             raise ValueError("y must be [rows, %d]" % H)
         rows = y.shape[0]
+        _need(y, torch.bfloat16, "y", dev, (rows, H))
     elif need_w:
         raise ValueError("the gradient of topk_weights needs y")
     if grad_y is not None:
@@ -620,11 +638,11 @@ def ep_combine_backward(handle: Handle, grad_out, y=None, topk_weights=None, gra
             rows = grad_y.shape[0]
         _need(grad_y, torch.bfloat16, "grad_y", dev, (rows, H))
     elif need_grad_y:
-        grad_y = _on_stream(stream, torch.empty, (rows, H), dtype=torch.bfloat16, device=dev)
+        grad_y = _empty(stream, grad_out, (rows, H))
     if grad_topk_weights is not None:
         _need(grad_topk_weights, torch.float32, "grad_topk_weights", dev, (T, K))
     elif need_w:
-        grad_topk_weights = _on_stream(stream, torch.empty, (T, K), dtype=torch.float32, device=dev)
+        grad_topk_weights = _empty(stream, grad_out, (T, K), torch.float32)
     _check(_lib.ep_combine_backward(handle.ptr, _ptr(grad_out), H, _ptr(y), rows, _ptr(topk_weights), _ptr(grad_y),
                                     _ptr(grad_topk_weights), _stream(stream)), "ep_combine_backward")
     return grad_y, grad_topk_weights
@@ -662,7 +680,7 @@ def _ffn_workspace(handle, H, I, backward, workspace, device, stream):
     n = ep_expert_ffn_workspace_bytes(handle, H, I, backward)
     if n == 0:
         raise EPError("ep_expert_ffn_workspace_bytes rejected the sizes (hidden=%d intermediate=%d)" % (H, I))
-    return _on_stream(stream, torch.empty, n, dtype=torch.uint8, device=device)
+    return _empty(stream, handle.topk_idx, n, torch.uint8)
 
 
 def ep_expert_ffn(handle: Handle, recv_x, w13, w2, recv_x_scales=None, w13_scales=None, w2_scales=None, y=None, pre=None,
@@ -676,15 +694,16 @@ def ep_expert_ffn(handle: Handle, recv_x, w13, w2, recv_x_scales=None, w13_scale
         raise TypeError("recv_x must be a bfloat16 or uint8 (e4m3) tensor")
     fp8 = recv_x.dtype == torch.uint8
     dev, El = _device(handle), handle.num_local_experts
-    H = _matrix(recv_x, recv_x.dtype, "recv_x", dev)
+    H = _columns(recv_x, "recv_x")
     rows = recv_x.shape[0]
+    _need(recv_x, recv_x.dtype, "recv_x", dev, (rows, H))
     if w13 is None:
         raise ValueError("w13 is required")
     I = check_ffn_weights(w13, w2, recv_x.dtype, El, H, dev)
     if fp8:
         check_ffn_scales(recv_x_scales, w13_scales, w2_scales, rows, El, H, I, dev)
     if y is None:
-        y = _on_stream(stream, torch.empty, (rows, H), dtype=torch.bfloat16, device=dev)
+        y = _empty(stream, recv_x, (rows, H))
     else:
         _need(y, torch.bfloat16, "y", dev, (rows, H))
     if pre is not None:
@@ -703,8 +722,9 @@ def ep_expert_ffn_backward(handle: Handle, dy, recv_x, pre, w13, w2, dx=None, dw
     w13, dw2 like w2), bf16, None where not needed.  Rows of dx that are not valid rows keep what it held; dw13 and dw2
     are written whole."""
     dev, El = _device(handle), handle.num_local_experts
-    H = _matrix(dy, torch.bfloat16, "dy", dev)
+    H = _columns(dy, "dy")
     rows = dy.shape[0]
+    _need(dy, torch.bfloat16, "dy", dev, (rows, H))
     need_dx, need_dw13, need_dw2 = need_dx or dx is not None, need_dw13 or dw13 is not None, need_dw2 or dw2 is not None
     if need_dx and w13 is None:
         raise ValueError("dx needs w13")
@@ -718,7 +738,7 @@ def ep_expert_ffn_backward(handle: Handle, dy, recv_x, pre, w13, w2, dx=None, dw
     def grad(t, name, shape, needed):
         if t is not None:
             return _need(t, torch.bfloat16, name, dev, shape)
-        return _on_stream(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev) if needed else None
+        return _empty(stream, dy, shape) if needed else None
 
     dx = grad(dx, "dx", (rows, H), need_dx)
     dw13 = grad(dw13, "dw13", (El, 2 * I, H), need_dw13)
@@ -739,7 +759,7 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
     adapter in the handle (a layout over the adapter ids [T, 1], -1 = none).  x bf16 [T, H], a bf16 [El, r, H], b bf16
     [El, N, r], scales fp32 [El], base bf16 [T, N] (None: zeros).  Returns out bf16 [T, N] (may be base itself)."""
     dev, T, El = _device(handle), handle.num_tokens, handle.num_local_experts
-    H = _matrix(x, torch.bfloat16, "x", dev)
+    H = _columns(x, "x")
     _need(x, torch.bfloat16, "x", dev, (T, H))
     if not isinstance(b, torch.Tensor) or b.dim() != 3:
         raise ValueError("b must be [num_local_experts, out_features, rank]")
@@ -751,7 +771,7 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
     if base is not None:
         _need(base, torch.bfloat16, "base", dev, (T, N))
     if out is None:
-        out = _on_stream(stream, torch.empty, (T, N), dtype=torch.bfloat16, device=dev)
+        out = _empty(stream, x, (T, N))
     else:
         _need(out, torch.bfloat16, "out", dev, (T, N))
     if workspace is not None:
@@ -760,7 +780,7 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
         n = ep_adapter_workspace_bytes(handle, H, r)
         if n == 0:
             raise EPError("ep_adapter_workspace_bytes rejected the sizes (hidden=%d rank=%d)" % (H, r))
-        workspace = _on_stream(stream, torch.empty, n, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, x, n, torch.uint8)
     _check(_lib.ep_adapter(handle.ptr, _ptr(x), H, _ptr(a), _ptr(b), r, N, _ptr(scales), _ptr(base), _ptr(out),
                            _ptr(workspace), workspace.numel(), _stream(stream)), "ep_adapter")
     return out

@@ -10,7 +10,8 @@
 //   expand   the partial sums are added in order, scaled and rounded to bf16 in LDS; then B_a's rows times v, added to
 //            base and stored.  More workgroups copy base where a token has no adapter.
 // Both are bound by memory (x and A; base, out and B): matrix instructions only keep the arithmetic out of the way.
-// The layout maps tokens to rows; a tile finds its tokens by going over that map once (4 bytes a token, from L2).
+// The layout maps tokens to rows; a tile finds its tokens by going over that map once (4 bytes a token, from L2), or, where
+// there are many tokens, a kernel before turns the map round for all tiles.
 #include "ep_expert_tiles.hpp"
 #include "ep_gemm_core.hpp"
 #include "ep_internal.hpp"
@@ -37,6 +38,9 @@ struct Params {
     const uint16_t* base;
     uint16_t* out;
     float* part;          // [chunks][T][r]
+    int32_t* tokens;      // many tokens: [tiles][64], a tile's tokens in the layout's order; else nullptr
+    const int64_t* ids;
+    int lo;
     int H, r, N;
     int chunk, chunks;    // hidden channels per chunk
 };
@@ -45,9 +49,14 @@ struct Params {
 // before the tile is known.  Ends with a barrier.
 __device__ __forceinline__ i32x4 first_slots(const Params& p) {
     const int i = threadIdx.x;
-    return i < p.T / 4 ? reinterpret_cast<const i32x4*>(p.slot)[i] : i32x4{-1, -1, -1, -1};
+    return p.tokens == nullptr && i < p.T / 4 ? reinterpret_cast<const i32x4*>(p.slot)[i] : i32x4{-1, -1, -1, -1};
 }
-__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, i32x4 first, int* tok) {
+__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int tile, i32x4 first, int* tok) {
+    if (p.tokens != nullptr) {
+        if ((int)threadIdx.x < t.rows) tok[threadIdx.x] = p.tokens[(int64_t)tile * kRows + threadIdx.x];
+        __syncthreads();
+        return;
+    }
     const int quads = p.T / 4;
     const i32x4* q = reinterpret_cast<const i32x4*>(p.slot);
     auto put = [&](int s, int token) {
@@ -66,8 +75,28 @@ __device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, i
     __syncthreads();
 }
 
+// tokens[tile][m] for every token with an adapter.
+__global__ __launch_bounds__(kThreads) void k_tokens(Params p) {
+    __shared__ int before[kMaxExperts];      // tiles of the adapters before each
+    if (threadIdx.x < kWave) {
+        const RowTiles<kRows, 0> tiles(p.cnt, p.psum, p.El);
+        int at = tiles.incl - tiles.sum;
+        for (int i = 0; i < tiles.per; ++i) {
+            const int e = lane_id() * tiles.per + i;
+            if (e >= p.El) break;
+            before[e] = at;
+            at += (p.cnt[e] + kRows - 1) / kRows;
+        }
+    }
+    __syncthreads();
+    const int t = blockIdx.x * kThreads + threadIdx.x;
+    if (t >= p.T || p.slot[t] < 0) return;
+    const int e = (int)(p.ids[t] - p.lo);
+    p.tokens[(int64_t)before[e] * kRows + (p.slot[t] - p.psum[e])] = t;      // a tile's rows are consecutive, and so are tiles
+}
+
 template <int NF, int MT>
-__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int chunk, i32x4 slots, int* tok, float* sums) {
+__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int tile, int chunk, i32x4 slots, int* tok, float* sums) {
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
     const uint16_t* f[NF];
     bool f_there[NF];
@@ -97,7 +126,7 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ch
             }
     };
     load_f(next, first);       // A's rows do not depend on the tokens
-    find_tokens(p, t, slots, tok);
+    find_tokens(p, t, tile, slots, tok);
     const uint16_t* s[MT];
     bool s_there[MT];
 #pragma unroll
@@ -156,9 +185,9 @@ __global__ __launch_bounds__(kThreads) void k_shrink(Params p) {
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int chunk = blockIdx.x % p.chunks;
-    if (t.rows <= 16) shrink<NF, 1>(p, t, chunk, slots, tok, sums);
-    else if (t.rows <= 32) shrink<NF, 2>(p, t, chunk, slots, tok, sums);
-    else shrink<NF, 4>(p, t, chunk, slots, tok, sums);
+    if (t.rows <= 16) shrink<NF, 1>(p, t, tile, chunk, slots, tok, sums);
+    else if (t.rows <= 32) shrink<NF, 2>(p, t, tile, chunk, slots, tok, sums);
+    else shrink<NF, 4>(p, t, tile, chunk, slots, tok, sums);
 }
 
 // NK: steps of 32 over the rank.  A workgroup takes `steps` times 256 channels.
@@ -222,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
     };
     int nw = first + wave * 64;
     Rows next = load_b(nw);
-    find_tokens(p, t, slots, tok);
+    find_tokens(p, t, tile, slots, tok);
     const float scale = p.scales ? p.scales[t.expert] : 1.0f;
     // v of the tile's tokens, zeros past the last token and past the rank, 4 ranks per item; the chunks are added in a fixed
     // order.  A few tokens: the workgroup's threads share an item's chunks and meet in LDS.  Many: two items a thread,
@@ -357,19 +386,30 @@ int chunk_of(int T, int El, int H) {
 
 }  // namespace
 
+// From so many tokens on their tiles are worked out once, by a kernel of its own (3 us, and a launch): a tile's own search
+// is 4 bytes a token, 64 KiB of L2 reads at 16384 tokens, and all searches together go with the square of the tokens.
+static constexpr int kManyTokens = 8192;
+
 size_t adapter_workspace_bytes(int T, int El, int hidden, int rank) {
     const int chunk = chunk_of(T, El, hidden), chunks = (hidden + chunk - 1) / chunk;
-    const size_t bytes = (size_t)chunks * (size_t)T * (size_t)rank * sizeof(float);
-    return bytes > 256 ? bytes : 256;
+    const size_t parts = ((size_t)chunks * (size_t)T * (size_t)rank * sizeof(float) + 255) / 256 * 256;
+    return parts + (T >= kManyTokens ? (size_t)max_tiles(T, El) * kRows * sizeof(int32_t) : 256);
 }
 
 hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t stream) {
     if (h.T == 0) return hipSuccess;
     const int chunk = chunk_of(h.T, h.El, a.hidden), chunks = (a.hidden + chunk - 1) / chunk, tiles = max_tiles(h.T, h.El);
+    const size_t parts = ((size_t)chunks * (size_t)h.T * (size_t)a.rank * sizeof(float) + 255) / 256 * 256;
+    int32_t* tokens = h.T >= kManyTokens ? reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + parts) : nullptr;
     const Params p{h.ws.cnt_local, h.ws.psum, h.ws.slot, h.T, h.El, (const uint16_t*)a.x, (const uint16_t*)a.a,
-                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws,
-                   a.hidden, a.rank, a.n_out, chunk, chunks};
-    const dim3 shrink_grid((unsigned)(tiles * chunks)), block(kThreads);
+                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens, h.topk_idx,
+                   h.lo, a.hidden, a.rank, a.n_out, chunk, chunks};
+    if (tokens) {
+        hipLaunchKernelGGL(k_tokens, dim3((unsigned)((h.T + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 shrink_grid((unsigned)((int64_t)tiles * chunks)), block(kThreads);
     if (a.rank <= 16) hipLaunchKernelGGL(k_shrink<1>, shrink_grid, block, 0, stream, p);
     else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, shrink_grid, block, 0, stream, p);
     else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, shrink_grid, block, 0, stream, p);

@@ -62,6 +62,9 @@ CASES = [
     (1500, 256, 256, 2, 1, 0, 8, "one"),
     (600, 320, 136, 4, 1, 0, 16, "none"),
     (3000, 136, 2056, 64, 1, 0, 32, "any"),
+    (8192, 72, 40, 5, 1, 0, 16, "holes"),          # the tiles' tokens worked out beforehand
+    (9001, 264, 72, 700, 1, 0, 8, "any"),
+    (20011, 64, 64, 6, 3, 1, 24, "runs"),
 ]
 
 

@@ -236,9 +236,7 @@ hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f,
 
 hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
-    // Up to so many rows an expert is one row tile and its weights pass by once.  32 experts of 7168 x 2048, us with ONCE and
-    // without: 16 rows 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373; 900 rows (four row tiles) 1409 and 1262.
-    return mean_rows(h) <= 128 ? rows_launch<kGateUp, true>(h, p, stream) : rows_launch<kGateUp>(h, p, stream);
+    return weights_once(h, a) ? rows_launch<kGateUp, true>(h, p, stream) : rows_launch<kGateUp>(h, p, stream);
 }
 
 hipError_t launch_tile_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

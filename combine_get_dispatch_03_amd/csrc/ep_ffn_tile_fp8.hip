@@ -173,10 +173,8 @@ hipError_t up_launch(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// ONCE: where weights pass by once and decide the time.  256 experts of 7168 x 2048, us with it and without: 4 rows each
-// 1103 and 1209, 128 rows 1681 and 1582; 32 experts, 16 rows 158 and 167, 64 rows 183 and 184.
 hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    return mean_rows(h) <= 64 ? up_launch<true>(h, a, stream) : up_launch<false>(h, a, stream);
+    return weights_once(h, a) ? up_launch<true>(h, a, stream) : up_launch<false>(h, a, stream);
 }
 
 hipError_t launch_tile_fp8_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

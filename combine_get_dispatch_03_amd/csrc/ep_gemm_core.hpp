@@ -126,8 +126,9 @@ struct KcOperand {
             for (int i = 0; i < kCopies; ++i) offset[i] = chunk() * 16 < left ? offset[i] : kNoElement;
         }
         const i32x4 res = resource(base);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + threadIdx.x / kWave * 1024);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(to + i * kGemmWaves * 1024, offset[i], res);
         base += 128;
     }
     // LDS offset of the lane's 16 bytes of the rows from row0, first half of the line; the second half is at ^ 64, the
@@ -176,8 +177,9 @@ struct KsOperand {
             for (int i = 0; i < kCopies; ++i) offset[i] = row(i) < left ? offset[i] : kNoElement;
         }
         const i32x4 res = resource(base);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + threadIdx.x / kWave * 1024);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(lds + (i * kGemmWaves + wave_id()) * 1024, offset[i], res);
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds<ONCE>(to + i * kGemmWaves * 1024, offset[i], res);
         base += step;
     }
     // LDS offset of the lane's part of 16 columns: k-rows 8g .. 8g + 3; + 4 * kRowBytes for 8g + 4 .. 8g + 7,
@@ -398,7 +400,7 @@ struct Fp8Tiles {
     __device__ __forceinline__ void copy_s(int buf) {
         const uint32_t lds0 = lds_address(smem);
         s.copy(lds0 + buf * SOp::kBytes, s_left);
-        copy4_to_lds(lds0 + kRowScales + buf * kRowScaleBytes + wave_id() * 256, scale_offset, resource(scales, s_left > 0 ? kNoElement : 0u));
+        copy4_to_lds(__builtin_amdgcn_readfirstlane(lds0 + kRowScales + buf * kRowScaleBytes + threadIdx.x / kWave * 256), scale_offset, resource(scales, s_left > 0 ? kNoElement : 0u));
         scales += 4;
         s_left -= 128;
     }
@@ -554,9 +556,9 @@ struct Bf16ByFp8Tiles {
     }
     __device__ __forceinline__ void copy_f(int buf) {
         const i32x4 res = resource(f, f_left > 0 ? kNoElement : 0u);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds_address(smem) + kF + buf * kFBytes + threadIdx.x / kWave * 1024);
 #pragma unroll
-        for (int i = 0; i < kFCopies; ++i)
-            copy16_to_lds(lds_address(smem) + kF + buf * kFBytes + (i * kGemmWaves + wave_id()) * 1024, f_offset[i], res);
+        for (int i = 0; i < kFCopies; ++i) copy16_to_lds(to + i * kGemmWaves * 1024, f_offset[i], res);
         f += 64;
         f_left -= 64;
     }

@@ -323,14 +323,16 @@ const char* adapter_shape(int hidden, int rank, int n_out) {
     return nullptr;
 }
 
-// Scratch of the feed-forward block: h [cap, inter] bf16 first, then (backward) dp [cap, 2 * inter] bf16.
+// Scratch of the feed-forward block: h [cap, inter] bf16 first, then (backward) dp [cap, 2 * inter] bf16, rows padded to
+// row_pitch().
 struct FfnWorkspace {
     size_t dp, bytes;
 };
 FfnWorkspace ffn_workspace(int64_t cap, int inter, bool backward) {
     FfnWorkspace w;
-    w.dp = align_up((size_t)(cap > 0 ? cap : 1) * (size_t)inter * 2, 256);
-    w.bytes = backward ? 3 * w.dp : w.dp;
+    const size_t rows = cap > 0 ? (size_t)cap : 1;
+    w.dp = align_up(rows * (size_t)row_pitch(inter) * 2, 256);
+    w.bytes = backward ? w.dp + align_up(rows * (size_t)row_pitch(2 * inter) * 2, 256) : w.dp;
     return w;
 }
 

@@ -28,13 +28,13 @@ inline bool few_rows(const Handle& h, double limit, int cols) {
 }
 
 // Whether the gate and up projection's weights are worth marking as read once (copy16_to_lds): one row tile per expert, whole
-// lines, and more of them than the 256 MB memory-side cache holds.  us with the mark and without: 32 experts of 7168 x 2048,
+// lines, and more of them than the 256 MB memory-side cache keeps beside the rest of a layer.  us with the mark and without: 32 experts of 7168 x 2048,
 // bf16, 16 rows each 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373, 900 rows (four row tiles) 1409 and 1262; 256
-// experts, e4m3, 4 rows 1103 and 1209, 128 rows 1681 and 1582; 20 experts of 1352 x 512, 80 rows 39 and 27 (rows of 2704
-// bytes), of 1344 x 512 28 and 27.
+// experts, e4m3, 4 rows 1103 and 1209, 128 rows 1681 and 1582; 20 experts of 2112 x 1352 (228 MB), 117 rows 68 and 85;
+// of 1344 x 512 (55 MB), 80 rows 28 and 23, of 1352 x 512 (rows of 2704 bytes) 39 and 27.
 inline bool weights_once(const Handle& h, const FfnArgs& a) {
     const int64_t row = (int64_t)a.hidden * (a.fp8 ? 1 : 2);
-    return mean_rows(h) <= (a.fp8 ? 64 : 128) && row % 128 == 0 && row * 2 * a.inter * h.El > (256ll << 20);
+    return mean_rows(h) <= (a.fp8 ? 64 : 128) && row % 128 == 0 && row * 2 * a.inter * h.El > (128ll << 20);
 }
 
 hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream);           // bf16

@@ -25,6 +25,7 @@ struct Params {
     uint16_t* out;
     float* pre;
     int N, K;      // channels of a projection's output, of its input
+    int sp, op;    // elements between rows of s and of out
 };
 
 enum Format { kBf16, kFp8 };
@@ -64,11 +65,11 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
     }
     const char* s[MT];
     bool s_there[MT];
-    const int s_bytes = UP ? f_bytes : p.K * 2;
+    const int s_bytes = UP ? f_bytes : p.K * 2, s_pitch = p.sp * (UP ? kWide : 2);
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
         s_there[a] = a * 16 + r < t.rows;
-        s[a] = (const char*)p.s + (row0 + (s_there[a] ? a * 16 + r : 0)) * s_bytes + (F == kFp8 && !UP ? g * 32 : g * 16);
+        s[a] = (const char*)p.s + (row0 + (s_there[a] ? a * 16 + r : 0)) * s_pitch + (F == kFp8 && !UP ? g * 32 : g * 16);
     }
 
     auto load_f = [&](int st) {
@@ -191,9 +192,9 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
                     *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.N + n0 + n4) = v;
                     *reinterpret_cast<f32x4*>(p.pre + row * 2 * p.N + p.N + n0 + n4) = u;
                 }
-                store4(p.out + row * p.N + n0 + n4, h[0], h[1], h[2], h[3]);
+                store4(p.out + row * p.op + n0 + n4, h[0], h[1], h[2], h[3]);
             } else {
-                store4(p.out + row * p.N + n0 + n4, v[0], v[1], v[2], v[3]);
+                store4(p.out + row * p.op + n0 + n4, v[0], v[1], v[2], v[3]);
             }
         }
     }
@@ -238,13 +239,15 @@ bool narrow(const Handle& h, int N, bool up) {
 }  // namespace
 
 hipError_t launch_stream_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden};
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden,
+                   a.hidden, row_pitch(a.inter)};
     if (a.fp8) return stream_launch<kFp8, true, 64>(h, p, stream);
     return narrow(h, a.inter, true) ? stream_launch<kBf16, true, 32>(h, p, stream) : stream_launch<kBf16, true, 64>(h, p, stream);
 }
 
 hipError_t launch_stream_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter};
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter,
+                   row_pitch(a.inter), a.hidden};
     if (a.fp8) return stream_launch<kFp8, false, 64>(h, p, stream);
     return narrow(h, a.hidden, false) ? stream_launch<kBf16, false, 32>(h, p, stream) : stream_launch<kBf16, false, 64>(h, p, stream);
 }

@@ -50,7 +50,7 @@ __device__ __forceinline__ void store_rows(const Params& p, const f32x4 (&acc)[M
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[b][i] = gate[i] * sigmoid(gate[i]) * up[i];
             }
-            store8(p.out + row * p.I + n, h[0], h[1]);
+            store8(p.out + row * row_pitch(p.I) + n, h[0], h[1]);
         } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -71,9 +71,9 @@ __device__ __forceinline__ void store_rows(const Params& p, const f32x4 (&acc)[M
                             h[b][i] = act * up[i];
                         }
                     }
-                    store8(p.out + row * 2 * p.I + n, dg[0], dg[1]);
-                    store8(p.out + row * 2 * p.I + p.I + n, du[0], du[1]);
-                    store8(p.out2 + row * p.I + n, h[0], h[1]);
+                    store8(p.out + row * row_pitch(2 * p.I) + n, dg[0], dg[1]);
+                    store8(p.out + row * row_pitch(2 * p.I) + p.I + n, du[0], du[1]);
+                    store8(p.out2 + row * row_pitch(p.I) + n, h[0], h[1]);
                 } else {
                     store8(p.out + row * N + n, acc[a][j * 2], acc[a][j * 2 + 1]);
                 }
@@ -109,7 +109,8 @@ struct RowsKernel {
         const int n0 = at.col * kCols;
         next = Target{t.row0, t.rows, n0};
         g.next_k = K;
-        g.next_s.init(p.s + (int64_t)t.row0 * K, [&](int r) { return r < t.rows ? r * (2u * K) : kNoElement; });
+        const uint32_t pitch = P == kDown || P == kInGrad ? row_pitch(K) : K;
+        g.next_s.init(p.s + (int64_t)t.row0 * pitch, [&](int r) { return r < t.rows ? r * (2u * pitch) : kNoElement; });
         if constexpr (P == kGateUp) {
             // a wave's 64 rows of F: 32 gate channels (fragments 0, 1), then the same 32 up channels
             const uint64_t up = (uint64_t)p.I * p.H * 2;
@@ -163,9 +164,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_rows(Params p) {
     k.g.end();
 }
 
-// out[e] [M, N] = sum over the expert's rows of s[row, m] f[row, n]
+// out[e] [M, N] = sum over the expert's rows of s[row, m] f[row, n]; rows of s and f are sp and fp elements apart.
 __global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt, const int32_t* psum, int El, const uint16_t* s,
-                                                             const uint16_t* f, uint16_t* out, int M, int N) {
+                                                             const uint16_t* f, uint16_t* out, int M, int N, int sp, int fp) {
     typedef Bf16Tiles<true, true> Tiles;
     extern __shared__ __align__(1024) char smem[];
     const ExpertRows experts(cnt, psum, El);
@@ -185,8 +186,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_weights(const int32_t* cnt,
         const RowTile e = experts.get(at.row / mt);
         next = Out{(int64_t)e.expert * M * N, at.row % mt * Tiles::kBM, at.col * kBN, e.rows};
         g.next_k = e.rows;
-        g.next_s.init(s + (int64_t)e.row0 * M + next.m0, (int64_t)M * 2, M - next.m0);
-        g.next_f.init(f + (int64_t)e.row0 * N + next.n0, (int64_t)N * 2, N - next.n0);
+        g.next_s.init(s + (int64_t)e.row0 * sp + next.m0, (int64_t)sp * 2, M - next.m0);
+        g.next_f.init(f + (int64_t)e.row0 * fp + next.n0, (int64_t)fp * 2, N - next.n0);
     };
     look_ahead();
     if (!more) return;
@@ -222,13 +223,14 @@ hipError_t rows_launch(const Handle& h, const Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f, uint16_t* out, int M, int N, hipStream_t stream) {
+hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f, uint16_t* out, int M, int N, int sp, int fp,
+                          hipStream_t stream) {
     typedef Bf16Tiles<true, true> Tile;
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_weights), Tile::kLds);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t)h.El * ((M + Tile::kBM - 1) / Tile::kBM) * ((N + kBN - 1) / kBN);
     hipLaunchKernelGGL(k_weights, dim3(walking_blocks(tiles)), dim3(kGemmThreads), Tile::kLds, stream, h.ws.cnt_local, h.ws.psum,
-                       h.El, s, f, out, M, N);
+                       h.El, s, f, out, M, N, sp, fp);
     return hipGetLastError();
 }
 
@@ -255,9 +257,10 @@ hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a,
             e = rows_launch<kInGrad>(h, ig, stream);
         }
     }
-    if (e == hipSuccess && a.dw2) e = weights_launch(h, dy, a.h, (uint16_t*)a.dw2, a.hidden, a.inter, stream);
+    if (e == hipSuccess && a.dw2) e = weights_launch(h, dy, a.h, (uint16_t*)a.dw2, a.hidden, a.inter, a.hidden, row_pitch(a.inter), stream);
     if (e == hipSuccess && a.dw13)
-        e = weights_launch(h, a.dp, (const uint16_t*)a.x, (uint16_t*)a.dw13, 2 * a.inter, a.hidden, stream);
+        e = weights_launch(h, a.dp, (const uint16_t*)a.x, (uint16_t*)a.dw13, 2 * a.inter, a.hidden,
+                           row_pitch(2 * a.inter), a.hidden, stream);
     return e;
 }
 

@@ -110,6 +110,9 @@ struct CombineBackwardArgs {
 };
 hipError_t launch_combine_backward(const Handle& h, const CombineBackwardArgs& a, hipStream_t stream);
 
+// Row pitch, in elements, of the feed-forward block's bf16 workspace rows: whole 128-byte lines, whatever the width.
+constexpr int row_pitch(int width) { return (width + 63) / 64 * 64; }
+
 struct FfnArgs {
     const void* x;             // bf16 or e4m3 [rows, hidden]
     const float* x_scales;     // e4m3: [rows, hidden / 128]
@@ -119,7 +122,7 @@ struct FfnArgs {
     const float* w2_scales;    // e4m3: [El, hidden / 128, inter / 128]
     void* y;                   // bf16 [rows, hidden]
     float* pre;                // fp32 [rows, 2 * inter] or nullptr
-    uint16_t* h;               // workspace: bf16 [cap, inter]
+    uint16_t* h;               // workspace: bf16 [cap, row_pitch(inter)]
     int hidden, inter;
     bool fp8;
 };
@@ -134,8 +137,8 @@ struct FfnBackwardArgs {
     void* dx;                  // bf16 [rows, hidden] or nullptr
     void* dw13;                // bf16 like w13, or nullptr
     void* dw2;                 // bf16 like w2, or nullptr
-    uint16_t* dp;              // workspace: bf16 [cap, 2 * inter], gradient of the pre-activations
-    uint16_t* h;               // workspace: bf16 [cap, inter]
+    uint16_t* dp;              // workspace: bf16 [cap, row_pitch(2 * inter)], gradient of the pre-activations
+    uint16_t* h;               // workspace: bf16 [cap, row_pitch(inter)]
     int hidden, inter;
 };
 hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a, hipStream_t stream);

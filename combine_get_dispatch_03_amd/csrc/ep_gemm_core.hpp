@@ -91,7 +91,9 @@ __device__ __forceinline__ int channel_of(int b, int i) { return (b >> 1) * 32 +
 
 // An operand whose k is contiguous: ROWS rows, 128 bytes of each per stage (64 bf16, or 128 e4m3).  A row is a line of LDS,
 // its 16-byte chunks permuted by the row number.
-template <int ROWS>
+// SPREAD: fragment() and fragment() ^ 64 give lane group g the row's chunks 2g and 2g + 1 (otherwise g and g + 4), the 16
+// terms for which one read fetches the other operand's e4m3.
+template <int ROWS, bool SPREAD = false>
 struct KcOperand {
     static constexpr int kCopies = ROWS / 8 / kGemmWaves;     // copies of a stage per wave
     static constexpr int kBytes = ROWS * 128;
@@ -104,7 +106,10 @@ struct KcOperand {
         asm volatile("s_nop 4" : "+s"(base));
     }
 
-    static __device__ __forceinline__ int chunk() { return (lane_id() & 7) ^ (lane_id() >> 3); }   // the lane's, of 8
+    static __device__ __forceinline__ int chunk() {      // the lane's, of 8
+        const int at = (lane_id() & 7) ^ (lane_id() >> 3);
+        return SPREAD ? (at & 3) << 1 | at >> 2 : at;
+    }
 
     // row_offset(r): byte offset of tile row r from `start`, or kNoElement.
     template <class RowOffset>
@@ -537,7 +542,7 @@ struct Fp8Tiles {
 // 64 k per stage: 128 bytes of a row of S, 64 of F (two rows a line of LDS).  S is three stages deep and F four.
 struct Bf16ByFp8Tiles {
     static constexpr int kBM = 160, NT = 4;
-    typedef KcOperand<192> SOp;                      // whole copies per wave; rows from 160 on do not exist
+    typedef KcOperand<192, true> SOp;                // whole copies per wave; rows from 160 on do not exist
     static constexpr int kFBytes = kBN * 64, kFCopies = 2;
     static constexpr int kSBuffers = 3, kFBuffers = 4, kF = SOp::kBytes * kSBuffers;
     static constexpr int kFScales = kF + kFBytes * kFBuffers;     // [2 tiles][2 rows of up to 256 fp32]: channels 0..127, 128..255
@@ -624,10 +629,10 @@ struct Bf16ByFp8Tiles {
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // a lane reads the 8 e4m3 of k 8g .. 8g + 7, and 32 k on the next 8 (the chunk at ^ 32); its bf16 of S are as in Bf16Tiles
+        // a lane reads the 16 e4m3 of k 16g .. 16g + 15; half h of them goes with the bf16 at SOp's half h
         const int r = lane_id() & 15, g = lane_id() >> 4;
         const uint32_t s_at = SOp::fragment(wm * MT * 16);
-        const uint32_t f_at = (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | (g >> 1)) ^ (r >> 1)) << 4) + (g & 1) * 8;
+        const uint32_t f_at = (wn * 64 + (r & ~1)) * 64 + (((((r & 1) << 2) | g) ^ (r >> 1)) << 4);
         const float* fs = reinterpret_cast<const float*>(smem + kFScales + tile * 2048) + (wn >> 1) * 256;
         meet();
         if (wm == 1) meet();
@@ -649,12 +654,9 @@ struct Bf16ByFp8Tiles {
                 copy_s(sbuf == 0 ? kSBuffers - 1 : sbuf - 1);
                 copy_f((fbuf + kFBuffers - 1) % kFBuffers);
                 bf16x8 sv[MT][2];
-                i32x2 fq[NT][2];
+                i32x4 fq[NT];
 #pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    fq[b][0] = *reinterpret_cast<const i32x2*>(lf + f_at + b * 1024);
-                    fq[b][1] = *reinterpret_cast<const i32x2*>(lf + (f_at ^ 32) + b * 1024);
-                }
+                for (int b = 0; b < NT; ++b) fq[b] = *reinterpret_cast<const i32x4*>(lf + f_at + b * 1024);
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
                     sv[a][0] = read_kc(ls, s_at + a * 2048);
@@ -667,7 +669,7 @@ struct Bf16ByFp8Tiles {
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        const bf16x8 fv = widen_e4m3x8(fq[b][h]);
+                        const bf16x8 fv = widen_e4m3x8(i32x2{fq[b][2 * h], fq[b][2 * h + 1]});
 #pragma unroll
                         for (int a = 0; a < MT; ++a)
                             part[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a][h], q + h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[a][b], 0, 0, 0);

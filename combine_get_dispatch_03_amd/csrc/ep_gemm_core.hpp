@@ -14,7 +14,7 @@
 //   k contiguous (KC): 128 bytes a row, 16-byte chunks permuted by the row number so that a fragment read (16 rows, 16
 //     bytes at one place of each) is spread over all banks.
 //   k strided (KS): a k-row of all columns; fragments come from the transposing LDS read (four k of a column per
-//     lane), chunk pairs permuted by the k-row for the same reason.
+//     lane), chunks permuted by the k-row for the same reason.
 #pragma once
 
 #include "ep_device.hpp"
@@ -221,6 +221,7 @@ __device__ __forceinline__ bf16x8 widen_e4m3x8(i32x2 q) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Sums of a k-strided F (KsOperand::fragment_f): back in channel_of()'s order.
 template <int MT, int NT>
 __device__ __forceinline__ void restore_channels(f32x4 (&acc)[MT][NT]) {
     const bool odd = lane_id() >> 4 & 1;

@@ -1,12 +1,12 @@
 // ep_ffn_stream.hip -- the expert block's forward pass for few rows per expert (decode): bound by reading the weights.
 //
-// A workgroup takes up to 64 rows of an expert and 64 (or 32) rows of its weights: half gate and the same up channels, or
-// output channels.  Its four waves split k: each streams its part of the weight rows from memory straight into the
+// A workgroup takes up to 16, 32 or 64 rows of an expert and 32 or 64 rows of its weights: half gate and the same up
+// channels, or output channels.  Its four waves split k: each streams its part of the weight rows from memory straight into the
 // fragments of the matrix instruction, the next step's loads in flight while the current one is multiplied; nothing is
 // shared, so no barrier stands in the loop.  The rows' fragments come from the caches.  At the end the waves' sums meet
 // in LDS.
 // Measured, 7168 x 2048: one token of 8 experts, bf16, gate and up 80 us (5.9 TB/s), down 46 us (5.1); 256 experts, e4m3, 4
-// rows each, down 0.72 ms (5.2 TB/s).  Experts of 256 x 512 with 32 rows: 6.0 us each, launch and latency.
+// rows each, down 0.65 ms (5.7 TB/s).  Experts of 256 x 512 with 32 rows: 6.0 and 5.0 us, launch and latency.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"
@@ -14,7 +14,7 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave, kRows = 64;
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
 
 struct Params {
     const int32_t* cnt;
@@ -202,37 +202,38 @@ __device__ __forceinline__ void product(const Params& p, const RowTile& t, int n
     }
 }
 
-template <Format F, bool UP, int COLS>
+// Rows in steps of 16, up to MAX; half as many registers with one or two leave room for twice the waves, and their loads.
+template <Format F, bool UP, int COLS, int MAX>
 __global__ __launch_bounds__(kThreads) void k_stream(Params p) {
     __shared__ __align__(16) char smem[kWaves * 16 * (COLS + 4) * 4];
-    const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
+    const RowTiles<MAX * 16> tiles(p.cnt, p.psum, p.El);
     constexpr int kChannels = UP ? COLS / 2 : COLS;
     const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int n0 = blockIdx.x % cols * kChannels;
-    switch ((t.rows + 15) / 16) {
-        case 1: product<F, UP, COLS, 1>(p, t, n0, smem); break;
-        case 2: product<F, UP, COLS, 2>(p, t, n0, smem); break;
-        case 3: product<F, UP, COLS, 3>(p, t, n0, smem); break;
-        default: product<F, UP, COLS, 4>(p, t, n0, smem); break;
-    }
+    const int steps = (t.rows + 15) / 16;
+    if (MAX == 1 || steps == 1) product<F, UP, COLS, 1>(p, t, n0, smem);
+    else if (MAX == 2 || steps == 2) product<F, UP, COLS, 2>(p, t, n0, smem);
+    else if (steps == 3) product<F, UP, COLS, 3>(p, t, n0, smem);
+    else product<F, UP, COLS, 4>(p, t, n0, smem);
 }
 
-template <Format F, bool UP, int COLS>
+template <Format F, bool UP, int COLS, int MAX>
 hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
-    constexpr int kChannels = UP ? COLS / 2 : COLS;
-    // tiles that any routing can give: no more than entries, and every expert may end in a short one
-    const int64_t entries = (int64_t)h.T * h.K, tiles = entries / kRows + h.El;
-    hipLaunchKernelGGL((k_stream<F, UP, COLS>), dim3((unsigned)((tiles < entries ? tiles : entries) * ((p.N + kChannels - 1) / kChannels))),
-                       dim3(kThreads), 0, stream, p);
+    constexpr int kChannels = UP ? COLS / 2 : COLS, kRows = MAX * 16;
+    // tiles that any routing can give: every expert with rows may end in a short one
+    const int64_t tiles = ((int64_t)h.T * h.K + (int64_t)(kRows - 1) * busy_experts(h)) / kRows;
+    hipLaunchKernelGGL((k_stream<F, UP, COLS, MAX>), dim3((unsigned)(tiles * ((p.N + kChannels - 1) / kChannels))), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
 // 64 weight rows per workgroup, or 32 (bf16) where that leaves the chip short of workgroups or, in the down projection, a
-// few rows per expert make more and smaller ones the better stream.  Measured, 32 experts of 7168 x 2048: down projection
-// at 2 rows per expert 171 us with 64, 160 with 32; at 16 rows 180 and 196; gate and up 297 and 295, 327 and 388.
-// 8 experts of 256 x 512, 32 rows each: 7.0 and 6.0 us, down 7.2 and 6.4.
+// few rows per expert make more and smaller ones the better stream; then it takes 16 rows.  Measured, 32 experts of 7168 x
+// 2048: down projection at 2 rows per expert 171 us with 64 weight rows, 162 with 32, 153 with 16 rows too; at 8 rows 178,
+// 167 and 170; at 16 rows 180 and 196; gate and up 297 and 295, 327 and 388.  8 experts of 256 x 512, 32 rows each: 7.0 and
+// 6.0 us, down 7.2, 6.4 and 5.0.
+// e4m3, down: 32 rows, not 64, at 4 rows per expert 651 and 712 us (256 experts; with 16 rows 668), at 8 94 and 100 (32).
 bool narrow(const Handle& h, int N, bool up) {
     const int64_t blocks = (int64_t)busy_experts(h) * ((N + (up ? 31 : 63)) / (up ? 32 : 64));
     return blocks < 512 || (!up && mean_rows(h) <= 8);
@@ -243,15 +244,15 @@ bool narrow(const Handle& h, int N, bool up) {
 hipError_t launch_stream_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden,
                    a.hidden, row_pitch(a.inter)};
-    if (a.fp8) return stream_launch<kFp8, true, 64>(h, p, stream);
-    return narrow(h, a.inter, true) ? stream_launch<kBf16, true, 32>(h, p, stream) : stream_launch<kBf16, true, 64>(h, p, stream);
+    if (a.fp8) return stream_launch<kFp8, true, 64, 4>(h, p, stream);
+    return narrow(h, a.inter, true) ? stream_launch<kBf16, true, 32, 4>(h, p, stream) : stream_launch<kBf16, true, 64, 4>(h, p, stream);
 }
 
 hipError_t launch_stream_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter,
                    row_pitch(a.inter), a.hidden};
-    if (a.fp8) return stream_launch<kFp8, false, 64>(h, p, stream);
-    return narrow(h, a.hidden, false) ? stream_launch<kBf16, false, 32>(h, p, stream) : stream_launch<kBf16, false, 64>(h, p, stream);
+    if (a.fp8) return stream_launch<kFp8, false, 64, 2>(h, p, stream);
+    return narrow(h, a.hidden, false) ? stream_launch<kBf16, false, 32, 1>(h, p, stream) : stream_launch<kBf16, false, 64, 4>(h, p, stream);
 }
 
 }  // namespace ep

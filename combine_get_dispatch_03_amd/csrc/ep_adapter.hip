@@ -42,8 +42,6 @@ struct Params {
     uint16_t* out;
     float* part;          // [chunks][T][r]
     int32_t* tokens;      // many tokens: [tiles][64], a tile's tokens in the layout's order; else nullptr
-    const int64_t* ids;
-    int lo;
     int H, r, N;
     int chunk, chunks;    // hidden channels per chunk
 };
@@ -81,6 +79,8 @@ __device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, i
 // tokens[tile][m] for every token with an adapter.
 __global__ __launch_bounds__(kThreads) void k_tokens(Params p) {
     __shared__ int before[kMaxExperts];      // tiles of the adapters before each
+    __shared__ int start[kMaxExperts];       // their first rows
+    for (int e = threadIdx.x; e < p.El; e += kThreads) start[e] = p.psum[e];
     if (threadIdx.x < kWave) {
         const RowTiles<kRows, 0> tiles(p.cnt, p.psum, p.El);
         int at = tiles.incl - tiles.sum;
@@ -93,9 +93,16 @@ __global__ __launch_bounds__(kThreads) void k_tokens(Params p) {
     }
     __syncthreads();
     const int t = blockIdx.x * kThreads + threadIdx.x;
-    if (t >= p.T || p.slot[t] < 0) return;
-    const int e = (int)(p.ids[t] - p.lo);
-    p.tokens[(int64_t)before[e] * kRows + (p.slot[t] - p.psum[e])] = t;      // a tile's rows are consecutive, and so are tiles
+    if (t >= p.T) return;
+    const int slot = p.slot[t];
+    if (slot < 0) return;
+    int e = 0;                               // the last adapter that starts at or before the row: the others there are empty
+    for (int n = p.El; n > 1;) {
+        const int half = n / 2;
+        if (start[e + half] <= slot) e += half;
+        n -= half;
+    }
+    p.tokens[(int64_t)before[e] * kRows + (slot - start[e])] = t;      // a tile's rows are consecutive, and so are tiles
 }
 
 template <int NF, int MT>
@@ -405,8 +412,8 @@ hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t str
     const size_t parts = ((size_t)chunks * (size_t)h.T * (size_t)a.rank * sizeof(float) + 255) / 256 * 256;
     int32_t* tokens = h.T >= kManyTokens ? reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + parts) : nullptr;
     const Params p{h.ws.cnt_local, h.ws.psum, h.ws.slot, h.T, h.El, (const uint16_t*)a.x, (const uint16_t*)a.a,
-                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens, h.topk_idx,
-                   h.lo, a.hidden, a.rank, a.n_out, chunk, chunks};
+                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens,
+                   a.hidden, a.rank, a.n_out, chunk, chunks};
     if (tokens) {
         hipLaunchKernelGGL(k_tokens, dim3((unsigned)((h.T + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, p);
         const hipError_t e = hipGetLastError();

@@ -266,15 +266,15 @@ hipError_t launch_expert_ffn_backward(const Handle& h, const FfnBackwardArgs& a,
     if (h.T > 0) {
         const Params dg{h.ws.cnt_local, h.ws.psum, h.El, dy, (const uint16_t*)a.w2, a.dp, a.h, const_cast<float*>(a.pre), a.hidden, a.inter};
         e = rows_launch<kDownGrad>(h, dg, stream);
-        if (e == hipSuccess && a.dx) {
-            const Params ig{h.ws.cnt_local, h.ws.psum, h.El, a.dp, (const uint16_t*)a.w13, (uint16_t*)a.dx, nullptr, nullptr, a.hidden, a.inter};
-            e = rows_launch<kInGrad>(h, ig, stream);
-        }
     }
     if (e == hipSuccess && a.dw2) e = weights_launch(h, dy, a.h, (uint16_t*)a.dw2, a.hidden, a.inter, a.hidden, row_pitch(a.inter), stream);
     if (e == hipSuccess && a.dw13)
         e = weights_launch(h, a.dp, (const uint16_t*)a.x, (uint16_t*)a.dw13, 2 * a.inter, a.hidden,
                            row_pitch(2 * a.inter), a.hidden, stream);
+    if (e == hipSuccess && a.dx && h.T > 0) {
+        const Params ig{h.ws.cnt_local, h.ws.psum, h.El, a.dp, (const uint16_t*)a.w13, (uint16_t*)a.dx, nullptr, nullptr, a.hidden, a.inter};
+        e = rows_launch<kInGrad>(h, ig, stream);
+    }
     return e;
 }
 

@@ -2,13 +2,15 @@
 MI355X (gfx950) GPU.
 
 The functions keep the C names (ep_get_layout, ep_dispatch, ep_layout_dispatch, ep_combine, ep_combine_tokens,
-ep_dispatch_rows, ep_combine_reduce, ep_handle_free, ep_recv_capacity, ep_layout_workspace_bytes).  They only marshal arguments: tensors become device pointers, the stream is
+ep_dispatch_rows, ep_combine_reduce, ep_expert_ffn, ep_expert_ffn_backward, ep_combine_backward, ep_adapter,
+ep_handle_free, ep_recv_capacity and the ep_*_workspace_bytes).  They only marshal arguments: tensors become device pointers, the stream is
 torch's current HIP stream, and output tensors are allocated by torch when the caller does not pass them.
 Every step of the path runs in the HIP kernels of the library; there is no other implementation, and if
 the library is not built or cannot be loaded the import of this binding fails.
 
     h, lay = ep_get_layout(topk_idx, num_experts=256, expert_alignment=128)
     d = ep_dispatch(h, x, topk_weights, fp8=True, do_zero_padding=True)
+    y = ep_expert_ffn(h, d["recv_x"], w13, w2, d["recv_x_scales"], w13_scales, w2_scales)
     out = ep_combine(h, y, topk_weights, bias=None)
 """
 from __future__ import annotations

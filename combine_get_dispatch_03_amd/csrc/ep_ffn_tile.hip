@@ -11,8 +11,8 @@
 // GHz here): they are busy 68% of the cycles, 56% in k_weights, whose sums are short and stores many (without the stores
 // 1.59 instead of 1.83 ms).  No bank conflicts in LDS.  With few rows, by the weights' bytes.
 // Measured, 32 experts of 7168 x 2048, 32768 rows (TFLOP/s): gate and up 1.53 ms (1256), down 0.79 (1216), down's grad
-// 0.97 (990), input's grad 1.57 (1225), dW13 1.80 (1070), dW2 0.96 (1000).  20 experts of 2112 x 1352, 12 with rows, 2331
-// rows: 68, 50, 64, 74, 91 and 52 us.
+// 0.97 (990), input's grad 1.57 (1225), dW13 1.80 (1070), dW2 0.96 (1000).  20 experts of 2112 x 1352, 2211
+// rows, 33 to 540 each: 55, 45, 67, 87, 90 and 51 us.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"

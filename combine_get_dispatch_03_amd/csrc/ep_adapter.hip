@@ -5,8 +5,8 @@
 // Two kernels, both over tiles of up to 64 tokens of one adapter (the layout's segments), so an adapter's matrices are
 // read once per 64 of its tokens and not once per token:
 //   shrink   v: the tile's tokens against A_a's rows.  hidden is split over workgroups until the grid fills the chip (a
-//            decode batch has few tiles), and over a workgroup's four waves; each workgroup leaves its partial sums per
-//            token in the workspace.
+//            decode batch has few tiles), and over a workgroup's four waves; each workgroup leaves its partial sums
+//            in the workspace, tile by tile, and the first of a tile which tokens they are.
 //   expand   the partial sums are added in order, scaled and rounded to bf16 in LDS; then B_a's rows times v, added to
 //            base and stored.  More workgroups copy base where a token has no adapter.
 // Both are bound by memory (x and A; base, out and B): matrix instructions only keep the arithmetic out of the way.
@@ -40,39 +40,54 @@ struct Params {
     const float* scales;
     const uint16_t* base;
     uint16_t* out;
-    float* part;          // [chunks][T][r]
-    int32_t* tokens;      // many tokens: [tiles][64], a tile's tokens in the layout's order; else nullptr
+    float* part;          // [chunks][tiles][64][r]
+    int32_t* tokens;      // [tiles][64], a tile's tokens in the layout's order
+    int tiles;            // that any routing can give
+    bool listed;          // tokens come from k_tokens (many tokens), not from shrink
     int H, r, N;
     int chunk, chunks;    // hidden channels per chunk
 };
 
-// Tokens of a tile, in the layout's order, to LDS.  The thread's first four slots are loaded at the start of the kernel,
-// before the tile is known.  Ends with a barrier.
-__device__ __forceinline__ i32x4 first_slots(const Params& p) {
-    const int i = threadIdx.x;
-    return p.tokens == nullptr && i < p.T / 4 ? reinterpret_cast<const i32x4*>(p.slot)[i] : i32x4{-1, -1, -1, -1};
+// From so many tokens on their tiles are worked out once, by a kernel of its own (3 us, and a launch): a tile's own search
+// is 4 bytes a token, and all searches together go with the square of the tokens.
+constexpr int kManyTokens = 8192;
+
+// The thread's part of the layout's map, all of it requested at the start of the kernel, before the tile is known: with one
+// piece at the start and the others one by one after it, shrink and expand took 3 us longer at 4096 tokens.
+struct Slots {
+    i32x4 quad[kManyTokens / 4 / kThreads];
+    int rest;
+};
+__device__ __forceinline__ Slots load_slots(const Params& p) {
+    Slots s;
+    const int quads = p.T / 4;
+#pragma unroll
+    for (int u = 0; u < kManyTokens / 4 / kThreads; ++u) {
+        const int i = u * kThreads + (int)threadIdx.x;
+        s.quad[u] = !p.listed && i < quads ? reinterpret_cast<const i32x4*>(p.slot)[i] : i32x4{-1, -1, -1, -1};
+    }
+    const int i = quads * 4 + (int)threadIdx.x;
+    s.rest = !p.listed && i < p.T ? p.slot[i] : -1;
+    return s;
 }
-__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int tile, i32x4 first, int* tok) {
-    if (p.tokens != nullptr) {
+// Tokens of a tile, in the layout's order, to LDS.  Ends with a barrier.
+__device__ __forceinline__ void find_tokens(const Params& p, const RowTile& t, int tile, const Slots& slots, int* tok) {
+    if (p.listed) {
         if ((int)threadIdx.x < t.rows) tok[threadIdx.x] = p.tokens[(int64_t)tile * kRows + threadIdx.x];
         __syncthreads();
         return;
     }
-    const int quads = p.T / 4;
-    const i32x4* q = reinterpret_cast<const i32x4*>(p.slot);
     auto put = [&](int s, int token) {
         const uint32_t m = (uint32_t)(s - t.row0);
         if (m < (uint32_t)t.rows) tok[m] = token;
     };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) put(first[j], threadIdx.x * 4 + j);
-    for (int i = threadIdx.x + kThreads; i < quads; i += kThreads) {
-        const i32x4 s = q[i];
+    for (int u = 0; u < kManyTokens / 4 / kThreads; ++u) {
+        if (u * kThreads * 4 >= p.T) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put(s[j], i * 4 + j);
+        for (int j = 0; j < 4; ++j) put(slots.quad[u][j], (u * kThreads + (int)threadIdx.x) * 4 + j);
     }
-    const int rest = quads * 4 + (int)threadIdx.x;
-    if (rest < p.T) put(p.slot[rest], rest);
+    put(slots.rest, p.T / 4 * 4 + (int)threadIdx.x);
     __syncthreads();
 }
 
@@ -106,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void k_tokens(Params p) {
 }
 
 template <int NF, int MT>
-__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int tile, int chunk, i32x4 slots, int* tok, float* sums) {
+__device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int tile, int chunk, const Slots& slots, int* tok, float* sums) {
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
     const uint16_t* f[NF];
     bool f_there[NF];
@@ -137,6 +152,7 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ti
     };
     load_f(next, first);       // A's rows do not depend on the tokens
     find_tokens(p, t, tile, slots, tok);
+    if (chunk == 0 && !p.listed && (int)threadIdx.x < t.rows) p.tokens[(int64_t)tile * kRows + threadIdx.x] = tok[threadIdx.x];
     const uint16_t* s[MT];
     bool s_there[MT];
 #pragma unroll
@@ -180,7 +196,7 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ti
             f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(sums + (w * 16 + m) * kPitch + n4);
-            *reinterpret_cast<f32x4*>(p.part + ((int64_t)chunk * p.T + tok[a * 16 + m]) * p.r + n4) = v;
+            *reinterpret_cast<f32x4*>(p.part + (((int64_t)chunk * p.tiles + tile) * kRows + a * 16 + m) * p.r + n4) = v;
         }
     }
 }
@@ -189,7 +205,7 @@ template <int NF>
 __global__ __launch_bounds__(kThreads) void k_shrink(Params p) {
     __shared__ __align__(16) float sums[kWaves * 16 * (NF * 16 + 4)];
     __shared__ int tok[kRows];
-    const i32x4 slots = first_slots(p);
+    const Slots slots = load_slots(p);
     const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     const int tile = blockIdx.x / p.chunks;
     if (tile >= tiles.total) return;
@@ -200,17 +216,24 @@ __global__ __launch_bounds__(kThreads) void k_shrink(Params p) {
     else shrink<NF, 4>(p, t, tile, chunk, slots, tok, sums);
 }
 
+// What the lanes of a wave wrote to LDS is there for all of them, and what they read has been read.
+__device__ __forceinline__ void wave_meets() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // NK: steps of 32 over the rank.  A workgroup takes `steps` times 256 channels.
 template <int NK>
-__global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, int steps) {
+__global__ __launch_bounds__(kThreads) void k_expand(Params p, int steps) {
     constexpr int kPitch = NK * 32 + 8;
     __shared__ __align__(16) uint16_t v[kRows * kPitch];
     __shared__ __align__(16) f32x4 shared_sums[kThreads];
-    __shared__ int tok[kRows];
+    constexpr int kTurnPitch = 64 + 4;
+    __shared__ __align__(16) float turn[kWaves][16 * kTurnPitch];
     const int cols = (p.N + kOut * steps - 1) / (kOut * steps), tile = blockIdx.x / cols, first = blockIdx.x % cols * kOut * steps;
     const int last = min(p.N, first + kOut * steps);
-    if (tile >= max_tiles) {      // tokens without an adapter: base as it is
-        const int t0 = (tile - max_tiles) * kRows, width = (last - first) / 8;
+    if (tile >= p.tiles) {      // tokens without an adapter: base as it is
+        const int t0 = (tile - p.tiles) * kRows, width = (last - first) / 8;
         uint64_t bare = ballot(t0 + lane_id() < p.T && p.slot[min(t0 + lane_id(), p.T - 1)] < 0);
         for (int i = 0; bare != 0; ++i, bare &= bare - 1) {
             if (i % kWaves != wave_id()) continue;
@@ -220,13 +243,16 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
         }
         return;
     }
-    const i32x4 slots = first_slots(p);
     const RowTiles<kRows> tiles(p.cnt, p.psum, p.El);
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
-    // 64 channels per wave and step, dealt to the fragments' rows as channel_of() says: a lane ends up with twice 8
-    // consecutive channels of a token.
+    // A wave's product is 64 channels of 16 tokens at a time, a lane's share of it four channels of a token 16 lanes from the
+    // next.  It goes round by LDS: base is read and out written with eight lanes on a token's 128 bytes, which the address
+    // unit takes at four lanes a cycle; lane by lane from as many rows it takes one.
+    int tok[kRows / 8];       // of the rows that the lane stores
+#pragma unroll
+    for (int a = 0; a < kRows / 8; ++a) tok[a] = a * 8 + (lane >> 3) < t.rows ? p.tokens[(int64_t)tile * kRows + a * 8 + (lane >> 3)] : 0;
     struct Rows {
         i32x4 v[4][NK];
     };
@@ -234,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
         Rows f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int n = nw + channel_of(b, r);
+            const int n = nw + b * 16 + r;
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 f.v[b][j] = i32x4{0, 0, 0, 0};
@@ -245,23 +271,22 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
         return f;
     };
     struct Base {
-        i32x4 v[kRows / 16][2];
+        i32x4 v[kRows / 8];
     };
+    const int n_in = (lane & 7) * 8;
     auto load_base = [&](int nw) {
         Base o;
 #pragma unroll
-        for (int a = 0; a < kRows / 16; ++a)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                o.v[a][j] = i32x4{0, 0, 0, 0};
-                const int m = a * 16 + r, n = nw + j * 32 + g * 8;
-                if (p.base && m < t.rows && n < last) o.v[a][j] = *reinterpret_cast<const i32x4*>(p.base + (int64_t)tok[m] * p.N + n);
-            }
+        for (int a = 0; a < kRows / 8; ++a) {
+            o.v[a] = i32x4{0, 0, 0, 0};
+            if (p.base && a * 8 + (lane >> 3) < t.rows && nw + n_in < last)
+                o.v[a] = *reinterpret_cast<const i32x4*>(p.base + (int64_t)tok[a] * p.N + nw + n_in);
+        }
         return o;
     };
     int nw = first + wave * 64;
     Rows next = load_b(nw);
-    find_tokens(p, t, tile, slots, tok);
+    Base next_base = load_base(nw);
     const float scale = p.scales ? p.scales[t.expert] : 1.0f;
     // v of the tile's tokens, zeros past the last token and past the rank, 4 ranks per item; the chunks are added in a fixed
     // order.  A few tokens: the workgroup's threads share an item's chunks and meet in LDS.  Many: two items a thread,
@@ -269,13 +294,13 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
     const int items = ((t.rows + 15) & ~15) * NK * 8;
     auto item = [&](int i, const float** from) {
         const int m = i / (NK * 8), k4 = i % (NK * 8) * 4;
-        *from = m < t.rows && k4 < p.r ? p.part + (int64_t)tok[m] * p.r + k4 : nullptr;
+        *from = m < t.rows && k4 < p.r ? p.part + ((int64_t)tile * kRows + m) * p.r + k4 : nullptr;
         return m * kPitch + k4;
     };
     auto put = [&](int at, f32x4 sum) {
         *reinterpret_cast<i32x2*>(v + at) = i32x2{(int)pack_bf16x2(sum[0] * scale, sum[1] * scale), (int)pack_bf16x2(sum[2] * scale, sum[3] * scale)};
     };
-    const int64_t stride = (int64_t)p.T * p.r;
+    const int64_t stride = (int64_t)p.tiles * kRows * p.r;
     if (t.rows <= 16) {
         // only rows that exist are shared out; the others' v is zero
         constexpr int kPerRow = NK * 8;
@@ -339,7 +364,6 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
                 if (at[q] >= 0) put(at[q], sum[q]);
         }
     }
-    Base next_base = load_base(nw);
     __syncthreads();
     for (; nw < last; nw += kOut) {
         const Rows cur = next;
@@ -351,28 +375,32 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int max_tiles, in
 #pragma unroll
         for (int a = 0; a < kRows / 16; ++a) {
             if (a * 16 >= t.rows) break;
-            const int m = a * 16 + r, n = nw + g * 8;
             f32x4 acc[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
-                const bf16x8 sv = *reinterpret_cast<const bf16x8*>(v + m * kPitch + j * 32 + g * 8);
+                const bf16x8 sv = *reinterpret_cast<const bf16x8*>(v + (a * 16 + r) * kPitch + j * 32 + g * 8);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
                     acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.v[b][j]), sv, acc[b], 0, 0, 0);
             }
-            const int64_t at = m < t.rows ? (int64_t)tok[m] * p.N + n : 0;
+            wave_meets();
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int b = 0; b < 4; ++b) *reinterpret_cast<f32x4*>(turn[wave] + r * kTurnPitch + b * 16 + g * 4) = acc[b];
+            wave_meets();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m8 = a * 2 + h;
+                const float* at = turn[wave] + (h * 8 + (lane >> 3)) * kTurnPitch + n_in;
+                const f32x4 d[2] = {*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4)};
                 i32x4 o;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4 d = acc[j * 2 + i / 2];
-                    const uint32_t two = (uint32_t)base.v[a][j][i];
-                    o[i] = (int)pack_bf16x2(bf16lo(two) + d[i % 2 * 2], bf16hi(two) + d[i % 2 * 2 + 1]);
+                    const uint32_t two = (uint32_t)base.v[m8][i];
+                    o[i] = (int)pack_bf16x2(bf16lo(two) + d[i / 2][i % 2 * 2], bf16hi(two) + d[i / 2][i % 2 * 2 + 1]);
                 }
-                if (m < t.rows && n + j * 32 < last) *reinterpret_cast<i32x4*>(p.out + at + j * 32) = o;
+                if (m8 * 8 + (lane >> 3) < t.rows && nw + n_in < last) *reinterpret_cast<i32x4*>(p.out + (int64_t)tok[m8] * p.N + nw + n_in) = o;
             }
         }
     }
@@ -396,25 +424,25 @@ int chunk_of(int T, int El, int H) {
 
 }  // namespace
 
-// From so many tokens on their tiles are worked out once, by a kernel of its own (3 us, and a launch): a tile's own search
-// is 4 bytes a token, 64 KiB of L2 reads at 16384 tokens, and all searches together go with the square of the tokens.
-static constexpr int kManyTokens = 8192;
+// The workspace: partial sums, then the tiles' tokens.
+static size_t part_bytes(int chunks, int tiles, int rank) {
+    return ((size_t)chunks * (size_t)tiles * kRows * (size_t)rank * sizeof(float) + 255) / 256 * 256;
+}
 
 size_t adapter_workspace_bytes(int T, int El, int hidden, int rank) {
-    const int chunk = chunk_of(T, El, hidden), chunks = (hidden + chunk - 1) / chunk;
-    const size_t parts = ((size_t)chunks * (size_t)T * (size_t)rank * sizeof(float) + 255) / 256 * 256;
-    return parts + (T >= kManyTokens ? (size_t)max_tiles(T, El) * kRows * sizeof(int32_t) : 256);
+    const int chunk = chunk_of(T, El, hidden), chunks = (hidden + chunk - 1) / chunk, tiles = max_tiles(T, El);
+    return part_bytes(chunks, tiles, rank) + (size_t)(tiles > 0 ? tiles : 1) * kRows * sizeof(int32_t);
 }
 
 hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t stream) {
     if (h.T == 0) return hipSuccess;
     const int chunk = chunk_of(h.T, h.El, a.hidden), chunks = (a.hidden + chunk - 1) / chunk, tiles = max_tiles(h.T, h.El);
-    const size_t parts = ((size_t)chunks * (size_t)h.T * (size_t)a.rank * sizeof(float) + 255) / 256 * 256;
-    int32_t* tokens = h.T >= kManyTokens ? reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + parts) : nullptr;
+    int32_t* tokens = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + part_bytes(chunks, tiles, a.rank));
+    const bool listed = h.T >= kManyTokens;
     const Params p{h.ws.cnt_local, h.ws.psum, h.ws.slot, h.T, h.El, (const uint16_t*)a.x, (const uint16_t*)a.a,
-                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens,
+                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens, tiles, listed,
                    a.hidden, a.rank, a.n_out, chunk, chunks};
-    if (tokens) {
+    if (listed) {
         hipLaunchKernelGGL(k_tokens, dim3((unsigned)((h.T + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -431,9 +459,9 @@ hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t str
     // as many channels per workgroup as leave the chip full: a workgroup adds up v before it starts
     const int columns = (a.n_out + kOut - 1) / kOut, want = (kExpandBlocks + tiles - 1) / tiles, steps = columns > want ? (columns + want - 1) / want : 1;
     const dim3 expand_grid((unsigned)((int64_t)(tiles + bare) * ((columns + steps - 1) / steps)));
-    if (a.rank <= 32) hipLaunchKernelGGL(k_expand<1>, expand_grid, block, 0, stream, p, tiles, steps);
-    else if (a.rank <= 64) hipLaunchKernelGGL(k_expand<2>, expand_grid, block, 0, stream, p, tiles, steps);
-    else hipLaunchKernelGGL(k_expand<4>, expand_grid, block, 0, stream, p, tiles, steps);
+    if (a.rank <= 32) hipLaunchKernelGGL(k_expand<1>, expand_grid, block, 0, stream, p, steps);
+    else if (a.rank <= 64) hipLaunchKernelGGL(k_expand<2>, expand_grid, block, 0, stream, p, steps);
+    else hipLaunchKernelGGL(k_expand<4>, expand_grid, block, 0, stream, p, steps);
     return hipGetLastError();
 }
 

@@ -10,8 +10,8 @@
 //   expand   the partial sums are added in order, scaled and rounded to bf16 in LDS; then B_a's rows times v, added to
 //            base and stored.  More workgroups copy base where a token has no adapter.
 // Both are bound by memory (x and A; base, out and B): matrix instructions only keep the arithmetic out of the way.
-// Measured, 7168 channels in and out: 4096 tokens, 8 adapters of rank 64, shrink 26 us (2.3 TB/s), expand 34 us (3.5 TB/s);
-// 128 tokens, 32 adapters of rank 16, 5.5 and 7.0 us; one token, rank 64, 2112 out, 4.8 and 5.8 us: latency, with each
+// Measured, 7168 channels in and out: 4096 tokens, 8 adapters of rank 64, shrink 25 us (2.4 TB/s), expand 31 us (3.8 TB/s);
+// 128 tokens, 32 adapters of rank 16, 5.4 and 6.7 us; one token, rank 64, 2112 out, 4.6 and 5.7 us: latency, with each
 // kernel's chain of dependent loads (segment, token, row).
 // The layout maps tokens to rows; a tile finds its tokens by going over that map once (4 bytes a token, from L2), or, where
 // there are many tokens, a kernel before turns the map round for all tiles.
@@ -52,8 +52,8 @@ struct Params {
 // is 4 bytes a token, and all searches together go with the square of the tokens.
 constexpr int kManyTokens = 8192;
 
-// The thread's part of the layout's map, all of it requested at the start of the kernel, before the tile is known: with one
-// piece at the start and the others one by one after it, shrink and expand took 3 us longer at 4096 tokens.
+// The thread's part of the layout's map, all of it requested at the start of the kernel, before the tile is known (4096
+// tokens: shrink 25.0 us, 25.8 with one piece at the start and the others one by one).
 struct Slots {
     i32x4 quad[kManyTokens / 4 / kThreads];
     int rest;
@@ -123,12 +123,23 @@ __global__ __launch_bounds__(kThreads) void k_tokens(Params p) {
 template <int NF, int MT>
 __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int tile, int chunk, const Slots& slots, int* tok, float* sums) {
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
+    // Up to 32 tokens: four lanes beside each other load 64 bytes of a row, and the fragments are put right by an exchange
+    // of lanes; 128 tokens of 32 adapters of rank 16 5.4 us, 5.9 without; 64 tokens a tile 25.6 and 24.9 us.
+    constexpr bool kTurn = MT <= 2;
+    const int lr = kTurn ? lane >> 2 : r, lg = kTurn ? lane & 3 : g;
+    auto turn = [&](i32x4 v) {
+        if constexpr (kTurn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_ds_bpermute((r * 4 + g) * 4, v[i]);
+        }
+        return v;
+    };
     const uint16_t* f[NF];
     bool f_there[NF];
 #pragma unroll
     for (int b = 0; b < NF; ++b) {
-        f_there[b] = b * 16 + r < p.r;
-        f[b] = p.a + ((int64_t)t.expert * p.r + (f_there[b] ? b * 16 + r : 0)) * p.H + g * 8;
+        f_there[b] = b * 16 + lr < p.r;
+        f[b] = p.a + ((int64_t)t.expert * p.r + (f_there[b] ? b * 16 + lr : 0)) * p.H + lg * 8;
     }
     f32x4 acc[MT][NF];
 #pragma unroll
@@ -147,7 +158,7 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ti
 #pragma unroll
             for (int b = 0; b < NF; ++b) {
                 v.f[b][j] = i32x4{0, 0, 0, 0};
-                if (k + j * 32 + g * 8 < end && f_there[b]) v.f[b][j] = *(const i32x4*)(f[b] + k + j * 32);
+                if (k + j * 32 + lg * 8 < end && f_there[b]) v.f[b][j] = *(const i32x4*)(f[b] + k + j * 32);
             }
     };
     load_f(next, first);       // A's rows do not depend on the tokens
@@ -157,8 +168,8 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ti
     bool s_there[MT];
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
-        s_there[a] = a * 16 + r < t.rows;
-        s[a] = p.x + (int64_t)tok[s_there[a] ? a * 16 + r : 0] * p.H + g * 8;
+        s_there[a] = a * 16 + lr < t.rows;
+        s[a] = p.x + (int64_t)tok[s_there[a] ? a * 16 + lr : 0] * p.H + lg * 8;
     }
     auto load_s = [&](Step& v, int k) {
 #pragma unroll
@@ -166,12 +177,19 @@ __device__ __forceinline__ void shrink(const Params& p, const RowTile& t, int ti
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
                 v.s[a][j] = i32x4{0, 0, 0, 0};
-                if (k + j * 32 + g * 8 < end && s_there[a]) v.s[a][j] = *(const i32x4*)(s[a] + k + j * 32);
+                if (k + j * 32 + lg * 8 < end && s_there[a]) v.s[a][j] = *(const i32x4*)(s[a] + k + j * 32);
             }
     };
     load_s(next, first);
     for (int k = first; k < end; k += kChunkUnit) {
-        const Step cur = next;
+        Step cur;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int b = 0; b < NF; ++b) cur.f[b][j] = turn(next.f[b][j]);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) cur.s[a][j] = turn(next.s[a][j]);
+        }
         load_f(next, k + kChunkUnit);     // past the end: nothing is read
         load_s(next, k + kChunkUnit);
 #pragma unroll

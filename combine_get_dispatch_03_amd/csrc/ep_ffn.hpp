@@ -1,6 +1,8 @@
 // ep_ffn.hpp -- the expert block's launchers and the rules that choose between them.
 #pragma once
 
+#include <cmath>
+
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
 
@@ -12,21 +14,6 @@ inline double mean_rows(const Handle& h) { return (double)h.T * h.K / h.E; }
 // Local experts that get a row, at most.
 inline int busy_experts(const Handle& h) { return (int64_t)h.T * h.K < h.El ? h.T * h.K : h.El; }
 
-// Weights streamed past the rows (ep_ffn_stream.hip) rather than tiles of both through LDS: where an expert has so few rows
-// that its weights' bytes decide, or where the tiles would leave most CUs idle.  `cols`: tiles side by side in the
-// product's output.  Measured, 32 experts of 7168 x 2048, us streamed / tiled at so many rows per expert:
-//              gate, up, bf16   down, bf16    gate, up, e4m3   down, e4m3
-//    2 rows    297 / 303        171 / 209     156 / 154         88 / 104
-//    8         313 / 318        178 / 217     166 / 164         98 / 107
-//   16         327 / 320        180 / 219     185 / 167        111 / 109
-//   32         367 / 323        204 / 224     226 / 169        133 / 120
-//   64         590 / 333        305 / 233     373 / 182        234 / 140
-// (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
-inline bool few_rows(const Handle& h, double limit, int cols) {
-    const double rows = mean_rows(h);
-    return rows < limit || (rows < 64 && (int64_t)busy_experts(h) * cols < 192);
-}
-
 // Whether the gate and up projection's weights are worth marking as read once (copy16_to_lds): one row tile per expert, whole
 // lines, and more of them than the 256 MB memory-side cache keeps beside the rest of a layer.  us with the mark and without: 32 experts of 7168 x 2048,
 // bf16, 16 rows each 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373, 900 rows (four row tiles) 1409 and 1262; 256
@@ -35,6 +22,34 @@ inline bool few_rows(const Handle& h, double limit, int cols) {
 inline bool weights_once(const Handle& h, const FfnArgs& a) {
     const int64_t row = (int64_t)a.hidden * (a.fp8 ? 1 : 2);
     return mean_rows(h) <= (a.fp8 ? 64 : 128) && row % 128 == 0 && row * 2 * a.inter * h.El > (128ll << 20);
+}
+
+// Weights streamed past the rows (ep_ffn_stream.hip) rather than tiles of both through LDS: where an expert has so few rows
+// that its weights' bytes decide, or where the tiles would leave most CUs idle.  `cols`: tiles side by side in the
+// product's output.  Measured, 32 experts of 7168 x 2048, us streamed / tiled at so many rows per expert (gate and up with
+// its weights marked as read once; in brackets tiled without the mark):
+//              gate, up, bf16       down, bf16    gate, up, e4m3       down, e4m3
+//    2 rows    296 / 279 (303)      154 / 206     155 / 143 (154)       81 / 105
+//    8         312 / 294 (318)      170 / 215     165 / 154 (164)       93 / 108
+//   16         326 / 298 (320)      179 / 219     186 / 158 (167)      109 / 111
+//   32         366 / 304 (323)      203 / 224     225 / 166 (169)      154 / 118
+//   64         584 / 317 (333)      299 / 235     366 / 187 (182)      272 / 142
+// (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
+inline bool few_rows(const Handle& h, double limit, int cols) {
+    const double rows = mean_rows(h);
+    return rows < limit || (rows < 64 && (int64_t)busy_experts(h) * cols < 192);
+}
+
+// The same for the gate and up projection.  With weights marked as read once both forms run at the memory's rate, and what
+// decides is how much of its last round the tiles fill, of those experts that uniform routing gives a row.  Measured as
+// above, us streamed / tiled: 1 token (8 experts, half a round) 80 / 117 bf16 and 41 / 59 e4m3; 2 tokens (0.88 of a round)
+// 142 / 131 and 75 / 66; 3 (1.16 rounds) 183 / 247 and 108 / 126; 4 (1.37) 214 / 254 and 114 / 128; 8 (1.80) 296 / 279 and 155 / 143.
+inline bool few_rows_up(const Handle& h, const FfnArgs& a) {
+    const int cols = (a.inter + 127) / 128;
+    if (!weights_once(h, a)) return few_rows(h, a.fp8 ? 4 : 12, cols);
+    if (mean_rows(h) >= 48) return false;
+    const double idle = std::pow(1.0 - (h.K < h.E ? (double)h.K / h.E : 1.0), h.T), rounds = h.El * (1.0 - idle) * cols / 256;
+    return rounds < 0.87 * std::ceil(rounds);
 }
 
 hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream);           // bf16

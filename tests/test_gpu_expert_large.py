@@ -1,4 +1,5 @@
-"""Offsets past 32 bits and calls side by side: the expert block, the combine's gradient and the adapters.
+"""Offsets past 32 bits, weights larger than the caches, calls side by side: the expert block, the combine's gradient and
+the adapters.
 
 The rows of a layout with a large alignment lie gigabytes apart; which kernels run and in which order they add depends on
 the sizes of the routing alone, so its results are those of the dense layout bit for bit.
@@ -10,6 +11,7 @@ import torch
 
 import expert_reference as R
 import test_gpu_adapter as A
+import test_gpu_expert_ffn as F
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -72,6 +74,21 @@ def test_rows_far_apart(ep, T, fmt):
         del xa
     for near, away in zip(*results):
         assert torch.isfinite(near.float()).all() and torch.equal(near, away)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("shape", [
+    # T, H, I, E, ranks, rank, K, A, routing; w13 holds 151 MB in e4m3: read past the caches, on one row tile each,
+    # on several, streamed where a call has too few tiles, and on a rank that owns half the experts
+    (60, 2048, 1152, 32, 1, 0, 4, 1, "uniform"),
+    (500, 4096, 1152, 16, 1, 0, 2, 16, "zipf"),
+    (1, 4096, 1152, 16, 1, 0, 3, 1, "uniform"),
+    (90, 2048, 1152, 64, 2, 1, 4, 8, "holes"),
+], ids=["tiles", "uneven", "one_token", "second_rank"])
+def test_weights_past_the_caches(ep, shape, fmt):
+    F.test_forward(ep, shape, fmt)
+    if fmt == "bf16":
+        F.test_backward(ep, shape)
 
 
 def test_adapter_tokens_far_apart(ep):

@@ -40,14 +40,19 @@ inline bool few_rows(const Handle& h, double limit, int cols) {
     return rows < limit || (rows < 64 && (int64_t)busy_experts(h) * cols < 192);
 }
 
-// The same for the gate and up projection.  With weights marked as read once both forms run at the memory's rate, and what
+// The same for the gate and up projection.  Without the mark: few rows, or so little work that a streamed product's finer
+// grid is what fills the chip, counted in 64 rows x 32 channels.  Measured, us streamed / tiled, bf16 and e4m3: 4 experts of 3328
+// x 384 with 70, 128 and 256 rows each (99, 143 and 239 such pieces) 23 / 45 and 21 / 32, 23 / 50 and 21 / 37, 41 / 60 and 21 /
+// 38; 8 of 2048 x 512, 100 rows (326) 28 / 33 and 18 / 24; 4 of 2048 x 1024, 256 rows (638) 50 / 42 and 27 / 25; 20 of 1352 x
+// 512, 80 rows (715) 29 / 26 and 25 / 17.  With weights marked as read once both forms run at the memory's rate, and what
 // decides is how much of its last round the tiles fill, of those experts that uniform routing gives a row.  Measured as
 // above, us streamed / tiled: 1 token (8 experts, half a round) 80 / 117 bf16 and 41 / 59 e4m3; 2 tokens (0.88 of a round)
 // 142 / 131 and 75 / 66; 3 (1.16 rounds) 183 / 247 and 108 / 126; 4 (1.37) 214 / 254 and 114 / 128; 8 (1.80) 296 / 279 and 155 / 143.
 inline bool few_rows_up(const Handle& h, const FfnArgs& a) {
+    const double rows = mean_rows(h);
+    if (!weights_once(h, a)) return rows < (a.fp8 ? 4 : 12) || (rows * h.El + 63.0 * busy_experts(h)) / 64 * ((a.inter + 31) / 32) < 400;
+    if (rows >= 48) return false;
     const int cols = (a.inter + 127) / 128;
-    if (!weights_once(h, a)) return few_rows(h, a.fp8 ? 4 : 12, cols);
-    if (mean_rows(h) >= 48) return false;
     const double idle = std::pow(1.0 - (h.K < h.E ? (double)h.K / h.E : 1.0), h.T), rounds = h.El * (1.0 - idle) * cols / 256;
     return rounds < 0.87 * std::ceil(rounds);
 }

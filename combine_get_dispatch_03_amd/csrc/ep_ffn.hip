@@ -5,13 +5,14 @@ namespace ep {
 
 hipError_t launch_expert_ffn(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     if (h.T == 0) return hipSuccess;
-    const hipError_t e = few_rows_up(h, a) ? launch_stream_up(h, a, stream)
-                         : a.fp8           ? launch_tile_fp8_up(h, a, stream)
-                                           : launch_tile_up(h, a, stream);
+    const FfnSizes s = sizes(h, a);
+    const hipError_t e = few_rows_up(s) ? launch_stream_up(h, a, stream)
+                         : a.fp8        ? launch_tile_fp8_up(h, a, stream)
+                                        : launch_tile_up(h, a, stream);
     if (e != hipSuccess) return e;
-    return few_rows(h, a.fp8 ? 16 : 48, (a.hidden + 255) / 256) ? launch_stream_down(h, a, stream)
-           : a.fp8                                              ? launch_tile_fp8_down(h, a, stream)
-                                                                : launch_tile_down(h, a, stream);
+    return few_rows_down(s) ? launch_stream_down(h, a, stream)
+           : a.fp8          ? launch_tile_fp8_down(h, a, stream)
+                            : launch_tile_down(h, a, stream);
 }
 
 }  // namespace ep

@@ -1,0 +1,64 @@
+// ep_ffn_rules.hpp -- which kernels a call of the expert block takes: plain host code on the call's sizes, so that a test can
+// ask it too.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+namespace ep {
+
+struct FfnSizes {
+    int T, K, E, El;
+    int hidden, inter;
+    bool fp8;
+};
+
+// Rows an expert gets on average.  The host knows sizes only, not the routing: of T * K entries, an expert's share.
+inline double mean_rows(const FfnSizes& s) { return (double)s.T * s.K / s.E; }
+
+// Local experts that get a row, at most.
+inline int busy_experts(const FfnSizes& s) { return (int64_t)s.T * s.K < s.El ? s.T * s.K : s.El; }
+
+// Whether the gate and up projection's weights are worth marking as read once (copy16_to_lds): one row tile per expert, whole
+// lines, and more of them than the 256 MB memory-side cache keeps beside the rest of a layer.  us with the mark and without: 32 experts of 7168 x 2048,
+// bf16, 16 rows each 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373, 900 rows (four row tiles) 1409 and 1262; 256
+// experts, e4m3, 4 rows 1103 and 1209, 128 rows 1681 and 1582; 20 experts of 2112 x 1352 (228 MB), 117 rows 68 and 85;
+// of 1344 x 512 (55 MB), 80 rows 28 and 23, of 1352 x 512 (rows of 2704 bytes) 39 and 27.
+inline bool weights_once(const FfnSizes& s) {
+    const int64_t row = (int64_t)s.hidden * (s.fp8 ? 1 : 2);
+    return mean_rows(s) <= (s.fp8 ? 64 : 128) && row % 128 == 0 && row * 2 * s.inter * s.El > (128ll << 20);
+}
+
+// Weights streamed past the rows (ep_ffn_stream.hip) rather than tiles of both through LDS: where an expert has so few rows
+// that its weights' bytes decide, or where the tiles would leave most CUs idle.  Measured, 32 experts of 7168 x 2048, us streamed / tiled at so many rows per expert (gate and up with
+// its weights marked as read once; in brackets tiled without the mark):
+//              gate, up, bf16       down, bf16    gate, up, e4m3       down, e4m3
+//    2 rows    296 / 279 (303)      154 / 206     155 / 143 (154)       81 / 105
+//    8         312 / 294 (318)      170 / 215     165 / 154 (164)       93 / 108
+//   16         326 / 298 (320)      179 / 219     186 / 158 (167)      109 / 111
+//   32         366 / 304 (323)      203 / 224     225 / 166 (169)      154 / 118
+//   64         584 / 317 (333)      299 / 235     366 / 187 (182)      272 / 142
+// (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
+inline bool few_rows_down(const FfnSizes& s) {
+    const double rows = mean_rows(s);
+    return rows < (s.fp8 ? 16 : 48) || (rows < 64 && (int64_t)busy_experts(s) * ((s.hidden + 255) / 256) < 192);
+}
+
+// The same for the gate and up projection.  Without the mark: few rows, or so little work that a streamed product's finer
+// grid is what fills the chip, counted in 64 rows x 32 channels.  Measured, us streamed / tiled, bf16 and e4m3: 4 experts of 3328
+// x 384 with 70, 128 and 256 rows each (99, 143 and 239 such pieces) 23 / 45 and 21 / 32, 23 / 50 and 21 / 37, 41 / 60 and 21 /
+// 38; 8 of 2048 x 512, 100 rows (326) 28 / 33 and 18 / 24; 4 of 2048 x 1024, 256 rows (638) 50 / 42 and 27 / 25; 20 of 1352 x
+// 512, 80 rows (715) 29 / 26 and 25 / 17.  With weights marked as read once both forms run at the memory's rate, and what
+// decides is how much of its last round the tiles fill, of those experts that uniform routing gives a row.  Measured as
+// above, us streamed / tiled: 1 token (8 experts, half a round) 80 / 117 bf16 and 41 / 59 e4m3; 2 tokens (0.88 of a round)
+// 142 / 131 and 75 / 66; 3 (1.16 rounds) 183 / 247 and 108 / 126; 4 (1.37) 214 / 254 and 114 / 128; 8 (1.80) 296 / 279 and 155 / 143.
+inline bool few_rows_up(const FfnSizes& s) {
+    const double rows = mean_rows(s);
+    if (!weights_once(s)) return rows < (s.fp8 ? 4 : 12) || (rows * s.El + 63.0 * busy_experts(s)) / 64 * ((s.inter + 31) / 32) < 400;
+    if (rows >= 48) return false;
+    const int cols = (s.inter + 127) / 128;
+    const double idle = std::pow(1.0 - (s.K < s.E ? (double)s.K / s.E : 1.0), s.T), rounds = s.El * (1.0 - idle) * cols / 256;
+    return rounds < 0.87 * std::ceil(rounds);
+}
+
+}  // namespace ep

@@ -220,10 +220,10 @@ __global__ __launch_bounds__(kThreads) void k_stream(Params p) {
 }
 
 template <Format F, bool UP, int COLS, int MAX>
-hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
+hipError_t stream_launch(const Handle& h, int busy, const Params& p, hipStream_t stream) {
     constexpr int kChannels = UP ? COLS / 2 : COLS, kRows = MAX * 16;
     // tiles that any routing can give: every expert with rows may end in a short one
-    const int64_t tiles = ((int64_t)h.T * h.K + (int64_t)(kRows - 1) * busy_experts(h)) / kRows;
+    const int64_t tiles = ((int64_t)h.T * h.K + (int64_t)(kRows - 1) * busy) / kRows;
     hipLaunchKernelGGL((k_stream<F, UP, COLS, MAX>), dim3((unsigned)(tiles * ((p.N + kChannels - 1) / kChannels))), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
@@ -234,9 +234,9 @@ hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
 // 167 and 170; at 16 rows 180 and 196; gate and up 297 and 295, 327 and 388.  8 experts of 256 x 512, 32 rows each: 7.0 and
 // 6.0 us, down 7.2, 6.4 and 5.0.
 // e4m3, down: 32 rows, not 64, at 4 rows per expert 651 and 712 us (256 experts; with 16 rows 668), at 8 94 and 100 (32).
-bool narrow(const Handle& h, int N, bool up) {
-    const int64_t blocks = (int64_t)busy_experts(h) * ((N + (up ? 31 : 63)) / (up ? 32 : 64));
-    return blocks < 512 || (!up && mean_rows(h) <= 8);
+bool narrow(const FfnSizes& s, int N, bool up) {
+    const int64_t blocks = (int64_t)busy_experts(s) * ((N + (up ? 31 : 63)) / (up ? 32 : 64));
+    return blocks < 512 || (!up && mean_rows(s) <= 8);
 }
 
 }  // namespace
@@ -244,15 +244,21 @@ bool narrow(const Handle& h, int N, bool up) {
 hipError_t launch_stream_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.x, a.x_scales, a.w13, a.w13_scales, a.h, a.pre, a.inter, a.hidden,
                    a.hidden, row_pitch(a.inter)};
-    if (a.fp8) return stream_launch<kFp8, true, 64, 4>(h, p, stream);
-    return narrow(h, a.inter, true) ? stream_launch<kBf16, true, 32, 4>(h, p, stream) : stream_launch<kBf16, true, 64, 4>(h, p, stream);
+    const FfnSizes s = sizes(h, a);
+    const int busy = busy_experts(s);
+    if (a.fp8) return stream_launch<kFp8, true, 64, 4>(h, busy, p, stream);
+    return narrow(s, a.inter, true) ? stream_launch<kBf16, true, 32, 4>(h, busy, p, stream)
+                                    : stream_launch<kBf16, true, 64, 4>(h, busy, p, stream);
 }
 
 hipError_t launch_stream_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, nullptr, a.w2, a.w2_scales, (uint16_t*)a.y, nullptr, a.hidden, a.inter,
                    row_pitch(a.inter), a.hidden};
-    if (a.fp8) return stream_launch<kFp8, false, 64, 2>(h, p, stream);
-    return narrow(h, a.hidden, false) ? stream_launch<kBf16, false, 32, 1>(h, p, stream) : stream_launch<kBf16, false, 64, 4>(h, p, stream);
+    const FfnSizes s = sizes(h, a);
+    const int busy = busy_experts(s);
+    if (a.fp8) return stream_launch<kFp8, false, 64, 2>(h, busy, p, stream);
+    return narrow(s, a.hidden, false) ? stream_launch<kBf16, false, 32, 1>(h, busy, p, stream)
+                                      : stream_launch<kBf16, false, 64, 4>(h, busy, p, stream);
 }
 
 }  // namespace ep

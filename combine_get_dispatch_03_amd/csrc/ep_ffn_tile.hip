@@ -252,7 +252,7 @@ hipError_t weights_launch(const Handle& h, const uint16_t* s, const uint16_t* f,
 
 hipError_t launch_tile_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, (const uint16_t*)a.w13, a.h, nullptr, a.pre, a.hidden, a.inter};
-    return weights_once(h, a) ? rows_launch<kGateUp, true>(h, p, stream) : rows_launch<kGateUp>(h, p, stream);
+    return weights_once(sizes(h, a)) ? rows_launch<kGateUp, true>(h, p, stream) : rows_launch<kGateUp>(h, p, stream);
 }
 
 hipError_t launch_tile_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

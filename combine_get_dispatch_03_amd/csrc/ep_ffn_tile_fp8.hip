@@ -179,7 +179,7 @@ hipError_t up_launch(const Handle& h, const FfnArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_tile_fp8_up(const Handle& h, const FfnArgs& a, hipStream_t stream) {
-    return weights_once(h, a) ? up_launch<true>(h, a, stream) : up_launch<false>(h, a, stream);
+    return weights_once(sizes(h, a)) ? up_launch<true>(h, a, stream) : up_launch<false>(h, a, stream);
 }
 
 hipError_t launch_tile_fp8_down(const Handle& h, const FfnArgs& a, hipStream_t stream) {

@@ -48,17 +48,29 @@ inline bool few_rows_down(const FfnSizes& s) {
 // grid is what fills the chip, counted in 64 rows x 32 channels.  Measured, us streamed / tiled, bf16 and e4m3: 4 experts of 3328
 // x 384 with 70, 128 and 256 rows each (99, 143 and 239 such pieces) 23 / 45 and 21 / 32, 23 / 50 and 21 / 37, 41 / 60 and 21 /
 // 38; 8 of 2048 x 512, 100 rows (326) 28 / 33 and 18 / 24; 4 of 2048 x 1024, 256 rows (638) 50 / 42 and 27 / 25; 20 of 1352 x
-// 512, 80 rows (715) 29 / 26 and 25 / 17.  With weights marked as read once both forms run at the memory's rate, and what
-// decides is how much of its last round the tiles fill, of those experts that uniform routing gives a row.  Measured as
-// above, us streamed / tiled: 1 token (8 experts, half a round) 80 / 117 bf16 and 41 / 59 e4m3; 2 tokens (0.88 of a round)
-// 142 / 131 and 75 / 66; 3 (1.16 rounds) 183 / 247 and 108 / 126; 4 (1.37) 214 / 254 and 114 / 128; 8 (1.80) 296 / 279 and 155 / 143.
+// 512, 80 rows (715) 29 / 26 and 25 / 17.
+//   With weights marked as read once both forms run at the memory's rate with a few rows per expert, and what decides is how
+// much of its last round the tiles fill, of those experts that uniform routing gives a row.  Streaming reads the rows again
+// for every 32 channels, so it falls behind as rows come on, in e4m3, with half the weights' bytes, twice as fast.  us of the
+// whole call, streamed / tiled, 32 experts of 7168 channels (the test beside this rule holds 110 such points):
+//   rounds            4 or 8 rows   16          32          47         e4m3: 4 or 8 rows   16          32          47
+//   0.25, 0.375        79 / 139      97 / 149   118 / 164   139 / 173         81 /  97      91 /  97   106 / 105   119 / 110
+//   0.5               134 / 168     151 / 182   172 / 197   209 / 206        102 / 109     108 / 113   121 / 123   131 / 131
+//   0.75              222 / 205     238 / 217   237 / 232   284 / 245        126 / 107     147 / 110   163 / 120   165 / 128
+//   1.125             297 / 363     326 / 372   350 / 387   387 / 400        177 / 185     198 / 198   216 / 212   240 / 218
+//   1.375             352 / 390     376 / 400   421 / 419   466 / 435        192 / 206     221 / 222   256 / 231   280 / 238
+//   1.625             425 / 428     429 / 436   490 / 459   539 / 477        236 / 226     261 / 243   294 / 255   326 / 263
+//   1.75              448 / 436     463 / 442   502 / 469   564 / 491        244 / 231     276 / 250   309 / 261   354 / 272
+// One round, however full, is spread over all XCDs; of several the last one is not, so it costs more of a whole one.
 inline bool few_rows_up(const FfnSizes& s) {
     const double rows = mean_rows(s);
     if (!weights_once(s)) return rows < (s.fp8 ? 4 : 12) || (rows * s.El + 63.0 * busy_experts(s)) / 64 * ((s.inter + 31) / 32) < 400;
     if (rows >= 48) return false;
     const int cols = (s.inter + 127) / 128;
     const double idle = std::pow(1.0 - (s.K < s.E ? (double)s.K / s.E : 1.0), s.T), rounds = s.El * (1.0 - idle) * cols / 256;
-    return rounds < 0.87 * std::ceil(rounds);
+    const double more = rows > 16 ? rows - 16 : 0;
+    const double fill = rounds <= 1 ? 0.58 - (s.fp8 ? 0.008 : 0.004) * more : s.fp8 ? 0.76 - 0.010 * more : 0.95 - 0.008 * more;
+    return rounds < fill * std::ceil(rounds);
 }
 
 }  // namespace ep

@@ -26,7 +26,7 @@ struct Params {
     uint16_t* gy;
     float* gw;
     const int32_t* slot;
-    int H, K;
+    int T, H, K;
 };
 
 constexpr int kChunks = 2, kBatch = 4;
@@ -51,7 +51,9 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float sum) {
 
 __global__ __launch_bounds__(kThreads) void k_combine_backward(Params p) {
     __shared__ float part[kWaves][kMaxTopk];
-    const int t = blockIdx.x, nchunk = p.H / 8, lane = lane_id(), wave = threadIdx.x / kWave;
+    const int64_t token = block_id();
+    if (token >= p.T) return;
+    const int t = (int)token, nchunk = p.H / 8, lane = lane_id(), wave = threadIdx.x / kWave;
     const int64_t entry = (int64_t)t * p.K + (lane < p.K ? lane : 0);
     const int slot = lane < p.K ? p.slot[entry] : -1;
     const float weight = p.w ? p.w[entry] : 1.0f;
@@ -129,8 +131,8 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(Params p) {
 hipError_t launch_combine_backward(const Handle& h, const CombineBackwardArgs& a, hipStream_t stream) {
     if (h.T == 0) return hipSuccess;
     const Params p{(const uint16_t*)a.grad_out, (const uint16_t*)a.y, a.topk_weights, (uint16_t*)a.grad_y, a.grad_w,
-                   h.ws.slot, a.hidden, h.K};
-    hipLaunchKernelGGL(k_combine_backward, dim3((unsigned)h.T), dim3(kThreads), 0, stream, p);
+                   h.ws.slot, h.T, a.hidden, h.K};
+    hipLaunchKernelGGL(k_combine_backward, grid_of(h.T), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -9,6 +9,15 @@ namespace ep {
 
 constexpr int kWave = 64;
 
+// Workgroups of a launch that can be very many.  A dimension of a grid holds 2^32 threads at most, and a launch of more wraps
+// round without an error; so past 2^20 workgroups (of up to 1024 threads) the grid gets rows of 2^20.  The last row is filled
+// up: block_id() can be past the last workgroup asked for.
+constexpr int64_t kGridRow = 1 << 20;
+inline dim3 grid_of(int64_t blocks) {
+    return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * kGridRow + blockIdx.x; }
+
 __device__ __forceinline__ int lane_id() { return (int)(threadIdx.x & (kWave - 1)); }
 
 __device__ __forceinline__ uint64_t ballot(bool p) { return __builtin_amdgcn_ballot_w64(p); }

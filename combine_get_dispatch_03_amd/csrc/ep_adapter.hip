@@ -43,6 +43,7 @@ struct Params {
     float* part;          // [chunks][tiles][64][r]
     int32_t* tokens;      // [tiles][64], a tile's tokens in the layout's order
     int tiles;            // that any routing can give
+    int bare;             // groups of kRows tokens to look through for those without an adapter
     bool listed;          // tokens come from k_tokens (many tokens), not from shrink
     int H, r, N;
     int chunk, chunks;    // hidden channels per chunk
@@ -248,9 +249,10 @@ __global__ __launch_bounds__(kThreads) void k_expand(Params p, int steps) {
     __shared__ __align__(16) f32x4 shared_sums[kThreads];
     constexpr int kTurnPitch = 64 + 4;
     __shared__ __align__(16) float turn[kWaves][16 * kTurnPitch];
-    const int cols = (p.N + kOut * steps - 1) / (kOut * steps), tile = blockIdx.x / cols, first = blockIdx.x % cols * kOut * steps;
+    const int cols = (p.N + kOut * steps - 1) / (kOut * steps), block = (int)block_id(), tile = block / cols, first = block % cols * kOut * steps;
     const int last = min(p.N, first + kOut * steps);
     if (tile >= p.tiles) {      // tokens without an adapter: base as it is
+        if (tile - p.tiles >= p.bare) return;
         const int t0 = (tile - p.tiles) * kRows, width = (last - first) / 8;
         uint64_t bare = ballot(t0 + lane_id() < p.T && p.slot[min(t0 + lane_id(), p.T - 1)] < 0);
         for (int i = 0; bare != 0; ++i, bare &= bare - 1) {
@@ -457,8 +459,10 @@ hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t str
     const int chunk = chunk_of(h.T, h.El, a.hidden), chunks = (a.hidden + chunk - 1) / chunk, tiles = max_tiles(h.T, h.El);
     int32_t* tokens = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + part_bytes(chunks, tiles, a.rank));
     const bool listed = h.T >= kManyTokens;
+    // in place, the tokens without an adapter already hold their base
+    const int bare = a.out == a.base ? 0 : (int)(((int64_t)h.T + kRows - 1) / kRows);
     const Params p{h.ws.cnt_local, h.ws.psum, h.ws.slot, h.T, h.El, (const uint16_t*)a.x, (const uint16_t*)a.a,
-                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens, tiles, listed,
+                   (const uint16_t*)a.b, a.scales, (const uint16_t*)a.base, (uint16_t*)a.out, (float*)a.ws, tokens, tiles, bare, listed,
                    a.hidden, a.rank, a.n_out, chunk, chunks};
     if (listed) {
         hipLaunchKernelGGL(k_tokens, dim3((unsigned)((h.T + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, p);
@@ -472,11 +476,9 @@ hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t str
     else hipLaunchKernelGGL(k_shrink<8>, shrink_grid, block, 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // in place, the tokens without an adapter already hold their base
-    const int bare = a.out == a.base ? 0 : (h.T + kRows - 1) / kRows;
     // as many channels per workgroup as leave the chip full: a workgroup adds up v before it starts
     const int columns = (a.n_out + kOut - 1) / kOut, want = (kExpandBlocks + tiles - 1) / tiles, steps = columns > want ? (columns + want - 1) / want : 1;
-    const dim3 expand_grid((unsigned)((int64_t)(tiles + bare) * ((columns + steps - 1) / steps)));
+    const dim3 expand_grid = grid_of((int64_t)(tiles + bare) * ((columns + steps - 1) / steps));
     if (a.rank <= 32) hipLaunchKernelGGL(k_expand<1>, expand_grid, block, 0, stream, p, steps);
     else if (a.rank <= 64) hipLaunchKernelGGL(k_expand<2>, expand_grid, block, 0, stream, p, steps);
     else hipLaunchKernelGGL(k_expand<4>, expand_grid, block, 0, stream, p, steps);

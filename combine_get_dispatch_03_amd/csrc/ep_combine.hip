@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(Params p) {
     __shared__ int cs_lds[kWavesPerBlock][kWave];
     __shared__ float cw_lds[kWavesPerBlock][kWave];
     const int lane = lane_id(), wv = threadIdx.x >> 6;
-    const int64_t item = (int64_t)blockIdx.x * kWavesPerBlock + wv;
+    const int64_t item = block_id() * kWavesPerBlock + wv;
     if (item >= p.nitems) return;
     const int t = (int)(item / p.nseg), seg = (int)(item % p.nseg);
 
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kBlock) void k_combine_reduce(ReduceParams p) {
     touch_kernargs<sizeof(ReduceParams)>();
     __shared__ int cs_lds[kWavesPerBlock][kWave];
     const int lane = lane_id(), wv = threadIdx.x >> 6;
-    const int64_t item = (int64_t)blockIdx.x * kWavesPerBlock + wv;
+    const int64_t item = block_id() * kWavesPerBlock + wv;
     if (item >= p.nitems) return;
     const int t = (int)(item / p.nseg), seg = (int)(item % p.nseg);
     int64_t row = -1;                                      // window row of token t for rank `lane`
@@ -212,8 +212,8 @@ hipError_t launch_combine_reduce(const Handle& h, const ReduceArgs& a, hipStream
     p.nseg = (a.hidden / 8 + kWave - 1) / kWave;
     p.nitems = (int64_t)h.T * p.nseg;
     p.stream_min = p.nitems >= kStreamMinWaves ? kReduceStreamRows : INT_MAX;
-    const unsigned nblocks = (unsigned)((p.nitems + kWavesPerBlock - 1) / kWavesPerBlock);
-    hipLaunchKernelGGL(k_combine_reduce, dim3(nblocks), dim3(kBlock), 0, stream, p);
+    const int64_t nblocks = (p.nitems + kWavesPerBlock - 1) / kWavesPerBlock;
+    hipLaunchKernelGGL(k_combine_reduce, grid_of(nblocks), dim3(kBlock), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -239,8 +239,8 @@ hipError_t launch_combine(const Handle& h, const CombineArgs& a, hipStream_t str
     p.nseg = (a.hidden / 8 + kWave - 1) / kWave;
     p.nitems = (int64_t)h.T * p.nseg;
     p.stream_min = p.nitems >= kStreamMinWaves ? kCombineStreamRows : INT_MAX;
-    const unsigned nblocks = (unsigned)((p.nitems + kWavesPerBlock - 1) / kWavesPerBlock);
-    hipLaunchKernelGGL(k_combine, dim3(nblocks), dim3(kBlock), 0, stream, p);
+    const int64_t nblocks = (p.nitems + kWavesPerBlock - 1) / kWavesPerBlock;
+    hipLaunchKernelGGL(k_combine, grid_of(nblocks), dim3(kBlock), 0, stream, p);
     return hipGetLastError();
 }
 

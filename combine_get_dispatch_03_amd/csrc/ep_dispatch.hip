@@ -87,7 +87,7 @@ __device__ __forceinline__ void pad_items(const Params& p, int64_t gw, int lane,
 template <int SPW, bool EARLY>
 __global__ __launch_bounds__(kBlock) void k_dispatch_fp8(Params p) {
     const int lane = lane_id();
-    const int64_t gw = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
+    const int64_t gw = block_id() * kWavesPerBlock + (threadIdx.x >> 6);
     PadWork pw;
     pad_prefetch(p, gw, lane, pw);
     if (gw < p.ntok_items) {
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kBlock) void k_dispatch_fp8(Params p) {
 
 __global__ __launch_bounds__(kBlock) void k_dispatch_raw(Params p) {
     const int lane = lane_id();
-    const int64_t gw = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
+    const int64_t gw = block_id() * kWavesPerBlock + (threadIdx.x >> 6);
     PadWork pw;
     pad_prefetch(p, gw, lane, pw);
     if (gw < p.ntok_items) {
@@ -165,14 +165,15 @@ hipError_t launch_dispatch(const Handle& h, const DispatchArgs& a, hipStream_t s
     const int64_t pad_waves = (max_pad_items + per_wave - 1) / per_wave;
     if (pad_waves > nwaves) nwaves = pad_waves;
     const int64_t nblocks = (nwaves + kWavesPerBlock - 1) / kWavesPerBlock;
-    p.nwaves = nblocks * kWavesPerBlock;
+    const dim3 grid = grid_of(nblocks);
+    p.nwaves = (int64_t)grid.x * grid.y * kWavesPerBlock;
     if (fp8 && p.send_slot != nullptr)
-        hipLaunchKernelGGL((k_dispatch_fp8<kFp8SegsPerItem, true>), dim3((unsigned)nblocks), dim3(kBlock), 0, stream, p);
+        hipLaunchKernelGGL((k_dispatch_fp8<kFp8SegsPerItem, true>), grid, dim3(kBlock), 0, stream, p);
     else if (fp8)
-        hipLaunchKernelGGL((k_dispatch_fp8<kFp8SegsPerItem, false>), dim3((unsigned)nblocks), dim3(kBlock), 0, stream,
+        hipLaunchKernelGGL((k_dispatch_fp8<kFp8SegsPerItem, false>), grid, dim3(kBlock), 0, stream,
                            p);
     else
-        hipLaunchKernelGGL(k_dispatch_raw, dim3((unsigned)nblocks), dim3(kBlock), 0, stream, p);
+        hipLaunchKernelGGL(k_dispatch_raw, grid, dim3(kBlock), 0, stream, p);
     return hipGetLastError();
 }
 

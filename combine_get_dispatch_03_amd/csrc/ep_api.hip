@@ -39,7 +39,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Shared shape checks of ep_get_layout / ep_layout_workspace_bytes / ep_recv_capacity.
 const char* check_shape(int T, int K, int E, int R, int rank, int A) {
-    if (T < 0) return "num_tokens must be >= 0";
+    if (T < 0 || T > kMaxTokens) return "num_tokens must be in [0, 1000000000]";
     if (K < 1 || K > kMaxTopk) return "num_topk must be in [1, 32]";
     if (E < 1 || E > kMaxExperts) return "num_experts must be in [1, 1024]";
     if (R < 1 || R > kMaxRanks) return "num_ranks must be in [1, 64]";
@@ -177,7 +177,7 @@ using namespace ep;
 extern "C" {
 
 int64_t ep_recv_capacity(int num_tokens, int num_topk, int num_local_experts, int expert_alignment) {
-    if (num_tokens < 0 || num_topk < 1 || num_topk > kMaxTopk || num_local_experts < 1 ||
+    if (num_tokens < 0 || num_tokens > kMaxTokens || num_topk < 1 || num_topk > kMaxTopk || num_local_experts < 1 ||
         num_local_experts > kMaxExperts || expert_alignment < 1 || expert_alignment > kMaxAlignment)
         return -1;
     const int64_t cap = (int64_t)num_tokens * num_topk + (int64_t)num_local_experts * (expert_alignment - 1);
@@ -702,7 +702,7 @@ ep_status_t ep_expert_ffn_backward(ep_handle_t handle, const void* dy, const voi
 }
 
 size_t ep_adapter_workspace_bytes(int num_tokens, int num_local_experts, int hidden, int rank) {
-    if (num_tokens < 0 || num_local_experts < 1 || num_local_experts > kMaxExperts || adapter_shape(hidden, rank, 8) != nullptr)
+    if (num_tokens < 0 || num_tokens > kMaxTokens || num_local_experts < 1 || num_local_experts > kMaxExperts || adapter_shape(hidden, rank, 8) != nullptr)
         return 0;
     return adapter_workspace_bytes(num_tokens, num_local_experts, hidden, rank);
 }

@@ -14,6 +14,7 @@ namespace ep {
 constexpr int kLayoutTileTokens = 256;           // tokens per layout tile (one 1024-thread block)
 constexpr int kMaxTopk = 32;
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxTokens = 1000000000;          // 4 threads each in the layout's grids, which hold 2^32
 constexpr int kMaxRanks = 64;
 constexpr int kMaxAlignment = 65536;
 constexpr int kMaxHidden = 32768;

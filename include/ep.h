@@ -38,7 +38,7 @@
  *     operation using it is still pending on its stream ([MoE-comm] §二, buffer and handle reuse).
  *   - Row-major layouts throughout.  x, y, out, bias, recv_x and send_x must be 16-byte aligned.
  *
- * Limits: 0 <= num_tokens; 1 <= num_topk <= 32; 1 <= num_experts <= 1024; 1 <= num_ranks <= 64 with
+ * Limits: 0 <= num_tokens <= 1,000,000,000; 1 <= num_topk <= 32; 1 <= num_experts <= 1024; 1 <= num_ranks <= 64 with
  * num_experts % num_ranks == 0; 0 <= rank < num_ranks; 1 <= expert_alignment <= 65536; the receive capacity
  * must fit in int32, and so must num_tokens * num_ranks (the send-window rows); hidden % 8 == 0,
  * 8 <= hidden <= 32768, and hidden % 128 == 0 for FP8.

@@ -414,7 +414,7 @@ struct Fp8Tiles {
         const int r = (int)threadIdx.x;
         next_scale_offset = r < rows ? (uint32_t)(r * blocks) * 4 : kNoElement;
     }
-    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first.
+    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first; zeros up to the 256th.
     __device__ __forceinline__ void copy_next_f_scales(const float* at, uint32_t second, int blocks, int which) {
         const int i = (wave_id() & 3) * 64 + lane_id();
         uint64_t base = uniform64((uint64_t)at);
@@ -505,7 +505,7 @@ struct Fp8Tiles {
 #pragma unroll
                     for (int a = 0; a < MT; ++a) row_scale[a] = rs[a * 16];
                 }
-                const float f_scale = fs[half * 256 + (st < k / 128 ? st : 0)];
+                const float f_scale = fs[half * 256 + st];      // zero in a stage past k, as all behind the last block
                 if (half == 0) wait_and_meet<63>();
                 else wait_and_meet<kAhead>();
                 __builtin_amdgcn_s_setprio(1);
@@ -567,7 +567,7 @@ struct Bf16ByFp8Tiles {
             next_f_offset[i] = o == kNoElement ? kNoElement : o + (x & 3) * 16;
         }
     }
-    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first.
+    // The next tile's F scales: two rows of `blocks`, the second `second` bytes behind the first; zeros up to the 256th.
     __device__ __forceinline__ void copy_next_f_scales(const float* at, uint32_t second, int blocks, int which) {
         const int i = (wave_id() & 3) * 64 + lane_id();
         uint64_t base = uniform64((uint64_t)at);
@@ -663,7 +663,7 @@ struct Bf16ByFp8Tiles {
                     sv[a][0] = read_kc(ls, s_at + a * 2048);
                     sv[a][1] = read_kc(ls, (s_at ^ 64) + a * 2048);
                 }
-                const float scale = q == 1 ? fs[st < k / 64 ? st / 2 : 0] : 0.0f;
+                const float scale = q == 1 ? fs[st / 2] : 0.0f;      // zero past k, as in Fp8Tiles
                 wait_and_meet<kAhead>();
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll

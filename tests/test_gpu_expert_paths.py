@@ -171,3 +171,27 @@ def test_graph_replay(ep, name):
         torch.cuda.synchronize()
         for k in o:
             assert torch.equal(o[k], ref[k]), "%s, replay %d" % (k, i)
+
+
+@pytest.mark.parametrize("name", ["hidden_128", "inter_128"])
+def test_infinite_block_scale(ep, name):
+    """A weight block's scale that has overflowed gives infinities, as the definition does, and no NaN: also in sums of one stage,
+    which the tiles pad with stages of zeros.  All values are positive, so no infinities meet with other signs."""
+    as_meant(name, "fp8")
+    h, d, m = F.setup(ep, CASES[name][0], "fp8")
+    for k in ("x", "w13", "w2"):
+        d[k].fill_(0x38)                             # 1.0
+    call = lambda: ep.ep_expert_ffn(h, d["x"], d["w13"], d["w2"], d["xs"], d["s13"], d["s2"])
+    clean = call()
+    e, I = 3, m["I"]
+    rows = slice(m["start"][e], m["start"][e] + m["count"][e])
+    want = clean.clone()
+    if name == "hidden_128":
+        d["s13"][e, I // 128, 0] = float("inf")      # up projection, first 128 channels: u, h and every y of the expert
+        want[rows] = float("inf")
+    else:
+        d["s2"][e, 5, 0] = float("inf")              # output channels 640 .. 767
+        want[rows, 640:768] = float("inf")
+    got = call()
+    assert bool(clean[m["valid"]].isfinite().all())
+    assert torch.equal(got[m["valid"]], want[m["valid"]])

@@ -57,18 +57,18 @@ __device__ __forceinline__ i32x4 resource(uint64_t base, uint32_t bytes = kNoEle
     return r;
 }
 
-// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16 (m0 holds nothing else on this target).  Counted
+// 64 lanes x 16 bytes from resource + offset into LDS at `lds` + lane * 16.  Counted
 // by vmcnt; the compiler does not see it, so whoever reads the LDS waits for it.  ONCE: marked non-temporal, for whole
 // lines that no other workgroup reads.
 template <bool ONCE = false>
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
     if constexpr (ONCE)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(offset), "s"(res));
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(offset), "s"(res) : "m0");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res) : "m0");
 }
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t offset, i32x4 res) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(res) : "m0");
 }
 
 // All LDS reads of this wave are back, and of its copies to LDS all but the newest `LEFT`; then the workgroup meets.

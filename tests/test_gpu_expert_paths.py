@@ -195,3 +195,16 @@ def test_infinite_block_scale(ep, name):
     got = call()
     assert bool(clean[m["valid"]].isfinite().all())
     assert torch.equal(got[m["valid"]], want[m["valid"]])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("T", [3, 70])
+def test_largest_sizes(ep, T, fmt):
+    """hidden and intermediate at their limits: one expert's w13 is 4 GiB in bf16.  Down projection streamed and on tiles."""
+    shape = (T, 32768, 32768, 1, 1, 0, 1, 1, "uniform")
+    assert Rules.path(T, 1, 1, 1, 32768, 32768, fmt) == (
+        "tile" if (T, fmt) == (70, "fp8") else "tile once", "tile" if T == 70 else "stream")
+    F.test_forward(ep, shape, fmt)
+    if fmt == "bf16" and T == 70:
+        F.test_backward(ep, shape)
+    torch.cuda.empty_cache()

@@ -765,6 +765,7 @@ def ep_expert_ffn_backward(handle: Handle, dy, recv_x, pre, w13, w2, dx=None, dw
 
 
 def ep_adapter_workspace_bytes(handle: Handle, hidden, rank) -> int:
+    """Bytes of workspace of ep_adapter for the handle's tokens and adapters."""
     return _adapter_bytes(handle.num_tokens, handle.num_local_experts, hidden, rank)
 
 

@@ -9,9 +9,12 @@
 //            in the workspace, tile by tile, and the first of a tile which tokens they are.
 //   expand   the partial sums are added in order, scaled and rounded to bf16 in LDS; then B_a's rows times v, added to
 //            base and stored.  More workgroups copy base where a token has no adapter.
+// v is rounded to bf16, the type the second product's matrix instruction takes.  That is 2^-8 of an element at most, 2^-9 on
+// average, beside the same of the output: 0.0019 to 0.0022 of the result in all, where the output's rounding alone leaves 0.0016.  Two bf16 parts
+// would keep 16 bits for twice the instructions and LDS.
 // Both are bound by memory (x and A; base, out and B): matrix instructions only keep the arithmetic out of the way.
-// Measured, 7168 channels in and out: 4096 tokens, 8 adapters of rank 64, shrink 25 us (2.4 TB/s), expand 31 us (3.8 TB/s);
-// 128 tokens, 32 adapters of rank 16, 5.4 and 6.7 us; one token, rank 64, 2112 out, 4.6 and 5.7 us: latency, with each
+// Measured, 7168 channels in and out: 4096 tokens, 8 adapters of rank 64, shrink 26 us (2.3 TB/s), expand 32 us (3.7 TB/s);
+// 128 tokens, 32 adapters of rank 16, 5.2 and 6.8 us; one token, rank 64, 2112 out, 4.7 and 5.8 us: latency, with each
 // kernel's chain of dependent loads (segment, token, row).
 // The layout maps tokens to rows; a tile finds its tokens by going over that map once (4 bytes a token, from L2), or, where
 // there are many tokens, a kernel before turns the map round for all tiles.

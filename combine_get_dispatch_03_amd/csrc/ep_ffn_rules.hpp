@@ -20,10 +20,16 @@ inline double mean_rows(const FfnSizes& s) { return (double)s.T * s.K / s.E; }
 inline int busy_experts(const FfnSizes& s) { return (int64_t)s.T * s.K < s.El ? s.T * s.K : s.El; }
 
 // Whether the gate and up projection's weights are worth marking as read once (copy16_to_lds): one row tile per expert, whole
-// lines, and more of them than the 256 MB memory-side cache keeps beside the rest of a layer.  us with the mark and without: 32 experts of 7168 x 2048,
-// bf16, 16 rows each 302 and 319, 64 rows 319 and 332, 128 rows 354 and 373, 900 rows (four row tiles) 1409 and 1262; 256
-// experts, e4m3, 4 rows 1103 and 1209, 128 rows 1681 and 1582; 20 experts of 2112 x 1352 (228 MB), 117 rows 68 and 85;
-// of 1344 x 512 (55 MB), 80 rows 28 and 23, of 1352 x 512 (rows of 2704 bytes) 39 and 27.
+// lines, and more of them than the 256 MB memory-side cache keeps beside the rest of a layer.
+//   Rows, us of the product with the mark and without: 32 experts of 7168 x 2048, bf16, 16 rows each 302 and 319, 64 rows 319 and
+// 332, 128 rows 354 and 373, 900 rows (four row tiles) 1409 and 1262; 256 experts, e4m3, 4 rows 1103 and 1209.  Of the whole
+// call: 128 experts, bf16, 96 rows 2107 and 2165, 128 to 200 rows within 1%, 256 rows (some with two tiles) 3279 and 3158; 256
+// experts, e4m3, 48 rows 2080 and 2144, 64 rows 2123 and 2194, 80 rows 2308 and 2298, 96 rows 2431 and 2413.
+//   Size: 20 experts of 2112 x 1352 (228 MB), 117 rows 68 and 85; of 1344 x 512 (55 MB), 80 rows 28 and 23, of 1352 x 512 (rows of
+// 2704 bytes) 39 and 27.  Of the whole call, 16 experts of 4096 channels, 8 rows, the same weights call after call, bf16 and e4m3: 128
+// MiB 80 and 64, 57 and 49; 160 MiB 83 and 71, 61 and 53; 192 MiB 86 and 90, 71 and 73; 256 MiB 99 and 105, 95 and 104.  Four sets
+// of weights in turn, as layers are: 64 MiB 73 and 75, 46 and 47; 128 MiB 82 and 85, 58 and 61; 160 MiB 88 and 91, 65 and 69.  So the
+// limit, between what one set in the cache and what several want, gives up a few percent on either side of it.
 inline bool weights_once(const FfnSizes& s) {
     const int64_t row = (int64_t)s.hidden * (s.fp8 ? 1 : 2);
     return mean_rows(s) <= (s.fp8 ? 64 : 128) && row % 128 == 0 && row * 2 * s.inter * s.El > (128ll << 20);

@@ -7,6 +7,7 @@
 // in LDS.
 // Measured, 7168 x 2048: one token of 8 experts, bf16, gate and up 80 us (5.9 TB/s), down 46 us (5.1); 256 experts, e4m3, 4
 // rows each, down 0.65 ms (5.7 TB/s).  Experts of 256 x 512 with 32 rows: 6.0 and 5.0 us, launch and latency.
+// h is rounded to bf16, as on tiles.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"

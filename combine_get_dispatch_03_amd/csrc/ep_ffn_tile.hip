@@ -7,12 +7,15 @@
 //                input's grad  dx = dp W13
 //   k_weights  out_e = s^T f over the expert's rows (dW2 = dy^T h, dW13 = dp^T x), sums in fp32, each written once
 //
-// With hundreds of rows per expert they are bound by the matrix units at the clock the power limit leaves (1.75 to 2.1
-// GHz here): they are busy 68% of the cycles, 56% in k_weights, whose sums are short and stores many (without the stores
-// 1.59 instead of 1.83 ms).  No bank conflicts in LDS.  With few rows, by the weights' bytes.
-// Measured, 32 experts of 7168 x 2048, 32768 rows (TFLOP/s): gate and up 1.53 ms (1256), down 0.79 (1216), down's grad
-// 0.97 (990), input's grad 1.57 (1225), dW13 1.80 (1070), dW2 0.96 (1000).  20 experts of 2112 x 1352, 2211
-// rows, 33 to 540 each: 55, 45, 67, 87, 90 and 51 us.
+// With hundreds of rows per expert they are bound by the matrix units at the clock the power limit leaves (1.73 to 1.89
+// GHz here): they are busy 60 to 71% of the cycles, 56% at 1.96 GHz in k_weights, whose sums are short and stores many (without
+// the stores 1.59 instead of 1.83 ms).  No bank conflicts in LDS.  With few rows, by the weights' bytes.
+// Measured, 32 experts of 7168 x 2048, 32768 rows, medians (TFLOP/s): gate and up 1.54 ms (1248), down 0.83 (1153), down's grad
+// 0.99 (971), input's grad 1.52 (1270), dW13 1.77 (1086), dW2 0.97 (996).  20 experts of 2112 x 1352, 2211
+// rows, 33 to 540 each: 54, 46, 67, 87, 90 and 51 us.
+//
+// h and dp are rounded to bf16 (2^-8 of an element at most, 2^-9 on average): it is the type the next product's matrix instruction takes, and in
+// two parts each would double that product.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"

@@ -4,9 +4,9 @@
 // the down projection is bf16 by e4m3 weights widened on the way to the matrix unit.
 //
 // An expert's rows rarely fill a tile in serving: the weights pass by once, and both kernels lie between the bytes and the
-// products.  Measured, 256 experts of 7168 x 2048, 128 rows each: gate and up 1.52 ms (8.1 GB read, 5.3 TB/s; the matrix
-// units are busy 40% of the cycles), down 1.19 ms (4.6 GB read and 0.5 written, 4.3 TB/s; 53%).  4 rows each, weights marked
-// as read once: gate and up 1.10 ms, 6.8 TB/s.
+// products.  Measured, 256 experts of 7168 x 2048, 128 rows each, medians: gate and up 1.57 ms (8.1 GB read, 5.2 TB/s; the matrix
+// units are busy 38% of the cycles), down 1.20 ms (4.7 GB read and 0.5 written, 4.4 TB/s; 52%).  With data of zeros, which leave
+// the clock higher, 1.49 and 1.00 ms.  4 rows each, weights marked as read once: gate and up 1.10 ms, 6.7 TB/s.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_gemm_core.hpp"

@@ -213,8 +213,9 @@ ep_status_t ep_layout_dispatch(const int64_t* topk_idx, int num_tokens, int num_
  *   alignment 128).  Every byte of the array that the kernels read is written earlier in the same call, so no
  *   contents need clearing between calls.
  *   Sharing: every call on a GPU uses that GPU's one array and one handle.  The returned handle is valid for
- *   ep_dispatch / ep_combine / ep_combine_tokens / ep_combine_reduce until the next ep_layout_dispatch_noalloc
- *   on the same GPU, which overwrites both (a handle kept from an earlier call then refers to the new layout).
+ *   ep_dispatch / ep_combine / ep_combine_tokens / ep_combine_reduce, and for the expert block, the combine's gradient and
+ *   the adapters, until the next ep_layout_dispatch_noalloc on the same GPU, which overwrites both (a handle kept
+ *   from an earlier call then refers to the new layout).
  *   Calls that overlap on one GPU -- from two host threads, or a new call enqueued on another stream while
  *   kernels of an earlier call or of its handle's dispatch / combine may still run -- race on the array.
  *   ep_handle_free on this handle is a no-op returning EP_OK.

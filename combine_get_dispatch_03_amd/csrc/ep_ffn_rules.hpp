@@ -36,8 +36,9 @@ inline bool weights_once(const FfnSizes& s) {
 }
 
 // Weights streamed past the rows (ep_ffn_stream.hip) rather than tiles of both through LDS: where an expert has so few rows
-// that its weights' bytes decide, or where the tiles would leave most CUs idle.  Measured, 32 experts of 7168 x 2048, us streamed / tiled at so many rows per expert (gate and up with
-// its weights marked as read once; in brackets tiled without the mark):
+// that its weights' bytes decide, or where the tiles would leave most CUs idle.  Measured, 32 experts of 7168 x 2048, us of the
+// product, streamed / tiled, at so many rows per expert (gate and up with its weights marked as read once; in brackets tiled
+// without the mark):
 //              gate, up, bf16       down, bf16    gate, up, e4m3       down, e4m3
 //    2 rows    296 / 279 (303)      154 / 206     155 / 143 (154)       81 / 105
 //    8         312 / 294 (318)      170 / 215     165 / 154 (164)       93 / 108
@@ -45,9 +46,14 @@ inline bool weights_once(const FfnSizes& s) {
 //   32         366 / 304 (323)      203 / 224     225 / 166 (169)      154 / 118
 //   64         584 / 317 (333)      299 / 235     366 / 187 (182)      272 / 142
 // (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
+// Down, us of the whole call at other sizes, bf16 at 24, 32 and 47 rows and e4m3 at 16, 24 and 32:
+//   4 experts of 7168 x 2048, 112 tiles     98 /  93  116 / 100  144 / 113       49 /  57   50 /  56   63 /  62
+//   8 of 4096 x 1408, 128                   73 /  79   80 /  85   90 /  94       46 /  51   48 /  53   55 /  56
+//   32 of 2048 x 1408, 256                 128 / 126  135 / 130  150 / 140       76 /  74   75 /  65   81 /  67
+//   64 of 4096 x 1408, 1024                466 / 447  479 / 454  501 / 464      257 / 256  270 / 261  305 / 268
 inline bool few_rows_down(const FfnSizes& s) {
-    const double rows = mean_rows(s);
-    return rows < (s.fp8 ? 16 : 48) || (rows < 64 && (int64_t)busy_experts(s) * ((s.hidden + 255) / 256) < 192);
+    const bool full = (int64_t)busy_experts(s) * ((s.hidden + 255) / 256) >= 192;
+    return mean_rows(s) < (s.fp8 && full ? 16 : 32);
 }
 
 // The same for the gate and up projection.  Without the mark: few rows, or so little work that a streamed product's finer

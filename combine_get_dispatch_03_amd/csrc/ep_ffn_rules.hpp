@@ -46,14 +46,20 @@ inline bool weights_once(const FfnSizes& s) {
 //   32         366 / 304 (323)      203 / 224     225 / 166 (169)      154 / 118
 //   64         584 / 317 (333)      299 / 235     366 / 187 (182)      272 / 142
 // (512 and 896 tiles: a tiled product takes a round of 256 for as long with fewer, a streamed one gets shorter.)
-// Down, us of the whole call at other sizes, bf16 at 24, 32 and 47 rows and e4m3 at 16, 24 and 32:
+// Down, us of the whole call at other sizes and tiles, bf16 at 24, 32 and 47 or 48 rows and e4m3 at 16, 24 and 32:
 //   4 experts of 7168 x 2048, 112 tiles     98 /  93  116 / 100  144 / 113       49 /  57   50 /  56   63 /  62
 //   8 of 4096 x 1408, 128                   73 /  79   80 /  85   90 /  94       46 /  51   48 /  53   55 /  56
 //   32 of 2048 x 1408, 256                 128 / 126  135 / 130  150 / 140       76 /  74   75 /  65   81 /  67
 //   64 of 4096 x 1408, 1024                466 / 447  479 / 454  501 / 464      257 / 256  270 / 261  305 / 268
+//   8 of  256 x  512,    8                  10 /  14   10 /  16   11 /  17       12 /  15   12 /  15   12 /  16
+//   8 of 1024 x  512,   32                  16 /  19   18 /  20   21 /  21       14 /  17   14 /  18   16 /  20
+//  16 of 1024 x  512,   64                  23 /  22   25 /  24   33 /  29       15 /  18   16 /  19   19 /  21
+// With few tiles it is the rows times the tiles, the work that streaming spreads over idle CUs; 8 tiles and 80 rows 15 / 20 and 13 / 18,
+// 32 tiles 30 / 28 and 21 / 23.
 inline bool few_rows_down(const FfnSizes& s) {
-    const bool full = (int64_t)busy_experts(s) * ((s.hidden + 255) / 256) >= 192;
-    return mean_rows(s) < (s.fp8 && full ? 16 : 32);
+    const double rows = mean_rows(s);
+    const int64_t tiles = (int64_t)busy_experts(s) * ((s.hidden + 255) / 256);
+    return rows < (s.fp8 ? 16 : 28) || (rows <= 80 && rows * tiles < (s.fp8 ? 3600 : 2100));
 }
 
 // The same for the gate and up projection.  Without the mark: few rows, or so little work that a streamed product's finer

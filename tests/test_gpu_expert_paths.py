@@ -34,16 +34,16 @@ CASES = {
     "one_short_tile_each": ((60, 1152, 2048, 32, 1, 0, 4, 1, "uniform"), ("bf16", "fp8"), ("tile once", "stream"), ("up",)),
     "one_short_tile_each_second_rank": ((64, 1152, 2048, 64, 2, 1, 8, 16, "holes"), ("bf16", "fp8"), ("tile once", "stream"), ("up",)),
     # uneven counts: hand-overs between tiles of different heights, experts and scales
-    "uneven": ((600, 256, 4352, 16, 1, 0, 2, 1, "zipf"), ("bf16", "fp8"), ("tile", "tile"), ("up", "dp")),
+    "uneven": ((700, 256, 4352, 16, 1, 0, 2, 1, "zipf"), ("bf16", "fp8"), ("tile", "tile"), ("up", "dp")),
     "uneven_wide_out": ((600, 4352, 256, 16, 1, 0, 2, 8, "zipf"), ("bf16", "fp8"), ("stream", "tile"), ("down", "dx")),
-    "even": ((1200, 512, 2304, 16, 1, 0, 1, 128, "uniform"), ("bf16", "fp8"), ("tile", "tile"), ("up",)),
+    "even": ((1200, 1024, 2304, 16, 1, 0, 1, 128, "uniform"), ("bf16", "fp8"), ("tile", "tile"), ("up",)),
     # e4m3 sums of one real stage (the tiles pad to two and four): 128 terms
     "hidden_128": ((1200, 128, 4352, 8, 1, 0, 1, 1, "uniform"), ("bf16", "fp8"), ("tile", "tile"), ("up",)),
     "inter_128": ((1200, 8704, 128, 8, 1, 0, 1, 1, "uniform"), ("bf16", "fp8"), ("stream", "tile"), ("down",)),
     "inter_256": ((1200, 8704, 256, 8, 1, 0, 1, 1, "zipf"), ("bf16", "fp8"), ("stream", "tile"), ("down",)),
     # scale rows of more than 64 and of more than 192 blocks
     "hidden_8320": ((300, 8320, 1536, 4, 1, 0, 1, 1, "uniform"), ("fp8",), ("tile", "tile"), ()),
-    "inter_8320": ((300, 256, 8320, 4, 1, 0, 1, 1, "uniform"), ("bf16", "fp8"), ("tile", "tile"), ("up",)),
+    "inter_8320": ((400, 256, 8320, 4, 1, 0, 1, 1, "uniform"), ("bf16", "fp8"), ("tile", "tile"), ("up",)),
     "hidden_24704": ((300, 24704, 2048, 2, 1, 0, 1, 1, "uniform"), ("fp8",), ("tile", "tile"), ()),
     "inter_24704": ((300, 256, 24704, 2, 1, 0, 1, 1, "uniform"), ("fp8",), ("tile", "tile"), ("up",)),
 }

@@ -62,11 +62,18 @@ inline bool few_rows_down(const FfnSizes& s) {
     return rows < (s.fp8 ? 16 : 28) || (rows <= 80 && rows * tiles < (s.fp8 ? 3600 : 2100));
 }
 
-// The same for the gate and up projection.  Without the mark: few rows, or so little work that a streamed product's finer
-// grid is what fills the chip, counted in 64 rows x 32 channels.  Measured, us streamed / tiled, bf16 and e4m3: 4 experts of 3328
-// x 384 with 70, 128 and 256 rows each (99, 143 and 239 such pieces) 23 / 45 and 21 / 32, 23 / 50 and 21 / 37, 41 / 60 and 21 /
-// 38; 8 of 2048 x 512, 100 rows (326) 28 / 33 and 18 / 24; 4 of 2048 x 1024, 256 rows (638) 50 / 42 and 27 / 25; 20 of 1352 x
-// 512, 80 rows (715) 29 / 26 and 25 / 17.
+// The same for the gate and up projection.  Without the mark the weights are few and mostly come from the caches.  Streaming
+// wins where its finer grid is what fills the chip: the fewer 128-channel tiles and, in e4m3, rows there are, and past one
+// row tile of its own (64 rows) by its pieces of 64 rows x 32 channels.  us of the whole call, streamed / tiled, at so many rows:
+//                                   bf16: 2          16         32         64        e4m3: 2         16         32         64
+//    8 experts of 2048 x 768, 48 tiles    22 / 33    28 / 36    36 / 42    53 / 45      16 / 23    19 / 25    25 / 30    40 / 36
+//   16 of 2048 x 768, 96                  34 / 46    41 / 50    48 / 53    78 / 57      23 / 26    28 / 28    35 / 34    46 / 37
+//   64 of 2048 x 256, 128                 47 / 59    62 / 70    69 / 76    88 / 70      31 / 33    35 / 34    40 / 38    63 / 44
+//   20 of 1280 x 1024, 160                36 / 38    47 / 48    60 / 58    71 / 55      26 / 23    32 / 26    37 / 32    48 / 34
+//   32 of 1024 x 768, 192                 36 / 33    43 / 38    48 / 41    67 / 46      25 / 22    31 / 25    38 / 30    47 / 31
+//  256 of  256 x 512, 1024                63 / 54    79 / 61    90 / 65   125 / 67      48 / 35    57 / 37    65 / 41    97 / 48
+// us of the product: 4 experts of 3328 x 384 with 70, 128 and 256 rows (99, 143 and 239 pieces) 23 / 45 and 21 / 32, 23 / 50 and 21 /
+// 37, 41 / 60 and 21 / 38; 8 of 2048 x 512, 100 rows (326) 28 / 33 and 18 / 24; 4 of 2048 x 1024, 256 rows (638) 50 / 42 and 27 / 25.
 //   With weights marked as read once both forms run at the memory's rate with a few rows per expert, and what decides is how
 // much of its last round the tiles fill, of those experts that uniform routing gives a row.  Streaming reads the rows again
 // for every 32 channels, so it falls behind as rows come on, in e4m3, with half the weights' bytes, twice as fast.  us of the
@@ -82,9 +89,14 @@ inline bool few_rows_down(const FfnSizes& s) {
 // One round, however full, is spread over all XCDs; of several the last one is not, so it costs more of a whole one.
 inline bool few_rows_up(const FfnSizes& s) {
     const double rows = mean_rows(s);
-    if (!weights_once(s)) return rows < (s.fp8 ? 4 : 12) || (rows * s.El + 63.0 * busy_experts(s)) / 64 * ((s.inter + 31) / 32) < 400;
-    if (rows >= 48) return false;
     const int cols = (s.inter + 127) / 128;
+    if (!weights_once(s)) {
+        const int64_t tiles = (int64_t)busy_experts(s) * cols;
+        if (rows > 52) return (rows * s.El + 63.0 * busy_experts(s)) / 64 * ((s.inter + 31) / 32) < 340;
+        if (s.fp8) return tiles < 130 && rows * tiles < 3100;
+        return rows < 12 ? tiles < 165 : tiles < 135 && rows * tiles < 4200;
+    }
+    if (rows >= 48) return false;
     const double idle = std::pow(1.0 - (s.K < s.E ? (double)s.K / s.E : 1.0), s.T), rounds = s.El * (1.0 - idle) * cols / 256;
     const double more = rows > 16 ? rows - 16 : 0;
     const double fill = rounds <= 1 ? 0.58 - (s.fp8 ? 0.008 : 0.004) * more : s.fp8 ? 0.76 - 0.010 * more : 0.95 - 0.008 * more;

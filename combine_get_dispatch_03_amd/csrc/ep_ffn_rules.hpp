@@ -77,7 +77,7 @@ inline bool few_rows_down(const FfnSizes& s) {
 //   With weights marked as read once both forms run at the memory's rate with a few rows per expert, and what decides is how
 // much of its last round the tiles fill, of those experts that uniform routing gives a row.  Streaming reads the rows again
 // for every 32 channels, so it falls behind as rows come on, in e4m3, with half the weights' bytes, twice as fast.  us of the
-// whole call, streamed / tiled, 32 experts of 7168 channels (the test beside this rule holds 110 such points):
+// whole call, streamed / tiled, 32 experts of 7168 channels (a test holds these and some 900 more sizes):
 //   rounds            4 or 8 rows   16          32          47         e4m3: 4 or 8 rows   16          32          47
 //   0.25, 0.375        79 / 139      97 / 149   118 / 164   139 / 173         81 /  97      91 /  97   106 / 105   119 / 110
 //   0.5               134 / 168     151 / 182   172 / 197   209 / 206        102 / 109     108 / 113   121 / 123   131 / 131

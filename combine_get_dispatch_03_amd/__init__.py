@@ -43,6 +43,14 @@ class _DispatchOut(ctypes.Structure):
     ]
 
 
+class _NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("residual", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("gate_per_token", ctypes.c_int), ("vectors_bf16", ctypes.c_int),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
+    ]
+
+
 def _load_library():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libep_mi355x.so is not built: run `python -m combine_get_dispatch_03_amd.build` "
@@ -91,6 +99,12 @@ def _load_library():
     lib.ep_adapter_workspace_bytes.argtypes = [I, I, I, I]
     lib.ep_adapter.restype = I
     lib.ep_adapter.argtypes = [P, P, I, P, P, I, I, P, P, P, P, SZ, P]
+    lib.ep_combine_norm_workspace_bytes.restype = SZ
+    lib.ep_combine_norm_workspace_bytes.argtypes = [I, I]
+    lib.ep_combine_norm.restype = I
+    lib.ep_combine_norm.argtypes = [P, P, I, I64, P, P, ctypes.POINTER(_NormArgs), P, P, P, P]
+    lib.ep_combine_norm_backward.restype = I
+    lib.ep_combine_norm_backward.argtypes = [P, P, P, I, I, I, ctypes.POINTER(_NormArgs), P, P, P, P, P, P, SZ, P]
     return lib
 
 
@@ -801,6 +815,138 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
     return out
 
 
+def ep_combine_norm_workspace_bytes(num_tokens, hidden) -> int:
+    """Bytes of workspace of ep_combine_norm_backward."""
+    return _norm_bytes(num_tokens, hidden)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(num_tokens, hidden):
+    return int(_lib.ep_combine_norm_workspace_bytes(num_tokens, hidden))
+
+
+def _on_current(t, name):
+    """The device of a call that has no handle: its first tensor's, which must be the current one (the stream is its)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    device = t.device
+    if device.type == "cuda" and device.index != (_cur_device or torch.cuda.current_device)():
+        raise ValueError("%s is on %s, which is not the current device" % (name, device))
+    return device
+
+
+def check_norm_args(T, H, device, residual, post_weight, gate, residual_scale, pre_weight, eps):
+    """What stands around a block, against the sizes the library reads; returns the library's arguments."""
+    a = _NormArgs()
+    kind = None
+    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (gate, "gate")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if name == "gate" and t.dim() == 2:
+            _need(t, torch.bfloat16, name, device, (T, H))
+            a.gate_per_token = 1
+        else:
+            if t.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+            if kind is not None and t.dtype != kind:
+                raise TypeError("%s is %s beside %s vectors" % (name, t.dtype, kind))
+            kind = t.dtype
+            _need(t, kind, name, device, (H,))
+        setattr(a, name, t.data_ptr())
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", device, (T, H))
+        a.residual = residual.data_ptr()
+    a.vectors_bf16 = int(kind is torch.bfloat16)
+    a.residual_scale, a.eps = residual_scale, eps
+    return a
+
+
+def ep_combine_norm(handle, y, topk_weights=None, bias=None, residual=None, post_weight=None, gate=None, residual_scale=1.0,
+                    pre_weight=None, eps=1e-6, out=None, normed=None, kept=None, need_out=True, stream=None):
+    """The combine with the norms, gate and residual around a block: f = combine(y, topk_weights, bias), or y + bias with
+    handle None; a = f / sqrt(mean f^2 + eps) * post_weight; r = residual_scale * residual + gate * a; n = r / sqrt(mean r^2
+    + eps) * pre_weight.  Returns (out = r, normed = n), bf16 [T, H]; normed is None without pre_weight, out with
+    need_out=False.  post_weight, pre_weight and gate [H] are all fp32 or all bf16; gate may be bf16 [T, H].  out may be
+    the residual itself.  kept: fp32 [T, H] to keep f for ep_combine_norm_backward."""
+    H = _columns(y, "y")
+    if handle is not None:
+        dev, T = _device(handle), handle.num_tokens
+        _need(y, torch.bfloat16, "y", dev)
+        if topk_weights is not None:
+            _need(topk_weights, torch.float32, "topk_weights", dev, (T, handle.num_topk))
+    else:
+        dev, T = _on_current(y, "y"), y.shape[0]
+        _need(y, torch.bfloat16, "y", dev)
+        if topk_weights is not None:
+            raise ValueError("topk_weights needs a handle")
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", dev, (T, H))
+    a = check_norm_args(T, H, dev, residual, post_weight, gate, residual_scale, pre_weight, eps)
+    if out is not None:
+        _need(out, torch.bfloat16, "out", dev, (T, H))
+    elif need_out:
+        out = _empty(stream, y, (T, H))
+    if normed is not None:
+        _need(normed, torch.bfloat16, "normed", dev, (T, H))
+    elif pre_weight is not None:
+        normed = _empty(stream, y, (T, H))
+    if kept is not None:
+        _need(kept, torch.float32, "kept", dev, (T, H))
+    _need(y, torch.bfloat16, "y")     # on a GPU, after the rules on shapes
+    _check(_lib.ep_combine_norm(None if handle is None else handle.ptr, _ptr(y), H, y.shape[0], _ptr(topk_weights), _ptr(bias),
+                                ctypes.byref(a), _ptr(out), _ptr(normed), _ptr(kept), _stream(stream)), "ep_combine_norm")
+    return out, normed
+
+
+def ep_combine_norm_backward(grad_out, grad_normed, f, residual=None, post_weight=None, gate=None, residual_scale=1.0,
+                             pre_weight=None, eps=1e-6, grad_f=None, grad_residual=None, grad_post=None, grad_pre=None,
+                             grad_gate=None, need_rows=True, need_vectors=True, workspace=None, stream=None):
+    """Gradients of ep_combine_norm from grad_out and grad_normed (bf16 [T, H], either may be None) and f: the fp32 [T, H]
+    that the forward pass kept, or the bf16 y of a call without handle and bias.  Returns a dict: grad_f and
+    grad_residual bf16 [T, H], grad_post and grad_pre fp32 [H], grad_gate fp32 [H] or bf16 [T, H] as the gate; None for what
+    the call did not have, and, unless given, for the rows with need_rows=False and the vectors with need_vectors=False.
+    grad_f goes on as grad_out of ep_combine_backward."""
+    H = _columns(f, "f")
+    dev, T = _on_current(f, "f"), f.shape[0]
+    if f.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("f must be float32 or bfloat16, got %s" % f.dtype)
+    _need(f, f.dtype, "f", dev)
+    for t, name in ((grad_out, "grad_out"), (grad_normed, "grad_normed")):
+        if t is not None:
+            _need(t, torch.bfloat16, name, dev, (T, H))
+    a = check_norm_args(T, H, dev, residual, post_weight, gate, residual_scale, pre_weight, eps)
+    per_token = bool(a.gate_per_token)
+
+    _need(f, f.dtype, "f")            # on a GPU, after the rules on shapes
+
+    def grad(t, name, dtype, shape, has, needed):
+        if t is not None:
+            return _need(t, dtype, name, dev, shape)
+        return _empty(stream, f, shape, dtype) if has and needed else None
+
+    g = dict(
+        grad_f=grad(grad_f, "grad_f", torch.bfloat16, (T, H), True, need_rows),
+        grad_residual=grad(grad_residual, "grad_residual", torch.bfloat16, (T, H), residual is not None, need_rows),
+        grad_post=grad(grad_post, "grad_post", torch.float32, (H,), post_weight is not None, need_vectors),
+        grad_pre=grad(grad_pre, "grad_pre", torch.float32, (H,), pre_weight is not None and grad_normed is not None, need_vectors),
+        grad_gate=grad(grad_gate, "grad_gate", torch.bfloat16 if per_token else torch.float32, (T, H) if per_token else (H,),
+                       gate is not None, need_rows if per_token else need_vectors))
+    if workspace is not None:
+        check_workspace(workspace, dev)
+    else:
+        n = ep_combine_norm_workspace_bytes(T, H)
+        if n == 0:
+            raise EPError("ep_combine_norm_workspace_bytes rejected the sizes (T=%d hidden=%d)" % (T, H))
+        workspace = _empty(stream, f, n, torch.uint8)
+    _check(_lib.ep_combine_norm_backward(
+        _ptr(grad_out), _ptr(grad_normed), _ptr(f), int(f.dtype is torch.bfloat16), T, H, ctypes.byref(a), _ptr(g["grad_f"]),
+        _ptr(g["grad_residual"]), _ptr(g["grad_post"]), _ptr(g["grad_pre"]), _ptr(g["grad_gate"]), _ptr(workspace),
+        workspace.numel(), _stream(stream)), "ep_combine_norm_backward")
+    return g
+
+
 def ep_handle_free(handle: Handle):
     handle.free()
 
@@ -808,5 +954,6 @@ def ep_handle_free(handle: Handle):
 __all__ = ["ep_get_layout", "ep_dispatch", "ep_layout_dispatch", "ep_layout_dispatch_noalloc", "ep_combine", "ep_combine_tokens", "ep_handle_free", "ep_recv_capacity",
            "ep_dispatch_rows", "ep_combine_reduce", "ep_combine_backward", "ep_expert_ffn", "ep_expert_ffn_backward",
            "ep_expert_ffn_workspace_bytes", "ep_adapter", "ep_adapter_workspace_bytes",
+           "ep_combine_norm", "ep_combine_norm_backward", "ep_combine_norm_workspace_bytes",
            "ep_layout_workspace_bytes", "alloc_dispatch_outputs", "Handle", "EPError", "LIB_PATH",
            "hip_runtimes_loaded"]

@@ -1,6 +1,7 @@
 // ep_api.hip -- the C ABI of include/ep.h: argument validation, workspace carve-up, handle lifetime and the
 // kernel launches.  Validation runs entirely on the host before anything is enqueued; nothing here
 // allocates device memory or synchronises.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -342,6 +343,24 @@ ep_status_t check_scratch(const void* workspace, size_t have, size_t need) {
         return fail(EP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (have < need) return fail(EP_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", have, need);
     return EP_OK;
+}
+
+// What ep_combine_norm and its gradient take around the block; nullptr: fine.
+const char* norm_args(const ep_norm_args_t* n, NormVectors* v) {
+    if (n == nullptr) return "norm is NULL";
+    if (!(n->eps > 0.0f) || std::isinf(n->eps)) return "eps must be positive and finite";
+    if (!std::isfinite(n->residual_scale)) return "residual_scale must be finite";
+    if (!aligned16(n->residual) || !aligned16(n->post_weight) || !aligned16(n->pre_weight) || !aligned16(n->gate))
+        return "residual, post_weight, pre_weight and gate must be 16-byte aligned";
+    v->residual = static_cast<const uint16_t*>(n->residual);
+    v->post = n->post_weight;
+    v->pre = n->pre_weight;
+    v->gate = n->gate;
+    v->gate_per_token = n->gate != nullptr && n->gate_per_token != 0;
+    v->bf16 = n->vectors_bf16 != 0;
+    v->residual_scale = n->residual_scale;
+    v->eps = n->eps;
+    return nullptr;
 }
 
 }  // namespace
@@ -737,6 +756,99 @@ ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void
     p.n_out = out_features;
     const hipError_t err = launch_adapter(*h, p, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return hip_fail(err, "adapter launch");
+    return EP_OK;
+}
+
+size_t ep_combine_norm_workspace_bytes(int num_tokens, int hidden) {
+    if (num_tokens < 0 || num_tokens > kMaxTokens || hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0) return 0;
+    return combine_norm_workspace_bytes(num_tokens, hidden);
+}
+
+ep_status_t ep_combine_norm(ep_handle_t handle, const void* y, int hidden, int64_t y_rows, const float* topk_weights,
+                            const void* bias, const ep_norm_args_t* norm, void* out, void* normed, float* kept, void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = nullptr;
+    if (handle != nullptr) {
+        h = check_handle(handle);
+        if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    }
+    if (hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0)
+        return fail(EP_ERR_INVALID_ARG, "hidden must be a multiple of 8 in [8, 32768]");
+    if (h == nullptr && (y_rows < 0 || y_rows > kMaxTokens))
+        return fail(EP_ERR_INVALID_ARG, "y_rows must be in [0, 1000000000] without a handle");
+    if (h == nullptr && topk_weights != nullptr) return fail(EP_ERR_INVALID_ARG, "topk_weights needs a handle");
+    CombineNormArgs a;
+    if (const char* why = norm_args(norm, &a.v)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    const int T = h != nullptr ? h->T : (int)y_rows;
+    if (T > 0) {
+        if (out == nullptr && normed == nullptr && kept == nullptr)
+            return fail(EP_ERR_INVALID_ARG, "out, normed and kept are all NULL");
+        if (normed != nullptr && norm->pre_weight == nullptr) return fail(EP_ERR_INVALID_ARG, "normed needs pre_weight");
+        if (y == nullptr || !aligned16(y)) return fail(EP_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned");
+        if (h != nullptr && y_rows < h->cap)
+            return fail(EP_ERR_INVALID_ARG, "y_rows %lld < required %lld", (long long)y_rows, (long long)h->cap);
+        if (!aligned16(bias)) return fail(EP_ERR_INVALID_ARG, "bias must be 16-byte aligned");
+        if (!aligned16(out) || !aligned16(normed) || !aligned16(kept))
+            return fail(EP_ERR_INVALID_ARG, "out, normed and kept must be 16-byte aligned");
+    }
+    a.y = y;
+    a.topk_weights = topk_weights;
+    a.slot = h != nullptr ? h->ws.slot : nullptr;
+    a.bias = bias;
+    a.out = out;
+    a.normed = normed;
+    a.kept = kept;
+    a.T = T;
+    a.K = h != nullptr ? h->K : 0;
+    a.hidden = hidden;
+    const hipError_t err = launch_combine_norm(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "combine_norm launch");
+    return EP_OK;
+}
+
+ep_status_t ep_combine_norm_backward(const void* grad_out, const void* grad_normed, const void* f, ep_norm_f_t f_type, int num_tokens,
+                                     int hidden, const ep_norm_args_t* norm, void* grad_f, void* grad_residual, float* grad_post,
+                                     float* grad_pre, void* grad_gate, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    if (num_tokens < 0 || num_tokens > kMaxTokens) return fail(EP_ERR_INVALID_ARG, "num_tokens must be in [0, 1000000000]");
+    if (hidden < 8 || hidden > kMaxHidden || hidden % 8 != 0)
+        return fail(EP_ERR_INVALID_ARG, "hidden must be a multiple of 8 in [8, 32768]");
+    if (f_type != EP_NORM_F_KEPT && f_type != EP_NORM_F_BF16) return fail(EP_ERR_INVALID_ARG, "f_type must be EP_NORM_F_KEPT or EP_NORM_F_BF16");
+    CombineNormBackwardArgs a;
+    if (const char* why = norm_args(norm, &a.v)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (grad_f == nullptr && grad_residual == nullptr && grad_post == nullptr && grad_pre == nullptr && grad_gate == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "no gradient is asked for");
+    if (grad_normed != nullptr && norm->pre_weight == nullptr) return fail(EP_ERR_INVALID_ARG, "grad_normed needs pre_weight");
+    if (grad_pre != nullptr && (norm->pre_weight == nullptr || (num_tokens > 0 && grad_normed == nullptr)))
+        return fail(EP_ERR_INVALID_ARG, "grad_pre needs pre_weight and grad_normed");
+    if (grad_post != nullptr && norm->post_weight == nullptr) return fail(EP_ERR_INVALID_ARG, "grad_post needs post_weight");
+    if (grad_gate != nullptr && norm->gate == nullptr) return fail(EP_ERR_INVALID_ARG, "grad_gate needs gate");
+    if (grad_residual != nullptr && norm->residual == nullptr && num_tokens > 0)
+        return fail(EP_ERR_INVALID_ARG, "grad_residual needs residual");
+    if (!aligned16(grad_f) || !aligned16(grad_residual) || !aligned16(grad_gate))
+        return fail(EP_ERR_INVALID_ARG, "grad_f, grad_residual and grad_gate must be 16-byte aligned");
+    if (num_tokens > 0) {
+        if (grad_out == nullptr && grad_normed == nullptr) return fail(EP_ERR_INVALID_ARG, "grad_out and grad_normed are both NULL");
+        if (!aligned16(grad_out) || !aligned16(grad_normed))
+            return fail(EP_ERR_INVALID_ARG, "grad_out and grad_normed must be 16-byte aligned");
+        if (f == nullptr || !aligned16(f)) return fail(EP_ERR_INVALID_ARG, "f must be non-NULL and 16-byte aligned");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, combine_norm_workspace_bytes(num_tokens, hidden));
+        if (st != EP_OK) return st;
+    }
+    a.grad_out = grad_out;
+    a.grad_normed = grad_normed;
+    a.f = f;
+    a.f_bf16 = f_type == EP_NORM_F_BF16;
+    a.grad_f = grad_f;
+    a.grad_residual = grad_residual;
+    a.grad_post = grad_post;
+    a.grad_pre = grad_pre;
+    a.grad_gate = grad_gate;
+    a.workspace = workspace;
+    a.T = num_tokens;
+    a.hidden = hidden;
+    const hipError_t err = launch_combine_norm_backward(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "combine_norm_backward launch");
     return EP_OK;
 }
 

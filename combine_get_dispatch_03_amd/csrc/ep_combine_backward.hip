@@ -31,15 +31,6 @@ struct Params {
 
 constexpr int kChunks = 2, kBatch = 4;
 
-// Sum over the 64 lanes, the same in every lane: within each 16 lanes by row rotations, then the four rows' sums.
-__device__ __forceinline__ float wave_sum(float v) {
-    v += dpp_f<0x128>(v);     // row_ror:8
-    v += dpp_f<0x124>(v);     // row_ror:4
-    v += dpp_f<0x122>(v);     // row_ror:2
-    v += dpp_f<0x121>(v);     // row_ror:1
-    return (readlane_f(v, 0) + readlane_f(v, 16)) + (readlane_f(v, 32) + readlane_f(v, 48));
-}
-
 __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float sum) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

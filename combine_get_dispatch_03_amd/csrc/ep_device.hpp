@@ -80,6 +80,15 @@ __device__ __forceinline__ float dpp_f(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
 }
 
+// Sum over the 64 lanes, the same in every lane: within each 16 lanes by row rotations, then the four rows' sums.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_f<0x128>(v);     // row_ror:8
+    v += dpp_f<0x124>(v);     // row_ror:4
+    v += dpp_f<0x122>(v);     // row_ror:2
+    v += dpp_f<0x121>(v);     // row_ror:1
+    return (readlane_f(v, 0) + readlane_f(v, 16)) + (readlane_f(v, 32) + readlane_f(v, 48));
+}
+
 // Max over groups of 8 consecutive lanes (lanes 8g..8g+7), in registers: swap neighbours (quad_perm 1,0,3,2),
 // swap pairs (quad_perm 2,3,0,1), then each lane meets the other quad of its 8 through the half-row mirror
 // (lane i <-> lane 7 - i within each 8).
@@ -115,6 +124,7 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 
 // 16-byte vector of four 32-bit words (a native vector type, so it maps to dwordx4 loads and stores).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Reads one dword of every 64-byte line of the kernel's first `bytes` argument bytes, all issued before one wait.
 // The compiler fetches argument fields on demand (it re-reads them rather than hold them in scalar registers),

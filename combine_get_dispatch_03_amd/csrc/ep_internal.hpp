@@ -157,4 +157,44 @@ struct AdapterArgs {
 size_t adapter_workspace_bytes(int T, int El, int hidden, int rank);
 hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t stream);
 
+// What stands around a block: its norm, gate and residual, and the next norm.  Vectors [hidden] are all bf16 or all fp32.
+struct NormVectors {
+    const uint16_t* residual;  // bf16 [T, hidden] or nullptr (zeros)
+    const void* post;          // [hidden] or nullptr (no norm)
+    const void* pre;           // [hidden] or nullptr
+    const void* gate;          // [hidden], or bf16 [T, hidden], or nullptr (1)
+    bool gate_per_token, bf16;
+    float residual_scale, eps;
+};
+
+struct CombineNormArgs {
+    const void* y;             // bf16 [rows, hidden]
+    const float* topk_weights; // [T, K] or nullptr (weights of 1)
+    const int32_t* slot;       // [T, K]; nullptr: y holds a row per token
+    const void* bias;          // bf16 [T, hidden] or nullptr
+    NormVectors v;
+    void* out;                 // bf16 [T, hidden] or nullptr
+    void* normed;              // bf16 [T, hidden] or nullptr
+    float* kept;               // [T, hidden] or nullptr
+    int T, K, hidden;
+};
+hipError_t launch_combine_norm(const CombineNormArgs& a, hipStream_t stream);
+
+struct CombineNormBackwardArgs {
+    const void* grad_out;      // bf16 [T, hidden] or nullptr (zeros)
+    const void* grad_normed;   // bf16 [T, hidden] or nullptr (zeros)
+    const void* f;             // fp32 or bf16 [T, hidden]
+    bool f_bf16;
+    NormVectors v;
+    void* grad_f;              // bf16 [T, hidden] or nullptr
+    void* grad_residual;       // bf16 [T, hidden] or nullptr
+    float* grad_post;          // [hidden] or nullptr
+    float* grad_pre;           // [hidden] or nullptr
+    void* grad_gate;           // fp32 [hidden], or bf16 [T, hidden], or nullptr
+    void* workspace;
+    int T, hidden;
+};
+size_t combine_norm_workspace_bytes(int T, int hidden);
+hipError_t launch_combine_norm_backward(const CombineNormBackwardArgs& a, hipStream_t stream);
+
 }  // namespace ep

@@ -397,6 +397,72 @@ ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void
                        int out_features, const float* scales, const void* base, void* out, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* What stands around a block of a layer, for ep_combine_norm and its gradient.  The vectors post_weight, pre_weight and a gate
+ * per channel are all fp32 (vectors_bf16 = 0) or all bf16; device pointers, 16-byte aligned. */
+typedef struct ep_norm_args {
+    const void* residual;     /* bf16 [num_tokens, hidden], nullable (zeros): the stream that the block adds to            */
+    const void* post_weight;  /* [hidden], nullable: weight of the norm after the block; NULL: no such norm                */
+    const void* pre_weight;   /* [hidden], nullable: weight of the norm before the next block                              */
+    const void* gate;         /* nullable (1): [hidden], or with gate_per_token bf16 [num_tokens, hidden]                  */
+    int gate_per_token;
+    int vectors_bf16;
+    float residual_scale;     /* finite                                                                                    */
+    float eps;                /* positive                                                                                  */
+} ep_norm_args_t;
+
+typedef enum ep_norm_f {
+    EP_NORM_F_KEPT = 0,       /* fp32 [num_tokens, hidden], `kept` of ep_combine_norm                                      */
+    EP_NORM_F_BF16 = 1        /* bf16 [num_tokens, hidden], y of a call without handle and bias                            */
+} ep_norm_f_t;
+
+/* Bytes of device workspace of ep_combine_norm_backward.  Host only.  Returns 0 for arguments outside the limits. */
+size_t ep_combine_norm_workspace_bytes(int num_tokens, int hidden);
+
+/*
+ * ep_combine_norm -- the combine with what stands between this block and the next, in one pass over the rows
+ * ([DeepEP->MegaMoE] §2.5: the top-k rows of a token are accumulated; what follows needs whole rows of that sum):
+ *   f[t] = sum_k w[t,k] * y[slot(t,k)] + bias[t]               as ep_combine, kept in fp32;  without a handle y[t] + bias[t]
+ *   a[t] = f[t] / sqrt(mean(f[t]^2) + eps) * post_weight       a = f without post_weight
+ *   r[t] = residual_scale * residual[t] + gate * a[t]
+ *   n[t] = r[t] / sqrt(mean(r[t]^2) + eps) * pre_weight
+ *   out = r and normed = n, each rounded once to bf16: n is the norm of r before that rounding.
+ * Sums are fp32 in a fixed order.  A token whose entries are all unused has f = bias, or zeros.
+ *
+ *   handle        as in ep_combine, or NULL: y is the output of some other block, a row per token.
+ *   y             device bf16 [y_rows, hidden];  y_rows >= ep_recv_capacity(...), or without a handle the number of tokens.
+ *   topk_weights  device fp32 [num_tokens, num_topk], nullable (1; NULL without a handle).
+ *   bias          device bf16 [num_tokens, hidden], nullable.
+ *   out           device bf16 [num_tokens, hidden], nullable; may be the residual itself.
+ *   normed        device bf16 [num_tokens, hidden], nullable; needs pre_weight.
+ *   kept          device fp32 [num_tokens, hidden], nullable: f, for ep_combine_norm_backward.
+ *   At least one of the three is required; every row of each is written.
+ */
+ep_status_t ep_combine_norm(ep_handle_t handle, const void* y, int hidden, int64_t y_rows, const float* topk_weights,
+                            const void* bias, const ep_norm_args_t* norm, void* out, void* normed, float* kept, void* stream);
+
+/*
+ * ep_combine_norm_backward -- gradients of ep_combine_norm.  With fhat = f * rf and rhat = r * rr (rf and rr the two norms'
+ * factors, computed again from f and the residual), dn = grad_normed, means over the channels of a token:
+ *   dr = grad_out + rr * (dn * pre - rhat * mean(dn * pre * rhat))         dpre  = sum over tokens of dn * rhat
+ *   grad_residual = residual_scale * dr                                    dgate = dr * a  (gate per channel: summed over tokens)
+ *   da = gate * dr                                                         dpost = sum over tokens of da * fhat
+ *   grad_f = rf * (da * post - fhat * mean(da * post * fhat))              (da without post_weight)
+ * grad_f is the gradient of the combine's output, grad_out of ep_combine_backward, and of its bias.
+ *
+ *   grad_out, grad_normed  device bf16 [num_tokens, hidden], each nullable (zeros), not both.
+ *   f                      device [num_tokens, hidden] of f_type.
+ *   norm                   as given to ep_combine_norm.
+ *   grad_f, grad_residual  device bf16 [num_tokens, hidden], nullable.
+ *   grad_post, grad_pre    device fp32 [hidden], nullable: written, not added to.
+ *   grad_gate              device, nullable: fp32 [hidden], or with gate_per_token bf16 [num_tokens, hidden].
+ *   workspace              device scratch of ep_combine_norm_workspace_bytes(...) bytes, 256-byte aligned, as in
+ *                          ep_expert_ffn.
+ *   At least one gradient is required.  No output may overlap an input.  Sums over tokens run in a fixed order.
+ */
+ep_status_t ep_combine_norm_backward(const void* grad_out, const void* grad_normed, const void* f, ep_norm_f_t f_type, int num_tokens,
+                                     int hidden, const ep_norm_args_t* norm, void* grad_f, void* grad_residual, float* grad_post,
+                                     float* grad_pre, void* grad_gate, void* workspace, size_t workspace_bytes, void* stream);
+
 /* End of a handle's life ([MoE-comm] §二: a handle and the buffers it refers to must outlive every operation
  * that uses them; §一: the handle carries the dispatch's grouping for the combine and backward).  Frees the host
  * object only: never blocks, never touches device memory, so kernels already enqueued with the handle are

@@ -27,6 +27,8 @@ LIB_PATH = os.path.join(_HERE, "libep_mi355x.so")
 EP_OK = 0
 EP_DTYPE_BF16 = 0
 EP_DTYPE_FP8_E4M3 = 1
+EP_WEIGHTS_BF16, EP_WEIGHTS_E4M3, EP_WEIGHTS_INT4, EP_WEIGHTS_E2M1 = 0, 1, 2, 3
+_W4_KINDS = {"int4": EP_WEIGHTS_INT4, "e2m1": EP_WEIGHTS_E2M1}
 
 
 class EPError(RuntimeError):
@@ -41,6 +43,10 @@ class _DispatchOut(ctypes.Structure):
         ("send_x", ctypes.c_void_p), ("send_x_scales", ctypes.c_void_p), ("send_src_idx", ctypes.c_void_p),
         ("send_topk_idx", ctypes.c_void_p), ("send_topk_weights", ctypes.c_void_p),
     ]
+
+
+class _Weights(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int), ("group", ctypes.c_int)]
 
 
 class _NormArgs(ctypes.Structure):
@@ -99,6 +105,19 @@ def _load_library():
     lib.ep_adapter_workspace_bytes.argtypes = [I, I, I, I]
     lib.ep_adapter.restype = I
     lib.ep_adapter.argtypes = [P, P, I, P, P, I, I, P, P, P, P, SZ, P]
+    W = ctypes.POINTER(_Weights)
+    lib.ep_w4_packed_bytes.restype = SZ
+    lib.ep_w4_packed_bytes.argtypes = [I, I, I, I]
+    lib.ep_w4_packed_scale_bytes.restype = SZ
+    lib.ep_w4_packed_scale_bytes.argtypes = [I, I, I, I]
+    lib.ep_w4_pack.restype = I
+    lib.ep_w4_pack.argtypes = [P, P, I, I, I, I, I, P, P, P]
+    lib.ep_expert_ffn_w4.restype = I
+    lib.ep_expert_ffn_w4.argtypes = [P, P, I, I, I64, W, W, P, P, SZ, P]
+    lib.ep_moe_few_workspace_bytes.restype = SZ
+    lib.ep_moe_few_workspace_bytes.argtypes = [I, I, I]
+    lib.ep_moe_few.restype = I
+    lib.ep_moe_few.argtypes = [P, P, P, I, I, I, I, I, I, I, W, W, P, P, P, SZ, P]
     lib.ep_combine_norm_workspace_bytes.restype = SZ
     lib.ep_combine_norm_workspace_bytes.argtypes = [I, I]
     lib.ep_combine_norm.restype = I
@@ -693,11 +712,13 @@ def check_ffn_weights(w13, w2, dtype, El, H, device):
 
 
 def check_ffn_scales(xs, s13, s2, rows, El, H, I, device):
-    """The scales of e4m3 rows and weights: per row and 128 channels, per 128 x 128 block."""
+    """The scales of e4m3 rows and weights: per row and 128 channels (xs False: the rows have none), per 128 x 128 block."""
     for t, name, shape in ((xs, "recv_x_scales", (rows, H // 128)), (s13, "w13_scales", (El, 2 * I // 128, H // 128)),
                            (s2, "w2_scales", (El, H // 128, I // 128))):
+        if t is False:
+            continue
         if t is None:
-            raise ValueError("e4m3 rows need %s" % name)
+            raise ValueError("e4m3 %s need %s" % ("rows" if xs is not False else "weights", name))
         _need(t, torch.float32, name, device, shape)
 
 
@@ -812,6 +833,147 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
         workspace = _empty(stream, x, n, torch.uint8)
     _check(_lib.ep_adapter(handle.ptr, _ptr(x), H, _ptr(a), _ptr(b), r, N, _ptr(scales), _ptr(base), _ptr(out),
                            _ptr(workspace), workspace.numel(), _stream(stream)), "ep_adapter")
+    return out
+
+
+class W4Weights:
+    """4-bit weights [matrices, rows, columns] as ep_w4_pack lays them out: `values` and `scales` (uint8 tensors, opaque), `kind`
+    ("int4" or "e2m1"), `group` and `shape`."""
+
+    def __init__(self, values, scales, kind, group, shape):
+        self.values, self.scales, self.kind, self.group, self.shape = values, scales, kind, group, tuple(shape)
+        self.device = values.device
+        self._args = _Weights(values.data_ptr(), scales.data_ptr(), _W4_KINDS[kind], group)
+
+
+def ep_w4_packed_bytes(matrices, rows, columns, group) -> int:
+    return int(_lib.ep_w4_packed_bytes(matrices, rows, columns, group))
+
+
+def ep_w4_packed_scale_bytes(matrices, rows, columns, group) -> int:
+    return int(_lib.ep_w4_packed_scale_bytes(matrices, rows, columns, group))
+
+
+def ep_w4_pack(codes, scales, kind, stream=None) -> W4Weights:
+    """Lays 4-bit weights out for ep_expert_ffn_w4 and ep_moe_few, once, when they are loaded: w = scales[..., k / group] *
+    value(code).  codes: uint8 [matrices, rows, columns / 2], two codes a byte, the even column in the lower half; scales: bf16
+    [matrices, rows, columns / group], group 32, 64 or 128; kind "int4" (code - 8) or "e2m1".  codes and scales are not needed
+    afterwards."""
+    if kind not in _W4_KINDS:
+        raise ValueError("kind must be one of %s" % sorted(_W4_KINDS))
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+        raise ValueError("codes must be [matrices, rows, columns / 2]")
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3:
+        raise ValueError("scales must be [matrices, rows, columns / group]")
+    dev = _on_current(codes, "codes")
+    M, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    _need(codes, torch.uint8, "codes", dev)
+    _need(scales, torch.bfloat16, "scales", dev, (M, N, scales.shape[2]))
+    if scales.shape[2] == 0 or K % scales.shape[2] != 0:
+        raise ValueError("scales must be [matrices, rows, columns / group]")
+    group = K // scales.shape[2]
+    n, m = ep_w4_packed_bytes(M, N, K, group), ep_w4_packed_scale_bytes(M, N, K, group)
+    if n == 0:
+        raise EPError("ep_w4_pack takes no weights of matrices=%d rows=%d columns=%d group=%d" % (M, N, K, group))
+    _need(codes, torch.uint8, "codes")     # on a GPU, after the rules on shapes
+    values, packed = _empty(stream, codes, n, torch.uint8), _empty(stream, codes, m, torch.uint8)
+    _check(_lib.ep_w4_pack(_ptr(codes), _ptr(scales), _W4_KINDS[kind], M, N, K, group, _ptr(values), _ptr(packed), _stream(stream)),
+           "ep_w4_pack")
+    return W4Weights(values, packed, kind, group, (M, N, K))
+
+
+def check_w4_weights(w13, w2, El, H, device):
+    """w13 [El, 2 I, H] and w2 [El, H, I], packed; returns I.  (Formats and groups are checked by the library.)"""
+    for w, name in ((w13, "w13"), (w2, "w2")):
+        if not isinstance(w, W4Weights):
+            raise TypeError("%s must be W4Weights (ep_w4_pack)" % name)
+        if w.device != device:
+            raise ValueError("%s must be on %s, got %s" % (name, device, w.device))
+    I = w2.shape[2]
+    for w, name, shape in ((w2, "w2", (El, H, I)), (w13, "w13", (El, 2 * I, H))):
+        if w.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, w.shape))
+    return I
+
+
+def ep_expert_ffn_w4(handle: Handle, recv_x, w13: W4Weights, w2: W4Weights, y=None, workspace=None, stream=None):
+    """ep_expert_ffn with bf16 rows [rows, H] and 4-bit weights: w13 [El, 2 I, H] (gate rows first) and w2 [El, H, I] from
+    ep_w4_pack.  Returns y bf16 [rows, H]; rows that are not valid rows of an expert keep what y held."""
+    dev, El = _device(handle), handle.num_local_experts
+    H = _columns(recv_x, "recv_x")
+    rows = recv_x.shape[0]
+    _need(recv_x, torch.bfloat16, "recv_x", dev, (rows, H))
+    I = check_w4_weights(w13, w2, El, H, dev)
+    if y is None:
+        y = _empty(stream, recv_x, (rows, H))
+    else:
+        _need(y, torch.bfloat16, "y", dev, (rows, H))
+    workspace = _ffn_workspace(handle, H, I, False, workspace, dev, stream)
+    _check(_lib.ep_expert_ffn_w4(handle.ptr, _ptr(recv_x), H, I, rows, ctypes.byref(w13._args), ctypes.byref(w2._args), _ptr(y),
+                                 _ptr(workspace), workspace.numel(), _stream(stream)), "ep_expert_ffn_w4")
+    return y
+
+
+@functools.lru_cache(maxsize=1024)
+def ep_moe_few_workspace_bytes(num_tokens, num_topk, intermediate) -> int:
+    """Bytes of workspace of ep_moe_few."""
+    return int(_lib.ep_moe_few_workspace_bytes(num_tokens, num_topk, intermediate))
+
+
+def ep_moe_few(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=None, num_experts=None, num_ranks=1, rank=0, bias=None,
+               out=None, workspace=None, stream=None):
+    """This rank's share of a whole mixture-of-experts layer for a few tokens (up to 128, and 1024 entries), in two kernels:
+    out[t] = sum_k topk_weights[t,k] * ffn_e(x[t]) + bias[t] over the entries whose expert e = topk_idx[t,k] is this rank's.
+    x bf16 [T, H], topk_idx int64 [T, K], topk_weights fp32 [T, K] or None (1).  w13 [El, 2 I, H] (gate rows first) and w2
+    [El, H, I]: both bf16, both uint8 holding e4m3 with w13_scales [El, 2 I / 128, H / 128] and w2_scales [El, H / 128, I / 128],
+    or both W4Weights (ep_w4_pack).  num_experts defaults to El * num_ranks.  Returns out bf16 [T, H] (may be bias itself)."""
+    H = _columns(x, "x")
+    dev, T = _on_current(x, "x"), x.shape[0]
+    _need(x, torch.bfloat16, "x", dev)
+    K = _columns(topk_idx, "topk_idx")
+    _need(topk_idx, torch.int64, "topk_idx", dev, (T, K))
+    if topk_weights is not None:
+        _need(topk_weights, torch.float32, "topk_weights", dev, (T, K))
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", dev, (T, H))
+    if not hasattr(w2, "shape") or len(w2.shape) != 3:
+        raise ValueError("w2 must be [num_local_experts, hidden, intermediate]")
+    El = w2.shape[0]
+    if num_ranks < 1 or El < 1:
+        raise ValueError("num_experts must be a positive multiple of num_ranks")
+    if num_experts is None:
+        num_experts = El * num_ranks
+    elif num_experts != El * num_ranks:
+        raise ValueError("num_experts must be %d (the experts of w2) * num_ranks" % El)
+    if isinstance(w2, W4Weights):
+        I = check_w4_weights(w13, w2, El, H, dev)
+        a13, a2 = w13._args, w2._args
+    else:
+        if w13 is None:
+            raise ValueError("w13 is required")
+        if w2.dtype not in (torch.bfloat16, torch.uint8):
+            raise TypeError("w2 must be bfloat16, uint8 (e4m3) or W4Weights, got %s" % w2.dtype)
+        fp8 = w2.dtype == torch.uint8
+        I = check_ffn_weights(w13, w2, w2.dtype, El, H, dev)
+        if fp8:
+            check_ffn_scales(False, w13_scales, w2_scales, 0, El, H, I, dev)
+        kind = EP_WEIGHTS_E4M3 if fp8 else EP_WEIGHTS_BF16
+        a13 = _Weights(w13.data_ptr(), w13_scales.data_ptr() if fp8 else None, kind, 0)
+        a2 = _Weights(w2.data_ptr(), w2_scales.data_ptr() if fp8 else None, kind, 0)
+    if out is None:
+        out = _empty(stream, x, (T, H))
+    else:
+        _need(out, torch.bfloat16, "out", dev, (T, H))
+    if workspace is not None:
+        check_workspace(workspace, dev)
+    else:
+        n = ep_moe_few_workspace_bytes(T, K, I)
+        if n == 0:
+            raise EPError("ep_moe_few takes no calls of T=%d K=%d intermediate=%d" % (T, K, I))
+        workspace = _empty(stream, x, n, torch.uint8)
+    _need(x, torch.bfloat16, "x")     # on a GPU, after the rules on shapes
+    _check(_lib.ep_moe_few(_ptr(x), _ptr(topk_idx), _ptr(topk_weights), T, K, num_experts, num_ranks, rank, H, I, ctypes.byref(a13),
+                           ctypes.byref(a2), _ptr(bias), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)), "ep_moe_few")
     return out
 
 
@@ -954,6 +1116,7 @@ def ep_handle_free(handle: Handle):
 __all__ = ["ep_get_layout", "ep_dispatch", "ep_layout_dispatch", "ep_layout_dispatch_noalloc", "ep_combine", "ep_combine_tokens", "ep_handle_free", "ep_recv_capacity",
            "ep_dispatch_rows", "ep_combine_reduce", "ep_combine_backward", "ep_expert_ffn", "ep_expert_ffn_backward",
            "ep_expert_ffn_workspace_bytes", "ep_adapter", "ep_adapter_workspace_bytes",
+           "ep_w4_pack", "W4Weights", "ep_w4_packed_bytes", "ep_w4_packed_scale_bytes", "ep_expert_ffn_w4", "ep_moe_few", "ep_moe_few_workspace_bytes",
            "ep_combine_norm", "ep_combine_norm_backward", "ep_combine_norm_workspace_bytes",
            "ep_layout_workspace_bytes", "alloc_dispatch_outputs", "Handle", "EPError", "LIB_PATH",
            "hip_runtimes_loaded"]

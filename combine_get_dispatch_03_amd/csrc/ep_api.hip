@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <unordered_set>
@@ -343,6 +344,44 @@ ep_status_t check_scratch(const void* workspace, size_t have, size_t need) {
         return fail(EP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (have < need) return fail(EP_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", have, need);
     return EP_OK;
+}
+
+const char* w4_group(int group) { return group == 32 || group == 64 || group == 128 ? nullptr : "group must be 32, 64 or 128"; }
+
+// Weights of the gated block in a format: the sizes that it allows; nullptr: fine.
+const char* weights_shape(const ep_weights_t* w13, const ep_weights_t* w2, int hidden, int inter) {
+    if (w13 == nullptr || w2 == nullptr) return "w13 and w2 must be non-NULL";
+    if (w13->format < EP_WEIGHTS_BF16 || w13->format > EP_WEIGHTS_E2M1) return "format must be EP_WEIGHTS_BF16, _E4M3, _INT4 or _E2M1";
+    if (w2->format != w13->format) return "w13 and w2 must have the same format";
+    if (const char* why = ffn_shape(hidden, inter, w13->format == EP_WEIGHTS_E4M3)) return why;
+    if (w13->format < EP_WEIGHTS_INT4) return nullptr;
+    if (const char* why = w4_group(w13->group)) return why;
+    if (w2->group != w13->group) return "w13 and w2 must have the same group";
+    if (hidden % w13->group != 0 || inter % w13->group != 0) return "4-bit weights need hidden and intermediate to be multiples of the group";
+    return nullptr;
+}
+const char* weights_pointers(const ep_weights_t* w13, const ep_weights_t* w2) {
+    const bool scaled = w13->format != EP_WEIGHTS_BF16;
+    for (const ep_weights_t* w : {w13, w2}) {
+        if (w->values == nullptr || !aligned16(w->values)) return "values of w13 and w2 must be non-NULL and 16-byte aligned";
+        if (scaled && (w->scales == nullptr || !aligned16(w->scales))) return "scales of w13 and w2 must be non-NULL and 16-byte aligned";
+    }
+    return nullptr;
+}
+
+const char* w4_shape(int matrices, int rows, int columns, int group) {
+    if (const char* why = w4_group(group)) return why;
+    if (matrices < 1 || matrices > kMaxExperts) return "matrices must be in [1, 1024]";
+    if (rows < 16 || rows > 2 * kMaxHidden || rows % 16 != 0) return "rows must be a multiple of 16 in [16, 65536]";
+    if (columns < group || columns > kMaxHidden || columns % group != 0) return "columns must be a multiple of the group, at most 32768";
+    return nullptr;
+}
+
+const char* few_shape(int num_tokens, int num_topk) {
+    if (num_tokens < 0 || num_tokens > kFewTokens) return "num_tokens must be in [0, 128]";
+    if (num_topk < 1 || num_topk > kMaxTopk) return "num_topk must be in [1, 32]";
+    if (num_tokens * num_topk > kFewEntries) return "num_tokens * num_topk must be at most 1024";
+    return nullptr;
 }
 
 // What ep_combine_norm and its gradient take around the block; nullptr: fine.
@@ -756,6 +795,82 @@ ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void
     p.n_out = out_features;
     const hipError_t err = launch_adapter(*h, p, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return hip_fail(err, "adapter launch");
+    return EP_OK;
+}
+
+size_t ep_w4_packed_bytes(int matrices, int rows, int columns, int group) {
+    return w4_shape(matrices, rows, columns, group) == nullptr ? w4_packed_bytes(matrices, rows, columns) : 0;
+}
+
+size_t ep_w4_packed_scale_bytes(int matrices, int rows, int columns, int group) {
+    return w4_shape(matrices, rows, columns, group) == nullptr ? w4_packed_scale_bytes(matrices, rows, columns, group) : 0;
+}
+
+ep_status_t ep_w4_pack(const uint8_t* codes, const void* scales, ep_weight_format_t format, int matrices, int rows, int columns, int group,
+                       void* packed, void* packed_scales, void* stream) {
+    g_last_error[0] = '\0';
+    if (format != EP_WEIGHTS_INT4 && format != EP_WEIGHTS_E2M1)
+        return fail(EP_ERR_INVALID_ARG, "format must be EP_WEIGHTS_INT4 or EP_WEIGHTS_E2M1");
+    if (const char* why = w4_shape(matrices, rows, columns, group)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (codes == nullptr || !aligned16(codes)) return fail(EP_ERR_INVALID_ARG, "codes must be non-NULL and 16-byte aligned");
+    if (scales == nullptr || !aligned16(scales)) return fail(EP_ERR_INVALID_ARG, "scales must be non-NULL and 16-byte aligned");
+    if (packed == nullptr || !aligned16(packed) || packed_scales == nullptr || !aligned16(packed_scales))
+        return fail(EP_ERR_INVALID_ARG, "packed and packed_scales must be non-NULL and 16-byte aligned");
+    const W4PackArgs a{codes, static_cast<const uint16_t*>(scales), packed, packed_scales, format == EP_WEIGHTS_INT4, matrices, rows, columns, group};
+    const hipError_t err = launch_w4_pack(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "w4_pack launch");
+    return EP_OK;
+}
+
+ep_status_t ep_expert_ffn_w4(ep_handle_t handle, const void* recv_x, int hidden, int intermediate, int64_t rows, const ep_weights_t* w13,
+                             const ep_weights_t* w2, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    const Handle* h = check_handle(handle);
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "invalid handle");
+    if (const char* why = weights_shape(w13, w2, hidden, intermediate)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (w13->format < EP_WEIGHTS_INT4) return fail(EP_ERR_INVALID_ARG, "ep_expert_ffn_w4 takes EP_WEIGHTS_INT4 or EP_WEIGHTS_E2M1");
+    if (h->T > 0) {
+        if (rows < h->cap)
+            return fail(EP_ERR_INVALID_ARG, "rows %lld < required %lld", (long long)rows, (long long)h->cap);
+        if (recv_x == nullptr || !aligned16(recv_x))
+            return fail(EP_ERR_INVALID_ARG, "recv_x must be non-NULL and 16-byte aligned");
+        if (const char* why = weights_pointers(w13, w2)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+        if (y == nullptr || !aligned16(y)) return fail(EP_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, ffn_workspace(h->cap, intermediate, false).bytes);
+        if (st != EP_OK) return st;
+    }
+    const W4Args a{recv_x, WeightTensor{w13->values, w13->scales}, WeightTensor{w2->values, w2->scales}, y, static_cast<uint16_t*>(workspace),
+                   hidden, intermediate, w13->format == EP_WEIGHTS_INT4, w13->group};
+    const hipError_t err = launch_expert_ffn_w4(*h, a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "expert_ffn_w4 launch");
+    return EP_OK;
+}
+
+size_t ep_moe_few_workspace_bytes(int num_tokens, int num_topk, int intermediate) {
+    if (few_shape(num_tokens, num_topk) != nullptr || intermediate < 8 || intermediate > kMaxHidden || intermediate % 8 != 0) return 0;
+    return align_up(few_workspace_bytes(num_tokens, num_topk, intermediate), 256);
+}
+
+ep_status_t ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, int num_tokens, int num_topk, int num_experts,
+                       int num_ranks, int rank, int hidden, int intermediate, const ep_weights_t* w13, const ep_weights_t* w2,
+                       const void* bias, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    if (const char* why = few_shape(num_tokens, num_topk)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (const char* why = check_shape(num_tokens, num_topk, num_experts, num_ranks, rank, 1)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (const char* why = weights_shape(w13, w2, hidden, intermediate)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+    if (num_tokens > 0) {
+        if (x == nullptr || !aligned16(x)) return fail(EP_ERR_INVALID_ARG, "x must be non-NULL and 16-byte aligned");
+        if (topk_idx == nullptr) return fail(EP_ERR_INVALID_ARG, "topk_idx is NULL");
+        if (const char* why = weights_pointers(w13, w2)) return fail(EP_ERR_INVALID_ARG, "%s", why);
+        if (!aligned16(bias)) return fail(EP_ERR_INVALID_ARG, "bias must be 16-byte aligned");
+        if (out == nullptr || !aligned16(out)) return fail(EP_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, few_workspace_bytes(num_tokens, num_topk, intermediate));
+        if (st != EP_OK) return st;
+    }
+    const FewArgs a{x, topk_idx, topk_weights, bias, WeightTensor{w13->values, w13->scales}, WeightTensor{w2->values, w2->scales}, out, workspace,
+                    (WeightFormat)w13->format, w13->group, num_tokens, num_topk, num_experts, num_ranks, rank, hidden, intermediate};
+    const hipError_t err = launch_few(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return hip_fail(err, "moe_few launch");
     return EP_OK;
 }
 

@@ -157,6 +157,53 @@ struct AdapterArgs {
 size_t adapter_workspace_bytes(int T, int El, int hidden, int rank);
 hipError_t launch_adapter(const Handle& h, const AdapterArgs& a, hipStream_t stream);
 
+// Formats of weights, as ep_weight_format_t.
+enum WeightFormat { kWeightsBf16, kWeightsE4m3, kWeightsInt4, kWeightsE2m1 };
+
+struct WeightTensor {
+    const void* values;        // bf16 or e4m3 rows, or packed codes
+    const void* scales;        // e4m3: fp32 per 128 x 128; 4-bit: packed bf16 scales
+};
+
+struct W4PackArgs {
+    const uint8_t* codes;      // [matrices, N, K / 2]
+    const uint16_t* scales;    // bf16 [matrices, N, K / group]
+    void* packed;
+    void* packed_scales;
+    bool int4;
+    int matrices, N, K, group;
+};
+size_t w4_packed_bytes(int64_t matrices, int N, int K);
+size_t w4_packed_scale_bytes(int64_t matrices, int N, int K, int group);
+hipError_t launch_w4_pack(const W4PackArgs& a, hipStream_t stream);
+
+struct W4Args {
+    const void* x;             // bf16 [rows, hidden]
+    WeightTensor w13, w2;
+    void* y;                   // bf16 [rows, hidden]
+    uint16_t* h;               // workspace: bf16 [cap, row_pitch(inter)]
+    int hidden, inter;
+    bool int4;
+    int group;
+};
+hipError_t launch_expert_ffn_w4(const Handle& h, const W4Args& a, hipStream_t stream);
+
+constexpr int kFewTokens = 128, kFewEntries = 1024;
+struct FewArgs {
+    const void* x;             // bf16 [T, hidden]
+    const int64_t* topk_idx;   // [T, K]
+    const float* topk_weights; // [T, K] or nullptr (weights of 1)
+    const void* bias;          // bf16 [T, hidden] or nullptr
+    WeightTensor w13, w2;
+    void* out;                 // bf16 [T, hidden]
+    void* workspace;           // bf16 [T * K, row_pitch(inter)]
+    WeightFormat format;
+    int group;                 // 4-bit
+    int T, K, E, R, rank, hidden, inter;
+};
+size_t few_workspace_bytes(int T, int K, int inter);
+hipError_t launch_few(const FewArgs& a, hipStream_t stream);
+
 // What stands around a block: its norm, gate and residual, and the next norm.  Vectors [hidden] are all bf16 or all fp32.
 struct NormVectors {
     const uint16_t* residual;  // bf16 [T, hidden] or nullptr (zeros)

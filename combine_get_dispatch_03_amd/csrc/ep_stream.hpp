@@ -1,0 +1,123 @@
+// ep_stream.hpp -- products of few rows with many weights: the weights stream from memory into the matrix instruction's
+// registers, past nothing (see ep_weights.hpp for what a piece of them is); the rows' fragments come from the caches.
+#pragma once
+
+#include "ep_ffn.hpp"
+#include "ep_weights.hpp"
+
+namespace ep {
+
+// 16 * MT rows' fragments beside a piece: lane (r, g) holds row r of each 16.
+template <int MT>
+struct RowPointers {
+    const char* at[MT];
+    bool there[MT];
+
+    template <class W>
+    __device__ __forceinline__ void load(i32x4 (&x)[MT][4], int piece, int K) const {
+        const int g = lane_id() >> 4;
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = piece * kPieceK + W::k_of(j, g);
+                x[a][j] = i32x4{0, 0, 0, 0};
+                if (there[a] && k < K) x[a][j] = *reinterpret_cast<const i32x4*>(at[a] + (int64_t)k * 2);
+            }
+    }
+};
+
+// acc[NF][MT] += pieces first, first + step, ... below `end` of NF rows of pieces, by the rows.  D pieces' loads are under way
+// while one is multiplied: the rows' too, since a wait for the newest load is one for all before it.
+template <class W, int MT, int NF, int D>
+__device__ __forceinline__ void stream_pieces(const W (&w)[NF], const RowPointers<MT>& rows, int K, int first, int step, int end,
+                                              f32x4 (&acc)[NF][MT]) {
+    struct Stage {
+        typename W::Raw w[NF];
+        i32x4 x[MT][4];
+    } stage[D];
+    auto load = [&](Stage& s, int piece) {
+        rows.template load<W>(s.x, piece, K);
+#pragma unroll
+        for (int b = 0; b < NF; ++b) s.w[b] = w[b].load(piece);
+    };
+    auto use = [&](const Stage& s) {
+#pragma unroll
+        for (int b = 0; b < NF; ++b) add_piece<W, MT>(s.w[b], s.x, acc[b]);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (first + d * step < end) load(stage[d], first + d * step);
+    int p = first;
+    for (; p + (2 * D - 1) * step < end; p += D * step)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            use(stage[d]);
+            load(stage[d], p + (D + d) * step);
+        }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        if (p + d * step >= end) return;
+        use(stage[d]);
+        if (p + (D + d) * step < end) load(stage[d], p + (D + d) * step);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        if (p + (D + d) * step >= end) return;
+        use(stage[d]);
+    }
+}
+
+// One workgroup's product: `count` rows (up to 16 * MT) by NF rows of pieces of an expert's weights, k split over the waves, whose
+// sums meet in LDS.  UP: half of the pieces are gate channels from n0 on, half the same up channels, N of each, and h = silu(g) u is
+// stored; otherwise output channels from n0 on.  out_row(m): where row m goes.
+constexpr int kStreamThreads = 256, kStreamWaves = kStreamThreads / kWave;
+template <int NF>
+constexpr int stream_lds() { return kStreamWaves * 16 * (NF * 16 + 4) * 4; }
+
+template <class W, bool UP, int MT, int NF, int D, class OutRow>
+__device__ __forceinline__ void stream_product(const WeightArgs& weights, int expert, int N, int K, int n0, const RowPointers<MT>& rows,
+                                               int count, float* sums, OutRow out_row) {
+    constexpr int kCols = NF * 16, kOut = UP ? kCols / 2 : kCols, kPitch = kCols + 4;
+    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
+    W w[NF];
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+        const int half = UP ? b / (NF / 2) : 0, n = n0 + (UP ? b % (NF / 2) : b) * 16;
+        w[b].init(weights, expert, half * N + (n < N ? n : 0), half * N + N);
+    }
+    f32x4 acc[NF][MT];
+#pragma unroll
+    for (int b = 0; b < NF; ++b)
+#pragma unroll
+        for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    stream_pieces<W, MT, NF, D>(w, rows, K, wave, kStreamWaves, pieces_of(K), acc);
+
+    // [wave][16 rows][channels], 16 rows at a time
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        if (a * 16 >= count) break;
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NF; ++b) *reinterpret_cast<f32x4*>(sums + (wave * 16 + r) * kPitch + b * 16 + g * 4) = acc[b][a];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * kOut / 4; i += kStreamThreads) {
+            const int m = i / (kOut / 4), n4 = i % (kOut / 4) * 4;
+            if (a * 16 + m >= count || n0 + n4 >= N) continue;
+            f32x4 v{0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+#pragma unroll
+            for (int q = 0; q < kStreamWaves; ++q) {
+                v += *reinterpret_cast<const f32x4*>(sums + (q * 16 + m) * kPitch + n4);
+                if constexpr (UP) u += *reinterpret_cast<const f32x4*>(sums + (q * 16 + m) * kPitch + kOut + n4);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] *= W::kUnit;
+                if constexpr (UP) v[j] = v[j] * sigmoid(v[j]) * (u[j] * W::kUnit);
+            }
+            store4(out_row(a * 16 + m) + n0 + n4, v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+}  // namespace ep

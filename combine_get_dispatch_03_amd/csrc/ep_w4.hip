@@ -1,0 +1,127 @@
+// ep_w4.hip -- experts with weights of four bits: laying the weights out (once, when they are loaded) and the gated feed-forward
+// block over the rows that a dispatch placed.
+//
+//   w[n][k] = s[n][k / group] * v(code[n][k])        v = code - 8, or the e2m1 value of the code
+#include "ep_expert_tiles.hpp"
+#include "ep_stream.hpp"
+
+namespace ep {
+namespace {
+
+// A thread writes 16 bytes of codes, one lane's part of a piece: k j * 32 + g * 8 .. + 7 for j = 0..3 (see ep_weights.hpp).
+__global__ __launch_bounds__(256) void k_pack_codes(const uint8_t* codes, char* packed, uint32_t flip, int N, int K, int64_t parts) {
+    const int64_t i = block_id() * 256 + threadIdx.x;
+    if (i >= parts) return;
+    const int pieces = pieces_of(K), lane = (int)(i & 63), r = lane & 15, g = lane >> 4;
+    const int64_t piece = i >> 6, row = piece / pieces * kPieceRows + r;       // of all matrices' rows: N is a multiple of 16
+    const int k0 = (int)(piece % pieces) * kPieceK;
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * 32 + g * 8;
+        v[j] = k < K ? *reinterpret_cast<const uint32_t*>(codes + (row * K + k) / 2) ^ flip : 0u;
+    }
+    reinterpret_cast<u32x4*>(packed)[i] = v;
+}
+
+// Scales of a piece: [g][group][4 rows], bf16; a thread writes one.
+__global__ __launch_bounds__(256) void k_pack_scales(const uint16_t* scales, uint16_t* packed, int K, int group, int64_t count) {
+    const int64_t i = block_id() * 256 + threadIdx.x;
+    if (i >= count) return;
+    const int pieces = pieces_of(K), groups = kPieceK / group, per = 16 * groups;
+    const int64_t piece = i / per;
+    const int at = (int)(i % per), g = at / (4 * groups), s = at / 4 % groups, r = g * 4 + at % 4;
+    const int64_t row = piece / pieces * kPieceRows + r;
+    const int k = (int)(piece % pieces) * groups + s;
+    packed[i] = k < K / group ? scales[row * (K / group) + k] : (uint16_t)0;
+}
+
+struct Params {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int El;
+    const uint16_t* s;     // rows
+    WeightArgs w;
+    uint16_t* out;
+    int N, K;              // channels of a projection's output, of its input
+    int sp, op;            // elements between rows of s and of out
+};
+
+template <class W, bool UP, int MT, int NF, int D>
+__device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, int n0, float* sums) {
+    const int r = lane_id() & 15;
+    RowPointers<MT> rows;
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+        rows.there[a] = a * 16 + r < t.rows;
+        rows.at[a] = reinterpret_cast<const char*>(p.s + (int64_t)(t.row0 + (rows.there[a] ? a * 16 + r : 0)) * p.sp);
+    }
+    stream_product<W, UP, MT, NF, D>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
+                                     [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
+}
+
+// Up to 16 * MT rows of an expert by 16 * NF rows of its weights.
+template <class W, bool UP, int MT, int NF>
+__global__ __launch_bounds__(kStreamThreads) void k_w4_stream(Params p) {
+    __shared__ __align__(16) float sums[stream_lds<NF>() / 4];
+    constexpr int kChannels = UP ? NF * 8 : NF * 16;
+    const RowTiles<MT * 16> tiles(p.cnt, p.psum, p.El);
+    const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
+    if (tile >= tiles.total) return;
+    const RowTile t = tiles.find(tile);
+    const int n0 = blockIdx.x % cols * kChannels, steps = (t.rows + 15) / 16;
+    if (MT == 1 || steps == 1) rows_product<W, UP, 1, NF, 2>(p, t, n0, sums);
+    else if (MT == 2 || steps == 2) rows_product<W, UP, 2, NF, 1>(p, t, n0, sums);
+    else rows_product<W, UP, 4, NF, 1>(p, t, n0, sums);
+}
+
+template <class W, bool UP, int MT, int NF>
+hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
+    constexpr int kChannels = UP ? NF * 8 : NF * 16, kRows = MT * 16;
+    const int64_t entries = (int64_t)h.T * h.K, busy = entries < h.El ? entries : h.El;
+    // tiles that any routing can give: every expert with rows may end in a short one
+    const int64_t tiles = (entries + (kRows - 1) * busy) / kRows;
+    hipLaunchKernelGGL((k_w4_stream<W, UP, MT, NF>), dim3((unsigned)(tiles * ((p.N + kChannels - 1) / kChannels))), dim3(kStreamThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <class W>
+hipError_t ffn(const Handle& h, const W4Args& a, hipStream_t stream) {
+    const Params up{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, WeightArgs{(const char*)a.w13.values, (const char*)a.w13.scales, 2 * a.inter, a.hidden},
+                    a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
+    const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
+                      (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
+    const hipError_t e = stream_launch<W, true, 4, 4>(h, up, stream);
+    return e != hipSuccess ? e : stream_launch<W, false, 4, 4>(h, down, stream);
+}
+
+template <WeightFormat F>
+hipError_t by_group(const Handle& h, const W4Args& a, hipStream_t stream) {
+    if (a.group == 128) return ffn<Weights<F, 1>>(h, a, stream);
+    if (a.group == 64) return ffn<Weights<F, 2>>(h, a, stream);
+    return ffn<Weights<F, 4>>(h, a, stream);
+}
+
+}  // namespace
+
+size_t w4_packed_bytes(int64_t matrices, int N, int K) { return (size_t)(matrices * (N / kPieceRows) * pieces_of(K)) * kPieceBytes; }
+size_t w4_packed_scale_bytes(int64_t matrices, int N, int K, int group) {
+    return (size_t)(matrices * (N / kPieceRows) * pieces_of(K)) * (32 * (kPieceK / group));
+}
+
+hipError_t launch_w4_pack(const W4PackArgs& a, hipStream_t stream) {
+    const int64_t parts = (int64_t)(w4_packed_bytes(a.matrices, a.N, a.K) / 16);
+    hipLaunchKernelGGL(k_pack_codes, grid_of((parts + 255) / 256), dim3(256), 0, stream, a.codes, (char*)a.packed, a.int4 ? 0x88888888u : 0u, a.N, a.K, parts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t count = (int64_t)(w4_packed_scale_bytes(a.matrices, a.N, a.K, a.group) / 2);
+    hipLaunchKernelGGL(k_pack_scales, grid_of((count + 255) / 256), dim3(256), 0, stream, a.scales, (uint16_t*)a.packed_scales, a.K, a.group, count);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_ffn_w4(const Handle& h, const W4Args& a, hipStream_t stream) {
+    if (h.T == 0) return hipSuccess;
+    return a.int4 ? by_group<kWeightsInt4>(h, a, stream) : by_group<kWeightsE2m1>(h, a, stream);
+}
+
+}  // namespace ep

@@ -17,7 +17,10 @@
  *   ep_expert_ffn / ep_expert_ffn_backward  the experts' gated feed-forward block over the rows that a dispatch
  *                  placed, and its gradients; ep_combine_backward the gradient of ep_combine;
  *   ep_adapter     low-rank adapters of many requests at once beside a shared projection, the requests grouped
- *                  by a layout over their adapter ids.
+ *                  by a layout over their adapter ids;
+ *   ep_w4_pack / ep_expert_ffn_w4  the block with weights of four bits;  ep_moe_few  a whole layer for a few tokens in
+ *                  two kernels;  ep_combine_norm / ep_combine_norm_backward  the combine with the norms, gate and residual
+ *                  around a block, and its gradient.
  *
  * Page names used in the citations:
  *   [DeepEP->MegaMoE]  "从 DeepEP 到 Mega MoE：MoE Runtime 演进的三向验证分析" (backyes.github.io)
@@ -396,6 +399,78 @@ size_t ep_adapter_workspace_bytes(int num_tokens, int num_local_experts, int hid
 ep_status_t ep_adapter(ep_handle_t handle, const void* x, int hidden, const void* a, const void* b, int rank,
                        int out_features, const float* scales, const void* base, void* out, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* Formats of expert weights. */
+typedef enum ep_weight_format {
+    EP_WEIGHTS_BF16 = 0,      /* rows [N, K] in bf16; no scales                                                            */
+    EP_WEIGHTS_E4M3 = 1,      /* rows [N, K] of OCP e4m3fn bytes, fp32 scales [N / 128, K / 128]                           */
+    EP_WEIGHTS_INT4 = 2,      /* as ep_w4_pack lays them out: code - 8, a bf16 scale per row and group                     */
+    EP_WEIGHTS_E2M1 = 3       /* the same with the e2m1 value of the code (0, 0.5, 1, 1.5, 2, 3, 4, 6; code 8 and up negative)*/
+} ep_weight_format_t;
+
+typedef struct ep_weights {
+    const void* values;       /* device, 16-byte aligned: rows, or packed codes                                            */
+    const void* scales;       /* device, 16-byte aligned: fp32 blocks, or packed scales; bf16: ignored                     */
+    ep_weight_format_t format;
+    int group;                /* 4-bit: 32, 64 or 128 columns per scale; otherwise ignored                                 */
+} ep_weights_t;
+
+/* Bytes of the packed codes and packed scales of 4-bit weights [matrices, rows, columns].  Host only.  Return 0 for arguments
+ * outside the limits (see ep_w4_pack). */
+size_t ep_w4_packed_bytes(int matrices, int rows, int columns, int group);
+size_t ep_w4_packed_scale_bytes(int matrices, int rows, int columns, int group);
+
+/*
+ * ep_w4_pack -- lays 4-bit weights out for the kernels, once, when they are loaded (16 rows x 128 columns to 1024 bytes in a
+ * row, so that streaming them reads whole lines).  w[m][n][k] = scales[m][n][k / group] * value(code[m][n][k]).
+ *
+ *   codes          device bytes [matrices, rows, columns / 2]: two codes a byte, the even column in the lower half.
+ *   scales         device bf16 [matrices, rows, columns / group] (a power-of-two scale of 8 bits is exact in bf16).
+ *   format         EP_WEIGHTS_INT4 or EP_WEIGHTS_E2M1.
+ *   matrices, rows, columns  1..1024; a multiple of 16 in [16, 65536]; a multiple of `group`, at most 32768.
+ *   packed, packed_scales    device, of the sizes above, 16-byte aligned; written whole.
+ */
+ep_status_t ep_w4_pack(const uint8_t* codes, const void* scales, ep_weight_format_t format, int matrices, int rows, int columns, int group,
+                       void* packed, void* packed_scales, void* stream);
+
+/*
+ * ep_expert_ffn_w4 -- ep_expert_ffn with bf16 rows and 4-bit weights.  The codes are widened exactly, a group's products are
+ * summed in fp32 and take the scale there; h is rounded once to bf16, y once.
+ *
+ *   handle, recv_x, rows, y, workspace   as in ep_expert_ffn (bf16; workspace of ep_expert_ffn_workspace_bytes(...)).
+ *   hidden, intermediate                 multiples of the group.
+ *   w13      packed [num_local_experts, 2 * intermediate, hidden], gate rows first.
+ *   w2       packed [num_local_experts, hidden, intermediate], of w13's format and group.
+ */
+ep_status_t ep_expert_ffn_w4(ep_handle_t handle, const void* recv_x, int hidden, int intermediate, int64_t rows, const ep_weights_t* w13,
+                             const ep_weights_t* w2, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace of ep_moe_few.  Host only.  Returns 0 for arguments outside the limits. */
+size_t ep_moe_few_workspace_bytes(int num_tokens, int num_topk, int intermediate);
+
+/*
+ * ep_moe_few -- this rank's share of a whole mixture-of-experts layer for a few tokens, in two kernels ([DeepEP->MegaMoE]
+ * §4.3: at small batches launches, not bytes, set the time): layout, dispatch, experts and combine of up to 128 tokens.
+ *   out[t] = sum_k w[t,k] * ffn_e(x[t]) + bias[t]      e = topk_idx[t,k], over the entries whose expert is this rank's
+ *   ffn_e(x) = (silu(x . w13[e][0..I)) * (x . w13[e][I..2I))) . w2[e]
+ * Sums are fp32, the one over k ascending; h is rounded once to bf16 between the two products, out once; the experts' outputs
+ * are not rounded before they are summed.  Rows are bf16 beside every format of weights.
+ *
+ *   x             device bf16 [num_tokens, hidden].
+ *   topk_idx      device int64 [num_tokens, num_topk]; entries outside this rank's experts, -1 or anything else, add nothing.  An
+ *                 expert may appear more than once in a row.
+ *   topk_weights  device fp32 [num_tokens, num_topk], nullable (1).
+ *   num_tokens    0..128, with num_tokens * num_topk <= 1024.
+ *   num_experts, num_ranks, rank   as in ep_get_layout; num_local_experts = num_experts / num_ranks.
+ *   w13, w2       [num_local_experts, 2 * intermediate, hidden], gate rows first, and [num_local_experts, hidden, intermediate],
+ *                 both of one format (and group).  Sizes as in ep_expert_ffn, with 4-bit weights multiples of the group.
+ *   bias          device bf16 [num_tokens, hidden], nullable: a shared expert's output.
+ *   out           device bf16 [num_tokens, hidden]; every row is written; may be the bias itself, not x.
+ *   workspace     device scratch of ep_moe_few_workspace_bytes(...) bytes, 256-byte aligned, as in ep_expert_ffn.
+ */
+ep_status_t ep_moe_few(const void* x, const int64_t* topk_idx, const float* topk_weights, int num_tokens, int num_topk, int num_experts,
+                       int num_ranks, int rank, int hidden, int intermediate, const ep_weights_t* w13, const ep_weights_t* w2,
+                       const void* bias, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* What stands around a block of a layer, for ep_combine_norm and its gradient.  The vectors post_weight, pre_weight and a gate
  * per channel are all fp32 (vectors_bf16 = 0) or all bf16; device pointers, 16-byte aligned. */

@@ -91,8 +91,10 @@ hipError_t ffn(const Handle& h, const W4Args& a, hipStream_t stream) {
                     a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
                       (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
-    const hipError_t e = stream_launch<W, true, 4, 4>(h, up, stream);
-    return e != hipSuccess ? e : stream_launch<W, false, 4, 4>(h, down, stream);
+    const bool tiled = (double)h.T * h.K / h.E > 12;
+    const hipError_t e = tiled ? launch_w4_tile_up(h, a, stream) : stream_launch<W, true, 4, 4>(h, up, stream);
+    if (e != hipSuccess) return e;
+    return tiled ? launch_w4_tile_down(h, a, stream) : stream_launch<W, false, 4, 4>(h, down, stream);
 }
 
 template <WeightFormat F>

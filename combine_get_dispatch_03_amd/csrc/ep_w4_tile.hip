@@ -1,0 +1,273 @@
+// ep_w4_tile.hip -- the expert block with 4-bit weights for many rows per expert: tiles of up to 128 rows by 256 channels.
+//
+// Eight waves, 2 along the rows by 4 along the channels.  Rows, codes and scales of 128 k (a stage) are copied to LDS without passing
+// registers, three stages deep; a piece of codes is 1024 bytes in a row in memory and in LDS, so copying and reading it
+// take whole lines and no two lanes meet in a bank.  A wave widens its codes (exactly) on their way from LDS to the matrix
+// instruction; a group's sums are kept apart and take their scale in fp32 on the way into acc.  Those second sums are what
+// limits a tile to 128 rows.  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
+#include "ep_expert_tiles.hpp"
+#include "ep_ffn.hpp"
+#include "ep_weights.hpp"
+
+namespace ep {
+namespace {
+
+struct Params {
+    const int32_t* cnt;
+    const int32_t* psum;
+    int El;
+    const uint16_t* s;     // rows
+    WeightArgs w;
+    uint16_t* out;
+    int N, K;              // channels of a projection's output, of its input
+    int sp, op;            // elements between rows of s and of out
+};
+
+template <WeightFormat F, int S>
+struct W4Tiles {
+    static constexpr int kBM = 128, NT = 4, kCodes = 16;                             // 16 rows of pieces: 256 channels
+    typedef KcOperand<kBM> SOp;                                                      // 64 k
+    static constexpr int kW = 2 * SOp::kBytes, kScales = kW + kCodes * kPieceBytes, kScaleBytes = kGemmWaves * 256;
+    static constexpr int kStage = kScales + kScaleBytes, kBuffers = 3, kLds = kStage * kBuffers;
+    static constexpr int kWCopies = kCodes / kGemmWaves, kCopies = 2 * SOp::kCopies + kWCopies + 1;      // of a stage per wave
+    static constexpr int kPieceScales = 32 * S;                                      // bytes
+
+    char* smem;
+    SOp s, next_s;
+    uint64_t w, next_w, scales, next_scales;
+    uint32_t w_offset[kWCopies], next_w_offset[kWCopies], scale_offset, next_scale_offset;
+    int next_k, k, left, buf;
+
+    // The next tile's weights: row_piece(i) is the number of its i-th row of pieces (of 16), from `start` and `scale` on, or -1.
+    template <class RowPiece>
+    __device__ __forceinline__ void init_next_w(const char* start, const char* scale, int pieces, RowPiece row_piece) {
+        next_w = uniform64((uint64_t)start);
+        next_scales = uniform64((uint64_t)scale);
+#pragma unroll
+        for (int i = 0; i < kWCopies; ++i) {
+            const int at = row_piece(i * kGemmWaves + wave_id());
+            next_w_offset[i] = at < 0 ? kNoElement : (uint32_t)at * (uint32_t)(pieces * kPieceBytes) + lane_id() * 16;
+        }
+        const int byte = (int)threadIdx.x * 4, i = byte / kPieceScales, at = i < kCodes ? row_piece(i) : -1;
+        next_scale_offset = at < 0 ? kNoElement : (uint32_t)at * (uint32_t)(pieces * kPieceScales) + byte % kPieceScales;
+    }
+    __device__ __forceinline__ void copy(int to) {
+        const uint32_t lds = lds_address(smem) + to * kStage;
+        s.copy(lds, left * 2);
+        s.copy(lds + SOp::kBytes, (left - 64) * 2);
+        const uint32_t size = left > 0 ? kNoElement : 0u;
+        const i32x4 rw = resource(w, size), rs = resource(scales, size);
+        const uint32_t lw = __builtin_amdgcn_readfirstlane(lds + kW + threadIdx.x / kWave * kPieceBytes);
+#pragma unroll
+        for (int i = 0; i < kWCopies; ++i) copy16_to_lds(lw + i * kGemmWaves * kPieceBytes, w_offset[i], rw);
+        copy4_to_lds(__builtin_amdgcn_readfirstlane(lds + kScales + threadIdx.x / kWave * 256), scale_offset, rs);
+        w += kPieceBytes;
+        scales += kPieceScales;
+        left -= kPieceK;
+    }
+    __device__ __forceinline__ void settle() {
+        s.settle();
+        next_s.settle();
+        w = uniform64(w);
+        next_w = uniform64(next_w);
+        scales = uniform64(scales);
+        next_scales = uniform64(next_scales);
+        asm volatile("s_nop 4" : "+s"(w), "+s"(next_w), "+s"(scales), "+s"(next_scales));
+    }
+    __device__ __forceinline__ void take_next() {
+        s = next_s, w = next_w, scales = next_scales, left = next_k;
+        scale_offset = next_scale_offset;
+#pragma unroll
+        for (int i = 0; i < kWCopies; ++i) w_offset[i] = next_w_offset[i];
+    }
+    // The workgroup's first tile, which next_* describe.
+    __device__ __forceinline__ void begin() {
+        w = scales = 0;
+        s = next_s;
+        settle();
+        take_next();
+        k = next_k;
+        buf = 0;
+        copy(0);
+        copy(1);
+    }
+
+    // The sums of the tile under way; afterwards the next one is.
+    template <int MT>
+    __device__ __forceinline__ void run(f32x4 (&acc)[NT][MT]) {
+        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, lane = lane_id(), g = lane >> 4;
+        const int stages = __builtin_amdgcn_readfirstlane(k > kPieceK ? pieces_of(k) : 2);      // enough that one tile ahead will do
+        left = __builtin_amdgcn_readfirstlane(left);
+        next_k = __builtin_amdgcn_readfirstlane(next_k);
+        buf = __builtin_amdgcn_readfirstlane(buf);
+        settle();
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t s_at = SOp::fragment(wm * MT * 16);
+        for (int st = 0; st < stages; ++st) {
+            if (st == stages - 2) {
+                stay_branch();
+                take_next();
+            }
+            // this stage has landed, and every wave has left the one before, whose buffer the copies go to
+            wait_and_meet<kCopies>();
+            copy(buf == 0 ? kBuffers - 1 : buf - 1);
+            const char* ls = smem + buf * kStage;
+            const char* lw = ls + kW + wn * NT * kPieceBytes + lane * 16;
+            const char* lc = ls + kScales + wn * NT * kPieceScales + g * (8 * S);
+            i32x4 code[NT];
+#pragma unroll
+            for (int b = 0; b < NT; ++b) code[b] = *reinterpret_cast<const i32x4*>(lw + b * kPieceBytes);
+            constexpr int kPer = 4 / S;
+#pragma unroll
+            for (int grp = 0; grp < S; ++grp) {
+                f32x4 part[NT][MT];
+#pragma unroll
+                for (int j = grp * kPer; j < (grp + 1) * kPer; ++j) {
+                    bf16x8 sv[MT];
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) sv[a] = read_kc(ls + (j >> 1) * SOp::kBytes, (s_at ^ ((j & 1) * 64)) + a * 2048);
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        const bf16x8 fv = F == kWeightsInt4 ? widen_int4x8((uint32_t)code[b][j]) : widen_e2m1x8((uint32_t)code[b][j]);
+#pragma unroll
+                        for (int a = 0; a < MT; ++a)
+                            part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a], j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    const i32x2 q = *reinterpret_cast<const i32x2*>(lc + b * kPieceScales + grp * 8);
+                    const f32x4 scale{bf16lo((uint32_t)q[0]), bf16hi((uint32_t)q[0]), bf16lo((uint32_t)q[1]), bf16hi((uint32_t)q[1])};
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[b][a][i] = fmaf(part[b][a][i], scale[i], acc[b][a][i]);
+                }
+            }
+            buf = buf == kBuffers - 1 ? 0 : buf + 1;
+        }
+        k = next_k;
+    }
+
+    // No copy may land after the workgroup has left its LDS.
+    static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
+};
+
+// UP: a wave's four rows of pieces are 32 gate channels and the same up channels, and h = silu(g) u is stored.
+template <WeightFormat F, int S, bool UP>
+struct Kernel {
+    typedef W4Tiles<F, S> Tiles;
+    static constexpr int kCols = UP ? 128 : 256;
+    static constexpr float kUnit = Weights<F, S>::kUnit;
+
+    const Params& p;
+    RowTiles<Tiles::kBM, 0> rows;
+    Tiles g;
+    int round = 0;
+    struct Target {
+        int64_t row0;
+        int rows, n0;
+    } now, next;
+
+    __device__ __forceinline__ explicit Kernel(const Params& params) : p(params), rows(params.cnt, params.psum, params.El) {}
+
+    __device__ __forceinline__ void look_ahead() {
+        TileAt at;
+        next.rows = g.next_k = 0;
+        if (!tile_at((int)blockIdx.x, round++, rows.total, (p.N + kCols - 1) / kCols, &at)) return;
+        const RowTile t = rows.find(at.row, 32);
+        const int n0 = at.col * kCols, pieces = pieces_of(p.K);
+        next = Target{t.row0, t.rows, n0};
+        g.next_k = p.K;
+        g.next_s.init(p.s + (int64_t)t.row0 * p.sp, [&](int r) { return r < t.rows ? r * (2u * p.sp) : kNoElement; });
+        const int64_t piece = ((int64_t)t.expert * (p.w.N / kPieceRows) + n0 / kPieceRows) * pieces;
+        g.init_next_w(p.w.values + piece * kPieceBytes, p.w.scales + piece * (32 * S), pieces, [&](int i) {
+            const int c = UP ? i / 4 * 32 + (i & 1) * 16 : i * 16;
+            return n0 + c < p.N ? (c + (UP && (i & 2) ? p.N : 0)) / kPieceRows : -1;
+        });
+    }
+
+    template <int MT>
+    __device__ __forceinline__ void tile() {
+        f32x4 acc[4][MT];
+        g.template run<MT>(acc);
+        const int wave = wave_id(), m_at = (wave >> 2) * MT * 16 + (lane_id() & 15), n_in = (lane_id() >> 4) * 4;
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+            const int m = m_at + a * 16;
+            if (m >= now.rows) continue;
+            uint16_t* out = p.out + (now.row0 + m) * p.op;
+#pragma unroll
+            for (int b = 0; b < (UP ? 2 : 4); ++b) {
+                const int n = now.n0 + (wave & 3) * (kCols / 4) + b * 16 + n_in;
+                if (n >= p.N) continue;
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = acc[b][a][i] * kUnit;
+                    if constexpr (UP) v[i] = v[i] * sigmoid(v[i]) * (acc[b + 2][a][i] * kUnit);
+                }
+                store4(out + n, v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+};
+
+template <WeightFormat F, int S, bool UP>
+__global__ __launch_bounds__(kGemmThreads, 2) void k_w4_tiles(Params p) {
+    extern __shared__ __align__(1024) char smem[];
+    Kernel<F, S, UP> k(p);
+    k.look_ahead();
+    if (k.next.rows == 0) return;
+    k.g.smem = smem;
+    k.g.begin();
+    do {
+        k.now = k.next;
+        k.look_ahead();
+        switch ((k.now.rows + 31) / 32) {
+            case 1: k.template tile<1>(); break;
+            case 2: k.template tile<2>(); break;
+            case 3: k.template tile<3>(); break;
+            default: k.template tile<4>(); break;
+        }
+    } while (k.next.rows > 0);
+    k.g.end();
+}
+
+template <WeightFormat F, int S, bool UP>
+hipError_t tiles_launch(const Handle& h, const Params& p, hipStream_t stream) {
+    typedef W4Tiles<F, S> Tiles;
+    const int cols = UP ? 128 : 256;
+    // row tiles that any routing can give: every expert may end in a short one
+    const int64_t rows = (int64_t)h.T * h.K / Tiles::kBM + h.El;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_w4_tiles<F, S, UP>), Tiles::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_w4_tiles<F, S, UP>), dim3(walking_blocks(rows * ((p.N + cols - 1) / cols))), dim3(kGemmThreads), Tiles::kLds, stream, p);
+    return hipGetLastError();
+}
+
+template <WeightFormat F, bool UP>
+hipError_t by_group(const Handle& h, const Params& p, int group, hipStream_t stream) {
+    if (group == 128) return tiles_launch<F, 1, UP>(h, p, stream);
+    if (group == 64) return tiles_launch<F, 2, UP>(h, p, stream);
+    return tiles_launch<F, 4, UP>(h, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_w4_tile_up(const Handle& h, const W4Args& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, WeightArgs{(const char*)a.w13.values, (const char*)a.w13.scales, 2 * a.inter, a.hidden},
+                   a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
+    return a.int4 ? by_group<kWeightsInt4, true>(h, p, a.group, stream) : by_group<kWeightsE2m1, true>(h, p, a.group, stream);
+}
+
+hipError_t launch_w4_tile_down(const Handle& h, const W4Args& a, hipStream_t stream) {
+    const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
+                   (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
+    return a.int4 ? by_group<kWeightsInt4, false>(h, p, a.group, stream) : by_group<kWeightsE2m1, false>(h, p, a.group, stream);
+}
+
+}  // namespace ep

@@ -150,26 +150,26 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
 
 // A workgroup's rows are an item's entries, its channels 16 * NF / 2 of I.
 template <class W, int MT, int NF, int D>
-__global__ __launch_bounds__(kStreamThreads) void k_few_up(Params p, int max_items, int cursors, int lists, int cols) {
+__global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void k_few_up(Params p, int max_items, int cursors, int lists, int cols) {
     extern __shared__ __align__(16) char smem[];
     const int item = blockIdx.x / cols, n0 = blockIdx.x % cols * (NF * 8);
     const Items it = find_items<16 * MT, kStreamThreads, false>(p, smem, max_items, cursors, item);
     if (item >= it.total) return;
     const int first = it.first[item], count = it.count[item], r = lane_id() & 15;
-    RowPointers<MT> rows;
+    RowFragments<W, MT> rows;
+    rows.init(p.x, p.H);
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
-        rows.there[a] = a * 16 + r < count;
-        const int entry = it.order[first + (rows.there[a] ? a * 16 + r : 0)];
-        rows.at[a] = reinterpret_cast<const char*>(p.x + (int64_t)(entry / p.K) * p.H);
+        const bool there = a * 16 + r < count;
+        rows.place(a, there, (uint32_t)(it.order[first + (there ? a * 16 + r : 0)] / p.K) * (uint32_t)(p.H * 2));
     }
-    stream_product<W, true, MT, NF, D>(p.w13, it.expert[item], p.I, p.H, n0, rows, count, reinterpret_cast<float*>(smem + lists),
+    stream_product<W, true, MT, NF, D>(p.w13, __builtin_amdgcn_readfirstlane(it.expert[item]), p.I, p.H, n0, rows, count, reinterpret_cast<float*>(smem + lists),
                                        [&](int m) { return p.h + (int64_t)it.order[first + m] * row_pitch(p.I); });
 }
 
 // Items (and, of few items, parts of their k) go to the waves in turn; parts = 1, 2, 4 or 8.
 template <class W, int MT, int D>
-__global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_items, int cursors, int lists, int max_values) {
+__global__ __launch_bounds__(kDownThreads, MT == 4 ? 2 : 4) void k_few_down(Params p, int max_items, int cursors, int lists, int max_values) {
     extern __shared__ __align__(16) char smem[];
     const Items it = find_items<16 * MT, kDownThreads, true>(p, smem, max_items, cursors, 0);
     float* values = reinterpret_cast<float*>(smem + lists);       // [parts][T * K][16]
@@ -180,24 +180,28 @@ __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_ite
     const int parts = 1 << log_parts, work = it.total << log_parts;
     for (int i = wave; i < work; i += kDownWaves) {
         const int item = i >> log_parts, part = i & (parts - 1);
-        const int expert = it.expert[item], first = it.first[item], count = it.count[item];
-        RowPointers<MT> rows;
-        int entry[MT];
+        const int expert = __builtin_amdgcn_readfirstlane(it.expert[item]), first = it.first[item], count = it.count[item];
+        RowFragments<W, MT> rows;
+        rows.init(p.h, p.I);
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
-            rows.there[a] = a * 16 + r < count;
-            entry[a] = it.order[first + (rows.there[a] ? a * 16 + r : 0)];
-            rows.at[a] = reinterpret_cast<const char*>(p.h + (int64_t)entry[a] * row_pitch(p.I));
+            const bool there = a * 16 + r < count;
+            rows.place(a, there, (uint32_t)it.order[first + (there ? a * 16 + r : 0)] * (uint32_t)(row_pitch(p.I) * 2));
         }
-        W w[1];
-        w[0].init(p.w2, expert, n0, p.H);
+        typename W::template Rows<1> w;
+        w.init(p.w2, expert, n0);
+        w.place(0, 0, p.H - n0);
         f32x4 acc[1][MT];
 #pragma unroll
         for (int a = 0; a < MT; ++a) acc[0][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        stream_pieces<W, MT, 1, D>(w, rows, p.I, part, parts, pieces, acc);
+        stream_pieces<W, MT, 1, D>(w, rows, part, parts, pieces, acc);
 #pragma unroll
         for (int a = 0; a < MT; ++a)
-            if (rows.there[a]) *reinterpret_cast<f32x4*>(values + ((int64_t)part * n + entry[a]) * 16 + g * 4) = acc[0][a];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int m = a * 16 + g * 4 + j;
+                if (m < count) values[(part * n + it.order[first + m]) * 16 + r] = acc[0][a][j];
+            }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.T * 4; i += kDownThreads) {

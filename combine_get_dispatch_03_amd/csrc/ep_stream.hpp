@@ -7,65 +7,56 @@
 
 namespace ep {
 
-// 16 * MT rows' fragments beside a piece: lane (r, g) holds row r of each 16.
-template <int MT>
-struct RowPointers {
-    const char* at[MT];
-    bool there[MT];
+// 16 * MT rows' fragments beside a piece: lane (r, g) holds row r of each 16.  A row that does not exist is kNoElement.
+template <class W, int MT>
+struct RowFragments {
+    Buffer rows;
+    uint32_t at[MT];
+    int K;
 
-    template <class W>
-    __device__ __forceinline__ void load(i32x4 (&x)[MT][4], int piece, int K) const {
-        const int g = lane_id() >> 4;
+    __device__ __forceinline__ void init(const void* base, int k) {
+        rows.init(base);
+        K = k;
+    }
+    __device__ __forceinline__ void place(int a, bool there, uint32_t offset) {
+        at[a] = there ? offset + W::k_of(0, lane_id() >> 4) * 2 : kNoElement;
+    }
+    __device__ __forceinline__ void load(i32x4 (&x)[MT][4], int piece, bool there) const {
+        const __amdgpu_buffer_rsrc_t buffer = rows.of(there);
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = piece * kPieceK + W::k_of(j, g);
-                x[a][j] = i32x4{0, 0, 0, 0};
-                if (there[a] && k < K) x[a][j] = *reinterpret_cast<const i32x4*>(at[a] + (int64_t)k * 2);
+                const bool in = !W::kTail || piece * kPieceK + W::k_of(j, lane_id() >> 4) < K;
+                x[a][j] = load16(buffer, in ? at[a] + W::k_of(j, 0) * 2 : kNoElement, (uint32_t)piece * kPieceK * 2);
             }
     }
 };
 
 // acc[NF][MT] += pieces first, first + step, ... below `end` of NF rows of pieces, by the rows.  D pieces' loads are under way
-// while one is multiplied: the rows' too, since a wait for the newest load is one for all before it.
+// while one is multiplied: the rows' too, since a wait for the newest load is one for all before it.  Pieces from `end` on are zero.
 template <class W, int MT, int NF, int D>
-__device__ __forceinline__ void stream_pieces(const W (&w)[NF], const RowPointers<MT>& rows, int K, int first, int step, int end,
-                                              f32x4 (&acc)[NF][MT]) {
+__device__ __forceinline__ void stream_pieces(const typename W::template Rows<NF>& w, const RowFragments<W, MT>& rows, int first, int step,
+                                              int end, f32x4 (&acc)[NF][MT]) {
     struct Stage {
         typename W::Raw w[NF];
         i32x4 x[MT][4];
     } stage[D];
     auto load = [&](Stage& s, int piece) {
-        rows.template load<W>(s.x, piece, K);
+        const bool there = piece < end;
+        rows.load(s.x, piece, there);
 #pragma unroll
-        for (int b = 0; b < NF; ++b) s.w[b] = w[b].load(piece);
-    };
-    auto use = [&](const Stage& s) {
-#pragma unroll
-        for (int b = 0; b < NF; ++b) add_piece<W, MT>(s.w[b], s.x, acc[b]);
+        for (int b = 0; b < NF; ++b) s.w[b] = w.load(b, piece, there);
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (first + d * step < end) load(stage[d], first + d * step);
-    int p = first;
-    for (; p + (2 * D - 1) * step < end; p += D * step)
+    for (int d = 0; d < D; ++d) load(stage[d], first + d * step);
+    for (int p = first; p < end; p += D * step)
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            use(stage[d]);
+#pragma unroll
+            for (int b = 0; b < NF; ++b) add_piece<W, MT>(stage[d].w[b], stage[d].x, acc[b]);
             load(stage[d], p + (D + d) * step);
         }
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        if (p + d * step >= end) return;
-        use(stage[d]);
-        if (p + (D + d) * step < end) load(stage[d], p + (D + d) * step);
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        if (p + (D + d) * step >= end) return;
-        use(stage[d]);
-    }
 }
 
 // One workgroup's product: `count` rows (up to 16 * MT) by NF rows of pieces of an expert's weights, k split over the waves, whose
@@ -76,22 +67,23 @@ template <int NF>
 constexpr int stream_lds() { return kStreamWaves * 16 * (NF * 16 + 4) * 4; }
 
 template <class W, bool UP, int MT, int NF, int D, class OutRow>
-__device__ __forceinline__ void stream_product(const WeightArgs& weights, int expert, int N, int K, int n0, const RowPointers<MT>& rows,
+__device__ __forceinline__ void stream_product(const WeightArgs& weights, int expert, int N, int K, int n0, const RowFragments<W, MT>& rows,
                                                int count, float* sums, OutRow out_row) {
     constexpr int kCols = NF * 16, kOut = UP ? kCols / 2 : kCols, kPitch = kCols + 4;
     const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4;
-    W w[NF];
+    typename W::template Rows<NF> w;
+    w.init(weights, expert, n0);
 #pragma unroll
     for (int b = 0; b < NF; ++b) {
-        const int half = UP ? b / (NF / 2) : 0, n = n0 + (UP ? b % (NF / 2) : b) * 16;
-        w[b].init(weights, expert, half * N + (n < N ? n : 0), half * N + N);
+        const int n = (UP ? b % (NF / 2) : b) * 16, exist = N - n0 - n;
+        w.place(b, (exist > 0 ? n : 0) + (UP ? b / (NF / 2) * N : 0), exist);
     }
     f32x4 acc[NF][MT];
 #pragma unroll
     for (int b = 0; b < NF; ++b)
 #pragma unroll
         for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_pieces<W, MT, NF, D>(w, rows, K, wave, kStreamWaves, pieces_of(K), acc);
+    stream_pieces<W, MT, NF, D>(w, rows, wave, kStreamWaves, pieces_of(K), acc);
 
     // [wave][16 rows][channels], 16 rows at a time
 #pragma unroll
@@ -99,7 +91,9 @@ __device__ __forceinline__ void stream_product(const WeightArgs& weights, int ex
         if (a * 16 >= count) break;
         __syncthreads();
 #pragma unroll
-        for (int b = 0; b < NF; ++b) *reinterpret_cast<f32x4*>(sums + (wave * 16 + r) * kPitch + b * 16 + g * 4) = acc[b][a];
+        for (int b = 0; b < NF; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums[(wave * 16 + g * 4 + j) * kPitch + b * 16 + r] = acc[b][a][j];
         __syncthreads();
         for (int i = threadIdx.x; i < 16 * kOut / 4; i += kStreamThreads) {
             const int m = i / (kOut / 4), n4 = i % (kOut / 4) * 4;

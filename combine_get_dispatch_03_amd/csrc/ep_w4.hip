@@ -24,15 +24,14 @@ __global__ __launch_bounds__(256) void k_pack_codes(const uint8_t* codes, char* 
     reinterpret_cast<u32x4*>(packed)[i] = v;
 }
 
-// Scales of a piece: [g][group][4 rows], bf16; a thread writes one.
+// Scales of a piece: [16 rows][groups], bf16; a thread writes one.
 __global__ __launch_bounds__(256) void k_pack_scales(const uint16_t* scales, uint16_t* packed, int K, int group, int64_t count) {
     const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= count) return;
     const int pieces = pieces_of(K), groups = kPieceK / group, per = 16 * groups;
     const int64_t piece = i / per;
-    const int at = (int)(i % per), g = at / (4 * groups), s = at / 4 % groups, r = g * 4 + at % 4;
-    const int64_t row = piece / pieces * kPieceRows + r;
-    const int k = (int)(piece % pieces) * groups + s;
+    const int at = (int)(i % per), k = (int)(piece % pieces) * groups + at % groups;
+    const int64_t row = piece / pieces * kPieceRows + at / groups;
     packed[i] = k < K / group ? scales[row * (K / group) + k] : (uint16_t)0;
 }
 
@@ -50,19 +49,17 @@ struct Params {
 template <class W, bool UP, int MT, int NF, int D>
 __device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, int n0, float* sums) {
     const int r = lane_id() & 15;
-    RowPointers<MT> rows;
+    RowFragments<W, MT> rows;
+    rows.init(p.s + (int64_t)t.row0 * p.sp, p.K);
 #pragma unroll
-    for (int a = 0; a < MT; ++a) {
-        rows.there[a] = a * 16 + r < t.rows;
-        rows.at[a] = reinterpret_cast<const char*>(p.s + (int64_t)(t.row0 + (rows.there[a] ? a * 16 + r : 0)) * p.sp);
-    }
+    for (int a = 0; a < MT; ++a) rows.place(a, a * 16 + r < t.rows, (uint32_t)(a * 16 + r) * (uint32_t)(p.sp * 2));
     stream_product<W, UP, MT, NF, D>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
                                      [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
 }
 
 // Up to 16 * MT rows of an expert by 16 * NF rows of its weights.
 template <class W, bool UP, int MT, int NF>
-__global__ __launch_bounds__(kStreamThreads) void k_w4_stream(Params p) {
+__global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void k_w4_stream(Params p) {
     __shared__ __align__(16) float sums[stream_lds<NF>() / 4];
     constexpr int kChannels = UP ? NF * 8 : NF * 16;
     const RowTiles<MT * 16> tiles(p.cnt, p.psum, p.El);

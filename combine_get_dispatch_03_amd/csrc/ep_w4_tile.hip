@@ -95,7 +95,7 @@ struct W4Tiles {
     // The sums of the tile under way; afterwards the next one is.
     template <int MT>
     __device__ __forceinline__ void run(f32x4 (&acc)[NT][MT]) {
-        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, lane = lane_id(), g = lane >> 4;
+        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, lane = lane_id();
         const int stages = __builtin_amdgcn_readfirstlane(k > kPieceK ? pieces_of(k) : 2);      // enough that one tile ahead will do
         left = __builtin_amdgcn_readfirstlane(left);
         next_k = __builtin_amdgcn_readfirstlane(next_k);
@@ -116,10 +116,14 @@ struct W4Tiles {
             copy(buf == 0 ? kBuffers - 1 : buf - 1);
             const char* ls = smem + buf * kStage;
             const char* lw = ls + kW + wn * NT * kPieceBytes + lane * 16;
-            const char* lc = ls + kScales + wn * NT * kPieceScales + g * (8 * S);
+            const char* lc = ls + kScales + wn * NT * kPieceScales + (lane & 15) * (2 * S);
             i32x4 code[NT];
+            GroupScales<S> scale[NT];
 #pragma unroll
-            for (int b = 0; b < NT; ++b) code[b] = *reinterpret_cast<const i32x4*>(lw + b * kPieceBytes);
+            for (int b = 0; b < NT; ++b) {
+                code[b] = *reinterpret_cast<const i32x4*>(lw + b * kPieceBytes);
+                scale[b].load(lc + b * kPieceScales);
+            }
             constexpr int kPer = 4 / S;
 #pragma unroll
             for (int grp = 0; grp < S; ++grp) {
@@ -134,17 +138,16 @@ struct W4Tiles {
                         const bf16x8 fv = F == kWeightsInt4 ? widen_int4x8((uint32_t)code[b][j]) : widen_e2m1x8((uint32_t)code[b][j]);
 #pragma unroll
                         for (int a = 0; a < MT; ++a)
-                            part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, sv[a], j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
+                            part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sv[a], fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
                     }
                 }
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
-                    const i32x2 q = *reinterpret_cast<const i32x2*>(lc + b * kPieceScales + grp * 8);
-                    const f32x4 scale{bf16lo((uint32_t)q[0]), bf16hi((uint32_t)q[0]), bf16lo((uint32_t)q[1]), bf16hi((uint32_t)q[1])};
+                    const float by = scale[b].get(grp);
 #pragma unroll
                     for (int a = 0; a < MT; ++a)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[b][a][i] = fmaf(part[b][a][i], scale[i], acc[b][a][i]);
+                        for (int i = 0; i < 4; ++i) acc[b][a][i] = fmaf(part[b][a][i], by, acc[b][a][i]);
                 }
             }
             buf = buf == kBuffers - 1 ? 0 : buf + 1;
@@ -194,23 +197,25 @@ struct Kernel {
     __device__ __forceinline__ void tile() {
         f32x4 acc[4][MT];
         g.template run<MT>(acc);
-        const int wave = wave_id(), m_at = (wave >> 2) * MT * 16 + (lane_id() & 15), n_in = (lane_id() >> 4) * 4;
+        // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows
+        const int wave = wave_id(), r = lane_id() & 15, odd = r & 1, m_at = (wave >> 2) * MT * 16 + (lane_id() >> 4) * 4 + odd * 2;
 #pragma unroll
-        for (int a = 0; a < MT; ++a) {
-            const int m = m_at + a * 16;
-            if (m >= now.rows) continue;
-            uint16_t* out = p.out + (now.row0 + m) * p.op;
+        for (int b = 0; b < (UP ? 2 : 4); ++b) {
+            const int n = now.n0 + (wave & 3) * (kCols / 4) + b * 16 + (r & ~1);
 #pragma unroll
-            for (int b = 0; b < (UP ? 2 : 4); ++b) {
-                const int n = now.n0 + (wave & 3) * (kCols / 4) + b * 16 + n_in;
-                if (n >= p.N) continue;
-                f32x4 v;
+            for (int a = 0; a < MT; ++a) {
+                float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[i] = acc[b][a][i] * kUnit;
                     if constexpr (UP) v[i] = v[i] * sigmoid(v[i]) * (acc[b + 2][a][i] * kUnit);
                 }
-                store4(out + n, v[0], v[1], v[2], v[3]);
+                const float x0 = dpp_f<0xB1>(odd ? v[0] : v[2]), x1 = dpp_f<0xB1>(odd ? v[1] : v[3]);
+                if (n >= p.N) continue;
+                const int m = m_at + a * 16;
+                uint16_t* out = p.out + (now.row0 + m) * p.op + n;
+                if (m < now.rows) *reinterpret_cast<uint32_t*>(out) = odd ? pack_bf16x2(x0, v[2]) : pack_bf16x2(v[0], x0);
+                if (m + 1 < now.rows) *reinterpret_cast<uint32_t*>(out + p.op) = odd ? pack_bf16x2(x1, v[3]) : pack_bf16x2(v[1], x1);
             }
         }
     }

@@ -9,7 +9,10 @@
 //   4-bit  laid out once (pack): a piece is 1024 bytes in a row, 16 a lane, so a wave's load is whole lines of one place; a group
 //          of 32, 64 or 128 k has a bf16 scale per row, which goes to the group's sums in fp32.  Codes are widened to bf16
 //          (exact): e2m1 by the conversion instruction, integers (-8 .. 7, two's complement) by way of v_cvt_off_f32_i4, which
-//          gives a sixteenth of them (kUnit).  K is filled up with zeros to whole pieces.
+//          gives a sixteenth of them (kUnit).  K is filled up with zeros to whole pieces.  A piece's scales are [16 rows][groups].
+//
+// The rows that meet the weights are the instruction's first operand, so lane (r, g) ends up with weight row r's sums of rows
+// 4 g .. 4 g + 3: one scale per group is all that it needs.
 #pragma once
 
 #include "ep_device.hpp"
@@ -27,6 +30,21 @@ struct WeightArgs {
     const char* scales;
     int N, K;
 };
+
+// Memory read through a buffer resource: base and what is added to it for a whole wave stand in scalar registers, and what lies
+// at kNoElement or beyond the size is zero without a branch or any traffic.
+struct Buffer {
+    uint64_t base;
+
+    __device__ __forceinline__ void init(const void* at) { base = uniform64((uint64_t)at); }
+    // `there`: whether anything is read at all
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(bool there) const {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, there ? (int)kNoElement : 0, 0x00020000);
+    }
+};
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t wave) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)wave, 0));
+}
 
 // Integers of four bits, bytes 0..3 of q: a sixteenth of each, low and high nibbles.
 template <int BYTE>
@@ -53,103 +71,151 @@ __device__ __forceinline__ bf16x8 widen_e2m1x8(uint32_t q) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// S: groups of a piece (4-bit).
+// The bf16 scales of a row's S groups.
+template <int S>
+struct GroupScales {
+    uint32_t v[S == 4 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const char* at) {
+        if constexpr (S == 1) {
+            v[0] = *reinterpret_cast<const uint16_t*>(at);
+        } else if constexpr (S == 2) {
+            v[0] = *reinterpret_cast<const uint32_t*>(at);
+        } else {
+            const i32x2 q = *reinterpret_cast<const i32x2*>(at);
+            v[0] = (uint32_t)q[0], v[1] = (uint32_t)q[1];
+        }
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t wave) {
+        if constexpr (S == 1) {
+            v[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)lane, (int)wave, 0);
+        } else if constexpr (S == 2) {
+            v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(b, (int)lane, (int)wave, 0);
+        } else {
+            const i32x2 q = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)lane, (int)wave, 0));
+            v[0] = (uint32_t)q[0], v[1] = (uint32_t)q[1];
+        }
+    }
+    __device__ __forceinline__ float get(int group) const { return group & 1 ? bf16hi(v[group / 2]) : bf16lo(v[group / 2]); }
+};
+
+// NF rows of pieces of one matrix; S: groups of a piece (4-bit).  init(): the first row of the workgroup (uniform), and of each
+// row of pieces how many weight rows behind it stands (a multiple of 16) and how many rows exist from there on.
 template <WeightFormat F, int S>
 struct Weights;
 
 template <>
 struct Weights<kWeightsBf16, 0> {
     static constexpr int kGroups = 1;
-    static constexpr bool kScaled = false;
+    static constexpr bool kScaled = false, kTail = true;
     static constexpr float kUnit = 1.0f;
     struct Raw {
         i32x4 v[4];
     };
-    const char* at;
-    int left;      // k of the lane's first fragment on
     static __device__ __forceinline__ int k_of(int j, int g) { return j * 32 + g * 8; }
-
-    // Rows row0 .. row0 + 15 of a matrix; those from `end` on are taken as its last one (nobody uses their sums).
-    __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0, int end) {
-        const int r = row0 + (lane_id() & 15), g = lane_id() >> 4;
-        at = w.values + (((int64_t)matrix * w.N + (r < end ? r : end - 1)) * w.K + g * 8) * 2;
-        left = w.K - g * 8;
-    }
-    __device__ __forceinline__ Raw load(int piece) const {
-        Raw raw;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            raw.v[j] = i32x4{0, 0, 0, 0};
-            if (piece * kPieceK + j * 32 < left) raw.v[j] = *reinterpret_cast<const i32x4*>(at + (int64_t)piece * kPieceK * 2 + j * 64);
-        }
-        return raw;
-    }
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) { return __builtin_bit_cast(bf16x8, raw.v[j]); }
+
+    template <int NF>
+    struct Rows {
+        Buffer values;
+        uint32_t at[NF];
+        int K;
+        __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0) {
+            values.init(w.values + ((int64_t)matrix * w.N + row0) * w.K * 2);
+            K = w.K;
+        }
+        __device__ __forceinline__ void place(int b, int behind, int exist) {
+            const int r = lane_id() & 15;
+            at[b] = r < exist ? (uint32_t)(behind + r) * (uint32_t)K * 2 + (lane_id() >> 4) * 16 : kNoElement;
+        }
+        __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
+            const __amdgpu_buffer_rsrc_t buffer = values.of(there);
+            Raw raw;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                raw.v[j] = load16(buffer, piece * kPieceK + k_of(j, lane_id() >> 4) < K ? at[b] + j * 64 : kNoElement, (uint32_t)piece * kPieceK * 2);
+            return raw;
+        }
+    };
 };
 
 template <>
 struct Weights<kWeightsE4m3, 0> {
     static constexpr int kGroups = 1;
-    static constexpr bool kScaled = true;
+    static constexpr bool kScaled = true, kTail = false;
     static constexpr float kUnit = 1.0f;
     struct Raw {
         i32x4 v[2];
         float scale;
     };
-    const char* at;
-    const float* scale;
     static __device__ __forceinline__ int k_of(int j, int g) { return (j >> 1) * 64 + g * 16 + (j & 1) * 8; }
-
-    __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0, int) {
-        at = w.values + ((int64_t)matrix * w.N + row0 + (lane_id() & 15)) * w.K + (lane_id() >> 4) * 16;
-        scale = reinterpret_cast<const float*>(w.scales) + ((int64_t)matrix * (w.N / 128) + row0 / 128) * (w.K / 128);
-    }
-    __device__ __forceinline__ Raw load(int piece) const {
-        Raw raw;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) raw.v[j] = *reinterpret_cast<const i32x4*>(at + (int64_t)piece * kPieceK + j * 64);
-        raw.scale = scale[piece];
-        return raw;
-    }
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) {
         const i32x4 q = raw.v[j >> 1];
         return widen_e4m3x8(j & 1 ? i32x2{q[2], q[3]} : i32x2{q[0], q[1]});
     }
-    static __device__ __forceinline__ f32x4 scales(const Raw& raw, int) { return f32x4{raw.scale, raw.scale, raw.scale, raw.scale}; }
+    static __device__ __forceinline__ float scale_of(const Raw& raw, int) { return raw.scale; }
+
+    template <int NF>
+    struct Rows {
+        Buffer values, scales;
+        uint32_t at, row[NF], scale_row[NF];
+        int K, in_block;
+        __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0) {
+            values.init(w.values + ((int64_t)matrix * w.N + row0) * w.K);
+            scales.init(w.scales + ((int64_t)matrix * (w.N / 128) + row0 / 128) * (w.K / 128) * 4);
+            at = (uint32_t)(lane_id() & 15) * (uint32_t)w.K + (lane_id() >> 4) * 16;
+            K = w.K;
+            in_block = row0 % 128;
+        }
+        __device__ __forceinline__ void place(int b, int behind, int) {
+            row[b] = (uint32_t)behind * (uint32_t)K;
+            scale_row[b] = (uint32_t)((in_block + behind) / 128 * (K / 128) * 4);
+        }
+        __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
+            const __amdgpu_buffer_rsrc_t buffer = values.of(there);
+            Raw raw;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) raw.v[j] = load16(buffer, at + j * 64, row[b] + (uint32_t)piece * kPieceK);
+            raw.scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(scales.of(there), 0, (int)(scale_row[b] + piece * 4), 0));
+            return raw;
+        }
+    };
 };
 
 template <WeightFormat F, int S>
 struct Weights {
     static constexpr int kGroups = S;
-    static constexpr bool kScaled = true;
+    static constexpr bool kScaled = true, kTail = true;
     static constexpr float kUnit = F == kWeightsInt4 ? 16.0f : 1.0f;
-    typedef int scale_regs __attribute__((ext_vector_type(2 * S)));
     struct Raw {
         i32x4 v;
-        scale_regs s;      // 4 rows of each group, as bf16
+        GroupScales<S> s;
     };
-    const char* at;
-    const char* scale;
     static __device__ __forceinline__ int k_of(int j, int g) { return j * 32 + g * 8; }
-
-    __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0, int) {
-        const int64_t piece = ((int64_t)matrix * (w.N / kPieceRows) + row0 / kPieceRows) * pieces_of(w.K);
-        at = w.values + piece * kPieceBytes + lane_id() * 16;
-        scale = w.scales + piece * (32 * S) + (lane_id() >> 4) * (8 * S);
-    }
-    __device__ __forceinline__ Raw load(int piece) const {
-        Raw raw;
-        raw.v = *reinterpret_cast<const i32x4*>(at + (int64_t)piece * kPieceBytes);
-        raw.s = *reinterpret_cast<const scale_regs*>(scale + (int64_t)piece * (32 * S));
-        return raw;
-    }
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) {
         return F == kWeightsInt4 ? widen_int4x8((uint32_t)raw.v[j]) : widen_e2m1x8((uint32_t)raw.v[j]);
     }
-    static __device__ __forceinline__ f32x4 scales(const Raw& raw, int group) {
-        const uint32_t a = (uint32_t)raw.s[2 * group], b = (uint32_t)raw.s[2 * group + 1];
-        return f32x4{bf16lo(a), bf16hi(a), bf16lo(b), bf16hi(b)};
-    }
+    static __device__ __forceinline__ float scale_of(const Raw& raw, int group) { return raw.s.get(group); }
+
+    template <int NF>
+    struct Rows {
+        Buffer values, scales;
+        uint32_t first[NF];
+        int pieces;
+        __device__ __forceinline__ void init(const WeightArgs& w, int matrix, int row0) {
+            pieces = pieces_of(w.K);
+            const int64_t piece = ((int64_t)matrix * (w.N / kPieceRows) + row0 / kPieceRows) * pieces;
+            values.init(w.values + piece * kPieceBytes);
+            scales.init(w.scales + piece * (32 * S));
+        }
+        __device__ __forceinline__ void place(int b, int behind, int) { first[b] = (uint32_t)(behind / kPieceRows * pieces); }
+        __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
+            Raw raw;
+            raw.v = load16(values.of(there), lane_id() * 16, (first[b] + piece) * kPieceBytes);
+            raw.s.load(scales.of(there), (lane_id() & 15) * (2 * S), (first[b] + piece) * (32 * S));
+            return raw;
+        }
+    };
 };
 
 // acc[MT] += the piece's products with 16 * MT rows (x: a fragment per row tile and instruction).
@@ -165,14 +231,14 @@ __device__ __forceinline__ void add_piece(const typename W::Raw& raw, const i32x
         for (int j = s * kPer; j < (s + 1) * kPer; ++j) {
             const bf16x8 f = W::fragment(raw, j);
 #pragma unroll
-            for (int a = 0; a < MT; ++a) part[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, x[a][j]), part[a], 0, 0, 0);
+            for (int a = 0; a < MT; ++a) part[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][j]), f, part[a], 0, 0, 0);
         }
         if constexpr (W::kScaled) {
-            const f32x4 scale = W::scales(raw, s);
+            const float scale = W::scale_of(raw, s);
 #pragma unroll
             for (int a = 0; a < MT; ++a)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[a][i] = fmaf(part[a][i], scale[i], acc[a][i]);
+                for (int i = 0; i < 4; ++i) acc[a][i] = fmaf(part[a][i], scale, acc[a][i]);
         } else {
 #pragma unroll
             for (int a = 0; a < MT; ++a) acc[a] = part[a];

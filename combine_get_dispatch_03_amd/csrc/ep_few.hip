@@ -13,7 +13,7 @@
 namespace ep {
 namespace {
 
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
+constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / kWave, kDownNF = 2, kDownCols = kDownNF * 16;
 
 struct Params {
     const uint16_t* x;        // [T, H]
@@ -40,17 +40,20 @@ struct Items {
     int* cursor;          // [El] (many entries)
     uint16_t* order;
     int total;
+    float* weight;        // [entries] (ALL): the routing weights, and which entries there are, a bit each
+    uint64_t* valid;
 };
 struct ItemsLayout {
-    int items, order, cursor;      // sizes
-    int bytes() const { return (3 * items + cursor + 4) * 4 + order * 2; }
+    int items, order, cursor, weights;      // sizes
+    int bytes() const { return (3 * items + cursor + 4) * 4 + (weights + 63) / 64 * (64 * 4 + 8) + order * 2; }
 };
 // Up to one wave's entries: every item has GROUP places in order.  Of more, all entries stand there, or one item's.
 inline ItemsLayout items_layout(int entries, int El, int group, bool all) {
     const int busy = entries < El ? entries : El;
     const int items = (int)((entries + (int64_t)(group - 1) * busy) / group);
-    if (entries <= kWave) return ItemsLayout{items, items * group, 0};
-    return ItemsLayout{items, all ? entries : group, El};
+    const int weights = all ? entries : 0;
+    if (entries <= kWave) return ItemsLayout{items, items * group, 0, weights};
+    return ItemsLayout{items, all ? entries : group, El, weights};
 }
 
 // Items are the same in every workgroup.  ALL: all of them are wanted, and the order of an expert's entries is whatever it is: a
@@ -61,12 +64,16 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
     Items it;
     int* at = reinterpret_cast<int*>(lds);
     int* total = at;
-    it.expert = at + 4;
+    const int n = p.T * p.K, lane = lane_id(), chunks = ALL ? (n + kWave - 1) / kWave : 0;
+    it.valid = reinterpret_cast<uint64_t*>(at + 4);
+    it.weight = reinterpret_cast<float*>(it.valid + chunks);
+    it.expert = reinterpret_cast<int*>(it.weight + chunks * kWave);
     it.first = it.expert + max_items;
     it.count = it.first + max_items;
     it.cursor = it.count + max_items;
     it.order = reinterpret_cast<uint16_t*>(it.cursor + cursors);
-    const int n = p.T * p.K, lane = lane_id();
+    if constexpr (ALL)
+        for (int i = threadIdx.x; i < n; i += THREADS) it.weight[i] = p.topk_w ? p.topk_w[i] : 1.0f;
     if (n <= kWave) {
         // every wave works it out in its registers; the first leaves it in LDS
         const int id = lane < n ? local_expert(p, lane) : -1, e = id < 0 ? 0 : id;
@@ -77,6 +84,8 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
         // an entry's item is that of the last head among its peers up to itself
         const uint64_t mine = peers & heads & (lanemask_lt() | (1ull << lane));
         const int head = mine ? 63 - __builtin_clzll(mine) : 0, item = popc64(heads & ((1ull << head) - 1));
+        const uint64_t valid = ballot(in);
+        if (ALL && threadIdx.x == 0) it.valid[0] = valid;
         if ((int)threadIdx.x < kWave && in) {
             if (head == lane) {
                 const int after = popc64(peers) - rank;
@@ -86,7 +95,7 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
             }
             it.order[item * GROUP + rank % GROUP] = (uint16_t)lane;
         }
-        it.total = popc64(heads);
+        it.total = popc64(heads);      // (uniform, a ballot)
         __syncthreads();
         return it;
     }
@@ -100,6 +109,8 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
         const int entry = i * THREADS + threadIdx.x;
         mine[i] = entry < n ? local_expert(p, entry) : -1;
         if (mine[i] >= 0) atomicAdd(&it.cursor[mine[i]], 1);
+        const uint64_t valid = ballot(mine[i] >= 0);
+        if (ALL && lane == 0 && entry < n) it.valid[entry / kWave] = valid;
     }
     __syncthreads();
     if (threadIdx.x < kWave) {
@@ -144,13 +155,13 @@ __device__ __forceinline__ Items find_items(const Params& p, char* lds, int max_
         __syncthreads();
         it.first[wanted] = 0;      // every thread, after all have read it
     }
-    it.total = *total;
+    it.total = __builtin_amdgcn_readfirstlane(*total);
     return it;
 }
 
 // A workgroup's rows are an item's entries, its channels 16 * NF / 2 of I.
-template <class W, int MT, int NF, int D>
-__global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void k_few_up(Params p, int max_items, int cursors, int lists, int cols) {
+template <class W, int MT, int NF>
+__global__ __launch_bounds__(kStreamThreads, MT == 4 ? 2 : 4) void k_few_up(Params p, int max_items, int cursors, int lists, int cols) {
     extern __shared__ __align__(16) char smem[];
     const int item = blockIdx.x / cols, n0 = blockIdx.x % cols * (NF * 8);
     const Items it = find_items<16 * MT, kStreamThreads, false>(p, smem, max_items, cursors, item);
@@ -163,20 +174,20 @@ __global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void
         const bool there = a * 16 + r < count;
         rows.place(a, there, (uint32_t)(it.order[first + (there ? a * 16 + r : 0)] / p.K) * (uint32_t)(p.H * 2));
     }
-    stream_product<W, true, MT, NF, D>(p.w13, __builtin_amdgcn_readfirstlane(it.expert[item]), p.I, p.H, n0, rows, count, reinterpret_cast<float*>(smem + lists),
+    stream_product<W, true, MT, NF>(p.w13, __builtin_amdgcn_readfirstlane(it.expert[item]), p.I, p.H, n0, rows, count, reinterpret_cast<float*>(smem + lists),
                                        [&](int m) { return p.h + (int64_t)it.order[first + m] * row_pitch(p.I); });
 }
 
-// Items (and, of few items, parts of their k) go to the waves in turn; parts = 1, 2, 4 or 8.
-template <class W, int MT, int D>
-__global__ __launch_bounds__(kDownThreads, MT == 4 ? 2 : 4) void k_few_down(Params p, int max_items, int cursors, int lists, int max_values) {
+// Items (and, of few items, parts of their k) go to the waves in turn; parts is a power of two.
+template <class W, int MT>
+__global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_items, int cursors, int lists, int max_values) {
     extern __shared__ __align__(16) char smem[];
     const Items it = find_items<16 * MT, kDownThreads, true>(p, smem, max_items, cursors, 0);
-    float* values = reinterpret_cast<float*>(smem + lists);       // [parts][T * K][16]
-    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4, n0 = blockIdx.x * 16, n = p.T * p.K;
+    float* values = reinterpret_cast<float*>(smem + lists);       // [parts][T * K][kDownCols]
+    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4, n0 = blockIdx.x * kDownCols, n = p.T * p.K;
     const int pieces = pieces_of(p.I);
     int log_parts = 0;
-    while (log_parts < 3 && (it.total << (log_parts + 1)) <= kDownWaves && (n << (log_parts + 1)) <= max_values) ++log_parts;
+    while ((it.total << (log_parts + 1)) <= kDownWaves && (2 << log_parts) <= pieces && (n << (log_parts + 1)) <= max_values) ++log_parts;
     const int parts = 1 << log_parts, work = it.total << log_parts;
     for (int i = wave; i < work; i += kDownWaves) {
         const int item = i >> log_parts, part = i & (parts - 1);
@@ -188,31 +199,40 @@ __global__ __launch_bounds__(kDownThreads, MT == 4 ? 2 : 4) void k_few_down(Para
             const bool there = a * 16 + r < count;
             rows.place(a, there, (uint32_t)it.order[first + (there ? a * 16 + r : 0)] * (uint32_t)(row_pitch(p.I) * 2));
         }
-        typename W::template Rows<1> w;
+        typename W::template Rows<kDownNF> w;
         w.init(p.w2, expert, n0);
-        w.place(0, 0, p.H - n0);
-        f32x4 acc[1][MT];
+        f32x4 acc[kDownNF][MT];
 #pragma unroll
-        for (int a = 0; a < MT; ++a) acc[0][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        stream_pieces<W, MT, 1, D>(w, rows, part, parts, pieces, acc);
+        for (int b = 0; b < kDownNF; ++b) {
+            const int exist = p.H - n0 - b * 16;
+            w.place(b, exist > 0 ? b * 16 : 0, exist);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        stream_pieces<W, MT, kDownNF>(w, rows, part, parts, pieces, acc);
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int m = a * 16 + g * 4 + j;
-                if (m < count) values[(part * n + it.order[first + m]) * 16 + r] = acc[0][a][j];
+                if (m >= count) continue;
+                float* to = values + (part * n + it.order[first + m]) * kDownCols + r;
+#pragma unroll
+                for (int b = 0; b < kDownNF; ++b) to[b * 16] = acc[b][a][j];
             }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 4; i += kDownThreads) {
-        const int t = i / 4, c = n0 + i % 4 * 4;
+    constexpr int kQuads = kDownCols / 4;
+    for (int i = threadIdx.x; i < p.T * kQuads; i += kDownThreads) {
+        const int t = i / kQuads, in = i % kQuads * 4, c = n0 + in;
         if (c >= p.H) continue;
         f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < p.K; ++k) {
-            if (local_expert(p, t * p.K + k) < 0) continue;
-            f32x4 v = *reinterpret_cast<const f32x4*>(values + (t * p.K + k) * 16 + i % 4 * 4);
-            for (int q = 1; q < parts; ++q) v += *reinterpret_cast<const f32x4*>(values + (q * n + t * p.K + k) * 16 + i % 4 * 4);
-            const float weight = W::kUnit * (p.topk_w ? p.topk_w[(int64_t)t * p.K + k] : 1.0f);
+            const int e = t * p.K + k;
+            if (!(it.valid[e / kWave] >> (e % kWave) & 1)) continue;
+            f32x4 v = *reinterpret_cast<const f32x4*>(values + e * kDownCols + in);
+            for (int q = 1; q < parts; ++q) v += *reinterpret_cast<const f32x4*>(values + (q * n + e) * kDownCols + in);
+            const float weight = W::kUnit * it.weight[e];
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] = fmaf(weight, v[j], sum[j]);
         }
@@ -225,42 +245,196 @@ __global__ __launch_bounds__(kDownThreads, MT == 4 ? 2 : 4) void k_few_down(Para
     }
 }
 
-template <class W, int MT, int UP_NF, int UP_D, int DOWN_D>
-hipError_t launch(const Params& p, hipStream_t stream) {
-    const int n = p.T * p.K;
-    ItemsLayout l = items_layout(n, p.El, 16 * MT, false);
-    int lists = (l.bytes() + 15) & ~15;
-    const int up_lds = lists + stream_lds<UP_NF>(), cols = (p.I + UP_NF * 8 - 1) / (UP_NF * 8);
-    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_up<W, MT, UP_NF, UP_D>), up_lds);
+template <class W, int MT, int NF>
+hipError_t launch_up(const Params& p, hipStream_t stream) {
+    const ItemsLayout l = items_layout(p.T * p.K, p.El, 16 * MT, false);
+    const int lists = (l.bytes() + 15) & ~15, lds = lists + stream_lds<NF>(), cols = (p.I + NF * 8 - 1) / (NF * 8);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_up<W, MT, NF>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_few_up<W, MT, UP_NF, UP_D>), dim3((unsigned)(l.items * cols)), dim3(kStreamThreads), up_lds, stream, p, l.items,
-                       l.cursor, lists, cols);
+    hipLaunchKernelGGL((k_few_up<W, MT, NF>), dim3((unsigned)(l.items * cols)), dim3(kStreamThreads), lds, stream, p, l.items, l.cursor, lists, cols);
+    return hipGetLastError();
+}
+
+template <class W, int MT>
+hipError_t launch_down(const Params& p, hipStream_t stream) {
+    const int n = p.T * p.K;
+    const ItemsLayout l = items_layout(n, p.El, 16 * MT, true);
+    // room for the parts of few items' entries
+    const int lists = (l.bytes() + 15) & ~15, values = n > 8 * 16 ? n : 8 * (n < 16 ? n : 16), lds = lists + values * kDownCols * 4;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_down<W, MT>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_few_down<W, MT>), dim3((p.H + kDownCols - 1) / kDownCols), dim3(kDownThreads), lds, stream, p, l.items, l.cursor, lists, values);
+    return hipGetLastError();
+}
+
+// ---- one token, or two ----------------------------------------------------------------------------------------------
+//
+// With no more entries than waves in a workgroup an entry is an item of its own: its expert is one load away, so the weights are
+// under way a microsecond into the kernel, and most of a wave's share of them at once.  (An expert that two tokens share is
+// read twice, the second time from a cache.)
+
+// acc[NF] += pieces first, first + step, ... below `end` of NF rows of pieces by one row x of K bf16; the wave's part of it stands
+// in LDS.  Every row of the instruction's first operand is x.
+template <class W, int NF>
+__device__ __forceinline__ void one_row(const typename W::template Rows<NF>& w, const uint16_t* x, int K, int first, int step, int end,
+                                        char* lds, f32x4 (&acc)[NF][1]) {
+    Buffer row;
+    row.init(x);
+    const int count = (end - first + step - 1) / step;
+    for (int c = lane_id(); c < count * 16; c += kWave) {      // 16 bytes
+        const int k = (first + c / 16 * step) * kPieceK + c % 16 * 8;
+        *reinterpret_cast<i32x4*>(lds + c * 16) = load16(row.resource(true), k < K ? (uint32_t)k * 2 : kNoElement, 0);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    typename W::Raw raw[NF];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int b = 0; b < NF; ++b) raw[b] = w.load(b, first + i * step, i < count);
+    };
+    load(0);
+    const char* at = lds + W::k_of(0, lane_id() >> 4) * 2;
+    for (int i = 0; i < count; ++i, at += kPieceK * 2) {
+        i32x4 v[1][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[0][j] = *reinterpret_cast<const i32x4*>(at + W::k_of(j, 0) * 2);
+#pragma unroll
+        for (int b = 0; b < NF; ++b) add_piece<W, 1>(raw[b], v, acc[b]);
+        load(i + 1);
+    }
+}
+
+template <class W, int NF>
+__global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols, int per_wave) {
+    constexpr int kHalf = NF * 8;
+    extern __shared__ __align__(16) char smem[];      // [waves][NF * 16] sums, then each wave's part of x
+    const int entry = blockIdx.x / cols, n0 = blockIdx.x % cols * kHalf, wave = wave_id();
+    const int expert = __builtin_amdgcn_readfirstlane(local_expert(p, entry));
+    if (expert < 0) return;
+    typename W::template Rows<NF> w;
+    w.init(p.w13, expert, n0);
+    f32x4 acc[NF][1];
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+        const int n = b % (NF / 2) * 16, exist = p.I - n0 - n;
+        w.place(b, (exist > 0 ? n : 0) + b / (NF / 2) * p.I, exist);
+        acc[b][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    float* sums = reinterpret_cast<float*>(smem);
+    char* mine = smem + kStreamWaves * NF * 64 + wave * per_wave * (kPieceK * 2);
+    if (wave < pieces_of(p.H)) one_row<W, NF>(w, p.x + (int64_t)(entry / p.K) * p.H, p.H, wave, kStreamWaves, pieces_of(p.H), mine, acc);
+    if (lane_id() < 16) {
+#pragma unroll
+        for (int b = 0; b < NF; ++b) sums[wave * NF * 16 + b * 16 + lane_id()] = acc[b][0][0];
+    }
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= kHalf || n0 + c >= p.I) return;
+    float gate = 0.0f, up = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kStreamWaves; ++v) {
+        gate += sums[v * NF * 16 + c];
+        up += sums[v * NF * 16 + kHalf + c];
+    }
+    gate *= W::kUnit;
+    const __bf16 h = (__bf16)(gate * sigmoid(gate) * (up * W::kUnit));
+    p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = __builtin_bit_cast(uint16_t, h);
+}
+
+// Wave i takes part i % parts of entry i / parts: per_part pieces.
+template <class W>
+__global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, int per_part) {
+    extern __shared__ __align__(16) char smem[];      // [waves][kDownCols] sums, then each wave's part of h
+    __shared__ float weight[kDownWaves];
+    __shared__ int valid[kDownWaves];
+    const int n0 = blockIdx.x * kDownCols, wave = wave_id(), entry = wave / parts, part = wave % parts, n = p.T * p.K;
+    float* sums = reinterpret_cast<float*>(smem);
+    // what the sum over k needs, asked for before the weights
+    const int t = threadIdx.x / kDownCols, c = threadIdx.x % kDownCols;
+    const bool mine_out = t < p.T && n0 + c < p.H;
+    const int64_t at = (int64_t)t * p.H + n0 + c;
+    const float bias = mine_out && p.bias ? __builtin_bit_cast(float, (uint32_t)p.bias[at] << 16) : 0.0f;
+    if ((int)threadIdx.x < n) {
+        valid[threadIdx.x] = local_expert(p, threadIdx.x) >= 0;
+        weight[threadIdx.x] = W::kUnit * (p.topk_w ? p.topk_w[threadIdx.x] : 1.0f);
+    }
+    const int expert = entry < n ? __builtin_amdgcn_readfirstlane(local_expert(p, entry)) : -1;
+    if (expert >= 0) {
+        typename W::template Rows<kDownNF> w;
+        w.init(p.w2, expert, n0);
+        f32x4 acc[kDownNF][1];
+#pragma unroll
+        for (int b = 0; b < kDownNF; ++b) {
+            const int exist = p.H - n0 - b * 16;
+            w.place(b, exist > 0 ? b * 16 : 0, exist);
+            acc[b][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        char* mine = smem + kDownWaves * kDownCols * 4 + wave * per_part * (kPieceK * 2);
+        if (part < pieces_of(p.I)) one_row<W, kDownNF>(w, p.h + (int64_t)entry * row_pitch(p.I), p.I, part, parts, pieces_of(p.I), mine, acc);
+        if (lane_id() < 16) {
+#pragma unroll
+            for (int b = 0; b < kDownNF; ++b) sums[wave * kDownCols + b * 16 + lane_id()] = acc[b][0][0];
+        }
+    }
+    __syncthreads();
+    if (!mine_out) return;
+    float y = 0.0f;
+    for (int k = 0; k < p.K; ++k) {
+        const int e = t * p.K + k;
+        if (!valid[e]) continue;
+        float v = 0.0f;
+        for (int q = 0; q < parts; ++q) v += sums[(e * parts + q) * kDownCols + c];
+        y = fmaf(weight[e], v, y);
+    }
+    p.out[at] = __builtin_bit_cast(uint16_t, (__bf16)(y + bias));
+}
+
+constexpr int kOneLds = 96 << 10;
+// Pieces of a wave's part of h, and how many parts there are.
+struct OneParts {
+    int parts, per_part;
+    OneParts(int entries, int I) {
+        const int pieces = pieces_of(I);
+        parts = kDownWaves / entries < pieces ? kDownWaves / entries : pieces;
+        per_part = (pieces + parts - 1) / parts;
+    }
+    int lds() const { return kDownWaves * (kDownCols * 4 + per_part * (kPieceK * 2)); }
+};
+// No more entries than waves, and rows whose parts fit beside each other.
+bool one_by_one(const Params& p) { return p.T * p.K <= kDownWaves && OneParts(p.T * p.K, p.I).lds() <= kOneLds; }
+
+template <class W, int NF>
+hipError_t launch_one(const Params& p, hipStream_t stream) {
+    const int n = p.T * p.K, cols = (p.I + NF * 8 - 1) / (NF * 8), per_wave = (pieces_of(p.H) + kStreamWaves - 1) / kStreamWaves;
+    const int up_lds = kStreamWaves * (NF * 64 + per_wave * (kPieceK * 2));
+    hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_up<W, NF>), up_lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_one_up<W, NF>), dim3((unsigned)(n * cols)), dim3(kStreamThreads), up_lds, stream, p, cols, per_wave);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    l = items_layout(n, p.El, 16 * MT, true);
-    lists = (l.bytes() + 15) & ~15;
-    // room for the parts of few items' entries
-    const int values = n > kDownWaves * 16 * MT ? n : kDownWaves * (n < 16 * MT ? n : 16 * MT), down_lds = lists + values * 64;
-    e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_down<W, MT, DOWN_D>), down_lds);
+    const OneParts o(n, p.I);
+    e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_down<W>), o.lds());
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_few_down<W, MT, DOWN_D>), dim3((p.H + 15) / 16), dim3(kDownThreads), down_lds, stream, p, l.items, l.cursor, lists, values);
+    hipLaunchKernelGGL((k_one_down<W>), dim3((p.H + kDownCols - 1) / kDownCols), dim3(kDownThreads), o.lds(), stream, p, o.parts, o.per_part);
     return hipGetLastError();
 }
 
 // Rows an expert has on average decide how many steps of 16 a workgroup takes past the weights at a time.
-template <class W, int UP_NF, int UP_D, int DOWN_D>
+template <class W, int NF>
 hipError_t by_rows(const Params& p, int E, hipStream_t stream) {
+    if (one_by_one(p)) return launch_one<W, NF>(p, stream);
     const double rows = (double)p.T * p.K / E;
-    if (rows <= 12) return launch<W, 1, UP_NF, UP_D, DOWN_D>(p, stream);
-    if (rows <= 24) return launch<W, 2, UP_NF, 1, 2>(p, stream);
-    return launch<W, 4, UP_NF, 1, 1>(p, stream);
+    const hipError_t e = rows <= 12 ? launch_up<W, 1, NF>(p, stream) : rows <= 24 ? launch_up<W, 2, NF>(p, stream) : launch_up<W, 4, NF>(p, stream);
+    if (e != hipSuccess) return e;
+    return rows <= 12 ? launch_down<W, 1>(p, stream) : launch_down<W, 2>(p, stream);
 }
 
 template <WeightFormat F>
 hipError_t by_group(const Params& p, int E, int group, hipStream_t stream) {
-    if (group == 128) return by_rows<Weights<F, 1>, 4, 2, 4>(p, E, stream);
-    if (group == 64) return by_rows<Weights<F, 2>, 4, 2, 4>(p, E, stream);
-    return by_rows<Weights<F, 4>, 4, 2, 4>(p, E, stream);
+    if (group == 128) return by_rows<Weights<F, 1>, 4>(p, E, stream);
+    if (group == 64) return by_rows<Weights<F, 2>, 4>(p, E, stream);
+    return by_rows<Weights<F, 4>, 4>(p, E, stream);
 }
 
 }  // namespace
@@ -275,8 +449,8 @@ hipError_t launch_few(const FewArgs& a, hipStream_t stream) {
                    WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
                    (uint16_t*)a.workspace, (uint16_t*)a.out, a.T, a.K, a.hidden, a.inter, a.rank * El, El};
     switch (a.format) {
-        case kWeightsBf16: return by_rows<Weights<kWeightsBf16, 0>, 2, 2, 2>(p, a.E, stream);
-        case kWeightsE4m3: return by_rows<Weights<kWeightsE4m3, 0>, 4, 2, 3>(p, a.E, stream);
+        case kWeightsBf16: return by_rows<Weights<kWeightsBf16, 0>, 2>(p, a.E, stream);
+        case kWeightsE4m3: return by_rows<Weights<kWeightsE4m3, 0>, 4>(p, a.E, stream);
         case kWeightsInt4: return by_group<kWeightsInt4>(p, a.E, a.group, stream);
         default: return by_group<kWeightsE2m1>(p, a.E, a.group, stream);
     }

@@ -46,14 +46,14 @@ struct Params {
     int sp, op;            // elements between rows of s and of out
 };
 
-template <class W, bool UP, int MT, int NF, int D>
+template <class W, bool UP, int MT, int NF>
 __device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, int n0, float* sums) {
     const int r = lane_id() & 15;
     RowFragments<W, MT> rows;
     rows.init(p.s + (int64_t)t.row0 * p.sp, p.K);
 #pragma unroll
     for (int a = 0; a < MT; ++a) rows.place(a, a * 16 + r < t.rows, (uint32_t)(a * 16 + r) * (uint32_t)(p.sp * 2));
-    stream_product<W, UP, MT, NF, D>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
+    stream_product<W, UP, MT, NF>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
                                      [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
 }
 
@@ -67,9 +67,9 @@ __global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
     const int n0 = blockIdx.x % cols * kChannels, steps = (t.rows + 15) / 16;
-    if (MT == 1 || steps == 1) rows_product<W, UP, 1, NF, 2>(p, t, n0, sums);
-    else if (MT == 2 || steps == 2) rows_product<W, UP, 2, NF, 1>(p, t, n0, sums);
-    else rows_product<W, UP, 4, NF, 1>(p, t, n0, sums);
+    if (MT == 1 || steps == 1) rows_product<W, UP, 1, NF>(p, t, n0, sums);
+    else if (MT == 2 || steps == 2) rows_product<W, UP, 2, NF>(p, t, n0, sums);
+    else rows_product<W, UP, 4, NF>(p, t, n0, sums);
 }
 
 template <class W, bool UP, int MT, int NF>

@@ -37,9 +37,10 @@ struct Buffer {
     uint64_t base;
 
     __device__ __forceinline__ void init(const void* at) { base = uniform64((uint64_t)at); }
-    // `there`: whether anything is read at all
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(bool there) const {
-        return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, there ? (int)kNoElement : 0, 0x00020000);
+    // `there`: whether anything is read at all (the same in the whole wave, and said so: a resource that the compiler takes to differ
+    // between lanes costs a loop per load)
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(bool there) const {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, __builtin_amdgcn_readfirstlane(there ? (int)kNoElement : 0), 0x00020000);
     }
 };
 __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t lane, uint32_t wave) {
@@ -129,7 +130,7 @@ struct Weights<kWeightsBf16, 0> {
             at[b] = r < exist ? (uint32_t)(behind + r) * (uint32_t)K * 2 + (lane_id() >> 4) * 16 : kNoElement;
         }
         __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
-            const __amdgpu_buffer_rsrc_t buffer = values.of(there);
+            const __amdgpu_buffer_rsrc_t buffer = values.resource(there);
             Raw raw;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -172,11 +173,11 @@ struct Weights<kWeightsE4m3, 0> {
             scale_row[b] = (uint32_t)((in_block + behind) / 128 * (K / 128) * 4);
         }
         __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
-            const __amdgpu_buffer_rsrc_t buffer = values.of(there);
+            const __amdgpu_buffer_rsrc_t buffer = values.resource(there);
             Raw raw;
 #pragma unroll
             for (int j = 0; j < 2; ++j) raw.v[j] = load16(buffer, at + j * 64, row[b] + (uint32_t)piece * kPieceK);
-            raw.scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(scales.of(there), 0, (int)(scale_row[b] + piece * 4), 0));
+            raw.scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(scales.resource(there), 0, (int)(scale_row[b] + piece * 4), 0));
             return raw;
         }
     };
@@ -211,8 +212,8 @@ struct Weights {
         __device__ __forceinline__ void place(int b, int behind, int) { first[b] = (uint32_t)(behind / kPieceRows * pieces); }
         __device__ __forceinline__ Raw load(int b, int piece, bool there) const {
             Raw raw;
-            raw.v = load16(values.of(there), lane_id() * 16, (first[b] + piece) * kPieceBytes);
-            raw.s.load(scales.of(there), (lane_id() & 15) * (2 * S), (first[b] + piece) * (32 * S));
+            raw.v = load16(values.resource(there), lane_id() * 16, (first[b] + piece) * kPieceBytes);
+            raw.s.load(scales.resource(there), (lane_id() & 15) * (2 * S), (first[b] + piece) * (32 * S));
             return raw;
         }
     };
@@ -236,9 +237,12 @@ __device__ __forceinline__ void add_piece(const typename W::Raw& raw, const i32x
         if constexpr (W::kScaled) {
             const float scale = W::scale_of(raw, s);
 #pragma unroll
-            for (int a = 0; a < MT; ++a)
+            for (int a = 0; a < MT; ++a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[a][i] = fmaf(part[a][i], scale, acc[a][i]);
+                // here, not wherever acc is used next: the compiler would sink it past the next loads' branch and keep all parts
+                asm volatile("" : "+v"(acc[a]));
+            }
         } else {
 #pragma unroll
             for (int a = 0; a < MT; ++a) acc[a] = part[a];

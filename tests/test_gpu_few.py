@@ -24,6 +24,9 @@ SHAPES = [
     (1, 1, 1, 1, 1, 0, 1, "uniform"),
     (1, 6, 3, 16, 1, 0, 8, "uniform"),
     (2, 5, 9, 4, 2, 1, 3, "uniform"),
+    (16, 2, 5, 8, 2, 0, 1, "holes"),
+    (4, 20, 13, 9, 1, 0, 4, "holes"),
+    (2, 3, 17, 1, 1, 0, 5, "one"),
     (8, 3, 2, 300, 1, 0, 8, "uniform"),
     (13, 9, 5, 6, 1, 0, 4, "holes"),
     (17, 4, 7, 32, 4, 3, 8, "holes"),
@@ -117,8 +120,9 @@ def test_same_layer_in_steps(ep, fmt):
     assert off < 2 * 2.0 ** -8, off
 
 
-def test_invalid_entries_add_nothing(ep):
-    shape = (6, 3, 2, 8, 2, 1, 3, "uniform")
+@pytest.mark.parametrize("T", [4, 6, 30])      # each entry by itself, in one wave's registers, through LDS
+def test_invalid_entries_add_nothing(ep, T):
+    shape = (T, 3, 2, 8, 2, 1, 3, "uniform")
     idx, x, w, bias, call, experts, m = setup(ep, shape, "bf16")
     idx[0] = torch.tensor([-1, -2 ** 63, 2 ** 63 - 1])
     idx[1] = torch.tensor([0, 3, 8])             # the other rank's, and past the last expert

@@ -13,7 +13,7 @@
 namespace ep {
 namespace {
 
-constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / kWave, kDownNF = 2, kDownCols = kDownNF * 16;
+constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / kWave;
 
 struct Params {
     const uint16_t* x;        // [T, H]
@@ -179,12 +179,13 @@ __global__ __launch_bounds__(kStreamThreads, MT == 4 ? 2 : 4) void k_few_up(Para
 }
 
 // Items (and, of few items, parts of their k) go to the waves in turn; parts is a power of two.
-template <class W, int MT>
+template <class W, int MT, int NF>
 __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_items, int cursors, int lists, int max_values) {
     extern __shared__ __align__(16) char smem[];
     const Items it = find_items<16 * MT, kDownThreads, true>(p, smem, max_items, cursors, 0);
-    float* values = reinterpret_cast<float*>(smem + lists);       // [parts][T * K][kDownCols]
-    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4, n0 = blockIdx.x * kDownCols, n = p.T * p.K;
+    constexpr int kCols = NF * 16;
+    float* values = reinterpret_cast<float*>(smem + lists);       // [parts][T * K][kCols]
+    const int lane = lane_id(), wave = wave_id(), r = lane & 15, g = lane >> 4, n0 = blockIdx.x * kCols, n = p.T * p.K;
     const int pieces = pieces_of(p.I);
     int log_parts = 0;
     while ((it.total << (log_parts + 1)) <= kDownWaves && (2 << log_parts) <= pieces && (n << (log_parts + 1)) <= max_values) ++log_parts;
@@ -199,30 +200,30 @@ __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_ite
             const bool there = a * 16 + r < count;
             rows.place(a, there, (uint32_t)it.order[first + (there ? a * 16 + r : 0)] * (uint32_t)(row_pitch(p.I) * 2));
         }
-        typename W::template Rows<kDownNF> w;
+        typename W::template Rows<NF> w;
         w.init(p.w2, expert, n0);
-        f32x4 acc[kDownNF][MT];
+        f32x4 acc[NF][MT];
 #pragma unroll
-        for (int b = 0; b < kDownNF; ++b) {
+        for (int b = 0; b < NF; ++b) {
             const int exist = p.H - n0 - b * 16;
             w.place(b, exist > 0 ? b * 16 : 0, exist);
 #pragma unroll
             for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        stream_pieces<W, MT, kDownNF>(w, rows, part, parts, pieces, acc);
+        stream_pieces<W, MT, NF>(w, rows, part, parts, pieces, acc);
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int m = a * 16 + g * 4 + j;
                 if (m >= count) continue;
-                float* to = values + (part * n + it.order[first + m]) * kDownCols + r;
+                float* to = values + (part * n + it.order[first + m]) * kCols + r;
 #pragma unroll
-                for (int b = 0; b < kDownNF; ++b) to[b * 16] = acc[b][a][j];
+                for (int b = 0; b < NF; ++b) to[b * 16] = acc[b][a][j];
             }
     }
     __syncthreads();
-    constexpr int kQuads = kDownCols / 4;
+    constexpr int kQuads = kCols / 4;
     for (int i = threadIdx.x; i < p.T * kQuads; i += kDownThreads) {
         const int t = i / kQuads, in = i % kQuads * 4, c = n0 + in;
         if (c >= p.H) continue;
@@ -230,8 +231,8 @@ __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_ite
         for (int k = 0; k < p.K; ++k) {
             const int e = t * p.K + k;
             if (!(it.valid[e / kWave] >> (e % kWave) & 1)) continue;
-            f32x4 v = *reinterpret_cast<const f32x4*>(values + e * kDownCols + in);
-            for (int q = 1; q < parts; ++q) v += *reinterpret_cast<const f32x4*>(values + (q * n + e) * kDownCols + in);
+            f32x4 v = *reinterpret_cast<const f32x4*>(values + e * kCols + in);
+            for (int q = 1; q < parts; ++q) v += *reinterpret_cast<const f32x4*>(values + (q * n + e) * kCols + in);
             const float weight = W::kUnit * it.weight[e];
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] = fmaf(weight, v[j], sum[j]);
@@ -255,15 +256,15 @@ hipError_t launch_up(const Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <class W, int MT>
+template <class W, int MT, int NF>
 hipError_t launch_down(const Params& p, hipStream_t stream) {
     const int n = p.T * p.K;
     const ItemsLayout l = items_layout(n, p.El, 16 * MT, true);
     // room for the parts of few items' entries
-    const int lists = (l.bytes() + 15) & ~15, values = n > 8 * 16 ? n : 8 * (n < 16 ? n : 16), lds = lists + values * kDownCols * 4;
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_down<W, MT>), lds);
+    const int lists = (l.bytes() + 15) & ~15, values = n > 8 * 16 ? n : 8 * (n < 16 ? n : 16), lds = lists + values * NF * 64;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_few_down<W, MT, NF>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_few_down<W, MT>), dim3((p.H + kDownCols - 1) / kDownCols), dim3(kDownThreads), lds, stream, p, l.items, l.cursor, lists, values);
+    hipLaunchKernelGGL((k_few_down<W, MT, NF>), dim3((p.H + NF * 16 - 1) / (NF * 16)), dim3(kDownThreads), lds, stream, p, l.items, l.cursor, lists, values);
     return hipGetLastError();
 }
 
@@ -343,15 +344,16 @@ __global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols
 }
 
 // Wave i takes part i % parts of entry i / parts: per_part pieces.
-template <class W>
+template <class W, int NF>
 __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, int per_part) {
-    extern __shared__ __align__(16) char smem[];      // [waves][kDownCols] sums, then each wave's part of h
+    constexpr int kCols = NF * 16;
+    extern __shared__ __align__(16) char smem[];      // [waves][kCols] sums, then each wave's part of h
     __shared__ float weight[kDownWaves];
     __shared__ int valid[kDownWaves];
-    const int n0 = blockIdx.x * kDownCols, wave = wave_id(), entry = wave / parts, part = wave % parts, n = p.T * p.K;
+    const int n0 = blockIdx.x * kCols, wave = wave_id(), entry = wave / parts, part = wave % parts, n = p.T * p.K;
     float* sums = reinterpret_cast<float*>(smem);
     // what the sum over k needs, asked for before the weights
-    const int t = threadIdx.x / kDownCols, c = threadIdx.x % kDownCols;
+    const int t = threadIdx.x / kCols, c = threadIdx.x % kCols;
     const bool mine_out = t < p.T && n0 + c < p.H;
     const int64_t at = (int64_t)t * p.H + n0 + c;
     const float bias = mine_out && p.bias ? __builtin_bit_cast(float, (uint32_t)p.bias[at] << 16) : 0.0f;
@@ -361,20 +363,20 @@ __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, 
     }
     const int expert = entry < n ? __builtin_amdgcn_readfirstlane(local_expert(p, entry)) : -1;
     if (expert >= 0) {
-        typename W::template Rows<kDownNF> w;
+        typename W::template Rows<NF> w;
         w.init(p.w2, expert, n0);
-        f32x4 acc[kDownNF][1];
+        f32x4 acc[NF][1];
 #pragma unroll
-        for (int b = 0; b < kDownNF; ++b) {
+        for (int b = 0; b < NF; ++b) {
             const int exist = p.H - n0 - b * 16;
             w.place(b, exist > 0 ? b * 16 : 0, exist);
             acc[b][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        char* mine = smem + kDownWaves * kDownCols * 4 + wave * per_part * (kPieceK * 2);
-        if (part < pieces_of(p.I)) one_row<W, kDownNF>(w, p.h + (int64_t)entry * row_pitch(p.I), p.I, part, parts, pieces_of(p.I), mine, acc);
+        char* mine = smem + kDownWaves * kCols * 4 + wave * per_part * (kPieceK * 2);
+        if (part < pieces_of(p.I)) one_row<W, NF>(w, p.h + (int64_t)entry * row_pitch(p.I), p.I, part, parts, pieces_of(p.I), mine, acc);
         if (lane_id() < 16) {
 #pragma unroll
-            for (int b = 0; b < kDownNF; ++b) sums[wave * kDownCols + b * 16 + lane_id()] = acc[b][0][0];
+            for (int b = 0; b < NF; ++b) sums[wave * kCols + b * 16 + lane_id()] = acc[b][0][0];
         }
     }
     __syncthreads();
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, 
         const int e = t * p.K + k;
         if (!valid[e]) continue;
         float v = 0.0f;
-        for (int q = 0; q < parts; ++q) v += sums[(e * parts + q) * kDownCols + c];
+        for (int q = 0; q < parts; ++q) v += sums[(e * parts + q) * kCols + c];
         y = fmaf(weight[e], v, y);
     }
     p.out[at] = __builtin_bit_cast(uint16_t, (__bf16)(y + bias));
@@ -399,10 +401,23 @@ struct OneParts {
         parts = kDownWaves / entries < pieces ? kDownWaves / entries : pieces;
         per_part = (pieces + parts - 1) / parts;
     }
-    int lds() const { return kDownWaves * (kDownCols * 4 + per_part * (kPieceK * 2)); }
+    int lds(int NF) const { return kDownWaves * (NF * 64 + per_part * (kPieceK * 2)); }
 };
 // No more entries than waves, and rows whose parts fit beside each other.
-bool one_by_one(const Params& p) { return p.T * p.K <= kDownWaves && OneParts(p.T * p.K, p.I).lds() <= kOneLds; }
+bool one_by_one(const Params& p) { return p.T * p.K <= kDownWaves && OneParts(p.T * p.K, p.I).lds(2) <= kOneLds; }
+
+// 32 channels a workgroup in the down projection: per byte of weights half as many loads of rows as with 16.  But 16 where that
+// leaves most of the chip without a workgroup.
+bool narrow_down(const Params& p) { return p.H < 6144; }
+
+template <class W, int NF>
+hipError_t launch_one_down(const Params& p, hipStream_t stream) {
+    const OneParts o(p.T * p.K, p.I);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_down<W, NF>), o.lds(NF));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_one_down<W, NF>), dim3((p.H + NF * 16 - 1) / (NF * 16)), dim3(kDownThreads), o.lds(NF), stream, p, o.parts, o.per_part);
+    return hipGetLastError();
+}
 
 template <class W, int NF>
 hipError_t launch_one(const Params& p, hipStream_t stream) {
@@ -413,11 +428,7 @@ hipError_t launch_one(const Params& p, hipStream_t stream) {
     hipLaunchKernelGGL((k_one_up<W, NF>), dim3((unsigned)(n * cols)), dim3(kStreamThreads), up_lds, stream, p, cols, per_wave);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const OneParts o(n, p.I);
-    e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_down<W>), o.lds());
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_one_down<W>), dim3((p.H + kDownCols - 1) / kDownCols), dim3(kDownThreads), o.lds(), stream, p, o.parts, o.per_part);
-    return hipGetLastError();
+    return narrow_down(p) ? launch_one_down<W, 1>(p, stream) : launch_one_down<W, 2>(p, stream);
 }
 
 // Rows an expert has on average decide how many steps of 16 a workgroup takes past the weights at a time.
@@ -427,7 +438,8 @@ hipError_t by_rows(const Params& p, int E, hipStream_t stream) {
     const double rows = (double)p.T * p.K / E;
     const hipError_t e = rows <= 12 ? launch_up<W, 1, NF>(p, stream) : rows <= 24 ? launch_up<W, 2, NF>(p, stream) : launch_up<W, 4, NF>(p, stream);
     if (e != hipSuccess) return e;
-    return rows <= 12 ? launch_down<W, 1>(p, stream) : launch_down<W, 2>(p, stream);
+    if (narrow_down(p)) return rows <= 12 ? launch_down<W, 1, 1>(p, stream) : launch_down<W, 2, 1>(p, stream);
+    return rows <= 12 ? launch_down<W, 1, 2>(p, stream) : launch_down<W, 2, 2>(p, stream);
 }
 
 template <WeightFormat F>

@@ -1,10 +1,11 @@
-// ep_w4_tile.hip -- the expert block with 4-bit weights for many rows per expert: tiles of up to 128 rows by 256 channels.
+// ep_w4_tile.hip -- the expert block with 4-bit weights on tiles: up to 32, 64 or 128 rows by 256 channels.
 //
-// Eight waves, 2 along the rows by 4 along the channels.  Rows, codes and scales of 128 k (a stage) are copied to LDS without passing
-// registers, three stages deep; a piece of codes is 1024 bytes in a row in memory and in LDS, so copying and reading it
-// take whole lines and no two lanes meet in a bank.  A wave widens its codes (exactly) on their way from LDS to the matrix
-// instruction; a group's sums are kept apart and take their scale in fp32 on the way into acc.  Those second sums are what
-// limits a tile to 128 rows.  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
+// Rows, codes and scales of 128 k (a stage) are copied to LDS without passing registers, three to six stages deep; a piece of
+// codes is 1024 bytes in a row in memory and in LDS, so copying and reading it take whole lines and no two lanes meet in a
+// bank.  A wave widens its codes (exactly) on their way from LDS to the matrix instruction; a group's sums are kept apart and take
+// their scale in fp32 on the way into acc.  Those second sums are what limits a tile to 128 rows.  With 128, eight waves stand 2
+// along the rows by 4 along the channels; with fewer rows all 8 along the channels, so that every code is widened once, and LDS
+// holds more stages: the weights come from HBM.  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_weights.hpp"
@@ -23,13 +24,59 @@ struct Params {
     int sp, op;            // elements between rows of s and of out
 };
 
-template <WeightFormat F, int S>
+// Rows with 128 k of each per stage, ROWS of them: 256 bytes, whose 16-byte chunks are permuted by the row number so that a
+// fragment read (16 rows, 16 bytes at one place of each) is spread over all banks.
+template <int ROWS>
+struct WideRows {
+    static constexpr int kCopies = ROWS / 4 / kGemmWaves, kBytes = ROWS * 256;
+    uint64_t base;
+    uint32_t offset[kCopies];
+
+    static __device__ __forceinline__ int row(int i) { return (i * kGemmWaves + wave_id()) * 4 + (lane_id() >> 4); }
+    static __device__ __forceinline__ int chunk(int i) { return (lane_id() & 15) ^ (row(i) & 15); }
+    __device__ __forceinline__ void settle() {
+        base = uniform64(base);
+        asm volatile("s_nop 4" : "+s"(base));
+    }
+    // row_offset(r): byte offset of row r from `start`, or kNoElement.
+    template <class RowOffset>
+    __device__ __forceinline__ void init(const void* start, RowOffset row_offset) {
+        base = uniform64((uint64_t)start);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const uint32_t o = row_offset(row(i));
+            offset[i] = o == kNoElement ? kNoElement : o + chunk(i) * 16;
+        }
+    }
+    // As KcOperand::copy: `left` bytes of each row to go.
+    __device__ __forceinline__ void copy(uint32_t lds, int left) {
+        if (left < 256) {
+            stay_branch();
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) offset[i] = chunk(i) * 16 < left ? offset[i] : kNoElement;
+        }
+        const i32x4 res = ep::resource(base);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + threadIdx.x / kWave * 1024);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) copy16_to_lds(to + i * kGemmWaves * 1024, offset[i], res);
+        base += 256;
+    }
+    // LDS offset of the lane's 16 bytes of the rows from row0 (a multiple of 16) for the first instruction; ^ 64 j for the j-th.
+    static __device__ __forceinline__ uint32_t fragment(int row0) {
+        const int r = lane_id() & 15, g = lane_id() >> 4;
+        return (row0 + r) * 256 + ((g ^ (r & 3)) << 4 | (r & 12) << 4);
+    }
+};
+
+template <WeightFormat F, int S, int BM>
 struct W4Tiles {
-    static constexpr int kBM = 128, NT = 4, kCodes = 16;                             // 16 rows of pieces: 256 channels
-    typedef KcOperand<kBM> SOp;                                                      // 64 k
-    static constexpr int kW = 2 * SOp::kBytes, kScales = kW + kCodes * kPieceBytes, kScaleBytes = kGemmWaves * 256;
-    static constexpr int kStage = kScales + kScaleBytes, kBuffers = 3, kLds = kStage * kBuffers;
-    static constexpr int kWCopies = kCodes / kGemmWaves, kCopies = 2 * SOp::kCopies + kWCopies + 1;      // of a stage per wave
+    static constexpr int kBM = BM, kCodes = 16;                                      // 16 rows of pieces: 256 channels
+    static constexpr int kWavesM = BM == 128 ? 2 : 1, kWavesN = kGemmWaves / kWavesM;
+    static constexpr int NT = kCodes / kWavesN, kSteps = BM / 16 / kWavesM;          // of a wave: rows of pieces, 16-row steps
+    typedef WideRows<BM> SOp;
+    static constexpr int kW = SOp::kBytes, kScales = kW + kCodes * kPieceBytes, kStage = kScales + kGemmWaves * 256;
+    static constexpr int kBuffers = BM == 128 ? 3 : BM == 64 ? 4 : 6, kAhead = kBuffers - 1, kLds = kStage * kBuffers;
+    static constexpr int kWCopies = kCodes / kGemmWaves, kCopies = SOp::kCopies + kWCopies + 1;      // of a stage per wave
     static constexpr int kPieceScales = 32 * S;                                      // bytes
 
     char* smem;
@@ -54,7 +101,6 @@ struct W4Tiles {
     __device__ __forceinline__ void copy(int to) {
         const uint32_t lds = lds_address(smem) + to * kStage;
         s.copy(lds, left * 2);
-        s.copy(lds + SOp::kBytes, (left - 64) * 2);
         const uint32_t size = left > 0 ? kNoElement : 0u;
         const i32x4 rw = resource(w, size), rs = resource(scales, size);
         const uint32_t lw = __builtin_amdgcn_readfirstlane(lds + kW + threadIdx.x / kWave * kPieceBytes);
@@ -81,22 +127,23 @@ struct W4Tiles {
         for (int i = 0; i < kWCopies; ++i) w_offset[i] = next_w_offset[i];
     }
     // The workgroup's first tile, which next_* describe.
-    __device__ __forceinline__ void begin() {
+    __device__ __forceinline__ void begin(char* lds) {
+        smem = lds;
         w = scales = 0;
         s = next_s;
         settle();
         take_next();
         k = next_k;
         buf = 0;
-        copy(0);
-        copy(1);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) copy(i);
     }
 
     // The sums of the tile under way; afterwards the next one is.
     template <int MT>
     __device__ __forceinline__ void run(f32x4 (&acc)[NT][MT]) {
-        const int wave = wave_id(), wm = wave >> 2, wn = wave & 3, lane = lane_id();
-        const int stages = __builtin_amdgcn_readfirstlane(k > kPieceK ? pieces_of(k) : 2);      // enough that one tile ahead will do
+        const int wave = wave_id(), wm = wave / kWavesN, wn = wave % kWavesN, lane = lane_id();
+        const int stages = __builtin_amdgcn_readfirstlane(k > kAhead * kPieceK ? pieces_of(k) : kAhead);      // enough that one tile ahead will do
         left = __builtin_amdgcn_readfirstlane(left);
         next_k = __builtin_amdgcn_readfirstlane(next_k);
         buf = __builtin_amdgcn_readfirstlane(buf);
@@ -107,12 +154,12 @@ struct W4Tiles {
             for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t s_at = SOp::fragment(wm * MT * 16);
         for (int st = 0; st < stages; ++st) {
-            if (st == stages - 2) {
+            if (st == stages - kAhead) {
                 stay_branch();
                 take_next();
             }
             // this stage has landed, and every wave has left the one before, whose buffer the copies go to
-            wait_and_meet<kCopies>();
+            wait_and_meet<(kBuffers - 2) * kCopies>();
             copy(buf == 0 ? kBuffers - 1 : buf - 1);
             const char* ls = smem + buf * kStage;
             const char* lw = ls + kW + wn * NT * kPieceBytes + lane * 16;
@@ -132,7 +179,7 @@ struct W4Tiles {
                 for (int j = grp * kPer; j < (grp + 1) * kPer; ++j) {
                     bf16x8 sv[MT];
 #pragma unroll
-                    for (int a = 0; a < MT; ++a) sv[a] = read_kc(ls + (j >> 1) * SOp::kBytes, (s_at ^ ((j & 1) * 64)) + a * 2048);
+                    for (int a = 0; a < MT; ++a) sv[a] = read_kc(ls, (s_at ^ (j * 64)) + a * 4096);
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
                         const bf16x8 fv = F == kWeightsInt4 ? widen_int4x8((uint32_t)code[b][j]) : widen_e2m1x8((uint32_t)code[b][j]);
@@ -159,15 +206,16 @@ struct W4Tiles {
     static __device__ __forceinline__ void end() { wait_and_meet<0>(); }
 };
 
-// UP: a wave's four rows of pieces are 32 gate channels and the same up channels, and h = silu(g) u is stored.
-template <WeightFormat F, int S, bool UP>
+// UP: half of a wave's rows of pieces are gate channels, half the same up channels, and h = silu(g) u is stored.
+template <WeightFormat F, int S, int BM, bool UP>
 struct Kernel {
-    typedef W4Tiles<F, S> Tiles;
-    static constexpr int kCols = UP ? 128 : 256;
-    static constexpr float kUnit = Weights<F, S>::kUnit;
+    typedef W4Tiles<F, S, BM> Tiles;
+    static constexpr int NT = Tiles::NT, kOut = UP ? NT / 2 : NT;            // rows of pieces that a wave stores
+    static constexpr int kCols = Tiles::kWavesN * kOut * 16, kUnit = Tiles::kWavesM * 16;
+    static constexpr float kValue = Weights<F, S>::kUnit;
 
     const Params& p;
-    RowTiles<Tiles::kBM, 0> rows;
+    RowTiles<BM, 0> rows;
     Tiles g;
     int round = 0;
     struct Target {
@@ -181,34 +229,35 @@ struct Kernel {
         TileAt at;
         next.rows = g.next_k = 0;
         if (!tile_at((int)blockIdx.x, round++, rows.total, (p.N + kCols - 1) / kCols, &at)) return;
-        const RowTile t = rows.find(at.row, 32);
+        const RowTile t = rows.find(at.row, kUnit);
         const int n0 = at.col * kCols, pieces = pieces_of(p.K);
         next = Target{t.row0, t.rows, n0};
         g.next_k = p.K;
         g.next_s.init(p.s + (int64_t)t.row0 * p.sp, [&](int r) { return r < t.rows ? r * (2u * p.sp) : kNoElement; });
         const int64_t piece = ((int64_t)t.expert * (p.w.N / kPieceRows) + n0 / kPieceRows) * pieces;
         g.init_next_w(p.w.values + piece * kPieceBytes, p.w.scales + piece * (32 * S), pieces, [&](int i) {
-            const int c = UP ? i / 4 * 32 + (i & 1) * 16 : i * 16;
-            return n0 + c < p.N ? (c + (UP && (i & 2) ? p.N : 0)) / kPieceRows : -1;
+            const int b = i % NT, c = (i / NT * kOut + b % kOut) * 16;
+            return n0 + c < p.N ? (c + b / kOut * p.N) / kPieceRows : -1;
         });
     }
 
     template <int MT>
     __device__ __forceinline__ void tile() {
-        f32x4 acc[4][MT];
+        f32x4 acc[NT][MT];
         g.template run<MT>(acc);
         // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows
-        const int wave = wave_id(), r = lane_id() & 15, odd = r & 1, m_at = (wave >> 2) * MT * 16 + (lane_id() >> 4) * 4 + odd * 2;
+        const int wave = wave_id(), r = lane_id() & 15, odd = r & 1;
+        const int m_at = wave / Tiles::kWavesN * MT * 16 + (lane_id() >> 4) * 4 + odd * 2;
 #pragma unroll
-        for (int b = 0; b < (UP ? 2 : 4); ++b) {
-            const int n = now.n0 + (wave & 3) * (kCols / 4) + b * 16 + (r & ~1);
+        for (int b = 0; b < kOut; ++b) {
+            const int n = now.n0 + (wave % Tiles::kWavesN * kOut + b) * 16 + (r & ~1);
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = acc[b][a][i] * kUnit;
-                    if constexpr (UP) v[i] = v[i] * sigmoid(v[i]) * (acc[b + 2][a][i] * kUnit);
+                    v[i] = acc[b][a][i] * kValue;
+                    if constexpr (UP) v[i] = v[i] * sigmoid(v[i]) * (acc[b + kOut][a][i] * kValue);
                 }
                 const float x0 = dpp_f<0xB1>(odd ? v[0] : v[2]), x1 = dpp_f<0xB1>(odd ? v[1] : v[3]);
                 if (n >= p.N) continue;
@@ -221,44 +270,51 @@ struct Kernel {
     }
 };
 
-template <WeightFormat F, int S, bool UP>
+template <WeightFormat F, int S, int BM, bool UP>
 __global__ __launch_bounds__(kGemmThreads, 2) void k_w4_tiles(Params p) {
+    typedef Kernel<F, S, BM, UP> K;
     extern __shared__ __align__(1024) char smem[];
-    Kernel<F, S, UP> k(p);
+    K k(p);
     k.look_ahead();
     if (k.next.rows == 0) return;
-    k.g.smem = smem;
-    k.g.begin();
+    k.g.begin(smem);
     do {
         k.now = k.next;
         k.look_ahead();
-        switch ((k.now.rows + 31) / 32) {
-            case 1: k.template tile<1>(); break;
-            case 2: k.template tile<2>(); break;
-            case 3: k.template tile<3>(); break;
-            default: k.template tile<4>(); break;
-        }
+        const int steps = (k.now.rows + K::kUnit - 1) / K::kUnit;
+        if (steps == 1) k.template tile<1>();
+        else if (K::Tiles::kSteps == 2 || steps == 2) k.template tile<2>();
+        else if (steps == 3) k.template tile<(K::Tiles::kSteps < 3 ? 2 : 3)>();
+        else k.template tile<(K::Tiles::kSteps < 4 ? 2 : 4)>();
     } while (k.next.rows > 0);
     k.g.end();
 }
 
-template <WeightFormat F, int S, bool UP>
+template <WeightFormat F, int S, int BM, bool UP>
 hipError_t tiles_launch(const Handle& h, const Params& p, hipStream_t stream) {
-    typedef W4Tiles<F, S> Tiles;
-    const int cols = UP ? 128 : 256;
+    typedef Kernel<F, S, BM, UP> K;
     // row tiles that any routing can give: every expert may end in a short one
-    const int64_t rows = (int64_t)h.T * h.K / Tiles::kBM + h.El;
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_w4_tiles<F, S, UP>), Tiles::kLds);
+    const int64_t rows = (int64_t)h.T * h.K / BM + h.El;
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_w4_tiles<F, S, BM, UP>), K::Tiles::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_w4_tiles<F, S, UP>), dim3(walking_blocks(rows * ((p.N + cols - 1) / cols))), dim3(kGemmThreads), Tiles::kLds, stream, p);
+    hipLaunchKernelGGL((k_w4_tiles<F, S, BM, UP>), dim3(walking_blocks(rows * ((p.N + K::kCols - 1) / K::kCols))), dim3(kGemmThreads), K::Tiles::kLds,
+                       stream, p);
     return hipGetLastError();
+}
+
+template <WeightFormat F, int S, bool UP>
+hipError_t by_rows(const Handle& h, const Params& p, hipStream_t stream) {
+    const double rows = (double)h.T * h.K / h.E;
+    if (rows <= 22) return tiles_launch<F, S, 32, UP>(h, p, stream);
+    if (rows <= 48) return tiles_launch<F, S, 64, UP>(h, p, stream);
+    return tiles_launch<F, S, 128, UP>(h, p, stream);
 }
 
 template <WeightFormat F, bool UP>
 hipError_t by_group(const Handle& h, const Params& p, int group, hipStream_t stream) {
-    if (group == 128) return tiles_launch<F, 1, UP>(h, p, stream);
-    if (group == 64) return tiles_launch<F, 2, UP>(h, p, stream);
-    return tiles_launch<F, 4, UP>(h, p, stream);
+    if (group == 128) return by_rows<F, 1, UP>(h, p, stream);
+    if (group == 64) return by_rows<F, 2, UP>(h, p, stream);
+    return by_rows<F, 4, UP>(h, p, stream);
 }
 
 }  // namespace

@@ -25,9 +25,10 @@ constexpr int kXcds = 8, kGroup = 4, kBatch = 32;
 struct TileAt {
     int row, col;
 };
-// Tile number `round` of workgroup `block` of kXcds * kBatch; false: there is none, nor in later rounds.
+// Tile number `round` of workgroup `block` of kXcds * PER_XCD; false: there is none, nor in later rounds.
+template <int PER_XCD = kBatch>
 __device__ __forceinline__ bool tile_at(int block, int round, int rows, int cols, TileAt* t) {
-    const int total = rows * cols, batch = total >= kXcds * kBatch ? kBatch : (total + kXcds - 1) / kXcds;
+    const int total = rows * cols, batch = total >= kXcds * PER_XCD ? PER_XCD : (total + kXcds - 1) / kXcds;
     const int in_batch = block / kXcds;
     const int i = (round * kXcds + block % kXcds) * batch + in_batch;
     if (in_batch >= batch || i >= total) return false;
@@ -38,7 +39,9 @@ __device__ __forceinline__ bool tile_at(int block, int round, int rows, int cols
     return true;
 }
 // Workgroups to launch for at most `tiles` tiles: each walks through its rounds.
-inline unsigned walking_blocks(int64_t tiles) { return (unsigned)(tiles < kXcds * kBatch ? (tiles + kXcds - 1) / kXcds * kXcds : kXcds * kBatch); }
+inline unsigned walking_blocks(int64_t tiles, int per_xcd = kBatch) {
+    return (unsigned)(tiles < kXcds * per_xcd ? (tiles + kXcds - 1) / kXcds * kXcds : kXcds * per_xcd);
+}
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {

@@ -187,8 +187,6 @@ struct W4Args {
     int group;
 };
 hipError_t launch_expert_ffn_w4(const Handle& h, const W4Args& a, hipStream_t stream);
-hipError_t launch_w4_tile_up(const Handle& h, const W4Args& a, hipStream_t stream);      // many rows per expert
-hipError_t launch_w4_tile_down(const Handle& h, const W4Args& a, hipStream_t stream);
 
 constexpr int kFewTokens = 128, kFewEntries = 1024;
 struct FewArgs {

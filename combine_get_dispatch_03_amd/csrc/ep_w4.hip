@@ -4,6 +4,7 @@
 //   w[n][k] = s[n][k / group] * v(code[n][k])        v = code - 8, or the e2m1 value of the code
 #include "ep_expert_tiles.hpp"
 #include "ep_stream.hpp"
+#include "ep_w4.hpp"
 
 namespace ep {
 namespace {
@@ -88,10 +89,11 @@ hipError_t ffn(const Handle& h, const W4Args& a, hipStream_t stream) {
                     a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
                       (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
-    const bool tiled = (double)h.T * h.K / h.E > 12;
-    const hipError_t e = tiled ? launch_w4_tile_up(h, a, stream) : stream_launch<W, true, 4, 4>(h, up, stream);
+    W4Kernel kernel = w4_kernel(W4Sizes{h.T, h.K, h.E, h.El, a.inter, true});
+    const hipError_t e = kernel == kW4Stream ? stream_launch<W, true, 4, 4>(h, up, stream) : launch_w4_tile_up(h, a, kernel, stream);
     if (e != hipSuccess) return e;
-    return tiled ? launch_w4_tile_down(h, a, stream) : stream_launch<W, false, 4, 4>(h, down, stream);
+    kernel = w4_kernel(W4Sizes{h.T, h.K, h.E, h.El, a.hidden, false});
+    return kernel == kW4Stream ? stream_launch<W, false, 4, 4>(h, down, stream) : launch_w4_tile_down(h, a, kernel, stream);
 }
 
 template <WeightFormat F>

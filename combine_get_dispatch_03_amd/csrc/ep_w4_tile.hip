@@ -8,6 +8,7 @@
 // holds more stages: the weights come from HBM.  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
+#include "ep_w4.hpp"
 #include "ep_weights.hpp"
 
 namespace ep {
@@ -75,7 +76,8 @@ struct W4Tiles {
     static constexpr int NT = kCodes / kWavesN, kSteps = BM / 16 / kWavesM;          // of a wave: rows of pieces, 16-row steps
     typedef WideRows<BM> SOp;
     static constexpr int kW = SOp::kBytes, kScales = kW + kCodes * kPieceBytes, kStage = kScales + kGemmWaves * 256;
-    static constexpr int kBuffers = BM == 128 ? 3 : BM == 64 ? 4 : 6, kAhead = kBuffers - 1, kLds = kStage * kBuffers;
+    static constexpr int kPerCu = BM == 128 ? 1 : 2;                                 // workgroups
+    static constexpr int kBuffers = BM == 64 ? 2 : 3, kAhead = kBuffers - 1, kLds = kStage * kBuffers;
     static constexpr int kWCopies = kCodes / kGemmWaves, kCopies = SOp::kCopies + kWCopies + 1;      // of a stage per wave
     static constexpr int kPieceScales = 32 * S;                                      // bytes
 
@@ -182,7 +184,7 @@ struct W4Tiles {
                     for (int a = 0; a < MT; ++a) sv[a] = read_kc(ls, (s_at ^ (j * 64)) + a * 4096);
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        const bf16x8 fv = F == kWeightsInt4 ? widen_int4x8((uint32_t)code[b][j]) : widen_e2m1x8((uint32_t)code[b][j]);
+                        const bf16x8 fv = widen_codes<F == kWeightsInt4>((uint32_t)code[b][j]);
 #pragma unroll
                         for (int a = 0; a < MT; ++a)
                             part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sv[a], fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
@@ -228,7 +230,7 @@ struct Kernel {
     __device__ __forceinline__ void look_ahead() {
         TileAt at;
         next.rows = g.next_k = 0;
-        if (!tile_at((int)blockIdx.x, round++, rows.total, (p.N + kCols - 1) / kCols, &at)) return;
+        if (!tile_at<kBatch * Tiles::kPerCu>((int)blockIdx.x, round++, rows.total, (p.N + kCols - 1) / kCols, &at)) return;
         const RowTile t = rows.find(at.row, kUnit);
         const int n0 = at.col * kCols, pieces = pieces_of(p.K);
         next = Target{t.row0, t.rows, n0};
@@ -271,7 +273,7 @@ struct Kernel {
 };
 
 template <WeightFormat F, int S, int BM, bool UP>
-__global__ __launch_bounds__(kGemmThreads, 2) void k_w4_tiles(Params p) {
+__global__ __launch_bounds__(kGemmThreads, BM == 128 ? 2 : 4) void k_w4_tiles(Params p) {
     typedef Kernel<F, S, BM, UP> K;
     extern __shared__ __align__(1024) char smem[];
     K k(p);
@@ -297,38 +299,37 @@ hipError_t tiles_launch(const Handle& h, const Params& p, hipStream_t stream) {
     const int64_t rows = (int64_t)h.T * h.K / BM + h.El;
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_w4_tiles<F, S, BM, UP>), K::Tiles::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_w4_tiles<F, S, BM, UP>), dim3(walking_blocks(rows * ((p.N + K::kCols - 1) / K::kCols))), dim3(kGemmThreads), K::Tiles::kLds,
+    hipLaunchKernelGGL((k_w4_tiles<F, S, BM, UP>), dim3(walking_blocks(rows * ((p.N + K::kCols - 1) / K::kCols), kBatch * K::Tiles::kPerCu)), dim3(kGemmThreads), K::Tiles::kLds,
                        stream, p);
     return hipGetLastError();
 }
 
 template <WeightFormat F, int S, bool UP>
-hipError_t by_rows(const Handle& h, const Params& p, hipStream_t stream) {
-    const double rows = (double)h.T * h.K / h.E;
-    if (rows <= 22) return tiles_launch<F, S, 32, UP>(h, p, stream);
-    if (rows <= 48) return tiles_launch<F, S, 64, UP>(h, p, stream);
+hipError_t by_height(const Handle& h, const Params& p, W4Kernel kernel, hipStream_t stream) {
+    if (kernel == kW4Tile32) return tiles_launch<F, S, 32, UP>(h, p, stream);
+    if (kernel == kW4Tile64) return tiles_launch<F, S, 64, UP>(h, p, stream);
     return tiles_launch<F, S, 128, UP>(h, p, stream);
 }
 
 template <WeightFormat F, bool UP>
-hipError_t by_group(const Handle& h, const Params& p, int group, hipStream_t stream) {
-    if (group == 128) return by_rows<F, 1, UP>(h, p, stream);
-    if (group == 64) return by_rows<F, 2, UP>(h, p, stream);
-    return by_rows<F, 4, UP>(h, p, stream);
+hipError_t by_group(const Handle& h, const Params& p, int group, W4Kernel kernel, hipStream_t stream) {
+    if (group == 128) return by_height<F, 1, UP>(h, p, kernel, stream);
+    if (group == 64) return by_height<F, 2, UP>(h, p, kernel, stream);
+    return by_height<F, 4, UP>(h, p, kernel, stream);
 }
 
 }  // namespace
 
-hipError_t launch_w4_tile_up(const Handle& h, const W4Args& a, hipStream_t stream) {
+hipError_t launch_w4_tile_up(const Handle& h, const W4Args& a, W4Kernel kernel, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, WeightArgs{(const char*)a.w13.values, (const char*)a.w13.scales, 2 * a.inter, a.hidden},
                    a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
-    return a.int4 ? by_group<kWeightsInt4, true>(h, p, a.group, stream) : by_group<kWeightsE2m1, true>(h, p, a.group, stream);
+    return a.int4 ? by_group<kWeightsInt4, true>(h, p, a.group, kernel, stream) : by_group<kWeightsE2m1, true>(h, p, a.group, kernel, stream);
 }
 
-hipError_t launch_w4_tile_down(const Handle& h, const W4Args& a, hipStream_t stream) {
+hipError_t launch_w4_tile_down(const Handle& h, const W4Args& a, W4Kernel kernel, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
                    (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
-    return a.int4 ? by_group<kWeightsInt4, false>(h, p, a.group, stream) : by_group<kWeightsE2m1, false>(h, p, a.group, stream);
+    return a.int4 ? by_group<kWeightsInt4, false>(h, p, a.group, kernel, stream) : by_group<kWeightsE2m1, false>(h, p, a.group, kernel, stream);
 }
 
 }  // namespace ep

@@ -8,8 +8,8 @@
 //   e4m3   rows [N, K] of bytes, an fp32 scale per 128 x 128 block; widened to bf16 (exact); the scale goes to the piece's sums.
 //   4-bit  laid out once (pack): a piece is 1024 bytes in a row, 16 a lane, so a wave's load is whole lines of one place; a group
 //          of 32, 64 or 128 k has a bf16 scale per row, which goes to the group's sums in fp32.  Codes are widened to bf16
-//          (exact): e2m1 by the conversion instruction, integers (-8 .. 7, two's complement) by way of v_cvt_off_f32_i4, which
-//          gives a sixteenth of them (kUnit).  K is filled up with zeros to whole pieces.  A piece's scales are [16 rows][groups].
+//          (exact): e2m1 by the conversion instruction, integers (-8 .. 7, two's complement) by way of one that gives a sixteenth
+//          of them as fp32 (kUnit).  K is filled up with zeros to whole pieces.  A piece's scales are [16 rows][groups].
 //
 // The rows that meet the weights are the instruction's first operand, so lane (r, g) ends up with weight row r's sums of rows
 // 4 g .. 4 g + 3: one scale per group is all that it needs.
@@ -47,29 +47,40 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t lane,
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)wave, 0));
 }
 
-// Integers of four bits, bytes 0..3 of q: a sixteenth of each, low and high nibbles.
-template <int BYTE>
-__device__ __forceinline__ float sixteenth(uint32_t q) {
-    float f;
-    if constexpr (BYTE == 0) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(q));
-    if constexpr (BYTE == 1) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(q));
-    if constexpr (BYTE == 2) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(q));
-    if constexpr (BYTE == 3) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(q));
-    return f;
-}
 // The upper halves of two floats that bf16 holds exactly.
 __device__ __forceinline__ int upper_halves(float lo, float hi) {
     return (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
 }
-__device__ __forceinline__ bf16x8 widen_int4x8(uint32_t q) {
-    const uint32_t h = q >> 4;
-    return __builtin_bit_cast(bf16x8, i32x4{upper_halves(sixteenth<0>(q), sixteenth<0>(h)), upper_halves(sixteenth<1>(q), sixteenth<1>(h)),
-                                            upper_halves(sixteenth<2>(q), sixteenth<2>(h)), upper_halves(sixteenth<3>(q), sixteenth<3>(h))});
-}
-__device__ __forceinline__ bf16x8 widen_e2m1x8(uint32_t q) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 1);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 3);
-    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+// Eight codes, widened pair by pair.
+template <bool INT4>
+struct Codes;
+// Integers: a sixteenth of each.  The odd ones are shifted down once, and every byte of the two words is an operand of its own
+// (left alone, the compiler shifts each nibble by itself).
+template <>
+struct Codes<true> {
+    uint32_t even, odd;
+    __device__ __forceinline__ explicit Codes(uint32_t q) : even(q), odd(q >> 4) { asm("" : "+v"(odd)); }
+    static __device__ __forceinline__ float sixteenth(uint32_t q, int i) {
+        return __builtin_amdgcn_cvt_off_f32_i4((int)(i == 0 ? q : i == 3 ? q >> 24 : q >> (i * 8) & 0xffu));
+    }
+    __device__ __forceinline__ int pair(int i) const { return upper_halves(sixteenth(even, i), sixteenth(odd, i)); }
+};
+template <>
+struct Codes<false> {
+    uint32_t q;
+    __device__ __forceinline__ explicit Codes(uint32_t v) : q(v) {}
+    __device__ __forceinline__ int pair(int i) const {
+        const bf16x2 v = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 0)
+                         : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 1)
+                         : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 2)
+                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 3);
+        return __builtin_bit_cast(int, v);
+    }
+};
+template <bool INT4>
+__device__ __forceinline__ bf16x8 widen_codes(uint32_t q) {
+    const Codes<INT4> c(q);
+    return __builtin_bit_cast(bf16x8, i32x4{c.pair(0), c.pair(1), c.pair(2), c.pair(3)});
 }
 
 // The bf16 scales of a row's S groups.
@@ -194,7 +205,7 @@ struct Weights {
     };
     static __device__ __forceinline__ int k_of(int j, int g) { return j * 32 + g * 8; }
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) {
-        return F == kWeightsInt4 ? widen_int4x8((uint32_t)raw.v[j]) : widen_e2m1x8((uint32_t)raw.v[j]);
+        return widen_codes<F == kWeightsInt4>((uint32_t)raw.v[j]);
     }
     static __device__ __forceinline__ float scale_of(const Raw& raw, int group) { return raw.s.get(group); }
 

@@ -9,7 +9,7 @@
 // every row of y is read once, out and normed are written once, and what a norm needs of the whole row is one sum over
 // the workgroup (lanes by register exchange, waves through LDS, in a fixed order).  Memory bounds it: without a handle (8 bytes
 // a channel) 4096 rows of 7168 take 37 us (6.3 TB/s), 4096 of 2048 13.5 us; 4096 tokens of 7168 through a handle with
-// top-8 bf16 rows, residual and two outputs 118 us (704 MB, 6.0 TB/s).
+// top-8 bf16 rows, bias, residual and two outputs 118 us (704 MB, 6.0 TB/s).
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
 

@@ -7,6 +7,11 @@
 // routing table itself (items: up to 16 * MT entries of one expert).  Both are bound by reading the weights of the experts in
 // use, once each.  In the second the waves take items in turn, and each entry's 16 values stand in LDS until they are
 // weighted and summed in ascending k, so that nothing depends on the order in which waves finish.
+//
+// Measured: 32 tokens, 256 e4m3 experts of 7168 x 2048, top-8 (7.2 GB): 804 us (6.0 TB/s) and 447 (5.4 TB/s; 224 workgroups on 256
+// CUs).  One token, int4: 24 and 15 us (5.0 and 4.0 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 126 and 92 us
+// (4.2 and 2.9 TB/s): with some 16 rows beside a piece of 1 KiB the rows' 4 KiB from L2 bound it, not the weights.
+// Splitting all items' pieces evenly over the waves of the second kernel gained nothing (227 and 231 us in all, 1262 and 1271).
 #include "ep_ffn.hpp"
 #include "ep_stream.hpp"
 

@@ -9,6 +9,8 @@
 namespace ep {
 namespace {
 
+// Laying out is a copy: 3.8 GB of codes (256 experts' gate and up of 7168 x 2048) take 2.3 ms (3.3 TB/s, reads and writes).
+//
 // A thread writes 16 bytes of codes, one lane's part of a piece: k j * 32 + g * 8 .. + 7 for j = 0..3 (see ep_weights.hpp).
 __global__ __launch_bounds__(256) void k_pack_codes(const uint8_t* codes, char* packed, uint32_t flip, int N, int K, int64_t parts) {
     const int64_t i = block_id() * 256 + threadIdx.x;
@@ -58,7 +60,8 @@ __device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, 
                                      [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
 }
 
-// Up to 16 * MT rows of an expert by 16 * NF rows of its weights.
+// Up to 16 * MT rows of an expert by 16 * NF rows of its weights.  Few tiles spread over idle CUs, and a short sum's latency is what
+// they cost: 128 tokens, 8 experts of 256 x 512 take 6.3 us a product.
 template <class W, bool UP, int MT, int NF>
 __global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void k_w4_stream(Params p) {
     __shared__ __align__(16) float sums[stream_lds<NF>() / 4];

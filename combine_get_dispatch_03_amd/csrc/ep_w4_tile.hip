@@ -1,11 +1,17 @@
 // ep_w4_tile.hip -- the expert block with 4-bit weights on tiles: up to 32, 64 or 128 rows by 256 channels.
 //
-// Rows, codes and scales of 128 k (a stage) are copied to LDS without passing registers, three to six stages deep; a piece of
+// Rows, codes and scales of 128 k (a stage) are copied to LDS without passing registers, one or two stages ahead; a piece of
 // codes is 1024 bytes in a row in memory and in LDS, so copying and reading it take whole lines and no two lanes meet in a
 // bank.  A wave widens its codes (exactly) on their way from LDS to the matrix instruction; a group's sums are kept apart and take
 // their scale in fp32 on the way into acc.  Those second sums are what limits a tile to 128 rows.  With 128, eight waves stand 2
-// along the rows by 4 along the channels; with fewer rows all 8 along the channels, so that every code is widened once, and LDS
-// holds more stages: the weights come from HBM.  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
+// along the rows by 4 along the channels, one workgroup a CU; with fewer rows all 8 along the channels, so that every code is
+// widened once, and two workgroups a CU, each of which waits while the other works (16 tokens, 32 experts of 7168 x 2048, int4: 148 us,
+// with one workgroup of six stages 158).  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
+//
+// What bounds them: with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and products
+// together, gate and up 117 us (4.1 TB/s), down 69 (3.5 TB/s).  With 1024 rows (4096 tokens, e2m1 in groups of 32: 2.14 and 1.11 ms,
+// 0.9 and 0.87 PFLOP/s) the sum of the matrix unit's time and the vector unit's: the same in groups of 128, a quarter of the
+// scalings, takes 2.62 ms in all (1.1 PFLOP/s) instead of 3.3, int4, with three times the widening, 3.15.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_w4.hpp"

@@ -183,6 +183,8 @@ struct W4Tiles {
 #pragma unroll
             for (int grp = 0; grp < S; ++grp) {
                 f32x4 part[NT][MT];
+                // the wave that multiplies goes first, while another of its SIMD scales: 2 to 3% (4096 tokens 3.38 and 3.28 ms)
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int j = grp * kPer; j < (grp + 1) * kPer; ++j) {
                     bf16x8 sv[MT];
@@ -196,6 +198,7 @@ struct W4Tiles {
                             part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sv[a], fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
                     }
                 }
+                __builtin_amdgcn_s_setprio(0);
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
                     const float by = scale[b].get(grp);

@@ -3,15 +3,16 @@
 // Rows, codes and scales of 128 k (a stage) are copied to LDS without passing registers, one or two stages ahead; a piece of
 // codes is 1024 bytes in a row in memory and in LDS, so copying and reading it take whole lines and no two lanes meet in a
 // bank.  A wave widens its codes (exactly) on their way from LDS to the matrix instruction; a group's sums are kept apart and take
-// their scale in fp32 on the way into acc.  Those second sums are what limits a tile to 128 rows.  With 128, eight waves stand 2
-// along the rows by 4 along the channels, one workgroup a CU; with fewer rows all 8 along the channels, so that every code is
-// widened once, and two workgroups a CU, each of which waits while the other works (16 tokens, 32 experts of 7168 x 2048, int4: 148 us,
-// with one workgroup of six stages 158).  A workgroup stays on its CU and its tiles form one stream of stages, as in Bf16Tiles.
+// their scale in fp32 on the way into acc.  Those second sums are what limits a tile to 128 rows.  All eight waves stand along the
+// channels, so that every code is widened once (with two rows of waves, int4: 4096 tokens 2.97 and 2.75 ms).  A tile of 128 rows
+// has a CU to itself; of 32 and 64 rows there are two, each of which works while the other waits (16 tokens, 32 experts of 7168 x
+// 2048, int4: 148 us, one workgroup of six stages 158).  A workgroup stays on its CU and its tiles form one stream of stages, as in
+// Bf16Tiles.
 //
 // What bounds them: with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and products
-// together, gate and up 117 us (4.1 TB/s), down 69 (3.5 TB/s).  With 1024 rows (4096 tokens, e2m1 in groups of 32: 2.14 and 1.11 ms,
-// 0.9 and 0.87 PFLOP/s) the sum of the matrix unit's time and the vector unit's: the same in groups of 128, a quarter of the
-// scalings, takes 2.62 ms in all (1.1 PFLOP/s) instead of 3.3, int4, with three times the widening, 3.15.
+// together, gate and up 108 us (4.5 TB/s), down 67 (3.6 TB/s).  With 1024 rows (4096 tokens, 2.89 TFLOP) the sum of the matrix unit's time
+// and the vector unit's: e2m1 in groups of 128 takes 2.56 ms (1.13 PFLOP/s), in groups of 32, four times the scalings, 3.13, int4,
+// with three times the widening, 2.75.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_w4.hpp"
@@ -78,8 +79,7 @@ struct WideRows {
 template <WeightFormat F, int S, int BM>
 struct W4Tiles {
     static constexpr int kBM = BM, kCodes = 16;                                      // 16 rows of pieces: 256 channels
-    static constexpr int kWavesM = BM == 128 ? 2 : 1, kWavesN = kGemmWaves / kWavesM;
-    static constexpr int NT = kCodes / kWavesN, kSteps = BM / 16 / kWavesM;          // of a wave: rows of pieces, 16-row steps
+    static constexpr int NT = kCodes / kGemmWaves, kSteps = BM / 16;                 // of a wave: rows of pieces, 16-row steps
     typedef WideRows<BM> SOp;
     static constexpr int kW = SOp::kBytes, kScales = kW + kCodes * kPieceBytes, kStage = kScales + kGemmWaves * 256;
     static constexpr int kPerCu = BM == 128 ? 1 : 2;                                 // workgroups
@@ -150,7 +150,7 @@ struct W4Tiles {
     // The sums of the tile under way; afterwards the next one is.
     template <int MT>
     __device__ __forceinline__ void run(f32x4 (&acc)[NT][MT]) {
-        const int wave = wave_id(), wm = wave / kWavesN, wn = wave % kWavesN, lane = lane_id();
+        const int wave = wave_id(), lane = lane_id();
         const int stages = __builtin_amdgcn_readfirstlane(k > kAhead * kPieceK ? pieces_of(k) : kAhead);      // enough that one tile ahead will do
         left = __builtin_amdgcn_readfirstlane(left);
         next_k = __builtin_amdgcn_readfirstlane(next_k);
@@ -160,7 +160,7 @@ struct W4Tiles {
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint32_t s_at = SOp::fragment(wm * MT * 16);
+        const uint32_t s_at = SOp::fragment(0);
         for (int st = 0; st < stages; ++st) {
             if (st == stages - kAhead) {
                 stay_branch();
@@ -170,8 +170,8 @@ struct W4Tiles {
             wait_and_meet<(kBuffers - 2) * kCopies>();
             copy(buf == 0 ? kBuffers - 1 : buf - 1);
             const char* ls = smem + buf * kStage;
-            const char* lw = ls + kW + wn * NT * kPieceBytes + lane * 16;
-            const char* lc = ls + kScales + wn * NT * kPieceScales + (lane & 15) * (2 * S);
+            const char* lw = ls + kW + wave * NT * kPieceBytes + lane * 16;
+            const char* lc = ls + kScales + wave * NT * kPieceScales + (lane & 15) * (2 * S);
             i32x4 code[NT];
             GroupScales<S> scale[NT];
 #pragma unroll
@@ -222,7 +222,7 @@ template <WeightFormat F, int S, int BM, bool UP>
 struct Kernel {
     typedef W4Tiles<F, S, BM> Tiles;
     static constexpr int NT = Tiles::NT, kOut = UP ? NT / 2 : NT;            // rows of pieces that a wave stores
-    static constexpr int kCols = Tiles::kWavesN * kOut * 16, kUnit = Tiles::kWavesM * 16;
+    static constexpr int kCols = kGemmWaves * kOut * 16;
     static constexpr float kValue = Weights<F, S>::kUnit;
 
     const Params& p;
@@ -240,7 +240,7 @@ struct Kernel {
         TileAt at;
         next.rows = g.next_k = 0;
         if (!tile_at<kBatch * Tiles::kPerCu>((int)blockIdx.x, round++, rows.total, (p.N + kCols - 1) / kCols, &at)) return;
-        const RowTile t = rows.find(at.row, kUnit);
+        const RowTile t = rows.find(at.row, 16);
         const int n0 = at.col * kCols, pieces = pieces_of(p.K);
         next = Target{t.row0, t.rows, n0};
         g.next_k = p.K;
@@ -258,10 +258,11 @@ struct Kernel {
         g.template run<MT>(acc);
         // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows
         const int wave = wave_id(), r = lane_id() & 15, odd = r & 1;
-        const int m_at = wave / Tiles::kWavesN * MT * 16 + (lane_id() >> 4) * 4 + odd * 2;
+        int m_at = (lane_id() >> 4) * 4 + odd * 2;
+        asm("" : "+v"(m_at));      // not to be looked into: all rows' addresses in registers (20 more) would slow the tile down by 2%
 #pragma unroll
         for (int b = 0; b < kOut; ++b) {
-            const int n = now.n0 + (wave % Tiles::kWavesN * kOut + b) * 16 + (r & ~1);
+            const int n = now.n0 + (wave * kOut + b) * 16 + (r & ~1);
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
                 float v[4];
@@ -292,11 +293,19 @@ __global__ __launch_bounds__(kGemmThreads, BM == 128 ? 2 : 4) void k_w4_tiles(Pa
     do {
         k.now = k.next;
         k.look_ahead();
-        const int steps = (k.now.rows + K::kUnit - 1) / K::kUnit;
-        if (steps == 1) k.template tile<1>();
-        else if (K::Tiles::kSteps == 2 || steps == 2) k.template tile<2>();
-        else if (steps == 3) k.template tile<(K::Tiles::kSteps < 3 ? 2 : 3)>();
-        else k.template tile<(K::Tiles::kSteps < 4 ? 2 : 4)>();
+        const int steps = (k.now.rows + 15) / 16;
+        constexpr int kSteps = K::Tiles::kSteps;
+        if constexpr (kSteps == 8) {
+            if (steps <= 2) k.template tile<2>();
+            else if (steps <= 4) k.template tile<4>();
+            else if (steps <= 6) k.template tile<6>();
+            else k.template tile<8>();
+        } else {
+            if (steps == 1) k.template tile<1>();
+            else if (kSteps == 2 || steps == 2) k.template tile<2>();
+            else if (steps == 3) k.template tile<(kSteps < 3 ? 2 : 3)>();
+            else k.template tile<(kSteps < 4 ? 2 : 4)>();
+        }
     } while (k.next.rows > 0);
     k.g.end();
 }

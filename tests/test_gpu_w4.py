@@ -7,6 +7,7 @@ import expert_reference as R
 import harness as Hn
 import w4_reference as Q
 from test_gpu_expert_ffn import poison, table, untouched
+from test_w4_rules_cpu import TILE128, w4
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -84,6 +85,19 @@ def test_forward(ep, shape, kind, group):
     Hn.assert_guards(gw)
     again = ep.ep_expert_ffn_w4(h, d["x"], d["p13"], d["p2"])
     assert torch.equal(again.view(torch.int16)[m["valid"]], y.view(torch.int16)[m["valid"]])
+
+
+@pytest.mark.parametrize("T,how", [(480, "uniform"), (1600, "zipf")])
+@pytest.mark.parametrize("kind,group,H,I", [("int4", 128, 13, 7), ("e2m1", 32, 50, 26), ("int4", 64, 25, 13)])
+def test_tall_tiles(ep, kind, group, H, I, T, how):
+    """Tiles of 128 rows, filled to any height."""
+    E, K = 64, 8
+    assert w4(T, K, E, I * group, True) == w4(T, K, E, H * group, False) == TILE128
+    h, d, m = setup(ep, (T, H, I, E, 1, 0, K, 1, how), kind, group)
+    y = torch.zeros(m["cap"], m["H"], dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_ffn_w4(h, d["x"], d["p13"], d["p2"], y=y)
+    check(y, d, m, kind)
+    assert not y[~m["valid"]].any()
 
 
 @pytest.mark.parametrize("kind,group", KINDS)

@@ -47,8 +47,19 @@ def test_tiles_grow_with_the_rows():
     for E, N in [(1, 128), (8, 2048), (64, 1408), (1024, 256)]:
         for up in (False, True):
             kernels = [w4(T, 4, E, N, up) for T in [1, 2, 5, 16, 60, 200, 1000, 5000, 40000, 300000]]
-            assert kernels == sorted(kernels)
             assert kernels[-1] == TILE128
+            # streamed first, tiles of 32 rows next, then tiles of 64 and 128
+            low = [min(k, TILE64) for k in kernels]
+            assert low == sorted(low)
+
+
+@pytest.mark.parametrize("E,H,I,rows,up,down", [
+    (32, 7168, 2048, 40, TILE64, TILE64), (32, 7168, 2048, 56, TILE128, TILE128), (32, 7168, 2048, 96, TILE128, TILE128),
+    (32, 7168, 2048, 128, TILE64, TILE64), (32, 7168, 2048, 192, TILE128, TILE128), (16, 2048, 768, 80, TILE64, TILE64),
+    (4, 4096, 1408, 256, TILE64, TILE64), (16, 2048, 768, 400, TILE128, TILE128), (8, 1024, 512, 400, TILE64, TILE64),
+])
+def test_measured_heights(E, H, I, rows, up, down):
+    assert (w4(rows * E, 1, E, I, True), w4(rows * E, 1, E, H, False)) == (up, down)
 
 
 @pytest.mark.parametrize("up", [False, True])

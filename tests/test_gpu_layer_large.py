@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import expert_reference as R
+import norm_reference as N
 import w4_reference as Q
 from test_gpu_expert_ffn import table
 from test_gpu_few import run, setup, weights
@@ -41,6 +42,26 @@ def test_largest_expert(ep, fmt):
             f = R.ffn_expert(x.double(), w13, w2)
             R.assert_within(y, f["y"], f["ey"], "y")
     del w13, w2, call, expert
+    torch.cuda.empty_cache()
+
+
+def test_norm_rows_far_apart(ep):
+    """More than 2^31 channels in all: the first and last rows."""
+    T, H, eps = 66000, 32768, 1e-5
+    g = torch.Generator(device=DEV).manual_seed(2)
+    n = lambda *z: torch.randn(*z, generator=g, device=DEV, dtype=torch.bfloat16)
+    y, res, go, gn, post, pre = n(T, H), n(T, H), n(T, H), n(T, H), n(H), n(H)
+    out, normed = ep.ep_combine_norm(None, y, residual=res, post_weight=post, pre_weight=pre, eps=eps)
+    d = ep.ep_combine_norm_backward(go, gn, y, residual=res, post_weight=post, pre_weight=pre, eps=eps, need_vectors=False)
+    for rows in (slice(0, 3), slice(T - 3, T)):
+        f = y[rows].double()
+        o = N.around(f, torch.zeros_like(f), res[rows], post, None, 1.0, pre, eps)
+        R.assert_within(out[rows], o["out"], o["eout"], "out")
+        R.assert_within(normed[rows], o["n"], o["en"], "normed")
+        want = N.gradients(f, res[rows], post, None, 1.0, pre, eps, go[rows], gn[rows])
+        for k in ("grad_f", "grad_residual"):
+            R.assert_within(d[k][rows], *want[k], k)
+    del y, res, go, gn, out, normed, d
     torch.cuda.empty_cache()
 
 

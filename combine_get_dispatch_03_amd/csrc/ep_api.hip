@@ -931,7 +931,8 @@ ep_status_t ep_combine_norm_backward(const void* grad_out, const void* grad_norm
     if (f_type != EP_NORM_F_KEPT && f_type != EP_NORM_F_BF16) return fail(EP_ERR_INVALID_ARG, "f_type must be EP_NORM_F_KEPT or EP_NORM_F_BF16");
     CombineNormBackwardArgs a;
     if (const char* why = norm_args(norm, &a.v)) return fail(EP_ERR_INVALID_ARG, "%s", why);
-    if (grad_f == nullptr && grad_residual == nullptr && grad_post == nullptr && grad_pre == nullptr && grad_gate == nullptr)
+    if (num_tokens > 0 && grad_f == nullptr && grad_residual == nullptr && grad_post == nullptr &&
+        grad_pre == nullptr && grad_gate == nullptr)
         return fail(EP_ERR_INVALID_ARG, "no gradient is asked for");
     if (grad_normed != nullptr && norm->pre_weight == nullptr) return fail(EP_ERR_INVALID_ARG, "grad_normed needs pre_weight");
     if (grad_pre != nullptr && (norm->pre_weight == nullptr || (num_tokens > 0 && grad_normed == nullptr)))

@@ -532,7 +532,8 @@ ep_status_t ep_combine_norm(ep_handle_t handle, const void* y, int hidden, int64
  *   grad_gate              device, nullable: fp32 [hidden], or with gate_per_token bf16 [num_tokens, hidden].
  *   workspace              device scratch of ep_combine_norm_workspace_bytes(...) bytes, 256-byte aligned, as in
  *                          ep_expert_ffn.
- *   At least one gradient is required.  No output may overlap an input.  Sums over tokens run in a fixed order.
+ *   At least one gradient is required, with no tokens none.  No output may overlap an input.  Sums over tokens run in a
+ *   fixed order.
  */
 ep_status_t ep_combine_norm_backward(const void* grad_out, const void* grad_normed, const void* f, ep_norm_f_t f_type, int num_tokens,
                                      int hidden, const ep_norm_args_t* norm, void* grad_f, void* grad_residual, float* grad_post,

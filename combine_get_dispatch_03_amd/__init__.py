@@ -838,12 +838,34 @@ def ep_adapter(handle: Handle, x, a, b, scales=None, base=None, out=None, worksp
 
 class W4Weights:
     """4-bit weights [matrices, rows, columns] as ep_w4_pack lays them out: `values` and `scales` (uint8 tensors, opaque), `kind`
-    ("int4" or "e2m1"), `group` and `shape`."""
+    ("int4" or "e2m1"), `group` and `shape`.  A program may keep these and put them together again; they stay as they are then."""
 
     def __init__(self, values, scales, kind, group, shape):
-        self.values, self.scales, self.kind, self.group, self.shape = values, scales, kind, group, tuple(shape)
-        self.device = values.device
+        if kind not in _W4_KINDS:
+            raise ValueError("kind must be one of %s" % sorted(_W4_KINDS))
+        shape = tuple(shape)
+        if len(shape) != 3:
+            raise ValueError("shape must be (matrices, rows, columns)")
+        n = _w4_bytes(*shape, group)
+        _need(values, torch.uint8, "values", getattr(values, "device", None), (n[0],))
+        _need(scales, torch.uint8, "scales", values.device, (n[1],))
+        self._parts = values, scales, kind, group, shape, values.device
         self._args = _Weights(values.data_ptr(), scales.data_ptr(), _W4_KINDS[kind], group)
+
+    values = property(lambda self: self._parts[0])
+    scales = property(lambda self: self._parts[1])
+    kind = property(lambda self: self._parts[2])
+    group = property(lambda self: self._parts[3])
+    shape = property(lambda self: self._parts[4])
+    device = property(lambda self: self._parts[5])
+
+
+def _w4_bytes(matrices, rows, columns, group):
+    """Sizes of packed values and scales."""
+    n = ep_w4_packed_bytes(matrices, rows, columns, group)
+    if n == 0:
+        raise EPError("ep_w4_pack takes no weights of matrices=%d rows=%d columns=%d group=%d" % (matrices, rows, columns, group))
+    return n, ep_w4_packed_scale_bytes(matrices, rows, columns, group)
 
 
 def ep_w4_packed_bytes(matrices, rows, columns, group) -> int:
@@ -872,9 +894,7 @@ def ep_w4_pack(codes, scales, kind, stream=None) -> W4Weights:
     if scales.shape[2] == 0 or K % scales.shape[2] != 0:
         raise ValueError("scales must be [matrices, rows, columns / group]")
     group = K // scales.shape[2]
-    n, m = ep_w4_packed_bytes(M, N, K, group), ep_w4_packed_scale_bytes(M, N, K, group)
-    if n == 0:
-        raise EPError("ep_w4_pack takes no weights of matrices=%d rows=%d columns=%d group=%d" % (M, N, K, group))
+    n, m = _w4_bytes(M, N, K, group)
     _need(codes, torch.uint8, "codes")     # on a GPU, after the rules on shapes
     values, packed = _empty(stream, codes, n, torch.uint8), _empty(stream, codes, m, torch.uint8)
     _check(_lib.ep_w4_pack(_ptr(codes), _ptr(scales), _W4_KINDS[kind], M, N, K, group, _ptr(values), _ptr(packed), _stream(stream)),

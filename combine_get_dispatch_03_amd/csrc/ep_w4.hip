@@ -49,40 +49,44 @@ struct Params {
     int sp, op;            // elements between rows of s and of out
 };
 
-template <class W, bool UP, int MT, int NF>
+constexpr int kStreamRows = 64, kStreamPieces = 4;      // of a workgroup: rows, and rows of pieces
+template <bool UP>
+constexpr int kStreamChannels = kStreamPieces * (UP ? 8 : 16);
+
+template <class W, bool UP, int MT>
 __device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, int n0, float* sums) {
     const int r = lane_id() & 15;
     RowFragments<W, MT> rows;
     rows.init(p.s + (int64_t)t.row0 * p.sp, p.K);
 #pragma unroll
     for (int a = 0; a < MT; ++a) rows.place(a, a * 16 + r < t.rows, (uint32_t)(a * 16 + r) * (uint32_t)(p.sp * 2));
-    stream_product<W, UP, MT, NF>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
-                                     [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
+    stream_product<W, UP, MT, kStreamPieces>(p.w, t.expert, p.N, p.K, n0, rows, t.rows, sums,
+                                             [&](int m) { return p.out + (int64_t)(t.row0 + m) * p.op; });
 }
 
-// Up to 16 * MT rows of an expert by 16 * NF rows of its weights.  Few tiles spread over idle CUs, and a short sum's latency is what
-// they cost: 128 tokens, 8 experts of 256 x 512 take 6.3 us a product.
-template <class W, bool UP, int MT, int NF>
-__global__ __launch_bounds__(kStreamThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) void k_w4_stream(Params p) {
-    __shared__ __align__(16) float sums[stream_lds<NF>() / 4];
-    constexpr int kChannels = UP ? NF * 8 : NF * 16;
-    const RowTiles<MT * 16> tiles(p.cnt, p.psum, p.El);
-    const int cols = (p.N + kChannels - 1) / kChannels, tile = blockIdx.x / cols;
+// Up to 64 rows of an expert by four rows of pieces of its weights.  Few tiles spread over idle CUs, and a short sum's latency is what
+// they cost: 128 tokens, 8 experts of 256 x 512 take 6.3 us a product.  64 rows' sums and fragments (192 to 217 registers) leave a CU
+// room for two workgroups, also where there are fewer rows.
+template <class W, bool UP>
+__global__ __launch_bounds__(kStreamThreads, 2) void k_w4_stream(Params p) {
+    __shared__ __align__(16) float sums[stream_lds<kStreamPieces>() / 4];
+    const RowTiles<kStreamRows> tiles(p.cnt, p.psum, p.El);
+    const int cols = (p.N + kStreamChannels<UP> - 1) / kStreamChannels<UP>, tile = blockIdx.x / cols;
     if (tile >= tiles.total) return;
     const RowTile t = tiles.find(tile);
-    const int n0 = blockIdx.x % cols * kChannels, steps = (t.rows + 15) / 16;
-    if (MT == 1 || steps == 1) rows_product<W, UP, 1, NF>(p, t, n0, sums);
-    else if (MT == 2 || steps == 2) rows_product<W, UP, 2, NF>(p, t, n0, sums);
-    else rows_product<W, UP, 4, NF>(p, t, n0, sums);
+    const int n0 = blockIdx.x % cols * kStreamChannels<UP>;
+    if (t.rows <= 16) rows_product<W, UP, 1>(p, t, n0, sums);
+    else if (t.rows <= 32) rows_product<W, UP, 2>(p, t, n0, sums);
+    else rows_product<W, UP, 4>(p, t, n0, sums);
 }
 
-template <class W, bool UP, int MT, int NF>
+template <class W, bool UP>
 hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
-    constexpr int kChannels = UP ? NF * 8 : NF * 16, kRows = MT * 16;
     const int64_t entries = (int64_t)h.T * h.K, busy = entries < h.El ? entries : h.El;
     // tiles that any routing can give: every expert with rows may end in a short one
-    const int64_t tiles = (entries + (kRows - 1) * busy) / kRows;
-    hipLaunchKernelGGL((k_w4_stream<W, UP, MT, NF>), dim3((unsigned)(tiles * ((p.N + kChannels - 1) / kChannels))), dim3(kStreamThreads), 0, stream, p);
+    const int64_t tiles = (entries + (kStreamRows - 1) * busy) / kStreamRows;
+    const int cols = (p.N + kStreamChannels<UP> - 1) / kStreamChannels<UP>;
+    hipLaunchKernelGGL((k_w4_stream<W, UP>), dim3((unsigned)(tiles * cols)), dim3(kStreamThreads), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -93,10 +97,10 @@ hipError_t ffn(const Handle& h, const W4Args& a, hipStream_t stream) {
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
                       (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
     W4Kernel kernel = w4_kernel(W4Sizes{h.T, h.K, h.E, h.El, a.inter, true});
-    const hipError_t e = kernel == kW4Stream ? stream_launch<W, true, 4, 4>(h, up, stream) : launch_w4_tile_up(h, a, kernel, stream);
+    const hipError_t e = kernel == kW4Stream ? stream_launch<W, true>(h, up, stream) : launch_w4_tile_up(h, a, kernel, stream);
     if (e != hipSuccess) return e;
     kernel = w4_kernel(W4Sizes{h.T, h.K, h.E, h.El, a.hidden, false});
-    return kernel == kW4Stream ? stream_launch<W, false, 4, 4>(h, down, stream) : launch_w4_tile_down(h, a, kernel, stream);
+    return kernel == kW4Stream ? stream_launch<W, false>(h, down, stream) : launch_w4_tile_down(h, a, kernel, stream);
 }
 
 template <WeightFormat F>

@@ -1,24 +1,25 @@
 // ep_few.hip -- a whole mixture-of-experts layer for a few tokens, in two kernels: from tokens and routing to tokens.
 //
 //   k_few_up     h[t,k] = silu(g) u,  g | u = x[t] W13_e^T           one workgroup: rows of one expert x 16 * NF / 2 channels of I
-//   k_few_down   out[t] = sum_k w[t,k] h[t,k] W2_e^T + bias[t]       one workgroup: all experts in use x 16 channels of H
+//   k_few_down   out[t] = sum_k w[t,k] h[t,k] W2_e^T + bias[t]       one workgroup: all experts in use x 16 or 32 channels of H
 //
 // No layout, dispatch or combine runs before or between: every workgroup finds the experts in use and their entries from the
 // routing table itself (items: up to 16 * MT entries of one expert).  Both are bound by reading the weights of the experts in
-// use, once each.  In the second the waves take items in turn, and each entry's 16 values stand in LDS until they are
-// weighted and summed in ascending k, so that nothing depends on the order in which waves finish.
+// use, once each.  In the second the waves take items in turn, and each entry's values of the channels stand in LDS until they
+// are weighted and summed in ascending k, so that nothing depends on the order in which waves finish.
 //
 // Measured: 32 tokens, 256 e4m3 experts of 7168 x 2048, top-8 (7.2 GB): 804 us (6.0 TB/s) and 447 (5.4 TB/s; 224 workgroups on 256
 // CUs).  One token, int4: 24 and 15 us (5.0 and 4.0 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 126 and 92 us
 // (4.2 and 2.9 TB/s): with some 16 rows beside a piece of 1 KiB the rows' 4 KiB from L2 bound it, not the weights.
 // Splitting all items' pieces evenly over the waves of the second kernel gained nothing (227 and 231 us in all, 1262 and 1271).
+#include "ep_few_rules.hpp"
 #include "ep_ffn.hpp"
 #include "ep_stream.hpp"
 
 namespace ep {
 namespace {
 
-constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / kWave;
+constexpr int kDownWaves = kFewWaves, kDownThreads = kDownWaves * kWave;
 
 struct Params {
     const uint16_t* x;        // [T, H]
@@ -273,11 +274,11 @@ hipError_t launch_down(const Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// ---- one token, or two ----------------------------------------------------------------------------------------------
+// ---- up to 16 entries on as many experts ----------------------------------------------------------------------------
 //
-// With no more entries than waves in a workgroup an entry is an item of its own: its expert is one load away, so the weights are
-// under way a microsecond into the kernel, and most of a wave's share of them at once.  (An expert that two tokens share is
-// read twice, the second time from a cache.)
+// An entry is an item of its own: its expert is one load away, so the weights are under way a microsecond into the kernel, and
+// most of a wave's share of them at once.  (An expert that two entries share is read twice, the second time from a cache;
+// few_by_entry says when that pays.)
 
 // acc[NF] += pieces first, first + step, ... below `end` of NF rows of pieces by one row x of K bf16; the wave's part of it stands
 // in LDS.  Every row of the instruction's first operand is x.
@@ -408,13 +409,6 @@ struct OneParts {
     }
     int lds(int NF) const { return kDownWaves * (NF * 64 + per_part * (kPieceK * 2)); }
 };
-// No more entries than waves, and rows whose parts fit beside each other.
-bool one_by_one(const Params& p) { return p.T * p.K <= kDownWaves && OneParts(p.T * p.K, p.I).lds(2) <= kOneLds; }
-
-// 32 channels a workgroup in the down projection: per byte of weights half as many loads of rows as with 16.  But 16 where that
-// leaves most of the chip without a workgroup.
-bool narrow_down(const Params& p) { return p.H < 6144; }
-
 template <class W, int NF>
 hipError_t launch_one_down(const Params& p, hipStream_t stream) {
     const OneParts o(p.T * p.K, p.I);
@@ -433,18 +427,19 @@ hipError_t launch_one(const Params& p, hipStream_t stream) {
     hipLaunchKernelGGL((k_one_up<W, NF>), dim3((unsigned)(n * cols)), dim3(kStreamThreads), up_lds, stream, p, cols, per_wave);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return narrow_down(p) ? launch_one_down<W, 1>(p, stream) : launch_one_down<W, 2>(p, stream);
+    return few_narrow(p.H) ? launch_one_down<W, 1>(p, stream) : launch_one_down<W, 2>(p, stream);
 }
 
-// Rows an expert has on average decide how many steps of 16 a workgroup takes past the weights at a time.
 template <class W, int NF>
 hipError_t by_rows(const Params& p, int E, hipStream_t stream) {
-    if (one_by_one(p)) return launch_one<W, NF>(p, stream);
-    const double rows = (double)p.T * p.K / E;
-    const hipError_t e = rows <= 12 ? launch_up<W, 1, NF>(p, stream) : rows <= 24 ? launch_up<W, 2, NF>(p, stream) : launch_up<W, 4, NF>(p, stream);
+    // (by itself only where the parts of the rows fit beside each other)
+    if (few_by_entry(p.T, p.K, E) && OneParts(p.T * p.K, p.I).lds(2) <= kOneLds) return launch_one<W, NF>(p, stream);
+    const double rows = few_rows(p.T, p.K, E);
+    const int up = few_up_steps(rows), down = few_down_steps(rows);
+    const hipError_t e = up == 1 ? launch_up<W, 1, NF>(p, stream) : up == 2 ? launch_up<W, 2, NF>(p, stream) : launch_up<W, 4, NF>(p, stream);
     if (e != hipSuccess) return e;
-    if (narrow_down(p)) return rows <= 12 ? launch_down<W, 1, 1>(p, stream) : launch_down<W, 2, 1>(p, stream);
-    return rows <= 12 ? launch_down<W, 1, 2>(p, stream) : launch_down<W, 2, 2>(p, stream);
+    if (few_narrow(p.H)) return down == 1 ? launch_down<W, 1, 1>(p, stream) : launch_down<W, 2, 1>(p, stream);
+    return down == 1 ? launch_down<W, 1, 2>(p, stream) : launch_down<W, 2, 2>(p, stream);
 }
 
 template <WeightFormat F>

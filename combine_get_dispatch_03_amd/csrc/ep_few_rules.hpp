@@ -24,8 +24,17 @@ inline bool few_by_entry(int T, int K, int E) {
     return n <= kFewWaves && (T == 1 || (n <= 8 ? n : 2 * n) <= E);
 }
 
-// 16 output channels a workgroup of the second kernel, or 32, which have half as many loads of rows per byte of weights.
-inline bool few_narrow(int H) { return H < 6144; }
+// 16 output channels a workgroup of the second kernel, or 32, which have half as many loads of rows per byte of weights.  A CU has room for
+// one workgroup: 16 as long as they are one round on the 256 CUs, otherwise 32.  us of the whole call, 16 / 32 channels, 64 experts of H x
+// 1024, top-8:
+//                     H = 2048     3584      4096       4224       4608      5632       7168       12288
+//    int4, 1 token    14 / 16    17 / 19    18 / 20    22 / 20    23 / 21    27 / 25    31 / 29    51 / 47
+//         32 tokens   68 / 80    86 / 98    91 / 102  130 / 107  132 / 110  145 / 123  163 / 141  255 / 244
+//        128 tokens  121 / 130  143 / 152  147 / 156  224 / 161  231 / 167  247 / 183  270 / 207  418 / 362
+//    bf16, 32 tokens 190 / 244  246 / 300  273 / 324  352 / 328  370 / 344  412 / 389  480 / 458  787 / 835
+// The limit is the same with e4m3 and e2m1.
+constexpr int kFewCus = 256;
+inline bool few_narrow(int H) { return H <= 16 * kFewCus; }
 
 // Steps of 16 rows that a workgroup takes past the weights at a time, by the rows that an expert has on average.  us of the whole call, 32
 // experts of 7168 x 2048, top-8, one / two / four steps in the first kernel (one in the second):

@@ -53,6 +53,6 @@ def test_steps(T, K, E, up, down):
     assert rules().steps(T, K, E) == 10 * up + down
 
 
-@pytest.mark.parametrize("H,narrow", [(8, True), (2048, True), (4096, True), (6144, False), (7168, False), (32768, False)])
+@pytest.mark.parametrize("H,narrow", [(8, True), (2048, True), (4096, True), (4104, False), (4608, False), (6144, False), (7168, False), (32768, False)])
 def test_channels(H, narrow):
     assert bool(rules().narrow(H)) == narrow

@@ -345,6 +345,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols
         up += sums[v * NF * 16 + kHalf + c];
     }
     gate *= W::kUnit;
+    // rounded as in stream_product: a token's result keeps the same roundings, however many come with it
     const __bf16 h = (__bf16)(gate * sigmoid(gate) * (up * W::kUnit));
     p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = __builtin_bit_cast(uint16_t, h);
 }

@@ -7,9 +7,11 @@
 //
 // One workgroup per token, a thread holds V 16-byte chunks of the row in registers from the first load to the last store:
 // every row of y is read once, out and normed are written once, and what a norm needs of the whole row is one sum over
-// the workgroup (lanes by register exchange, waves through LDS, in a fixed order).  Memory bounds it: without a handle (8 bytes
-// a channel) 4096 rows of 7168 take 37 us (6.3 TB/s), 4096 of 2048 13.5 us; 4096 tokens of 7168 through a handle with
-// top-8 bf16 rows, bias, residual and two outputs 118 us (704 MB, 6.0 TB/s).
+// the workgroup (lanes by register exchange, waves through LDS, in a fixed order).  Memory bounds it: 4096 tokens of 7168 through a
+// handle with top-8 bf16 rows, bias, residual and two outputs 118 us (704 MB, 6.0 TB/s); without a handle, with residual (8 bytes a
+// channel), 4096 rows of 7168 50 us (4.7 TB/s), 38 where y and residual are still in the memory-side cache.  Rows of more than 8192
+// channels (four chunks a thread, 12 of its 128 registers spilled, room for 16 such waves a CU): 4096 of 8200 98 us (2.7 TB/s), of 16384
+// 124 us (4.3 TB/s), of 32768 252 us (4.3 TB/s).
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
 
@@ -223,10 +225,11 @@ struct GradParams {
     int T, H;
 };
 
-// Rows of up to 8192 channels: one chunk a thread.  The vectors and their sums stay in registers for all of a workgroup's tokens, and
-// the next token's rows are under way while one is worked on.  With fp32 f, residual, both gradients and both outputs (14 bytes a
-// channel) 4096 rows of 7168 take 111 us (3.7 TB/s), 4096 of 4096 53 us, 4096 of 2048 33 us, with the sums over workgroups: three
-// sums over a row, one after the other, leave memory idle in between, and a CU's registers hold one workgroup of 8192 channels.
+// Rows of up to 8192 channels: one chunk a thread.  The vectors and their sums stay in registers for all of a workgroup's tokens (with
+// fp32 f four of the 128 are spilled), and the next token's rows are under way while one is worked on.  With fp32 f, residual, both
+// gradients and both outputs (14 bytes a channel) and a gate per channel 4096 rows of 7168 take 110 us (3.7 TB/s), 4096 of 4096 59 us, 4096
+// of 2048 34 us (53 and 32 where the rows are still in the memory-side cache), with the sums over workgroups: three sums over a row,
+// one after the other, leave memory idle in between, and a CU's registers hold one workgroup of 8192 channels.
 // Taking the next token's first sum together with this one's last was slower (135 us: its rows are waited for earlier).
 template <bool F_BF16>
 __global__ __launch_bounds__(1024) void k_combine_norm_backward(GradParams p) {
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(1024) void k_combine_norm_backward(GradParams p) {
 
 // Rows of more: a thread's chunks do not fit its registers, so each of the three sums over the row reads the chunks again (from L2) and
 // works out what the one before it has.  The vectors' sums are added up in the workgroup's own place in memory.  1024 rows of 32768
-// take 277 us, with eight chunks a thread in (spilled) registers 602; 1000 rows of 8200 74 and 84.
+// take 277 us (with a gate per channel 340), with eight chunks a thread in (spilled) registers 602; 1000 rows of 8200 74 and 84.
 __global__ __launch_bounds__(1024) void k_combine_norm_backward_long(GradParams p) {
     __shared__ float sums1[kMaxWaves][1], sums2[kMaxWaves][2], sums3[kMaxWaves][1];
     const int chunks = p.H / 8;

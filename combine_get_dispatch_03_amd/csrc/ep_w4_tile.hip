@@ -9,10 +9,11 @@
 // 2048, int4: 148 us, one workgroup of six stages 158).  A workgroup stays on its CU and its tiles form one stream of stages, as in
 // Bf16Tiles.
 //
-// What bounds them: with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and products
-// together, gate and up 108 us (4.5 TB/s), down 67 (3.6 TB/s).  With 1024 rows (4096 tokens, 2.89 TFLOP) the sum of the matrix unit's time
-// and the vector unit's: e2m1 in groups of 128 takes 2.56 ms (1.13 PFLOP/s), in groups of 32, four times the scalings, 3.13, int4,
-// with three times the widening, 2.75.
+// What bounds them (kernels alone): with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and
+// products together, gate and up 108 us (4.5 TB/s), down 67 (3.6 TB/s).  With 1024 rows (4096 tokens, 2.89 TFLOP) the sum of the matrix
+// unit's time and the vector unit's: e2m1 in groups of 128 takes 2.56 ms (1.13 PFLOP/s), in groups of 32, four times the scalings, 3.13,
+// int4, with three times the widening, 2.75.  Tiles of 64 rows have 128 registers, and spill 1 to 12 of them in groups of 64 and 128 (most
+// in the down product of int4 in groups of 64); of 32 and 128 rows none.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_w4.hpp"
@@ -256,7 +257,8 @@ struct Kernel {
     __device__ __forceinline__ void tile() {
         f32x4 acc[NT][MT];
         g.template run<MT>(acc);
-        // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows
+        // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows.  Both are rounded to bf16: y for
+        // good, h as the 16-bit operand of the next product (see stream_product for what that costs)
         const int wave = wave_id(), r = lane_id() & 15, odd = r & 1;
         int m_at = (lane_id() >> 4) * 4 + odd * 2;
         asm("" : "+v"(m_at));      // not to be looked into: all rows' addresses in registers (20 more) would slow the tile down by 2%

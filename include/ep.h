@@ -510,7 +510,8 @@ size_t ep_combine_norm_workspace_bytes(int num_tokens, int hidden);
  *   out           device bf16 [num_tokens, hidden], nullable; may be the residual itself.
  *   normed        device bf16 [num_tokens, hidden], nullable; needs pre_weight.
  *   kept          device fp32 [num_tokens, hidden], nullable: f, for ep_combine_norm_backward.
- *   At least one of the three is required; every row of each is written.
+ *   At least one of the three is required; every row of each is written.  But for out in the residual's place, no output may
+ *   overlap an input.  A row's squares are summed in fp32: they are finite for |f| and |r| up to 1e17 at any width.
  */
 ep_status_t ep_combine_norm(ep_handle_t handle, const void* y, int hidden, int64_t y_rows, const float* topk_weights,
                             const void* bias, const ep_norm_args_t* norm, void* out, void* normed, float* kept, void* stream);

@@ -685,7 +685,7 @@ def ep_combine_backward(handle: Handle, grad_out, y=None, topk_weights=None, gra
 
 
 def ep_expert_ffn_workspace_bytes(handle: Handle, hidden, intermediate, backward=False) -> int:
-    """Bytes of workspace of ep_expert_ffn (or, with backward, of either pass) for the handle's rows."""
+    """Bytes of workspace of ep_expert_ffn and ep_expert_ffn_w4 (or, with backward, of either pass) for the handle's rows."""
     return _ffn_bytes(handle.recv_capacity, hidden, intermediate, bool(backward))
 
 

@@ -338,6 +338,9 @@ FfnWorkspace ffn_workspace(int64_t cap, int inter, bool backward) {
     return w;
 }
 
+// Of the block with 4-bit weights: h [cap] in 32 bits a channel.
+size_t w4_workspace(int64_t cap, int inter) { return align_up((size_t)(cap > 0 ? cap : 1) * (size_t)h_pitch(inter) * 2, 256); }
+
 ep_status_t check_scratch(const void* workspace, size_t have, size_t need) {
     if (workspace == nullptr) return fail(EP_ERR_INVALID_ARG, "workspace is NULL");
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -669,7 +672,8 @@ ep_status_t ep_combine_backward(ep_handle_t handle, const void* grad_out, int hi
 
 size_t ep_expert_ffn_workspace_bytes(int64_t recv_capacity, int hidden, int intermediate, int backward) {
     if (recv_capacity < 0 || recv_capacity > INT32_MAX || ffn_shape(hidden, intermediate, false) != nullptr) return 0;
-    return ffn_workspace(recv_capacity, intermediate, backward != 0).bytes;
+    const size_t own = ffn_workspace(recv_capacity, intermediate, backward != 0).bytes, w4 = w4_workspace(recv_capacity, intermediate);
+    return own > w4 ? own : w4;
 }
 
 ep_status_t ep_expert_ffn(ep_handle_t handle, const void* recv_x, const float* recv_x_scales, ep_dtype_t dtype, int hidden,
@@ -836,7 +840,7 @@ ep_status_t ep_expert_ffn_w4(ep_handle_t handle, const void* recv_x, int hidden,
             return fail(EP_ERR_INVALID_ARG, "recv_x must be non-NULL and 16-byte aligned");
         if (const char* why = weights_pointers(w13, w2)) return fail(EP_ERR_INVALID_ARG, "%s", why);
         if (y == nullptr || !aligned16(y)) return fail(EP_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned");
-        const ep_status_t st = check_scratch(workspace, workspace_bytes, ffn_workspace(h->cap, intermediate, false).bytes);
+        const ep_status_t st = check_scratch(workspace, workspace_bytes, w4_workspace(h->cap, intermediate));
         if (st != EP_OK) return st;
     }
     const W4Args a{recv_x, WeightTensor{w13->values, w13->scales}, WeightTensor{w2->values, w2->scales}, y, static_cast<uint16_t*>(workspace),

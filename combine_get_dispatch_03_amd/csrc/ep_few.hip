@@ -8,9 +8,9 @@
 // use, once each.  In the second the waves take items in turn, and each entry's values of the channels stand in LDS until they
 // are weighted and summed in ascending k, so that nothing depends on the order in which waves finish.
 //
-// Measured: 32 tokens, 256 e4m3 experts of 7168 x 2048, top-8 (7.2 GB): 804 us (6.0 TB/s) and 447 (5.4 TB/s; 224 workgroups on 256
-// CUs).  One token, int4: 24 and 15 us (5.0 and 4.0 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 126 and 92 us
-// (4.2 and 2.9 TB/s): with some 16 rows beside a piece of 1 KiB the rows' 4 KiB from L2 bound it, not the weights.
+// Measured: 32 tokens, 256 e4m3 experts of 7168 x 2048, top-8 (7.2 GB): 808 us (6.0 TB/s) and 465 (5.2 TB/s; 224 workgroups on 256
+// CUs).  One token, int4: 24 and 17 us (5.0 and 3.6 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 128 and 98 us
+// (4.1 and 2.7 TB/s): with some 16 rows beside a piece of 1 KiB the rows' 4 KiB from L2 bound it, not the weights.
 // Splitting all items' pieces evenly over the waves of the second kernel gained nothing (227 and 231 us in all, 1262 and 1271).
 #include "ep_few_rules.hpp"
 #include "ep_ffn.hpp"
@@ -27,7 +27,7 @@ struct Params {
     const float* topk_w;      // [T, K] or nullptr
     const uint16_t* bias;
     WeightArgs w13, w2;       // [El, 2 I, H], [El, H, I]
-    uint16_t* h;              // workspace [T * K, row_pitch(I)]
+    uint16_t* h;              // workspace [T * K, h_pitch(I)] (ep_h_rows.hpp), or [T * K, row_pitch(I)] where entries stand by themselves
     uint16_t* out;            // [T, H]
     int T, K, H, I, lo, El;
 };
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kStreamThreads, MT == 4 ? 2 : 4) void k_few_up(Para
     const Items it = find_items<16 * MT, kStreamThreads, false>(p, smem, max_items, cursors, item);
     if (item >= it.total) return;
     const int first = it.first[item], count = it.count[item], r = lane_id() & 15;
-    RowFragments<W, MT> rows;
+    RowFragments<W, MT, false> rows;
     rows.init(p.x, p.H);
 #pragma unroll
     for (int a = 0; a < MT; ++a) {
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kStreamThreads, MT == 4 ? 2 : 4) void k_few_up(Para
         rows.place(a, there, (uint32_t)(it.order[first + (there ? a * 16 + r : 0)] / p.K) * (uint32_t)(p.H * 2));
     }
     stream_product<W, true, MT, NF>(p.w13, __builtin_amdgcn_readfirstlane(it.expert[item]), p.I, p.H, n0, rows, count, reinterpret_cast<float*>(smem + lists),
-                                       [&](int m) { return p.h + (int64_t)it.order[first + m] * row_pitch(p.I); });
+                                       [&](int m) { return p.h + (int64_t)it.order[first + m] * h_pitch(p.I); });
 }
 
 // Items (and, of few items, parts of their k) go to the waves in turn; parts is a power of two.
@@ -199,12 +199,12 @@ __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_ite
     for (int i = wave; i < work; i += kDownWaves) {
         const int item = i >> log_parts, part = i & (parts - 1);
         const int expert = __builtin_amdgcn_readfirstlane(it.expert[item]), first = it.first[item], count = it.count[item];
-        RowFragments<W, MT> rows;
+        RowFragments<W, MT, true> rows;
         rows.init(p.h, p.I);
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
             const bool there = a * 16 + r < count;
-            rows.place(a, there, (uint32_t)it.order[first + (there ? a * 16 + r : 0)] * (uint32_t)(row_pitch(p.I) * 2));
+            rows.place(a, there, (uint32_t)it.order[first + (there ? a * 16 + r : 0)] * (uint32_t)(h_pitch(p.I) * 2));
         }
         typename W::template Rows<NF> w;
         w.init(p.w2, expert, n0);
@@ -216,16 +216,17 @@ __global__ __launch_bounds__(kDownThreads) void k_few_down(Params p, int max_ite
 #pragma unroll
             for (int a = 0; a < MT; ++a) acc[b][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        stream_pieces<W, MT, NF>(w, rows, part, parts, pieces, acc);
+        stream_pieces(w, rows, part, parts, pieces, acc);
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int m = a * 16 + g * 4 + j;
+                const float unit = rows.unit(a, j);
                 if (m >= count) continue;
                 float* to = values + (part * n + it.order[first + m]) * kCols + r;
 #pragma unroll
-                for (int b = 0; b < NF; ++b) to[b * 16] = acc[b][a][j];
+                for (int b = 0; b < NF; ++b) to[b * 16] = acc[b][a][j] * unit;
             }
     }
     __syncthreads();
@@ -274,41 +275,81 @@ hipError_t launch_down(const Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// ---- up to 16 entries on as many experts ----------------------------------------------------------------------------
+// ---- one token, or up to 16 entries on enough experts ---------------------------------------------------------------
 //
 // An entry is an item of its own: its expert is one load away, so the weights are under way a microsecond into the kernel, and
 // most of a wave's share of them at once.  (An expert that two entries share is read twice, the second time from a cache;
 // few_by_entry says when that pays.)
+//
+// Every row of the instruction's first operand is the entry's, so half of them can be second parts, at no cost.  h takes 16 bits in
+// the workspace: eight channels share the exponent of the largest, E, each has 15 bits m of m 2^(E - 140) (2^-14 of the largest at most is
+// lost), and the lowest bit of the i-th holds bit i of E.  Infinities and NaN: E = 255, m = 1, -1 and 2, and 0 beside them.
 
-// acc[NF] += pieces first, first + step, ... below `end` of NF rows of pieces by one row x of K bf16; the wave's part of it stands
-// in LDS.  Every row of the instruction's first operand is x.
-template <class W, int NF>
+// Channel c of the lanes' eight; all of them call it.
+__device__ __forceinline__ uint16_t shared_exponent(float v, int c) {
+    const uint32_t size = size_bits(v);
+    const int e = (int)(max_bits<8>(size) >> 23);
+    int m;
+    if (e == 255) m = size > 0x7f800000u ? 2 : size < 0x7f800000u ? 0 : v < 0.0f ? -1 : 1;
+    else m = (int)__builtin_amdgcn_fmed3f(rintf(ldexpf(v, 140 - e)), -16383.0f, 16383.0f);
+    return (uint16_t)(m * 2 | (e >> (c & 7) & 1));
+}
+// Eight channels' two parts.
+__device__ __forceinline__ void two_parts(i32x4 q, i32x4* first, i32x4* second) {
+    const uint32_t t = (uint32_t)((q[0] & 0x10001) | (q[1] & 0x10001) << 2 | (q[2] & 0x10001) << 4 | (q[3] & 0x10001) << 6);
+    const int e = (int)((t & 0x55u) | (t >> 15 & 0xaau));
+    const bool special = ballot(e == 255) != 0;
+    const auto value = [&](int m) {
+        float v = ldexpf((float)m, e - 140);
+        if (special && e == 255) v = m == 0 ? 0.0f : m == 2 ? __builtin_nanf("") : m > 0 ? __builtin_inff() : -__builtin_inff();
+        return v;
+    };
+    const auto rest = [&](float v) { return special ? rest_of(v) : v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u); };
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float a = value((int)((uint32_t)q[d] << 16) >> 17), b = value(q[d] >> 17);
+        (*first)[d] = upper_halves(a, b);
+        (*second)[d] = (int)pack_bf16x2(rest(a), rest(b));
+    }
+}
+
+// acc[NF] += pieces first, first + step, ... below `end` of NF rows of pieces by one row x of K channels; the wave's part of it stands
+// in LDS, up to `room` pieces at a time.  PARTS 1: bf16, and every row of the instruction's first operand is x.  PARTS 2: as
+// shared_exponent leaves them, and even rows are first parts, odd ones second.
+template <class W, int PARTS, int NF>
 __device__ __forceinline__ void one_row(const typename W::template Rows<NF>& w, const uint16_t* x, int K, int first, int step, int end,
-                                        char* lds, f32x4 (&acc)[NF][1]) {
+                                        char* lds, int room, f32x4 (&acc)[NF][1]) {
     Buffer row;
     row.init(x);
-    const int count = (end - first + step - 1) / step;
-    for (int c = lane_id(); c < count * 16; c += kWave) {      // 16 bytes
-        const int k = (first + c / 16 * step) * kPieceK + c % 16 * 8;
-        *reinterpret_cast<i32x4*>(lds + c * 16) = load16(row.resource(true), k < K ? (uint32_t)k * 2 : kNoElement, 0);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int count = (end - first + step - 1) / step, lane = lane_id();
     typename W::Raw raw[NF];
     auto load = [&](int i) {
 #pragma unroll
         for (int b = 0; b < NF; ++b) raw[b] = w.load(b, first + i * step, i < count);
     };
-    load(0);
-    const char* at = lds + W::k_of(0, lane_id() >> 4) * 2;
-    for (int i = 0; i < count; ++i, at += kPieceK * 2) {
-        i32x4 v[1][4];
+    for (int i0 = 0; i0 < count; i0 += room) {
+        const int n = count - i0 < room ? count - i0 : room;
+        for (int c = lane; c < n * 16; c += kWave) {      // 16 bytes
+            const int k = (first + (i0 + c / 16) * step) * kPieceK + c % 16 * 8;
+            const i32x4 q = load16(row.resource(true), k < K ? (uint32_t)k * 2 : kNoElement, 0);
+            i32x4* to = reinterpret_cast<i32x4*>(lds + c * 16);
+            if constexpr (PARTS == 1) *to = q;
+            else two_parts(q, to, to + room * 16);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (i0 == 0) load(0);
+        const char* at = lds + W::k_of(0, lane >> 4) * 2 + (PARTS == 2 && (lane & 1) ? room * (kPieceK * 2) : 0);
+        for (int i = i0; i < i0 + n; ++i, at += kPieceK * 2) {
+            i32x4 v[1][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[0][j] = *reinterpret_cast<const i32x4*>(at + W::k_of(j, 0) * 2);
-#pragma unroll
-        for (int b = 0; b < NF; ++b) add_piece<W, 1>(raw[b], v, acc[b]);
-        load(i + 1);
+            for (int j = 0; j < 4; ++j) v[0][j] = *reinterpret_cast<const i32x4*>(at + W::k_of(j, 0) * 2);
+            add_pieces<W, false>(raw, v, acc);
+            load(i + 1);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");      // before the next of them come
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -330,7 +371,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols
     }
     float* sums = reinterpret_cast<float*>(smem);
     char* mine = smem + kStreamWaves * NF * 64 + wave * per_wave * (kPieceK * 2);
-    if (wave < pieces_of(p.H)) one_row<W, NF>(w, p.x + (int64_t)(entry / p.K) * p.H, p.H, wave, kStreamWaves, pieces_of(p.H), mine, acc);
+    if (wave < pieces_of(p.H)) one_row<W, 1, NF>(w, p.x + (int64_t)(entry / p.K) * p.H, p.H, wave, kStreamWaves, pieces_of(p.H), mine, per_wave, acc);
     if (lane_id() < 16) {
 #pragma unroll
         for (int b = 0; b < NF; ++b) sums[wave * NF * 16 + b * 16 + lane_id()] = acc[b][0][0];
@@ -345,19 +386,17 @@ __global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols
         up += sums[v * NF * 16 + kHalf + c];
     }
     gate *= W::kUnit;
-    // rounded as in stream_product: a token's result keeps the same roundings, however many come with it
-    const __bf16 h = (__bf16)(gate * sigmoid(gate) * (up * W::kUnit));
-    p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = __builtin_bit_cast(uint16_t, h);
+    p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = shared_exponent(gate * sigmoid(gate) * (up * W::kUnit), c);
 }
 
-// Wave i takes part i % parts of entry i / parts: per_part pieces.
+// Waves take parts of entries in turn, i % parts of i / parts, `room` pieces of them at a time.
 template <class W, int NF>
-__global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, int per_part) {
+__global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, int room) {
     constexpr int kCols = NF * 16;
-    extern __shared__ __align__(16) char smem[];      // [waves][kCols] sums, then each wave's part of h
-    __shared__ float weight[kDownWaves];
-    __shared__ int valid[kDownWaves];
-    const int n0 = blockIdx.x * kCols, wave = wave_id(), entry = wave / parts, part = wave % parts, n = p.T * p.K;
+    extern __shared__ __align__(16) char smem[];      // [entries][parts][kCols] sums, then each wave's part of h
+    __shared__ float weight[kMaxTopk];
+    __shared__ int valid[kMaxTopk];
+    const int n0 = blockIdx.x * kCols, wave = wave_id(), n = p.T * p.K;
     float* sums = reinterpret_cast<float*>(smem);
     // what the sum over k needs, asked for before the weights
     const int t = threadIdx.x / kCols, c = threadIdx.x % kCols;
@@ -368,8 +407,9 @@ __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, 
         valid[threadIdx.x] = local_expert(p, threadIdx.x) >= 0;
         weight[threadIdx.x] = W::kUnit * (p.topk_w ? p.topk_w[threadIdx.x] : 1.0f);
     }
-    const int expert = entry < n ? __builtin_amdgcn_readfirstlane(local_expert(p, entry)) : -1;
-    if (expert >= 0) {
+    for (int i = wave; i < n * parts; i += kDownWaves) {
+        const int entry = i / parts, part = i % parts, expert = __builtin_amdgcn_readfirstlane(local_expert(p, entry));
+        if (expert < 0) continue;
         typename W::template Rows<NF> w;
         w.init(p.w2, expert, n0);
         f32x4 acc[NF][1];
@@ -379,11 +419,11 @@ __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, 
             w.place(b, exist > 0 ? b * 16 : 0, exist);
             acc[b][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        char* mine = smem + kDownWaves * kCols * 4 + wave * per_part * (kPieceK * 2);
-        if (part < pieces_of(p.I)) one_row<W, NF>(w, p.h + (int64_t)entry * row_pitch(p.I), p.I, part, parts, pieces_of(p.I), mine, acc);
+        char* mine = smem + n * parts * kCols * 4 + wave * room * (kPieceK * 4);
+        one_row<W, 2, NF>(w, p.h + (int64_t)entry * row_pitch(p.I), p.I, part, parts, pieces_of(p.I), mine, room, acc);
         if (lane_id() < 16) {
 #pragma unroll
-            for (int b = 0; b < NF; ++b) sums[wave * kCols + b * 16 + lane_id()] = acc[b][0][0];
+            for (int b = 0; b < NF; ++b) sums[i * kCols + b * 16 + lane_id()] = acc[b][0][0] + acc[b][0][1];
         }
     }
     __syncthreads();
@@ -399,23 +439,25 @@ __global__ __launch_bounds__(kDownThreads) void k_one_down(Params p, int parts, 
     p.out[at] = __builtin_bit_cast(uint16_t, (__bf16)(y + bias));
 }
 
-constexpr int kOneLds = 96 << 10;
-// Pieces of a wave's part of h, and how many parts there are.
+// Parts of an entry's pieces, one at least, and how many of them a wave has in LDS: up to 16, 128 KB of a workgroup's.
 struct OneParts {
-    int parts, per_part;
+    int parts, room;
     OneParts(int entries, int I) {
-        const int pieces = pieces_of(I);
-        parts = kDownWaves / entries < pieces ? kDownWaves / entries : pieces;
-        per_part = (pieces + parts - 1) / parts;
+        const int pieces = pieces_of(I), most = entries < kDownWaves ? kDownWaves / entries : 1;
+        parts = most < pieces ? most : pieces;
+        room = (pieces + parts - 1) / parts;
+        room = room < 16 ? room : 16;
     }
-    int lds(int NF) const { return kDownWaves * (NF * 64 + per_part * (kPieceK * 2)); }
+    int lds(int entries, int NF) const { return entries * parts * NF * 64 + kDownWaves * room * (kPieceK * 4); }
 };
+
 template <class W, int NF>
 hipError_t launch_one_down(const Params& p, hipStream_t stream) {
-    const OneParts o(p.T * p.K, p.I);
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_down<W, NF>), o.lds(NF));
+    const int n = p.T * p.K;
+    const OneParts o(n, p.I);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(&k_one_down<W, NF>), o.lds(n, NF));
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_one_down<W, NF>), dim3((p.H + NF * 16 - 1) / (NF * 16)), dim3(kDownThreads), o.lds(NF), stream, p, o.parts, o.per_part);
+    hipLaunchKernelGGL((k_one_down<W, NF>), dim3((p.H + NF * 16 - 1) / (NF * 16)), dim3(kDownThreads), o.lds(n, NF), stream, p, o.parts, o.room);
     return hipGetLastError();
 }
 
@@ -433,8 +475,7 @@ hipError_t launch_one(const Params& p, hipStream_t stream) {
 
 template <class W, int NF>
 hipError_t by_rows(const Params& p, int E, hipStream_t stream) {
-    // (by itself only where the parts of the rows fit beside each other)
-    if (few_by_entry(p.T, p.K, E) && OneParts(p.T * p.K, p.I).lds(2) <= kOneLds) return launch_one<W, NF>(p, stream);
+    if (few_by_entry(p.T, p.K, E)) return launch_one<W, NF>(p, stream);
     const double rows = few_rows(p.T, p.K, E);
     const int up = few_up_steps(rows), down = few_down_steps(rows);
     const hipError_t e = up == 1 ? launch_up<W, 1, NF>(p, stream) : up == 2 ? launch_up<W, 2, NF>(p, stream) : launch_up<W, 4, NF>(p, stream);
@@ -452,7 +493,10 @@ hipError_t by_group(const Params& p, int E, int group, hipStream_t stream) {
 
 }  // namespace
 
-size_t few_workspace_bytes(int T, int K, int inter) { return (size_t)(T * K > 0 ? T * K : 1) * row_pitch(inter) * sizeof(uint16_t); }
+// (one token's entries stand by themselves)
+size_t few_workspace_bytes(int T, int K, int inter) {
+    return (size_t)(T * K > 0 ? T * K : 1) * (T > 1 ? h_pitch(inter) : row_pitch(inter)) * sizeof(uint16_t);
+}
 
 hipError_t launch_few(const FewArgs& a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;

@@ -21,7 +21,7 @@ constexpr int kFewWaves = 16;      // of a workgroup of the second kernel: as ma
 // of 8 15.7 / 15.3.  One token's entries have an expert each; of several tokens enough experts for few to be shared.
 inline bool few_by_entry(int T, int K, int E) {
     const int n = T * K;
-    return n <= kFewWaves && (T == 1 || (n <= 8 ? n : 2 * n) <= E);
+    return T == 1 || (n <= kFewWaves && (n <= 8 ? n : 2 * n) <= E);
 }
 
 // 16 output channels a workgroup of the second kernel, or 32, which have half as many loads of rows per byte of weights.  A CU has room for

@@ -113,6 +113,8 @@ hipError_t launch_combine_backward(const Handle& h, const CombineBackwardArgs& a
 
 // Row pitch, in elements, of the feed-forward block's bf16 workspace rows: whole 128-byte lines, whatever the width.
 constexpr int row_pitch(int width) { return (width + 63) / 64 * 64; }
+// The same of rows of h beside numbers (ep_h_rows.hpp).
+constexpr int h_pitch(int inter) { return row_pitch(2 * inter); }
 
 struct FfnArgs {
     const void* x;             // bf16 or e4m3 [rows, hidden]
@@ -181,7 +183,7 @@ struct W4Args {
     const void* x;             // bf16 [rows, hidden]
     WeightTensor w13, w2;
     void* y;                   // bf16 [rows, hidden]
-    uint16_t* h;               // workspace: bf16 [cap, row_pitch(inter)]
+    uint16_t* h;               // workspace [cap, h_pitch(inter)]
     int hidden, inter;
     bool int4;
     int group;
@@ -196,7 +198,7 @@ struct FewArgs {
     const void* bias;          // bf16 [T, hidden] or nullptr
     WeightTensor w13, w2;
     void* out;                 // bf16 [T, hidden]
-    void* workspace;           // bf16 [T * K, row_pitch(inter)]
+    void* workspace;           // few_workspace_bytes
     WeightFormat format;
     int group;                 // 4-bit
     int T, K, E, R, rank, hidden, inter;

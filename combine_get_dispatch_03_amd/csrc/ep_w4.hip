@@ -56,7 +56,7 @@ constexpr int kStreamChannels = kStreamPieces * (UP ? 8 : 16);
 template <class W, bool UP, int MT>
 __device__ __forceinline__ void rows_product(const Params& p, const RowTile& t, int n0, float* sums) {
     const int r = lane_id() & 15;
-    RowFragments<W, MT> rows;
+    RowFragments<W, MT, !UP> rows;
     rows.init(p.s + (int64_t)t.row0 * p.sp, p.K);
 #pragma unroll
     for (int a = 0; a < MT; ++a) rows.place(a, a * 16 + r < t.rows, (uint32_t)(a * 16 + r) * (uint32_t)(p.sp * 2));
@@ -93,9 +93,9 @@ hipError_t stream_launch(const Handle& h, const Params& p, hipStream_t stream) {
 template <class W>
 hipError_t ffn(const Handle& h, const W4Args& a, hipStream_t stream) {
     const Params up{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, WeightArgs{(const char*)a.w13.values, (const char*)a.w13.scales, 2 * a.inter, a.hidden},
-                    a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
+                    a.h, a.inter, a.hidden, a.hidden, h_pitch(a.inter)};
     const Params down{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
-                      (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
+                      (uint16_t*)a.y, a.hidden, a.inter, h_pitch(a.inter), a.hidden};
     W4Kernel kernel = w4_kernel(W4Sizes{h.T, h.K, h.E, h.El, a.inter, true});
     const hipError_t e = kernel == kW4Stream ? stream_launch<W, true>(h, up, stream) : launch_w4_tile_up(h, a, kernel, stream);
     if (e != hipSuccess) return e;

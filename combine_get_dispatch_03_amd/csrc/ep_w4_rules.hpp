@@ -13,20 +13,26 @@ struct W4Sizes {
     bool up;       // gate and up: a tile holds 128 of them, otherwise 256
 };
 
-// us of the whole call (int4 in groups of 64, uniform routing), streamed / tiles of 32 / of 64 / of 128 rows, at so many rows per
-// expert; in brackets the tiles of 32 rows of the gate and up product:
-//                                       1 or 2 rows          12                   40                   64                   128
-//    8 experts of 1024 x 512 (32)     10 / 18 / 19 / 22    11 / 18 / 18 / 21    16 / 21 / 23 / 27    19 / 21 / 26 / 30    26 / 21 / 26 / 35
-//   16 of 2048 x 768 (96)             14 / 25 / 26 / 32    19 / 29 / 29 / 32    29 / 31 / 34 / 42    48 / 36 / 39 / 46    77 / 61 / 47 / 57
-//    8 of 7168 x 2048 (128)           39 / 60 / 65 / 78    46 / 61 / 65 / 80    78 / 88 / 87 / 104  155 / 145 / 112 / 120 225 / 231 / 175 / 175
-//   20 of 2112 x 1344 (198, 220)      26 / 29 / 30 / 38    37 / 35 / 34 / 39    58 / 56 / 42 / 49    92 / 85 / 72 / 60   132 / 107 / 90 / 130
-//   64 of 2048 x 768 (384)            34 / 30 / 32 / 60    53 / 45 / 44 / 62    89 / 85 / 61 / 79   140 / 100 / 106 / 94 233 / 183 / 141 / 158
-//   64 of 4096 x 1408 (704)           96 / 89 / 91 / 159  154 / 148 / 147 / 164 253 / 244 / 196 / 219 385 / 314 / 254 / 253 662 / 543 / 439 / 429
-// 32 of 7168 x 2048, int4 in groups of 128: 2 rows 164 / 155 / 167 / 180, 16 rows 197 / 166 / 187 / 190, 24 rows 222 / 194 / 189 / 210.
-// Tiles of 64 / of 128 rows there: 40 rows 229 / 268, 56 rows 297 / 278, 96 rows 391 / 365, 128 rows 510 / 538, 192 rows 689 / 647, 256 rows
-// 870 / 792; 16 of 2048 x 768: 80 rows 36 / 47, 160 rows 61 / 52, 400 rows 119 / 110; 4 of 4096 x 1408: 256 rows 75 / 92, 400 rows 104 / 95.
-// us of the down product, streamed / 32 / 64: 180 tiles (20 of 2112 x 1344), 12 rows 14.1 / 14.2 / 14.4, 40 rows 22.5 / 23.1 / 17.4; 224
-// tiles (8 of 7168 x 2048), 1 row 14.8 / 16.2 / 16.8, 12 rows 18.6 / 17.3 / 17.8.
+// us of the whole call (int4 in groups of 64, uniform routing), one product streamed / on tiles of 32 / of 64 / of 128 rows while the other is on tiles
+// of 64, at so many rows per expert; in brackets the busy experts' tiles:
+//   gate and up                          1                   12                  40                  64                  128
+//    8 experts of 1024 x 512 (32)     16 / 20 / 20 / 23   17 / 21 / 21 / 23   23 / 25 / 27 / 29   25 / 25 / 29 / 33   29 / 26 / 29 / 36
+//   16 of 2048 x 768 (96)             22 / 28 / 29 / 33   25 / 31 / 31 / 34   34 / 34 / 38 / 42   44 / 36 / 41 / 47   68 / 53 / 48 / 60
+//    8 of 7168 x 2048 (128)           50 / 68 / 76 / 81   54 / 69 / 78 / 82   82 / 80 / 91 / 103 138 / 125 / 112 / 131 211 / 222 / 182 / 182
+//   20 of 2112 x 1344 (220)           35 / 35 / 36 / 40   44 / 40 / 42 / 43   61 / 54 / 47 / 51   91 / 85 / 72 / 66  123 / 96 / 102 / 113
+//   64 of 2048 x 768 (384)            42 / 40 / 41 / 49   56 / 53 / 51 / 61   84 / 87 / 68 / 84  129 / 102 / 110 / 106 201 / 170 / 140 / 169
+//   64 of 4096 x 1408 (704)          101 / 90 / 90 / 113 149 / 152 / 150 / 156 226 / 220 / 197 / 209 334 / 295 / 246 / 254 572 / 499 / 428 / 424
+//   32 of 7168 x 2048, groups of 128 (512): 2 rows 152 / 142 / 139 / 166, 16 rows 184 / 162 / 158 / 174, 24 rows 205 / 198 / 171 / 194, 64 rows
+//   396 / 351 / 325 / 288, 96 rows 534 / 459 / 373 / 356, 128 rows 683 / 576 / 510 / 489, 256 rows 1227 / 1012 / 880 / 814.
+//   down
+//    8 of 1024 x 512 (32)             15 / 20 / 20 / 21   16 / 20 / 21 / 21   22 / 25 / 27 / 27   24 / 26 / 29 / 30   28 / 26 / 29 / 31
+//   16 of 2048 x 768 (128)            24 / 27 / 29 / 29   26 / 29 / 31 / 31   35 / 35 / 38 / 38   48 / 41 / 41 / 42   59 / 53 / 48 / 45
+//   20 of 2112 x 1344 (180)           28 / 33 / 36 / 36   38 / 38 / 42 / 40   55 / 49 / 47 / 48   78 / 65 / 72 / 66  125 / 108 / 102 / 108
+//    8 of 7168 x 2048 (224)           70 / 71 / 76 / 76   77 / 74 / 78 / 78  103 / 95 / 91 / 93  126 / 118 / 112 / 103 206 / 169 / 182 / 178
+//   64 of 2048 x 768 (512)            41 / 38 / 41 / 43   56 / 47 / 51 / 50   86 / 71 / 68 / 69  136 / 109 / 110 / 102 186 / 142 / 140 / 131
+//   64 of 4096 x 1408 (1024)          82 / 80 / 90 / 87  163 / 142 / 150 / 154 260 / 217 / 197 / 211 315 / 250 / 246 / 240 576 / 458 / 428 / 422
+//   32 of 7168 x 2048, groups of 128 (896): 2 rows 134 / 130 / 139 / 148, 16 rows 167 / 154 / 158 / 169, 24 rows 193 / 166 / 171 / 182, 64 rows
+//   401 / 335 / 325 / 321, 128 rows 657 / 528 / 510 / 498, 256 rows 1175 / 945 / 880 / 844.
 //   Streaming spreads a few tiles' work over idle CUs; tiles share the rows over 256 channels. A tile of 64 rows has twice a
 // tile of 32's work, so there should be enough of them. A tile of 128 rows widens its codes once for twice the rows, but has a CU to
 // itself where two of 64 share one: it is better where there is more than a round of work and the experts' rows fill it, or half of

@@ -9,11 +9,13 @@
 // 2048, int4: 148 us, one workgroup of six stages 158).  A workgroup stays on its CU and its tiles form one stream of stages, as in
 // Bf16Tiles.
 //
-// What bounds them (kernels alone): with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and
-// products together, gate and up 108 us (4.5 TB/s), down 67 (3.6 TB/s).  With 1024 rows (4096 tokens, 2.89 TFLOP) the sum of the matrix
-// unit's time and the vector unit's: e2m1 in groups of 128 takes 2.56 ms (1.13 PFLOP/s), in groups of 32, four times the scalings, 3.13,
-// int4, with three times the widening, 2.75.  Tiles of 64 rows have 128 registers, and spill 1 to 12 of them in groups of 64 and 128 (most
-// in the down product of int4 in groups of 64); of 32 and 128 rows none.
+// h goes out in fp16 beside numbers (ep_h_rows.hpp) and comes back to the down product in fp16, a row in one unit.
+//
+// What bounds them: with 32 rows an expert (128 tokens, 32 such experts, int4 in groups of 128) bytes, widening and products together,
+// gate and up 110 us (4.5 TB/s), down 68 (3.6 TB/s). With 1024 rows (4096 tokens, 2.89 TFLOP) the sum of the matrix unit's time and the
+// vector unit's: the whole call with e2m1 in groups of 128 takes 2.65 ms (1.09 PFLOP/s), in groups of 32, four times the scalings, 3.2, with
+// int4 in groups of 128, three times the widening, 2.85. Tiles of 64 rows have 128 registers and spill up to 14 of them in the down product
+// of groups of 64 and 128 (and one for gate and up); tiles of 32 and 128 rows none.
 #include "ep_expert_tiles.hpp"
 #include "ep_ffn.hpp"
 #include "ep_w4.hpp"
@@ -26,12 +28,37 @@ struct Params {
     const int32_t* cnt;
     const int32_t* psum;
     int El;
-    const uint16_t* s;     // rows
+    const uint16_t* s;     // rows: x, or h with one number a row
     WeightArgs w;
-    uint16_t* out;
+    uint16_t* out;         // h, or y
     int N, K;              // channels of a projection's output, of its input
     int sp, op;            // elements between rows of s and of out
 };
+
+// h's rows go to LDS as they are, so a row needs one number for all of its blocks before: a wave looks at a row's numbers, brings
+// blocks with others to the largest where there are any, and leaves the row's unit, which the tiles multiply their sums by.  1024 rows 4.6
+// us, 32768 rows of 2048 channels 11.5 us (looking at all rows of the workspace, without finding those that experts have: 8.0 and 14).
+__device__ __forceinline__ float* row_unit(uint16_t* row, int I) { return reinterpret_cast<float*>(row + I + numbers_of(I)); }
+constexpr int kUnitRows = 4;
+__global__ __launch_bounds__(kUnitRows * kWave) void k_one_number(const int32_t* cnt, const int32_t* psum, int El, uint16_t* h, int I) {
+    const RowTiles<kUnitRows> tiles(cnt, psum, El);
+    const int64_t tile = block_id();
+    if (tile >= tiles.total) return;
+    const RowTile t = tiles.find((int)tile);
+    if (wave_id() >= t.rows) return;
+    uint16_t* row = h + (int64_t)(t.row0 + wave_id()) * h_pitch(I);
+    const uint32_t* numbers = reinterpret_cast<const uint32_t*>(row + I);      // two each: I is a multiple of 32
+    NumberRange range;
+    for (int i = lane_id(); i < I / (2 * kShared); i += kWave) range.add(numbers[i], 2);
+    const uint32_t most = max_bits<16>((uint32_t)range.top());
+    const int top = max(max(readlane((int)most, 0), readlane((int)most, 16)), max(readlane((int)most, 32), readlane((int)most, 48)));
+    if (ballot(range.low() < top))
+        for (int c = lane_id(); c < I / 8; c += kWave) {
+            u32x4* at = reinterpret_cast<u32x4*>(row) + c;
+            *at = bring_to(*at, (int)row[I + c / (kShared / 8)], top);
+        }
+    if (lane_id() == 0) *row_unit(row, I) = shared_unit(top);
+}
 
 // Rows with 128 k of each per stage, ROWS of them: 256 bytes, whose 16-byte chunks are permuted by the row number so that a
 // fragment read (16 rows, 16 bytes at one place of each) is spread over all banks.
@@ -77,7 +104,8 @@ struct WideRows {
     }
 };
 
-template <WeightFormat F, int S, int BM>
+// F16: the rows are fp16, otherwise bf16.
+template <WeightFormat F, int S, int BM, bool F16>
 struct W4Tiles {
     static constexpr int kBM = BM, kCodes = 16;                                      // 16 rows of pieces: 256 channels
     static constexpr int NT = kCodes / kGemmWaves, kSteps = BM / 16;                 // of a wave: rows of pieces, 16-row steps
@@ -193,10 +221,17 @@ struct W4Tiles {
                     for (int a = 0; a < MT; ++a) sv[a] = read_kc(ls, (s_at ^ (j * 64)) + a * 4096);
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        const bf16x8 fv = widen_codes<F == kWeightsInt4>((uint32_t)code[b][j]);
+                        if constexpr (F16) {
+                            const f16x8 fv = widen_codes16<F == kWeightsInt4>((uint32_t)code[b][j]);
 #pragma unroll
-                        for (int a = 0; a < MT; ++a)
-                            part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sv[a], fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
+                            for (int a = 0; a < MT; ++a)
+                                part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, sv[a]), fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
+                        } else {
+                            const bf16x8 fv = widen_codes<F == kWeightsInt4>((uint32_t)code[b][j]);
+#pragma unroll
+                            for (int a = 0; a < MT; ++a)
+                                part[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sv[a], fv, j == grp * kPer ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[b][a], 0, 0, 0);
+                        }
                     }
                 }
                 __builtin_amdgcn_s_setprio(0);
@@ -221,7 +256,7 @@ struct W4Tiles {
 // UP: half of a wave's rows of pieces are gate channels, half the same up channels, and h = silu(g) u is stored.
 template <WeightFormat F, int S, int BM, bool UP>
 struct Kernel {
-    typedef W4Tiles<F, S, BM> Tiles;
+    typedef W4Tiles<F, S, BM, !UP> Tiles;
     static constexpr int NT = Tiles::NT, kOut = UP ? NT / 2 : NT;            // rows of pieces that a wave stores
     static constexpr int kCols = kGemmWaves * kOut * 16;
     static constexpr float kValue = Weights<F, S>::kUnit;
@@ -253,12 +288,26 @@ struct Kernel {
         });
     }
 
+    // A lane has 4 rows of one channel; two neighbours swap, so that each has 2 rows of 2 channels: the even one the first two.
+    static __device__ __forceinline__ void swap_rows(const float (&v)[4], int odd, float (&x)[4]) {
+        const float x0 = dpp_f<0xB1>(odd ? v[0] : v[2]), x1 = dpp_f<0xB1>(odd ? v[1] : v[3]);
+        x[0] = odd ? x0 : v[0], x[1] = odd ? v[2] : x0;
+        x[2] = odd ? x1 : v[1], x[3] = odd ? v[3] : x1;
+    }
+
     template <int MT>
     __device__ __forceinline__ void tile() {
         f32x4 acc[NT][MT];
         g.template run<MT>(acc);
-        // a lane has 4 rows of one channel; two neighbours swap so that each has 2 channels of 2 rows.  Both are rounded to bf16: y for
-        // good, h as the 16-bit operand of the next product (see stream_product for what that costs)
+        // the units of the rows of h, one or two a lane
+        constexpr int kUnits = UP ? 1 : (MT * 16 + kWave - 1) / kWave;
+        float units[kUnits];
+        if constexpr (!UP)
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int m = i * kWave + lane_id();
+                units[i] = m < now.rows ? *row_unit(const_cast<uint16_t*>(p.s) + (now.row0 + m) * p.sp, p.K) : 0.0f;
+            }
         const int wave = wave_id(), r = lane_id() & 15, odd = r & 1;
         int m_at = (lane_id() >> 4) * 4 + odd * 2;
         asm("" : "+v"(m_at));      // not to be looked into: all rows' addresses in registers (20 more) would slow the tile down by 2%
@@ -273,12 +322,33 @@ struct Kernel {
                     v[i] = acc[b][a][i] * kValue;
                     if constexpr (UP) v[i] = v[i] * sigmoid(v[i]) * (acc[b + kOut][a][i] * kValue);
                 }
-                const float x0 = dpp_f<0xB1>(odd ? v[0] : v[2]), x1 = dpp_f<0xB1>(odd ? v[1] : v[3]);
-                if (n >= p.N) continue;
                 const int m = m_at + a * 16;
-                uint16_t* out = p.out + (now.row0 + m) * p.op + n;
-                if (m < now.rows) *reinterpret_cast<uint32_t*>(out) = odd ? pack_bf16x2(x0, v[2]) : pack_bf16x2(v[0], x0);
-                if (m + 1 < now.rows) *reinterpret_cast<uint32_t*>(out + p.op) = odd ? pack_bf16x2(x1, v[3]) : pack_bf16x2(v[1], x1);
+                uint16_t* out = p.out + (now.row0 + m) * p.op;
+                float x[4];
+                uint32_t first, second;
+                if constexpr (UP) {
+                    // a wave's 16 channels are a block, which 16 neighbouring lanes have; one of them for each row stores its number
+                    int e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[i] = block_number(max_bits<16>(size_bits(v[i])));
+                        v[i] = shared_value(v[i], e[i]);
+                    }
+                    const int row = m_at - odd * 2 + a * 16 + r;
+                    if (r < 4 && row < now.rows && n < p.N)
+                        p.out[(now.row0 + row) * p.op + p.N + now.n0 / kShared + wave] = (uint16_t)(r == 0 ? e[0] : r == 1 ? e[1] : r == 2 ? e[2] : e[3]);
+                    swap_rows(v, odd, x);
+                    first = pack_f16x2(x[0], x[1]);
+                    second = pack_f16x2(x[2], x[3]);
+                } else {
+                    const float u0 = __shfl(units[a / 4], m & 63), u1 = __shfl(units[a / 4], (m + 1) & 63);
+                    swap_rows(v, odd, x);
+                    first = pack_bf16x2(x[0] * u0, x[1] * u0);
+                    second = pack_bf16x2(x[2] * u1, x[3] * u1);
+                }
+                if (n < p.N && m < now.rows) *reinterpret_cast<uint32_t*>(out + n) = first;
+                if (n < p.N && m + 1 < now.rows) *reinterpret_cast<uint32_t*>(out + p.op + n) = second;
+                __builtin_amdgcn_sched_barrier(0);      // one step's after another's, for the registers
             }
         }
     }
@@ -342,13 +412,19 @@ hipError_t by_group(const Handle& h, const Params& p, int group, W4Kernel kernel
 
 hipError_t launch_w4_tile_up(const Handle& h, const W4Args& a, W4Kernel kernel, hipStream_t stream) {
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, (const uint16_t*)a.x, WeightArgs{(const char*)a.w13.values, (const char*)a.w13.scales, 2 * a.inter, a.hidden},
-                   a.h, a.inter, a.hidden, a.hidden, row_pitch(a.inter)};
+                   a.h, a.inter, a.hidden, a.hidden, h_pitch(a.inter)};
     return a.int4 ? by_group<kWeightsInt4, true>(h, p, a.group, kernel, stream) : by_group<kWeightsE2m1, true>(h, p, a.group, kernel, stream);
 }
 
 hipError_t launch_w4_tile_down(const Handle& h, const W4Args& a, W4Kernel kernel, hipStream_t stream) {
+    // row tiles that any routing can give
+    const int64_t entries = (int64_t)h.T * h.K, busy = entries < h.El ? entries : h.El;
+    hipLaunchKernelGGL(k_one_number, grid_of((entries + (kUnitRows - 1) * busy) / kUnitRows), dim3(kUnitRows * kWave), 0, stream, h.ws.cnt_local, h.ws.psum,
+                       h.El, a.h, a.inter);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const Params p{h.ws.cnt_local, h.ws.psum, h.El, a.h, WeightArgs{(const char*)a.w2.values, (const char*)a.w2.scales, a.hidden, a.inter},
-                   (uint16_t*)a.y, a.hidden, a.inter, row_pitch(a.inter), a.hidden};
+                   (uint16_t*)a.y, a.hidden, a.inter, h_pitch(a.inter), a.hidden};
     return a.int4 ? by_group<kWeightsInt4, false>(h, p, a.group, kernel, stream) : by_group<kWeightsE2m1, false>(h, p, a.group, kernel, stream);
 }
 

@@ -11,15 +11,20 @@
 //          (exact): e2m1 by the conversion instruction, integers (-8 .. 7, two's complement) by way of one that gives a sixteenth
 //          of them as fp32 (kUnit).  K is filled up with zeros to whole pieces.  A piece's scales are [16 rows][groups].
 //
+// e4m3 and 4-bit codes are exact in fp16, too (kFitsF16).
+//
 // The rows that meet the weights are the instruction's first operand, so lane (r, g) ends up with weight row r's sums of rows
 // 4 g .. 4 g + 3: one scale per group is all that it needs.
 #pragma once
 
 #include "ep_device.hpp"
 #include "ep_gemm_core.hpp"
+#include "ep_h_rows.hpp"
 #include "ep_internal.hpp"
 
 namespace ep {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kPieceK = 128, kPieceRows = 16, kPieceBytes = 1024;
 inline __host__ __device__ int pieces_of(int K) { return (K + kPieceK - 1) / kPieceK; }
@@ -47,10 +52,6 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t lane,
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)wave, 0));
 }
 
-// The upper halves of two floats that bf16 holds exactly.
-__device__ __forceinline__ int upper_halves(float lo, float hi) {
-    return (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
-}
 // Eight codes, widened pair by pair.
 template <bool INT4>
 struct Codes;
@@ -64,6 +65,7 @@ struct Codes<true> {
         return __builtin_amdgcn_cvt_off_f32_i4((int)(i == 0 ? q : i == 3 ? q >> 24 : q >> (i * 8) & 0xffu));
     }
     __device__ __forceinline__ int pair(int i) const { return upper_halves(sixteenth(even, i), sixteenth(odd, i)); }
+    __device__ __forceinline__ int pair16(int i) const { return __builtin_bit_cast(int, __builtin_amdgcn_cvt_pkrtz(sixteenth(even, i), sixteenth(odd, i))); }
 };
 template <>
 struct Codes<false> {
@@ -76,11 +78,23 @@ struct Codes<false> {
                                   : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 3);
         return __builtin_bit_cast(int, v);
     }
+    __device__ __forceinline__ int pair16(int i) const {
+        const f16x2 v = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 0)
+                        : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 1)
+                        : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 2)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 3);
+        return __builtin_bit_cast(int, v);
+    }
 };
 template <bool INT4>
 __device__ __forceinline__ bf16x8 widen_codes(uint32_t q) {
     const Codes<INT4> c(q);
     return __builtin_bit_cast(bf16x8, i32x4{c.pair(0), c.pair(1), c.pair(2), c.pair(3)});
+}
+template <bool INT4>
+__device__ __forceinline__ f16x8 widen_codes16(uint32_t q) {
+    const Codes<INT4> c(q);
+    return __builtin_bit_cast(f16x8, i32x4{c.pair16(0), c.pair16(1), c.pair16(2), c.pair16(3)});
 }
 
 // The bf16 scales of a row's S groups.
@@ -111,6 +125,10 @@ struct GroupScales {
     __device__ __forceinline__ float get(int group) const { return group & 1 ? bf16hi(v[group / 2]) : bf16lo(v[group / 2]); }
 };
 
+// of_block(): of the numbers of a piece's eight blocks (ep_h_rows.hpp), the one whose block the lane's terms of instruction j are in; here for
+// k_of(j, g) = 32 j + 8 g.
+__device__ __forceinline__ uint32_t of_block_32(i32x4 e, int j, int g) { return __builtin_amdgcn_ubfe((uint32_t)e[j], (g >> 1) * 16, 16); }
+
 // NF rows of pieces of one matrix; S: groups of a piece (4-bit).  init(): the first row of the workgroup (uniform), and of each
 // row of pieces how many weight rows behind it stands (a multiple of 16) and how many rows exist from there on.
 template <WeightFormat F, int S>
@@ -119,13 +137,14 @@ struct Weights;
 template <>
 struct Weights<kWeightsBf16, 0> {
     static constexpr int kGroups = 1;
-    static constexpr bool kScaled = false, kTail = true;
+    static constexpr bool kScaled = false, kTail = true, kFitsF16 = false;
     static constexpr float kUnit = 1.0f;
     struct Raw {
         i32x4 v[4];
     };
     static __device__ __forceinline__ int k_of(int j, int g) { return j * 32 + g * 8; }
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) { return __builtin_bit_cast(bf16x8, raw.v[j]); }
+    static __device__ __forceinline__ uint32_t of_block(i32x4 e, int j, int g) { return of_block_32(e, j, g); }
 
     template <int NF>
     struct Rows {
@@ -154,7 +173,7 @@ struct Weights<kWeightsBf16, 0> {
 template <>
 struct Weights<kWeightsE4m3, 0> {
     static constexpr int kGroups = 1;
-    static constexpr bool kScaled = true, kTail = false;
+    static constexpr bool kScaled = true, kTail = false, kFitsF16 = true;
     static constexpr float kUnit = 1.0f;
     struct Raw {
         i32x4 v[2];
@@ -164,6 +183,18 @@ struct Weights<kWeightsE4m3, 0> {
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) {
         const i32x4 q = raw.v[j >> 1];
         return widen_e4m3x8(j & 1 ? i32x2{q[2], q[3]} : i32x2{q[0], q[1]});
+    }
+    static __device__ __forceinline__ f16x8 fragment16(const Raw& raw, int j) {
+        const i32x4 q = raw.v[j >> 1];
+        const int a = q[j & 1 ? 2 : 0], b = q[j & 1 ? 3 : 1];
+        const f16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false), v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+        const f16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false), v3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+        return f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+    }
+    static __device__ __forceinline__ uint32_t of_block(i32x4 e, int j, int g) {
+        int lower = e[(j >> 1) * 2], upper = e[(j >> 1) * 2 + 1];
+        asm("" : "+v"(lower), "+v"(upper));      // (as an index that differs between lanes they would go to memory)
+        return __builtin_amdgcn_ubfe((uint32_t)(g >> 1 ? upper : lower), (g & 1) * 16, 16);
     }
     static __device__ __forceinline__ float scale_of(const Raw& raw, int) { return raw.scale; }
 
@@ -197,7 +228,7 @@ struct Weights<kWeightsE4m3, 0> {
 template <WeightFormat F, int S>
 struct Weights {
     static constexpr int kGroups = S;
-    static constexpr bool kScaled = true, kTail = true;
+    static constexpr bool kScaled = true, kTail = true, kFitsF16 = true;
     static constexpr float kUnit = F == kWeightsInt4 ? 16.0f : 1.0f;
     struct Raw {
         i32x4 v;
@@ -207,6 +238,10 @@ struct Weights {
     static __device__ __forceinline__ bf16x8 fragment(const Raw& raw, int j) {
         return widen_codes<F == kWeightsInt4>((uint32_t)raw.v[j]);
     }
+    static __device__ __forceinline__ f16x8 fragment16(const Raw& raw, int j) {
+        return widen_codes16<F == kWeightsInt4>((uint32_t)raw.v[j]);
+    }
+    static __device__ __forceinline__ uint32_t of_block(i32x4 e, int j, int g) { return of_block_32(e, j, g); }
     static __device__ __forceinline__ float scale_of(const Raw& raw, int group) { return raw.s.get(group); }
 
     template <int NF>
@@ -230,34 +265,60 @@ struct Weights {
     };
 };
 
-// acc[MT] += the piece's products with 16 * MT rows (x: a fragment per row tile and instruction).
-template <class W, int MT>
-__device__ __forceinline__ void add_piece(const typename W::Raw& raw, const i32x4 (&x)[MT][4], f32x4 (&acc)[MT]) {
-    constexpr int kPer = 4 / W::kGroups;
+// acc[NF][MT] += NF pieces' products with 16 * MT rows (x: a fragment per row tile and instruction).  H: the rows are h's, in fp16.
+template <class W, bool H, int MT, int NF>
+__device__ __forceinline__ void add_pieces(const typename W::Raw (&raw)[NF], const i32x4 (&x)[MT][4], f32x4 (&acc)[NF][MT]) {
+    if constexpr (H && !W::kFitsF16) {
+        static_assert(!W::kScaled);
 #pragma unroll
-    for (int s = 0; s < W::kGroups; ++s) {
-        f32x4 part[MT];
+        for (int j = 0; j < 4; ++j) {
+            i32x4 first[MT], second[MT];
 #pragma unroll
-        for (int a = 0; a < MT; ++a) part[a] = W::kScaled ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[a];
+            for (int a = 0; a < MT; ++a) two_bf16(x[a][j], &first[a], &second[a]);
 #pragma unroll
-        for (int j = s * kPer; j < (s + 1) * kPer; ++j) {
-            const bf16x8 f = W::fragment(raw, j);
+            for (int b = 0; b < NF; ++b)
 #pragma unroll
-            for (int a = 0; a < MT; ++a) part[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][j]), f, part[a], 0, 0, 0);
+                for (int a = 0; a < MT; ++a) {
+                    const bf16x8 f = W::fragment(raw[b], j);
+                    acc[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, first[a]), f, acc[b][a], 0, 0, 0);
+                    acc[b][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, second[a]), f, acc[b][a], 0, 0, 0);
+                }
         }
-        if constexpr (W::kScaled) {
-            const float scale = W::scale_of(raw, s);
+    } else {
+        constexpr int kPer = 4 / W::kGroups;
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
+        for (int b = 0; b < NF; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[a][i] = fmaf(part[a][i], scale, acc[a][i]);
-                // here, not wherever acc is used next: the compiler would sink it past the next loads' branch and keep all parts
-                asm volatile("" : "+v"(acc[a]));
+            for (int s = 0; s < W::kGroups; ++s) {
+                f32x4 part[MT];
+#pragma unroll
+                for (int a = 0; a < MT; ++a) part[a] = W::kScaled ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[b][a];
+#pragma unroll
+                for (int j = s * kPer; j < (s + 1) * kPer; ++j) {
+                    if constexpr (H) {
+                        const f16x8 f = W::fragment16(raw[b], j);
+#pragma unroll
+                        for (int a = 0; a < MT; ++a) part[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[a][j]), f, part[a], 0, 0, 0);
+                    } else {
+                        const bf16x8 f = W::fragment(raw[b], j);
+#pragma unroll
+                        for (int a = 0; a < MT; ++a) part[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][j]), f, part[a], 0, 0, 0);
+                    }
+                }
+                if constexpr (W::kScaled) {
+                    const float scale = W::scale_of(raw[b], s);
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[b][a][i] = fmaf(part[a][i], scale, acc[b][a][i]);
+                        // here, not wherever acc is used next: the compiler would sink it past the next loads' branch and keep all parts
+                        asm volatile("" : "+v"(acc[b][a]));
+                    }
+                } else {
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) acc[b][a] = part[a];
+                }
             }
-        } else {
-#pragma unroll
-            for (int a = 0; a < MT; ++a) acc[a] = part[a];
-        }
     }
 }
 

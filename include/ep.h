@@ -320,8 +320,8 @@ ep_status_t ep_combine_reduce(ep_handle_t handle, const void* partials, int hidd
 ep_status_t ep_combine_backward(ep_handle_t handle, const void* grad_out, int hidden, const void* y, int64_t y_rows,
                                 const float* topk_weights, void* grad_y, float* grad_topk_weights, void* stream);
 
-/* Bytes of device workspace of ep_expert_ffn (backward = 0) or ep_expert_ffn_backward (backward != 0; enough for the
- * forward pass too) for a handle of `recv_capacity` rows.  Host only.  Returns 0 for arguments outside the limits. */
+/* Bytes of device workspace of ep_expert_ffn and ep_expert_ffn_w4 (backward = 0) or ep_expert_ffn_backward (backward != 0;
+ * enough for the forward pass too) for a handle of `recv_capacity` rows.  Host only.  Returns 0 for arguments outside the limits. */
 size_t ep_expert_ffn_workspace_bytes(int64_t recv_capacity, int hidden, int intermediate, int backward);
 
 /*
@@ -435,7 +435,8 @@ ep_status_t ep_w4_pack(const uint8_t* codes, const void* scales, ep_weight_forma
 
 /*
  * ep_expert_ffn_w4 -- ep_expert_ffn with bf16 rows and 4-bit weights.  The codes are widened exactly, a group's products are
- * summed in fp32 and take the scale there; h is rounded once to bf16, y once.
+ * summed in fp32 and take the scale there; h keeps 11 bits (all but 2^-11 of a value, or 2^-23 of the largest of its row), y is
+ * rounded once to bf16.
  *
  *   handle, recv_x, rows, y, workspace   as in ep_expert_ffn (bf16; workspace of ep_expert_ffn_workspace_bytes(...)).
  *   hidden, intermediate                 multiples of the group.
@@ -453,8 +454,8 @@ size_t ep_moe_few_workspace_bytes(int num_tokens, int num_topk, int intermediate
  * §4.3: at small batches launches, not bytes, set the time): layout, dispatch, experts and combine of up to 128 tokens.
  *   out[t] = sum_k w[t,k] * ffn_e(x[t]) + bias[t]      e = topk_idx[t,k], over the entries whose expert is this rank's
  *   ffn_e(x) = (silu(x . w13[e][0..I)) * (x . w13[e][I..2I))) . w2[e]
- * Sums are fp32, the one over k ascending; h is rounded once to bf16 between the two products, out once; the experts' outputs
- * are not rounded before they are summed.  Rows are bf16 beside every format of weights.
+ * Sums are fp32, the one over k ascending; h keeps 11 bits between the two products (all but 2^-11 of a value, or 2^-14 of the
+ * largest of its eight neighbours), out is rounded once to bf16; the experts' outputs are not rounded before they are summed.  Rows are bf16 beside every format of weights.
  *
  *   x             device bf16 [num_tokens, hidden].
  *   topk_idx      device int64 [num_tokens, num_topk]; entries outside this rank's experts, -1 or anything else, add nothing.  An

@@ -282,40 +282,40 @@ hipError_t launch_down(const Params& p, hipStream_t stream) {
 // few_by_entry says when that pays.)
 //
 // Every row of the instruction's first operand is the entry's, so half of them can be second parts, at no cost.  h takes 16 bits in
-// the workspace: eight channels share the exponent of the largest, E, each has 15 bits m of m 2^(E - 140) (2^-14 of the largest at most is
-// lost), and the lowest bit of the i-th holds bit i of E.  Infinities and NaN: E = 255, m = 1, -1 and 2, and 0 beside them.
+// the workspace: fp16 as in ep_h_rows.hpp, but of eight channels, whose number E = 16 n + 4 (or 0, and n = 0) stands in the lowest bits of
+// the first five, bit i of n in the i-th; these keep a bit less (all but 2^-10 of a value, or 2^-22 of the largest of the eight).  The eight are
+// taken to fp32 and apart into two bf16, each by its number.
+constexpr int kNumberBits = 5;
 
 // Channel c of the lanes' eight; all of them call it.
-__device__ __forceinline__ uint16_t shared_exponent(float v, int c) {
-    const uint32_t size = size_bits(v);
-    const int e = (int)(max_bits<8>(size) >> 23);
-    int m;
-    if (e == 255) m = size > 0x7f800000u ? 2 : size < 0x7f800000u ? 0 : v < 0.0f ? -1 : 1;
-    else m = (int)__builtin_amdgcn_fmed3f(rintf(ldexpf(v, 140 - e)), -16383.0f, 16383.0f);
-    return (uint16_t)(m * 2 | (e >> (c & 7) & 1));
+__device__ __forceinline__ uint16_t value_and_bit(float v, int c) {
+    const int e = block_number(max_bits<8>(size_bits(v)));
+    uint32_t q = __builtin_bit_cast(uint16_t, (_Float16)shared_value(v, e));
+    if ((c & 7) < kNumberBits) {
+        q += q & q >> 1 & 1u;      // to the nearest without the last bit, or from the middle to the even one (an infinity's is 0)
+        q = (q & ~1u) | ((uint32_t)e >> (4 + (c & 7)) & 1u);
+    }
+    return (uint16_t)q;
 }
 // Eight channels' two parts.
 __device__ __forceinline__ void two_parts(i32x4 q, i32x4* first, i32x4* second) {
-    const uint32_t t = (uint32_t)((q[0] & 0x10001) | (q[1] & 0x10001) << 2 | (q[2] & 0x10001) << 4 | (q[3] & 0x10001) << 6);
-    const int e = (int)((t & 0x55u) | (t >> 15 & 0xaau));
-    const bool special = ballot(e == 255) != 0;
-    const auto value = [&](int m) {
-        float v = ldexpf((float)m, e - 140);
-        if (special && e == 255) v = m == 0 ? 0.0f : m == 2 ? __builtin_nanf("") : m > 0 ? __builtin_inff() : -__builtin_inff();
-        return v;
-    };
-    const auto rest = [&](float v) { return special ? rest_of(v) : v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u); };
+    const uint32_t n = (uint32_t)((q[0] & 1) | (q[0] >> 15 & 2) | (q[1] & 1) << 2 | (q[1] >> 13 & 8) | (q[2] & 1) << 4);
+    q[0] &= ~0x10001, q[1] &= ~0x10001, q[2] &= ~1;
+    const int by = (int)n * 16 + 4 - 154;
+    const bool large = ballot(n == 17) != 0;      // an infinity or NaN among them, perhaps
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const float a = value((int)((uint32_t)q[d] << 16) >> 17), b = value(q[d] >> 17);
+        const f16x2 v = __builtin_bit_cast(f16x2, (int)q[d]);
+        const float a = ldexpf((float)v[0], by), b = ldexpf((float)v[1], by);
         (*first)[d] = upper_halves(a, b);
-        (*second)[d] = (int)pack_bf16x2(rest(a), rest(b));
+        // (11 bits: what the first part leaves is exact in its upper half)
+        (*second)[d] = large ? upper_halves(rest_of(a), rest_of(b)) : upper_halves(a - upper_half(a), b - upper_half(b));
     }
 }
 
 // acc[NF] += pieces first, first + step, ... below `end` of NF rows of pieces by one row x of K channels; the wave's part of it stands
 // in LDS, up to `room` pieces at a time.  PARTS 1: bf16, and every row of the instruction's first operand is x.  PARTS 2: as
-// shared_exponent leaves them, and even rows are first parts, odd ones second.
+// value_and_bit leaves them, and even rows are first parts, odd ones second.
 template <class W, int PARTS, int NF>
 __device__ __forceinline__ void one_row(const typename W::template Rows<NF>& w, const uint16_t* x, int K, int first, int step, int end,
                                         char* lds, int room, f32x4 (&acc)[NF][1]) {
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void k_one_up(Params p, int cols
         up += sums[v * NF * 16 + kHalf + c];
     }
     gate *= W::kUnit;
-    p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = shared_exponent(gate * sigmoid(gate) * (up * W::kUnit), c);
+    p.h[(int64_t)entry * row_pitch(p.I) + n0 + c] = value_and_bit(gate * sigmoid(gate) * (up * W::kUnit), c);
 }
 
 // Waves take parts of entries in turn, i % parts of i / parts, `room` pieces of them at a time.

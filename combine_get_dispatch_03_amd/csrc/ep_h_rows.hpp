@@ -42,8 +42,9 @@ __device__ __forceinline__ uint32_t size_bits(float v) { return __builtin_bit_ca
 __device__ __forceinline__ int upper_halves(float lo, float hi) {
     return (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
 }
+__device__ __forceinline__ float upper_half(float v) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u); }
 __device__ __forceinline__ float rest_of(float v) {
-    const float rest = v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u);
+    const float rest = v - upper_half(v);
     return size_bits(v) >= 0x7f800000u ? 0.0f : rest;
 }
 

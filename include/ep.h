@@ -454,8 +454,8 @@ size_t ep_moe_few_workspace_bytes(int num_tokens, int num_topk, int intermediate
  * §4.3: at small batches launches, not bytes, set the time): layout, dispatch, experts and combine of up to 128 tokens.
  *   out[t] = sum_k w[t,k] * ffn_e(x[t]) + bias[t]      e = topk_idx[t,k], over the entries whose expert is this rank's
  *   ffn_e(x) = (silu(x . w13[e][0..I)) * (x . w13[e][I..2I))) . w2[e]
- * Sums are fp32, the one over k ascending; h keeps 11 bits between the two products (all but 2^-11 of a value, or 2^-14 of the
- * largest of its eight neighbours), out is rounded once to bf16; the experts' outputs are not rounded before they are summed.  Rows are bf16 beside every format of weights.
+ * Sums are fp32, the one over k ascending; h keeps 10 bits and more between the two products (all but 2^-10 of a value, or 2^-22 of
+ * the largest of its row), out is rounded once to bf16; the experts' outputs are not rounded before they are summed.  Rows are bf16 beside every format of weights.
  *
  *   x             device bf16 [num_tokens, hidden].
  *   topk_idx      device int64 [num_tokens, num_topk]; entries outside this rank's experts, -1 or anything else, add nothing.  An

@@ -144,3 +144,21 @@ def test_every_scale(ep, power):
             i, k = (idx == e).nonzero(as_tuple=True)
             want.index_add_(0, i, ffn64(x[i].double(), *expert(e)))
         assert_one_rounding(ep.ep_moe_few(x, idx, None, call[0], call[1], w13_scales=call[2], w2_scales=call[3]), want, "%s out" % fmt)
+
+
+@pytest.mark.parametrize("T,K,E", [(1, 2, 4), (1, 20, 24), (5, 2, 16), (20, 2, 4), (90, 4, 8)])
+@pytest.mark.parametrize("by", [9, -9])
+def test_single_channels_of_unlike_size(ep, T, K, E, by):
+    """The same with every other channel, so that neighbours differ."""
+    H, I = 256, 648
+    g = torch.Generator(device=DEV).manual_seed(T)
+    (w13, w2, _, _), expert = weights(ep, "bf16", g, E, H, I)
+    w13[:, I::2] *= 2.0 ** by
+    w2[:, :, ::2] *= 2.0 ** -by
+    idx = table(T, E, K, "uniform", 3).to(DEV)
+    x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+    want = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+    for e in idx.unique().tolist():
+        i, k = (idx == e).nonzero(as_tuple=True)
+        want.index_add_(0, i, ffn64(x[i].double(), *expert(e)))
+    assert_one_rounding(ep.ep_moe_few(x, idx, None, w13, w2), want, "out")

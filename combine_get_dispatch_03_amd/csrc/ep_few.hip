@@ -9,7 +9,7 @@
 // are weighted and summed in ascending k, so that nothing depends on the order in which waves finish.
 //
 // Measured: 32 tokens, 256 e4m3 experts of 7168 x 2048, top-8 (7.2 GB): 808 us (6.0 TB/s) and 465 (5.2 TB/s; 224 workgroups on 256
-// CUs).  One token, int4: 24 and 17 us (5.0 and 3.6 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 128 and 98 us
+// CUs).  One token, int4: 24 and 16.5 us (5.0 and 3.7 TB/s).  61 tokens on 32 e2m1 experts in groups of 32, uneven: 128 and 98 us
 // (4.1 and 2.7 TB/s): with some 16 rows beside a piece of 1 KiB the rows' 4 KiB from L2 bound it, not the weights.
 // Splitting all items' pieces evenly over the waves of the second kernel gained nothing (227 and 231 us in all, 1262 and 1271).
 #include "ep_few_rules.hpp"

@@ -30,16 +30,17 @@ def rules():
 
 # tokens, top-k, experts: sizes whose times stand beside the rule (us with int4, e4m3 and bf16 weights by themselves / together)
 @pytest.mark.parametrize("T,K,E,by_entry", [
-    (1, 8, 16, True),       # 41 / 43, 67 / 72, 132 / 131
-    (2, 4, 8, True),        # 40 / 43, 67 / 71, 130 / 129
-    (4, 2, 8, True),        # small experts 11.3 / 13.8
-    (2, 8, 32, True),       # 66 / 71, 117 / 119
-    (2, 4, 4, False),       # 35 / 33, 53 / 40, 114 / 69
-    (2, 8, 8, False),       # 60 / 44, 110 / 72, 235 / 130
-    (4, 4, 4, False),       # 56 / 33, 93 / 41, 206 / 69
-    (16, 1, 1, False),      # 51 / 32, 89 / 32, 165 / 34
-    (4, 4, 16, False),      # 62 / 57, 109 / 95, 235 / 185
-    (3, 4, 12, False),      # 53 / 43, 80 / 71, 168 / 128
+    (1, 8, 16, True),       # 42 / 45, 68 / 74, 132 / 132
+    (2, 4, 8, True),        # 41 / 44, 67 / 74, 132 / 130
+    (4, 2, 8, True),        # small experts 11.6 / 15.6
+    (2, 8, 32, True),       # 68 / 73, 117 / 121
+    (1, 32, 32, True),
+    (2, 4, 4, False),       # 36 / 35, 53 / 42, 119 / 70
+    (2, 8, 8, False),       # 62 / 45, 112 / 75, 242 / 131
+    (4, 4, 4, False),       # 58 / 35, 94 / 43, 212 / 71
+    (16, 1, 1, False),      # 53 / 34, 91 / 34, 168 / 40
+    (4, 4, 16, False),      # 64 / 58, 110 / 96, 238 / 190
+    (3, 4, 12, False),      # 54 / 44, 82 / 74, 170 / 130
     (17, 1, 1024, False),   # more entries than waves
 ])
 def test_entries_by_themselves(T, K, E, by_entry):

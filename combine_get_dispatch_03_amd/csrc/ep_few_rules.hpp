@@ -4,7 +4,7 @@
 
 namespace ep {
 
-constexpr int kFewWaves = 16;      // of a workgroup of the second kernel: as many entries can stand by themselves
+constexpr int kFewWaves = 16;      // of a workgroup of the second kernel: as many entries of several tokens can stand by themselves
 
 // Each entry by itself, or an expert's entries together.  An entry by itself has its weights under way at once, but reads them
 // itself; together, an expert's are read once, after its entries are found.  us of the whole call, by themselves / together, experts of
@@ -18,7 +18,8 @@ constexpr int kFewWaves = 16;      // of a workgroup of the second kernel: as ma
 //    4 tokens of top-4 (4)       58 /  35               94 /  43               212 /  71
 // Routed at random, 16 entries: of 16 experts (int4) 64 / 58, of 24 68 / 73, of 32 68 / 73, of 64 69 / 73; e4m3 110 / 96, 116 / 120, 113 / 121,
 // 116 / 124; 8 entries of 8 experts 41 / 43 and 72 / 78.  Small experts, 256 x 512 in bf16: 8 entries of 8 11.6 / 15.6, of 4 11.6 / 13.0, 16
-// of 8 16.0 / 16.3.  One token's entries have an expert each; of several tokens enough experts for few to be shared.
+// of 8 16.0 / 16.3.  One token's entries have an expert each (and its workspace room for no other form of
+// h); of several tokens enough experts for few to be shared.
 inline bool few_by_entry(int T, int K, int E) {
     const int n = T * K;
     return T == 1 || (n <= kFewWaves && (n <= 8 ? n : 2 * n) <= E);
